@@ -42,6 +42,7 @@ DS_MAX_DIM = 1 << 24
 DS_F32, DS_BF16 = 0, 1
 DS_ROPE_HALF_SPLIT, DS_ROPE_INTERLEAVED = 0, 1
 DS_ERR_TOKEN_RANGE, DS_ERR_POSITION, DS_ERR_WAIT_TIMEOUT, DS_ERR_SAMPLING = 1, 2, 4, 8
+DS_ERR_NO_BLOCKS = 16
 DS_STEP_ADVANCE = 1
 DS_STEP_PHASE_TIMES = 2
 DS_STEP_TRACE = 4
@@ -124,6 +125,15 @@ _sig("ds_silu_mul", ctypes.c_int, P, I64, P, I64, P, I64, P)
 _sig("ds_attention_workspace_bytes", SZ, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, I64)
 _sig("ds_gqa_decode_attn", ctypes.c_int, P, P, P, ctypes.c_int, I64, P, ctypes.c_int, ctypes.c_int, P,
      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, F32, P, P, SZ, P)
+_sig("ds_paged_plan_workspace_bytes", SZ)
+_sig("ds_paged_plan", ctypes.c_int, P, P, ctypes.c_int, P, I64, ctypes.c_int, I64, P, ctypes.c_int, P, P, P, P, P,
+     I64, P, P, SZ, P)
+_sig("ds_rope_append_workspace_bytes", SZ)
+_sig("ds_rope_append", ctypes.c_int, P, I64, ctypes.c_int, I64, I64, P, ctypes.c_int, P, ctypes.c_int, ctypes.c_int,
+     ctypes.c_int, ctypes.c_int, F64, ctypes.c_int, P, I64, ctypes.c_int, P, P, ctypes.c_int, I64, P, P, SZ, P)
+_sig("ds_chunk_attention_workspace_bytes", SZ, ctypes.c_int, I64, ctypes.c_int, ctypes.c_int, ctypes.c_int)
+_sig("ds_gqa_chunk_attn", ctypes.c_int, P, I64, ctypes.c_int, I64, P, P, ctypes.c_int, P, P, ctypes.c_int, I64, P,
+     ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, F32, P, I64, P, SZ, P)
 _sig("ds_argmax_workspace_bytes", SZ, ctypes.c_int, I64)
 _sig("ds_greedy_argmax", ctypes.c_int, P, I64, ctypes.c_int, I64, P, P, P, SZ, P)
 _sig("ds_sample_workspace_bytes", SZ, ctypes.c_int, I64)
@@ -269,6 +279,86 @@ def ds_gqa_decode_attn(q, k_cache, v_cache, cache_rows, block_table, max_blocks_
                                  ptr(block_table), max_blocks_per_seq, block_tokens, ptr(seq_lens), n_seqs, n_qh,
                                  n_kvh, head_dim, scale, ptr(out), ptr(ws), nbytes(ws), stream_handle(stream)),
           "ds_gqa_decode_attn")
+
+
+def _i32(t, n, name):
+    """Address of an int32 device tensor of at least n elements (contiguous)."""
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s: a contiguous int32 tensor of %d elements is needed" % (name, n))
+    return t.data_ptr()
+
+
+def _dense(t, n, name):
+    """Address of a contiguous tensor of at least n elements."""
+    if not t.is_contiguous() or t.numel() < n:
+        raise ValueError("%s: a contiguous tensor of %d elements is needed" % (name, n))
+    return t.data_ptr()
+
+
+def ds_paged_plan_workspace_bytes():
+    return lib.ds_paged_plan_workspace_bytes()
+
+
+def ds_paged_plan(cached_lens, new_lens, n_seqs, free_blocks, block_tokens, cache_rows, block_table,
+                  max_blocks_per_seq, row_starts, seq_lens, row_seq, positions, slots, max_rows, n_taken, ws,
+                  stream=None):
+    """Block table entries, row starts, positions and cache slots of a ragged
+    step from its lengths; free_blocks may be None (no block left)."""
+    n_free = 0 if free_blocks is None else free_blocks.numel()
+    check(lib.ds_paged_plan(_i32(cached_lens, n_seqs, "cached_lens"), _i32(new_lens, n_seqs, "new_lens"), n_seqs,
+                            _i32(free_blocks, n_free, "free_blocks") if n_free else None, n_free, block_tokens,
+                            cache_rows, _i32(block_table, n_seqs * max_blocks_per_seq, "block_table"),
+                            max_blocks_per_seq, _i32(row_starts, n_seqs + 1, "row_starts"),
+                            _i32(seq_lens, n_seqs, "seq_lens"), _i32(row_seq, max_rows, "row_seq"),
+                            _i32(positions, max_rows, "positions"), _i32(slots, max_rows, "slots"), max_rows,
+                            _i32(n_taken, 1, "n_taken"), ws.data_ptr(), nbytes(ws), stream_handle(stream)),
+          "ds_paged_plan")
+
+
+def ds_rope_append_workspace_bytes():
+    return lib.ds_rope_append_workspace_bytes()
+
+
+def ds_rope_append(qkv, row_stride, n_rows, positions, n_axes, pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout,
+                   q_out, k_cache, v_cache, cache_rows, slots, ws, stream=None):
+    """Rotate a ragged step's q|k|v rows and write k and v to their slots.
+    pair_axis: host uint8 numpy array of rot_dim / 2 axes, or None (one axis)."""
+    if pair_axis is not None and (pair_axis.dtype.str != "|u1" or not pair_axis.flags.c_contiguous or
+                                  pair_axis.size < rot_dim // 2):
+        raise ValueError("pair_axis: a contiguous uint8 array of rot_dim / 2 axes is needed")
+    if v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache: one dtype is needed")
+    n_kv = cache_rows * n_kvh * head_dim
+    # qkv may be a view of wider rows: its reach is what the storage holds from its start on
+    reach = qkv.untyped_storage().nbytes() // qkv.element_size() - qkv.storage_offset()
+    check(lib.ds_rope_append(qkv.data_ptr(), reach, dtype_code(qkv), row_stride, n_rows,
+                             _i32(positions, n_axes * n_rows, "positions"), n_axes,
+                             None if pair_axis is None else pair_axis.ctypes.data, n_qh, n_kvh, head_dim, rot_dim,
+                             base, layout, _dense(q_out, q_out.numel(), "q_out"), q_out.numel(), dtype_code(q_out),
+                             _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"), dtype_code(k_cache),
+                             cache_rows, _i32(slots, n_rows, "slots"), ws.data_ptr(), nbytes(ws),
+                             stream_handle(stream)), "ds_rope_append")
+
+
+def ds_chunk_attention_workspace_bytes(n_seqs, n_rows, n_qh, n_kvh, head_dim):
+    return lib.ds_chunk_attention_workspace_bytes(n_seqs, n_rows, n_qh, n_kvh, head_dim)
+
+
+def ds_gqa_chunk_attn(q, n_rows, row_starts, seq_lens, n_seqs, k_cache, v_cache, cache_rows, block_table,
+                      max_blocks_per_seq, block_tokens, n_qh, n_kvh, head_dim, scale, out, ws, stream=None):
+    """Causal attention of a ragged step's rows over each sequence's blocks;
+    block_table None: contiguous slots."""
+    if out.dtype != q.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError("q and out, and k_cache and v_cache, need one dtype each")
+    n_kv = cache_rows * n_kvh * head_dim
+    check(lib.ds_gqa_chunk_attn(_dense(q, 0, "q"), q.numel(), dtype_code(q), n_rows,
+                                _i32(row_starts, n_seqs + 1, "row_starts"), _i32(seq_lens, n_seqs, "seq_lens"), n_seqs,
+                                _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"),
+                                dtype_code(k_cache), cache_rows,
+                                None if block_table is None else _i32(block_table, n_seqs * max_blocks_per_seq,
+                                                                      "block_table"), max_blocks_per_seq,
+                                block_tokens, n_qh, n_kvh, head_dim, scale, _dense(out, 0, "out"), out.numel(),
+                                ws.data_ptr(), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
 
 
 def ds_argmax_workspace_bytes(n_rows, n):

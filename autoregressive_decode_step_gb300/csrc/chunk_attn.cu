@@ -1,0 +1,319 @@
+// Attention of every request's new rows over its blocks of the paged K/V pool
+// ("Inside the engine", section 1: prefill runs a chunk of prompt tokens as a
+// batch of rows, causal flash attention over the chunk; section 2: chunks and
+// decode rows side by side in one step): the entry point, and the plain-core
+// kernel for the shapes and types that the tensor-core kernel does not take.
+//
+// Row j of a sequence's n new rows, L positions long with them, attends
+// positions t <= L - n + j:
+//   s_t = scale * q . k_t,  m = max s_t,  out = sum_t e^(s_t - m) v_t / sum_t e^(s_t - m)
+// in one pass over the positions with a running maximum and sum.
+//
+// chunk_simt_kernel keeps everything in fp32 (an fp32 cache has more digits
+// than a bf16 product keeps): 64 (row, head) pairs by 64 positions a step,
+// 256 threads of 4 x 4 scores and 4 x hd/16 outputs in registers, Q, K and V
+// in shared memory.  The fp32 FMA rate bounds it (chunks); work split as in
+// chunk_attn.h.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "chunk_attn.cuh"
+
+namespace ds {
+
+constexpr int kCsThreads = 256;
+constexpr int kCsRows = 64;
+constexpr int kCsStep = 64;
+constexpr int kCsMinCost = 256;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Four consecutive elements as fp32 (the row starts on 4 elements).
+__device__ __forceinline__ float4 cs_load4(const void *base, long long i, int dtype) {
+    if (dtype == DS_F32) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i));
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(base) + i));
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                       __uint_as_float(w.y & 0xffff0000u));
+}
+
+template <int HD>
+__global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kernel(const ChunkArgs a) {
+    extern __shared__ __align__(16) float sm[];
+    constexpr int KS = HD + 4;  // K rows padded: sixteen rows read at once fall into different banks
+    constexpr int PS = kCsStep + 4;
+    static_assert(PS <= KS || HD < 64, "");
+    float *sQ = sm, *sK = sQ + kCsRows * HD, *sV = sK + kCsStep * KS;
+    float *sP = sK;  // the weights take K's place once the scores are formed
+    __shared__ long long s_red[34];
+    __shared__ int s_last;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    int flags = 0;
+
+    chunk_zero_empty_rows(a);
+    ChunkWalk walk;
+    walk.init(a, s_red);
+    flags |= walk.flags;
+    ChunkSeg g;
+    while (walk.next(a, g)) {
+        const ChunkHeads hh = chunk_heads(a, g.part);
+        const int rows = g.tokens * a.part_heads;
+        for (int i = tid; i < kCsRows * (HD / 4); i += kCsThreads) {
+            const int m = i / (HD / 4), d = (i % (HD / 4)) * 4;
+            const int tok = m / a.part_heads, h = m % a.part_heads;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (tok < g.tokens && h < hh.count && d < a.hd)
+                v = cs_load4(a.q, ((long long)(g.r0 + tok) * a.n_qh + hh.first + h) * a.hd + d, a.q_dtype);
+            *reinterpret_cast<float4 *>(sQ + m * HD + d) = v;
+        }
+        float acc[4][HD / 16], mx[4], sum[4];
+        int lim[4];  // last position of each row
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mx[i] = -INFINITY;
+            sum[i] = 0.0f;
+            lim[i] = g.pos0 + (ty * 4 + i) / a.part_heads;
+#pragma unroll
+            for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.0f;
+        }
+        for (int b = g.b0; b < g.b1; ++b) {
+            const int t0 = b * kCsStep, nt = min(kCsStep, g.len - t0);
+            __syncthreads();  // the last step's weights and values are read
+            for (int i = tid; i < kCsStep * (HD / 4); i += kCsThreads) {
+                const int t = i / (HD / 4), d = (i % (HD / 4)) * 4;
+                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
+                if (t < nt && d < a.hd) {
+                    const int pos = t0 + t;
+                    const long long row = chunk_block_row(a, g.seq, pos / a.bt, flags) + pos % a.bt;
+                    const long long e = (row * a.n_kvh + hh.kv) * a.hd + d;
+                    k = cs_load4(a.k_cache, e, a.kv_dtype);
+                    v = cs_load4(a.v_cache, e, a.kv_dtype);
+                }
+                *reinterpret_cast<float4 *>(sK + t * KS + d) = k;
+                *reinterpret_cast<float4 *>(sV + t * HD + d) = v;
+            }
+            __syncthreads();
+            float s[4][4] = {};
+#pragma unroll 4
+            for (int d = 0; d < HD; d += 4) {
+                float4 qv[4], kv[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    qv[i] = *reinterpret_cast<const float4 *>(sQ + (ty * 4 + i) * HD + d);
+                    kv[i] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * i) * KS + d);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
+                        s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
+                        s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
+                        s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                    }
+            }
+            __syncthreads();  // K is read
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float top = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    // a masked score is replaced, not added to: K may hold anything there
+                    s[i][j] = t0 + tx + 16 * j <= lim[i] ? s[i][j] * (a.scale * kLog2e) : -INFINITY;
+                    top = fmaxf(top, s[i][j]);
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+                const float m_new = fmaxf(mx[i], top);
+                const float m_use = m_new == -INFINITY ? 0.0f : m_new;
+                const float keep = exp2f(mx[i] - m_use);
+                float add = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float p = exp2f(s[i][j] - m_use);
+                    sP[(ty * 4 + i) * PS + tx + 16 * j] = p;
+                    add += p;
+                }
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
+                sum[i] = sum[i] * keep + add;
+                mx[i] = m_new;
+#pragma unroll
+                for (int c = 0; c < HD / 16; ++c) acc[i][c] *= keep;
+            }
+            __syncwarp();  // a warp reads the weights of its own rows only
+            const bool masked = t0 + kCsStep - 1 > g.pos0;
+            for (int t = 0; t < nt; t += 4) {
+                float4 p4[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * PS + t);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = k == 0 ? p4[i].x : k == 1 ? p4[i].y : k == 2 ? p4[i].z : p4[i].w;
+#pragma unroll
+                    for (int c = 0; c < HD / 64; ++c) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sV + (t + k) * HD + 64 * c + tx * 4);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            // a row skips what it does not attend: 0 x an infinity there would be NaN
+                            if (masked && t0 + t + k > lim[i]) continue;
+                            acc[i][4 * c] = fmaf(p[i], v.x, acc[i][4 * c]);
+                            acc[i][4 * c + 1] = fmaf(p[i], v.y, acc[i][4 * c + 1]);
+                            acc[i][4 * c + 2] = fmaf(p[i], v.z, acc[i][4 * c + 2]);
+                            acc[i][4 * c + 3] = fmaf(p[i], v.w, acc[i][4 * c + 3]);
+                        }
+                    }
+                }
+            }
+        }
+        ChunkShare share = {};
+        bool split = g.slot >= 0;
+        if (split) {
+            share = chunk_share(a, g, walk.unit);
+            split = share.first < share.last;
+        }
+        float *rec = split ? chunk_record(a, blockIdx.x, g.slot) : nullptr;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int m = ty * 4 + i, tok = m / a.part_heads, h = m % a.part_heads;
+            if (tok >= g.tokens || h >= hh.count) continue;
+            if (split) {
+                if (tx == 0) {
+                    rec[2 * m] = mx[i];
+                    rec[2 * m + 1] = sum[i];
+                }
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c) {
+                    const int d = 64 * c + tx * 4;
+                    if (d < a.hd)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) rec[2 * a.rec_rows + m * a.hd + d + e] = acc[i][4 * c + e];
+                }
+            } else {
+                const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + h) * a.hd;
+#pragma unroll
+                for (int c = 0; c < HD / 64; ++c) {
+                    const int d = 64 * c + tx * 4;
+                    if (d < a.hd)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) store_as(a.out, o + d + e, a.q_dtype, acc[i][4 * c + e] / sum[i]);
+                }
+            }
+        }
+        if (split) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                int *ctr = a.counters + share.counter * 2;
+                s_last = atomicAdd(ctr, 1) == share.last - share.first;
+                if (s_last) *ctr = 0;  // ready for the next launch
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                chunk_join(a, g, share, walk.unit, 0, rows, tid >> 5, kCsThreads / 32);
+            }
+        }
+    }
+    if (flags) flag_error(a.err, flags);
+}
+
+static size_t cs_smem(int HD) { return (size_t)(kCsRows * HD + kCsStep * (HD + 4) + kCsStep * HD) * sizeof(float); }
+static int cs_hd(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
+
+int chunk_simt_grid() { return 2 * sm_count(); }
+
+cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream) {
+    chunk_tile_shape(a, kCsRows, 1);
+    a.step = kCsStep;
+    a.min_cost = kCsMinCost;
+    const int HD = cs_hd(a.hd);
+    const size_t smem = cs_smem(HD);
+    const int grid = HD == 256 ? sm_count() : chunk_simt_grid();
+    void (*fn)(ChunkArgs) = HD == 64 ? chunk_simt_kernel<64> : HD == 128 ? chunk_simt_kernel<128> : chunk_simt_kernel<256>;
+    const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_ex(fn, dim3(grid), dim3(kCsThreads), smem, stream, false, a);
+}
+
+void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs) {
+    a.head_parts = (a.gq + sub_rows - 1) / sub_rows;
+    a.part_heads = (a.gq + a.head_parts - 1) / a.head_parts;
+    a.tile_tokens = subs * (sub_rows / a.part_heads);
+}
+
+}  // namespace ds
+
+using namespace ds;
+
+// (row, head) pairs of the largest tile any kernel uses, and so of a record.
+static int chunk_rec_rows(int64_t n_rows, int gq) { return (int)std::min<int64_t>(kChunkMaxTileRows, n_rows * gq); }
+
+extern "C" DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t n_rows, int n_qh, int n_kvh,
+                                                            int head_dim) {
+    if (n_seqs < 1 || n_rows < 1 || n_kvh < 1 || n_qh < n_kvh || n_qh % n_kvh || head_dim < 1 || head_dim > 256 ||
+        n_rows > DS_MAX_DIM || n_qh > DS_MAX_DIM)
+        return 0;
+    const size_t grid = chunk_simt_grid();
+    return kWsHeader + align_up(grid * 2 * sizeof(int), 256) +
+           grid * 2 * (size_t)chunk_rec_rows(n_rows, n_qh / n_kvh) * (head_dim + 2) * sizeof(float);
+}
+
+extern "C" DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtype, int64_t n_rows,
+                                        const int32_t *row_starts, const int32_t *seq_lens, int n_seqs,
+                                        const void *k_cache, const void *v_cache, int kv_dtype, int64_t cache_rows,
+                                        const int32_t *block_table, int max_blocks_per_seq, int block_tokens,
+                                        int n_qh, int n_kvh, int head_dim, float scale, void *out, int64_t out_len,
+                                        void *workspace, size_t workspace_bytes, ds_stream_t stream) {
+    if (n_rows < 1 || n_seqs < 1 || n_qh < 1 || n_kvh < 1 || head_dim < 1 || block_tokens < 1 ||
+        max_blocks_per_seq < 1 || cache_rows < 1)
+        return DS_EMPTY_DIMENSION;
+    if (n_rows > DS_MAX_DIM || n_seqs > DS_MAX_DIM || n_qh > DS_MAX_DIM || cache_rows > DS_MAX_DIM ||
+        (int64_t)max_blocks_per_seq * block_tokens > DS_MAX_DIM)
+        return DS_DIMENSION_TOO_LARGE;
+    if ((q_dtype != DS_F32 && q_dtype != DS_BF16) || (kv_dtype != DS_F32 && kv_dtype != DS_BF16)) return DS_BAD_DTYPE;
+    if (n_qh % n_kvh || head_dim % 4 || head_dim > 256 || !(scale > 0.0f) || !std::isfinite(scale)) return DS_BAD_ARGUMENT;
+    if (q_len != n_rows * n_qh * head_dim) return DS_A_LENGTH_MISMATCH;
+    if (out_len != q_len) return DS_B_LENGTH_MISMATCH;
+    if (!q || !row_starts || !seq_lens || !k_cache || !v_cache || !out) return DS_BAD_ARGUMENT;
+    if (((uintptr_t)q | (uintptr_t)out | (uintptr_t)k_cache | (uintptr_t)v_cache) & 15) return DS_BAD_ARGUMENT;
+    // a split tile's rows may be written while another block still reads their q
+    const size_t qb = (size_t)q_len * (q_dtype == DS_BF16 ? 2 : 4);
+    if ((uintptr_t)q < (uintptr_t)out + qb && (uintptr_t)out < (uintptr_t)q + qb) return DS_BAD_ARGUMENT;
+    if (!block_table && (int64_t)n_seqs * max_blocks_per_seq * block_tokens > cache_rows)
+        return DS_CACHE_CAPACITY_EXCEEDED;
+    if (cache_rows < block_tokens) return DS_CACHE_CAPACITY_EXCEEDED;
+    if (!workspace || workspace_bytes < ds_chunk_attention_workspace_bytes(n_seqs, n_rows, n_qh, n_kvh, head_dim))
+        return DS_WORKSPACE_TOO_SMALL;
+    if ((uintptr_t)workspace & 255) return DS_BAD_ARGUMENT;
+    ChunkArgs a = {};
+    a.q = q;
+    a.out = out;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.q_dtype = q_dtype;
+    a.kv_dtype = kv_dtype;
+    a.n_rows = (int)n_rows;
+    a.row_starts = row_starts;
+    a.seq_lens = seq_lens;
+    a.n_seqs = n_seqs;
+    a.cache_rows = cache_rows;
+    a.block_table = block_table;
+    a.max_blocks = max_blocks_per_seq;
+    a.bt = block_tokens;
+    a.pool_blocks = cache_rows / block_tokens;
+    a.n_qh = n_qh;
+    a.n_kvh = n_kvh;
+    a.hd = head_dim;
+    a.gq = n_qh / n_kvh;
+    a.scale = scale;
+    a.rec_rows = chunk_rec_rows(n_rows, a.gq);
+    char *ws = static_cast<char *>(workspace);
+    a.err = reinterpret_cast<int *>(ws);
+    a.counters = reinterpret_cast<int *>(ws + kWsHeader);
+    a.partials = reinterpret_cast<float *>(ws + kWsHeader + align_up((size_t)chunk_simt_grid() * 2 * sizeof(int), 256));
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = launch_chunk_simt(a, s);
+    return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
+}

@@ -1,0 +1,327 @@
+// Work split of the chunk attention (attention of every request's new rows
+// over its blocks of the paged K/V pool), shared by its two kernels.
+//
+// A tile is up to `tile_tokens` consecutive new rows of one sequence times the
+// query heads that share one KV head (a group of more than `sub_heads` heads
+// is cut into equal parts, each with tiles of its own).  Its cost is the
+// number of positions its last row attends.  The costs of all tiles, ordered
+// by sequence, head and row, form one line that is cut into equal ranges, one
+// per CTA, so the load is even whatever the mix of chunks and single tokens.
+// A tile that a cut falls into is worked on by several CTAs, the cut rounded
+// down to a whole K/V step of `step` positions; their (max, sum, accumulator)
+// records are joined in CTA order by whichever contributor arrives last (a
+// counter, never a wait), so results do not depend on timing.
+//
+// Costs have a closed form (a sum over a sequence's tiles is a quadratic in
+// their number), so no plan is kept in memory: a CTA finds its range by one
+// scan over the sequences' lengths and walks on from there.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace ds {
+
+constexpr int kChunkMaxTileRows = 256;  // (row, head) pairs of the largest tile
+
+struct ChunkArgs {
+    const void *q;          // [n_rows][n_qh * hd]
+    void *out;              // same
+    const void *k_cache, *v_cache;  // [cache_rows][n_kvh * hd]
+    int q_dtype, kv_dtype;
+    int n_rows;
+    const int *row_starts;  // [n_seqs + 1]
+    const int *seq_lens;    // [n_seqs]
+    int n_seqs;
+    long long cache_rows;
+    const int *block_table;  // [n_seqs][max_blocks] or nullptr (contiguous slots)
+    int max_blocks, bt;
+    long long pool_blocks;   // whole blocks of the cache
+    int n_qh, n_kvh, hd, gq;
+    float scale;
+    int head_parts;   // tiles' heads: each KV head's gq query heads in so many parts
+    int part_heads;   // query heads of a part (the last may have fewer)
+    int tile_tokens;  // rows of a sequence per tile
+    int step;         // positions of one K/V step
+    int min_cost;     // smallest range a CTA is given, at least `step`
+    int rec_rows;     // rows of a partial record
+    int *counters;    // [grid][2], zero between launches
+    float *partials;  // [grid][2] records of rec_rows * (hd + 2) floats (max, sum, then the accumulators)
+    int *err;
+};
+
+int chunk_simt_grid();  // the largest grid of any of the kernels
+cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream);
+// Set head_parts, part_heads and tile_tokens for tiles of `subs` parts of
+// sub_rows (row, head) pairs, each part holding whole rows.
+void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs);
+
+// One sequence of the batch as the walk sees it: its rows that attend
+// something, n of them from row r0 on, behind ctx earlier positions.
+struct ChunkSeq {
+    int s, r0, n, ctx;
+    int tiles;
+    long long cost;  // of one head part
+};
+
+// flags: DS_ERR_POSITION for lengths outside the buffers (clamped).
+__device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int s, int &flags) {
+    const int b = __ldg(a.row_starts + s), e = __ldg(a.row_starts + s + 1);
+    const int len = __ldg(a.seq_lens + s);
+    const int cap = a.max_blocks * a.bt;
+    ChunkSeq q;
+    q.s = s;
+    q.r0 = min(max(b, 0), a.n_rows);
+    const int r1 = min(max(e, q.r0), a.n_rows);
+    const int L = min(max(len, 0), cap);
+    if (q.r0 != b || r1 != e || L != len) flags |= DS_ERR_POSITION;
+    // rows before the first position attend nothing: they are no part of a tile
+    const int empty = max(0, r1 - q.r0 - L);
+    q.r0 += empty;
+    q.n = r1 - q.r0;
+    q.ctx = L - q.n;
+    q.tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens;
+    const long long T = q.tiles;
+    q.cost = T ? T * q.ctx + (long long)a.tile_tokens * (T * (T - 1) / 2) + q.n : 0;
+    return q;
+}
+
+// Cost of a sequence's tiles before tile t < tiles.
+__device__ __forceinline__ long long chunk_cost_before(const ChunkArgs &a, const ChunkSeq &q, long long t) {
+    return t * q.ctx + (long long)a.tile_tokens * (t * (t + 1) / 2);
+}
+
+// One piece of work: a tile's K/V steps [b0, b1).
+struct ChunkSeg {
+    int r0;          // first row of the tile in the batch
+    int tokens;      // rows
+    int pos0;        // position of the first row: row j attends positions 0 .. pos0 + j
+    int len;         // positions the tile attends
+    int seq, part;   // sequence; head part (kv head * head_parts + part)
+    int b0, b1;      // K/V steps of this CTA
+    int slot;        // partial record of this CTA (0 / 1), -1: the tile is all its own
+    long long start, cost;  // place of the tile on the line of costs
+};
+
+// The walk of one CTA over its range.  init() is called by every thread of
+// the block (it synchronises the block); then each role walks its own copy.
+struct ChunkWalk {
+    long long u, u1, unit;  // place, end of the range, range of one CTA
+    long long seq_start;    // of the current sequence
+    ChunkSeq q;
+    int part, tile;
+    int flags;
+
+    // s_red: 34 long longs of shared memory
+    __device__ void init(const ChunkArgs &a, long long *s_red) {
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nw = blockDim.x >> 5;
+        const int parts = a.n_kvh * a.head_parts;
+        flags = 0;
+        long long mine = 0;
+        for (int s = tid; s < a.n_seqs; s += blockDim.x) mine += chunk_seq(a, s, flags).cost;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        if (lane == 0) s_red[warp] = mine;
+        __syncthreads();
+        long long total = 0;
+        for (int w = 0; w < nw; ++w) total += s_red[w];
+        total *= parts;
+        unit = (total + gridDim.x - 1) / gridDim.x;
+        unit = max(unit, (long long)a.min_cost);
+        u = min((long long)blockIdx.x * unit, total);
+        u1 = min(u + unit, total);
+        // the sequence that holds u
+        if (tid == 0) s_red[32] = -1;
+        long long base = 0;
+        for (int s0 = 0; s0 < a.n_seqs && u < u1; s0 += blockDim.x) {
+            const int s = s0 + tid;
+            int dummy = 0;
+            const long long c = s < a.n_seqs ? chunk_seq(a, s, dummy).cost * parts : 0;
+            long long inc = c;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += v;
+            }
+            __syncthreads();
+            if (lane == 31) s_red[warp] = inc;
+            __syncthreads();
+            long long before = base;
+            for (int w = 0; w < nw; ++w) {
+                if (w < warp) before += s_red[w];
+                base += s_red[w];
+            }
+            inc += before;
+            if (u < inc && u >= inc - c) {
+                s_red[32] = s;
+                s_red[33] = inc - c;
+            }
+            if (base > u) break;  // the same for all threads
+        }
+        __syncthreads();
+        part = tile = 0;
+        q.s = -1;
+        q.tiles = 0;
+        if (u < u1) {
+            int dummy = 0;
+            q = chunk_seq(a, (int)s_red[32], dummy);
+            seq_start = s_red[33];
+            long long rem = u - seq_start;
+            part = (int)(rem / q.cost);
+            rem -= (long long)part * q.cost;
+            int lo = 0, hi = q.tiles;  // last tile with cost before it <= rem
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (chunk_cost_before(a, q, mid) <= rem)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            tile = lo;
+        }
+        __syncthreads();
+    }
+
+    // The next piece of work, or false at the range's end.
+    __device__ bool next(const ChunkArgs &a, ChunkSeg &g) {
+        const int parts = a.n_kvh * a.head_parts;
+        while (u < u1) {
+            if (tile == q.tiles) {
+                tile = 0;
+                if (++part == parts) {
+                    part = 0;
+                    seq_start += q.cost * parts;
+                    int dummy = 0;
+                    do {
+                        q = chunk_seq(a, q.s + 1, dummy);
+                    } while (q.tiles == 0);
+                }
+            }
+            const int j0 = tile * a.tile_tokens;
+            g.tokens = min(a.tile_tokens, q.n - j0);
+            g.r0 = q.r0 + j0;
+            g.pos0 = q.ctx + j0;
+            g.len = q.ctx + j0 + g.tokens;
+            g.seq = q.s;
+            g.part = part;
+            g.cost = g.len;
+            g.start = seq_start + (long long)part * q.cost + chunk_cost_before(a, q, tile);
+            const long long end = min(u1, g.start + g.cost);
+            g.b0 = (int)((u - g.start) / a.step);
+            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : (int)((end - g.start) / a.step);
+            const long long u0 = (long long)blockIdx.x * unit;
+            g.slot = g.start < u0 ? 0 : g.start + g.cost > u1 ? 1 : -1;
+            ++tile;
+            u = end;
+            if (g.b0 < g.b1) return true;
+        }
+        return false;
+    }
+};
+
+// The CTAs that share a split tile, in order.  The first CTA the tile reaches
+// into may have been left less than one step of it, which rounds to nothing.
+struct ChunkShare {
+    int first, last;  // contributors
+    int counter;      // the tile's counter: the CTA its cost starts in
+};
+__device__ __forceinline__ ChunkShare chunk_share(const ChunkArgs &a, const ChunkSeg &g, long long unit) {
+    ChunkShare h;
+    h.counter = (int)(g.start / unit);
+    h.last = (int)((g.start + g.cost - 1) / unit);
+    h.first = (h.counter + 1) * unit - g.start < a.step ? h.counter + 1 : h.counter;
+    return h;
+}
+// Is the tile's record in CTA c its slot 0 (it began before c's range) or 1?
+__device__ __forceinline__ int chunk_slot(const ChunkSeg &g, long long unit, int c) {
+    return g.start < (long long)c * unit ? 0 : 1;
+}
+
+// First cache row of the sequence's position `pos` block; a block number
+// outside the pool reads block 0 and flags.
+__device__ __forceinline__ long long chunk_block_row(const ChunkArgs &a, int seq, int blk, int &flags) {
+    long long id = a.block_table ? (long long)__ldg(a.block_table + (long long)seq * a.max_blocks + blk)
+                                 : (long long)seq * a.max_blocks + blk;
+    if (id < 0 || id >= a.pool_blocks) {
+        flags |= DS_ERR_POSITION;
+        id = 0;
+    }
+    return id * a.bt;
+}
+
+// Query heads of a head part: count heads from `first` on, of KV head kv.
+struct ChunkHeads {
+    int kv, first, count;
+};
+__device__ __forceinline__ ChunkHeads chunk_heads(const ChunkArgs &a, int part) {
+    ChunkHeads h;
+    h.kv = part / a.head_parts;
+    const int skip = (part % a.head_parts) * a.part_heads;
+    h.first = h.kv * a.gq + skip;
+    h.count = min(a.part_heads, a.gq - skip);
+    return h;
+}
+
+// Partial record of CTA c: (max in units of log2, sum) per (row, head) pair,
+// then rec_rows x hd accumulators.
+__device__ __forceinline__ float *chunk_record(const ChunkArgs &a, int c, int slot) {
+    return a.partials + ((size_t)c * 2 + slot) * a.rec_rows * (a.hd + 2);
+}
+
+// Rows in front of a sequence's first position (a length below the number of
+// new rows) attend nothing: their output is zero.
+__device__ inline void chunk_zero_empty_rows(const ChunkArgs &a) {
+    for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+        const int r0 = min(max(__ldg(a.row_starts + s), 0), a.n_rows);
+        const int r1 = min(max(__ldg(a.row_starts + s + 1), r0), a.n_rows);
+        const int L = min(max(__ldg(a.seq_lens + s), 0), a.max_blocks * a.bt);
+        if (r1 - r0 <= L) continue;
+        const long long w = (long long)a.n_qh * a.hd;
+        for (long long i = r0 * w + threadIdx.x; i < (r1 - L) * w; i += blockDim.x) store_as(a.out, i, a.q_dtype, 0.0f);
+    }
+}
+
+// Join the records of a split tile's (row, head) pairs [m0, m1) in CTA order
+// and write their outputs; warp w of n_warps.
+//   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
+__device__ inline void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h, long long unit, int m0,
+                                  int m1, int w, int n_warps) {
+    const int lane = threadIdx.x & 31;
+    const ChunkHeads hh = chunk_heads(a, g.part);
+    for (int m = m0 + w; m < m1; m += n_warps) {
+        const int tok = m / a.part_heads, head = m % a.part_heads;
+        if (head >= hh.count) continue;
+        float M = -INFINITY;
+        for (int c = h.first + lane; c <= h.last; c += 32)
+            M = fmaxf(M, __ldcg(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m));
+        M = warp_max(M);
+        const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd;
+        for (int d = lane * 4; d < a.hd; d += 128) {
+            float L = 0.0f, A[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            for (int c0 = h.first; c0 <= h.last; c0 += 4) {  // four records' loads in flight
+                float2 ml[4];
+                float v[4][4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c0 + k > h.last) break;
+                    const float *rec = chunk_record(a, c0 + k, chunk_slot(g, unit, c0 + k));
+                    ml[k] = make_float2(__ldcg(rec + 2 * m), __ldcg(rec + 2 * m + 1));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[k][e] = __ldcg(rec + 2 * a.rec_rows + (size_t)m * a.hd + d + e);
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c0 + k > h.last) break;
+                    const float f = exp2f(ml[k].x - M);
+                    L = fmaf(ml[k].y, f, L);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) A[e] = fmaf(v[k][e], f, A[e]);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) store_as(a.out, o + d + e, a.q_dtype, A[e] / L);
+        }
+    }
+}
+
+}  // namespace ds

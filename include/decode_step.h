@@ -88,7 +88,8 @@ enum {
     DS_ERR_TOKEN_RANGE = 1,   /* a device-side token id was outside [0, vocab); clamped */
     DS_ERR_POSITION = 2,      /* a device-side position or length exceeded the cache */
     DS_ERR_WAIT_TIMEOUT = 4,  /* a bounded wait inside a kernel gave up */
-    DS_ERR_SAMPLING = 8       /* a sampler row had no finite logits */
+    DS_ERR_SAMPLING = 8,      /* a sampler row had no finite logits */
+    DS_ERR_NO_BLOCKS = 16     /* a step's rows or new blocks did not fit (ds_paged_plan) */
 };
 
 /* Name of a status code ("ds_ok", "ds_a_length_mismatch", ...);
@@ -278,6 +279,122 @@ DS_API int ds_gqa_decode_attn(const float *q, const void *k_cache, const void *v
                               int n_seqs, int n_qh, int n_kvh, int head_dim, float scale,
                               float *out, void *workspace, size_t workspace_bytes,
                               ds_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * A ragged step: chunks and single tokens of many requests in one launch
+ *
+ * "Inside the engine", section 2: a step runs prompt chunks and decode rows
+ * side by side.  Sequence s of the step has n_s new positions (a chunk, one
+ * token, or none) behind c_s cached ones; the new rows of all sequences lie
+ * one after the other.  ds_paged_plan maps them to the pool, ds_rope_append
+ * turns a layer's fused q|k|v rows and writes k and v, ds_gqa_chunk_attn
+ * attends.  Calls whose GPU work may overlap (other streams, other graphs)
+ * need a workspace each.
+ * ------------------------------------------------------------------- */
+
+DS_API size_t ds_paged_plan_workspace_bytes(void);
+
+/* Block table entries, row starts, positions and cache slots of a step, from
+ * lengths in device memory ("Inside the engine", section 3: the pool's blocks
+ * and a request's block table).  Per sequence s, in order:
+ *   blocks: ceil((c_s + n_s) / block_tokens) - ceil(c_s / block_tokens) are
+ *     taken from the front of what is left of free_blocks and entered in
+ *     block_table from entry ceil(c_s / block_tokens) on; other entries stay;
+ *   row_starts[s] = sum of n_i over i < s; seq_lens[s] = c_s + n_s;
+ *   row r of s: row_seq[r] = s, positions[r] = c_s + r - row_starts[s] and
+ *     slots[r] = block * block_tokens + position % block_tokens, its cache row.
+ *   cached_lens, new_lens: int32 [n_seqs]; free_blocks: int32 [n_free] (may be
+ *   NULL when n_free is 0); block_table: int32 [n_seqs][max_blocks_per_seq],
+ *   updated in place; row_starts: int32 [n_seqs + 1]; seq_lens: int32
+ *   [n_seqs]; row_seq, positions, slots: int32 [max_rows], all -1 behind the
+ *   last row, so a batch padded to max_rows can be captured in a graph;
+ *   n_taken: int32 [1], how many of free_blocks are used up.  No output may
+ *   overlap an input or another output.
+ * The lengths are not changed: the same call again gives the same answer.
+ * A sequence with a negative length or one past its table row gets no rows
+ * (DS_ERR_POSITION).  The first sequence whose rows pass max_rows or whose
+ * blocks pass n_free ends the step: it and all behind it get no rows and no
+ * blocks (DS_ERR_NO_BLOCKS).  A sequence without rows has seq_lens[s] = c_s.
+ * A block number outside the cache's cache_rows / block_tokens whole blocks
+ * gives slot -1 (a new one also table entry -1) and DS_ERR_POSITION.
+ * 561 for a count < 1 (n_free may be 0), 564 past DS_MAX_DIM or 4096
+ * sequences.  One launch, no host copy, capturable. */
+DS_API int ds_paged_plan(const int32_t *cached_lens, const int32_t *new_lens, int n_seqs,
+                         const int32_t *free_blocks, int64_t n_free, int block_tokens, int64_t cache_rows,
+                         int32_t *block_table, int max_blocks_per_seq, int32_t *row_starts,
+                         int32_t *seq_lens, int32_t *row_seq, int32_t *positions, int32_t *slots,
+                         int64_t max_rows, int32_t *n_taken, void *workspace, size_t workspace_bytes,
+                         ds_stream_t stream);
+
+DS_API size_t ds_rope_append_workspace_bytes(void);
+
+/* Rotary positions and K/V write of a step's rows ("Inside the engine",
+ * section 1: qkPrep).  Row r of qkv holds n_qh query heads, n_kvh key heads
+ * and n_kvh value heads of head_dim elements, the fused projection's output,
+ * rows row_stride elements apart.  The first rot_dim dims of every q and k
+ * head are rotated: pair p turns by
+ *   positions[axis(p)][r] * base^(-2p / rot_dim),  axis(p) = pair_axis[p],
+ * pairs laid out over the rot_dim dims as in ds_rope (DS_ROPE_*); dims behind
+ * them stay.  With one axis this is the rotation of ds_rope; with several
+ * (time, height, width of an image's or a video's patches) each pair turns by
+ * the axis it is given, in runs or interleaved, as pair_axis says.  The angle
+ * is exact to 2^-33 of a turn at any position; the rotation is fp32, rounded
+ * once to the output's type.
+ *   q_out: [n_rows][n_qh][head_dim]; the rotated k and v as it is go to row
+ *   slots[r] of k_cache / v_cache (rows of n_kvh * head_dim elements).
+ *   qkv, q_out and the caches are fp32 or bf16 each (572).
+ *   positions: device int32 [n_axes][n_rows]; pair_axis: HOST bytes
+ *   [rot_dim / 2], each < n_axes (NULL for one axis), read before the call
+ *   returns; slots: device int32 [n_rows].
+ * A row with a negative slot is padding: nothing of it is read or written
+ * (its q_out stays).  A slot past the cache or a negative position skips the
+ * row and flags DS_ERR_POSITION.  Two rows with one slot: either may stay.
+ * qkv_len (562) must reach the last row's end and row_stride its width; q_len
+ * must be n_rows * n_qh * head_dim (563).  head_dim <= 256, rot_dim even and
+ * <= head_dim, n_axes <= 8, base finite and > 0, qkv and q_out not
+ * overlapping (577).  Rows with 16-byte aligned buffers, row_stride and
+ * head_dim multiples of 8 and rot_dim of 16 move 16 bytes at a time; others
+ * one element. */
+DS_API int ds_rope_append(const void *qkv, int64_t qkv_len, int qkv_dtype, int64_t row_stride,
+                          int64_t n_rows, const int32_t *positions, int n_axes, const uint8_t *pair_axis,
+                          int n_qh, int n_kvh, int head_dim, int rot_dim, double base, int layout,
+                          void *q_out, int64_t q_len, int q_dtype, void *k_cache, void *v_cache,
+                          int kv_dtype, int64_t cache_rows, const int32_t *slots, void *workspace,
+                          size_t workspace_bytes, ds_stream_t stream);
+
+/* Workspace bytes of ds_gqa_chunk_attn for up to n_rows rows; 0 for an
+ * unsupported shape. */
+DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t n_rows, int n_qh, int n_kvh,
+                                                 int head_dim);
+
+/* Grouped-query attention of every sequence's new rows over its cached
+ * positions, its new ones included ("Inside the engine", section 1: causal
+ * flash attention over a chunk).  Sequence s holds rows row_starts[s] ..
+ * row_starts[s + 1] - 1; with n of them and L = seq_lens[s], row j attends
+ * positions 0 .. L - n + j: out = softmax over t of (q . k_t * scale), times
+ * v_t, KV head g = h / (n_qh / n_kvh) as in ds_gqa_decode_attn.  One row per
+ * sequence is a decode step, any mix of lengths runs in one launch.
+ *   q, out: [n_rows][n_qh][head_dim], both fp32 or both bf16 (q_dtype), not
+ *   overlapping; k_cache, v_cache, cache_rows, block_table (NULL: contiguous
+ *   slots), max_blocks_per_seq, block_tokens as in ds_gqa_decode_attn, fp32
+ *   or bf16 (kv_dtype).  row_starts: device int32 [n_seqs + 1], seq_lens:
+ *   device int32 [n_seqs].
+ * A row that attends nothing (L < n) is zero.  Rows of no sequence (in front
+ * of row_starts[0], behind row_starts[n_seqs]) stay as they were.  What the
+ * cache holds at positions a row does not attend, NaN and infinities
+ * included, does not reach it.  Row starts that fall or pass n_rows and
+ * lengths outside the table row are clamped, a block number outside the cache
+ * reads block 0; all flag DS_ERR_POSITION.
+ * q_len = out_len = n_rows * n_qh * head_dim (562, 563); n_qh a multiple of
+ * n_kvh, head_dim a multiple of 4 up to 256, scale finite and > 0, q, out and
+ * the caches 16-byte aligned (577); contiguous slots and one block at least
+ * must fit the cache (571).  No allocation, no host copy, capturable. */
+DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtype, int64_t n_rows,
+                             const int32_t *row_starts, const int32_t *seq_lens, int n_seqs,
+                             const void *k_cache, const void *v_cache, int kv_dtype, int64_t cache_rows,
+                             const int32_t *block_table, int max_blocks_per_seq, int block_tokens,
+                             int n_qh, int n_kvh, int head_dim, float scale, void *out, int64_t out_len,
+                             void *workspace, size_t workspace_bytes, ds_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * Picking the next token
