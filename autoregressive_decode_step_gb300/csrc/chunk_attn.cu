@@ -247,8 +247,11 @@ void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs) {
 
 using namespace ds;
 
-// (row, head) pairs of the largest tile any kernel uses, and so of a record.
-static int chunk_rec_rows(int64_t n_rows, int gq) { return (int)std::min<int64_t>(kChunkMaxTileRows, n_rows * gq); }
+// (row, head) pairs of the largest tile any kernel uses, and so of a record
+// (a multiple of four: records and their accumulators start on 16 bytes).
+static int chunk_rec_rows(int64_t n_rows, int gq) {
+    return (int)std::min<int64_t>(kChunkMaxTileRows, (n_rows * gq + 3) / 4 * 4);
+}
 
 extern "C" DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t n_rows, int n_qh, int n_kvh,
                                                             int head_dim) {
@@ -314,6 +317,6 @@ extern "C" DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtyp
     a.counters = reinterpret_cast<int *>(ws + kWsHeader);
     a.partials = reinterpret_cast<float *>(ws + kWsHeader + align_up((size_t)chunk_simt_grid() * 2 * sizeof(int), 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = launch_chunk_simt(a, s);
+    const cudaError_t e = chunk_tc_supported(a) ? launch_chunk_tc(a, s) : launch_chunk_simt(a, s);
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
 }

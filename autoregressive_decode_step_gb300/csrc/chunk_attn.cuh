@@ -52,6 +52,8 @@ struct ChunkArgs {
 
 int chunk_simt_grid();  // the largest grid of any of the kernels
 cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream);
+bool chunk_tc_supported(const ChunkArgs &a);
+cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream);
 // Set head_parts, part_heads and tile_tokens for tiles of `subs` parts of
 // sub_rows (row, head) pairs, each part holding whole rows.
 void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs);

@@ -1,0 +1,876 @@
+// The chunk attention on the fifth-generation tensor cores (tcgen05), for a
+// bf16 cache of whole pages and heads of 64 or 128; the mathematics, the work
+// split and the joining of split tiles are those of chunk_attn.cuh.
+//
+// A tile's (row, head) pairs fill up to two parts of 128 MMA rows, a K/V step
+// is 128 positions.  Per part and step:
+//   S = Q K^T   (M 128, N 128, K hd): Q and K from shared memory, S in TMEM
+//   P = 2^(c S - c m)   by the part's warpgroup, thread r owning row r; P
+//       goes back to TMEM as bf16 over the columns S was in
+//   O += P V    (M 128, N hd, K 128): P from TMEM, V from shared memory
+// While one warpgroup turns its S into P the tensor core works for the other:
+// the MMA thread issues PV and the next QK of part 0, then those of part 1.
+// tcgen05.mma of one thread complete in issue order, so the S of a step being
+// complete means that the PV before it is, and S may overwrite the P it
+// follows.
+//
+// Two parts share one stream of K and V (one fetch serves 256 MMA rows; at
+// 128 rows a step takes as long to fetch from L2 as to multiply).  A tile that
+// fits one part (a single token's group of heads, or the end of a chunk) is
+// put in both parts instead, which then take turns at the K/V steps with a
+// running maximum and sum each, joined at the end: the same overlap.
+//
+// fp32 q (PARTS 3): q and P each go to the tensor core as three bf16 numbers
+// hi + mid + lo, 24 significant bits.  The three take the place of three rows
+// of the same warp (10 rows a warp instead of 32), so one MMA multiplies all
+// of them; S and O are added up over the three lanes.
+//
+// The running maximum that P is taken relative to is moved (and O rescaled)
+// only when a row's maximum has grown by more than 2^8: P then stays below
+// 2^8, which costs bf16 and fp32 no digits, and O is rescaled a few times in
+// a tile instead of every step.  P is rounded to bf16 (PARTS 1), the sum adds
+// the fp32 weights.
+//
+// A step that reaches past the first row's position is masked per row.  V
+// there may hold anything (another row's NaN, the stale rest of a page), and
+// 0 x NaN is NaN, so the warpgroups check the step's V in shared memory:
+// positions past the end are zeroed, and a non-finite value at a position
+// that only some of the rows attend is zeroed and noted, to be added to the
+// rows that do attend it at the end.
+//
+// Every wait is bounded; after one gives up all others return at once and the
+// kernel runs to its end without them (its barriers still pair up), flagged.
+#include <algorithm>
+#include <atomic>
+
+#include "chunk_attn.cuh"
+#include "tc.h"
+#include "tcgen05.cuh"
+
+namespace ds {
+
+constexpr int kCtStep = 128;
+constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, the producer and the walking warp
+constexpr int kCtSegs = 4;       // segments handed out and not yet done with
+constexpr int kCtMinCost = 256;
+constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
+constexpr int kCtMaxStages = 10;
+constexpr int kCtSmall = 3072;      // barriers, exchange words, notes
+constexpr size_t kCtSmemLimit = 227 * 1024;
+constexpr float kCtLog2e = 1.4426950408889634f;
+constexpr float kCtLag = 8.0f;      // log2 of the growth that moves the reference maximum
+
+template <int HD>
+struct CtCfg {
+    static constexpr int kHalves = HD / 64;
+    static constexpr int kTileBytes = kHalves * kCtHalf;  // 128 rows of one head
+    static constexpr int kStages = (int)((kCtSmemLimit - kCtSmall - 2 * kTileBytes) / kTileBytes) < kCtMaxStages
+                                       ? (int)((kCtSmemLimit - kCtSmall - 2 * kTileBytes) / kTileBytes)
+                                       : kCtMaxStages;
+    static constexpr size_t kSmem = kCtSmall + (size_t)(2 + kStages) * kTileBytes;
+};
+
+struct CtMaps {
+    CUtensorMap k, v;  // {64, cache_rows, n_kvh * hd / 64}, boxes {64, box_rows, 1}, 128-byte swizzle
+    int box_rows;
+};
+
+// D[tmem] (+)= A[tmem] x B[smem].
+__device__ __forceinline__ void ct_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 32 columns of this thread's lane; complete only after ct_wait_ld().
+__device__ __forceinline__ void ct_ld32(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]),
+          "=f"(v[8]), "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]),
+          "=f"(v[16]), "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]),
+          "=f"(v[24]), "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void ct_ld16(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void ct_st16(uint32_t taddr, const float *v) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
+        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void ct_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ct_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void ct_st32f(uint32_t taddr, const float *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
+        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
+        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
+        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void ct_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void ct_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ float ct_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// bf16 pair, a in the low half.
+__device__ __forceinline__ uint32_t ct_pack(float a, float b) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float ct_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+
+__device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int row, int half, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(half), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// Wait for a phase; once any wait of the block has given up, at once.
+__device__ __forceinline__ void ct_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
+    if (mbar_try_wait(bar, parity)) return;
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (mbar_try_wait(bar, parity)) return;
+        if ((it & 63u) == 0) {
+            if (*dead) return;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                flag_error(err, DS_ERR_WAIT_TIMEOUT);
+                *dead = 1;
+                return;
+            }
+        }
+    }
+}
+
+// Order of the 2 nb tiles of a segment in the ring, the order the MMA thread
+// needs them in.  Shared steps: K0 V0 K1 V1 ...  Steps taken in turns:
+// K0 K1 V0 K2 V1 K3 ... V(nb-2) V(nb-1).
+__device__ __forceinline__ int ct_k_place(bool turns, int j) { return !turns ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int ct_v_place(bool turns, int j, int nb) {
+    return !turns ? 2 * j + 1 : j == nb - 1 ? 2 * nb - 1 : 2 * j + 2;
+}
+
+// A segment as the walking warp hands it to the other roles.
+struct CtSeg {
+    ChunkSeg g;
+    ChunkShare share;
+    ChunkHeads heads;
+    int nb;     // K/V steps; 0: the walk is over
+    int turns;  // the parts take turns at the steps
+    int split;  // other CTAs contribute to the tile
+};
+
+struct CtShared {
+    CtSeg seg[kCtSegs];
+    uint64_t seg_full[kCtSegs], seg_empty[kCtSegs];
+    uint64_t full[kCtMaxStages], empty[kCtMaxStages];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+    uint32_t tmem;
+    int dead;
+    int noted[2];   // a part's notes hold something
+    int last[2];
+    union {
+        long long red[34];   // ChunkWalk::init
+        float2 ml[128];      // part 1's (max, sum) per row, for part 0 to join
+    };
+    unsigned note[2][128];  // non-finite V per dim: 10-bit first positions of NaN, +inf, -inf behind the tile's pos0
+};
+static_assert(sizeof(CtShared) <= kCtSmall, "shared words");
+
+constexpr unsigned kCtNoNote = 0x3fffffffu;
+
+// Note a non-finite value of dim d at position rel behind the first row's.
+__device__ inline void ct_note(unsigned *w, int rel, float v) {
+    const int sh = v != v ? 0 : v > 0.0f ? 10 : 20;
+    unsigned old = *reinterpret_cast<volatile unsigned *>(w);
+    while (((old >> sh) & 1023u) > (unsigned)rel) {
+        const unsigned want = (old & ~(1023u << sh)) | ((unsigned)rel << sh);
+        const unsigned was = atomicCAS(w, old, want);
+        if (was == old) break;
+        old = was;
+    }
+}
+// What the noted values add to a row that attends positions up to rel.
+__device__ __forceinline__ float ct_noted(unsigned w, int rel) {
+    const bool nan = (int)(w & 1023u) <= rel, pinf = (int)((w >> 10) & 1023u) <= rel, ninf = (int)(w >> 20) <= rel;
+    if (nan || (pinf && ninf)) return __int_as_float(0x7fffffff);
+    return pinf ? INFINITY : ninf ? -INFINITY : 0.0f;
+}
+
+// The sum of a row's weights times column d of V over positions [t0, t1), of
+// which the tensor core made NaN although the weights are finite: a weight (or
+// a part of it) that is zero or negative met an infinity.  Every weight is
+// positive, so the infinities decide.
+__device__ __noinline__ float ct_infinite(const ChunkArgs &a, int seq, int kv, int d, int t0, int t1) {
+    float sum = 0.0f;
+    int flags = 0;
+    for (int t = t0; t < t1 && sum == sum; ++t) {
+        const long long row = chunk_block_row(a, seq, t / a.bt, flags) + t % a.bt;
+        const float v = load_as(a.v_cache, (row * a.n_kvh + kv) * a.hd + d, DS_BF16);
+        if (!(fabsf(v) < INFINITY)) sum += v;
+    }
+    return sum == 0.0f ? __int_as_float(0x7fffffff) : sum;
+}
+
+// Hand-over of segments: these waits are not cut short when another wait has
+// given up (the roles must go on agreeing on the segments, their barriers pair
+// up by them) and outlast it by far: every role then runs through.
+__device__ __forceinline__ void ct_wait_seg(uint64_t *bar, uint32_t parity, int *err) {
+    for (int k = 0; k < 8; ++k) {
+        int none = 0;
+        if (mbar_wait(bar, parity, k == 7 ? err : &none)) return;
+    }
+}
+
+template <int HD, int PARTS>
+__global__ void __launch_bounds__(kCtThreads, 1)
+    chunk_tc_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CtMaps maps) {
+    using Cfg = CtCfg<HD>;
+    constexpr int ST = Cfg::kStages;
+    constexpr int RPW = PARTS == 1 ? 32 : 10;  // rows a warp
+    extern __shared__ __align__(1024) unsigned char ct_smem[];
+    CtShared &sh = *reinterpret_cast<CtShared *>(ct_smem);
+    unsigned char *s_q = ct_smem + kCtSmall, *s_ring = s_q + 2 * Cfg::kTileBytes;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    volatile int *dead = &sh.dead;
+    if (smem_u32(ct_smem) & 1023u) {  // swizzled tiles start on 1 KB; the same answer in every thread
+        if (tid == 0) flag_error(a.err, DS_ERR_WAIT_TIMEOUT);
+        return;
+    }
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(&sh.q_full[w], 4);
+            mbar_init(&sh.s_full[w], 1);
+            mbar_init(&sh.p_full[w], 4);
+            mbar_init(&sh.o_full[w], 1);
+            sh.noted[w] = 0;
+        }
+        for (int i = 0; i < kCtSegs; ++i) {
+            mbar_init(&sh.seg_full[i], 1);
+            mbar_init(&sh.seg_empty[i], 10);  // producer, MMA, eight softmax warps
+        }
+        mbar_init(&sh.done, 1);
+        sh.dead = 0;
+        fence_mbarrier_init();
+    }
+    for (int i = tid; i < 256; i += kCtThreads) sh.note[i >> 7][i & 127] = kCtNoNote;
+    if (warp == 8) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
+    }
+    chunk_zero_empty_rows(a);
+    ChunkWalk walk;
+    walk.init(a, sh.red);  // synchronises the block
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    const int half_tokens = a.tile_tokens >> 1;  // rows of the sequence in one part
+    int flags = walk.flags;
+    const long long unit = walk.unit;
+    auto seg_get = [&](uint32_t k) -> const CtSeg & {
+        ct_wait_seg(&sh.seg_full[k % kCtSegs], (k / kCtSegs) & 1, a.err);
+        return sh.seg[k % kCtSegs];
+    };
+    auto seg_done = [&](uint32_t k) { mbar_arrive(&sh.seg_empty[k % kCtSegs]); };  // one thread of the warp
+
+    if (warp == 10) {
+        // ------------------------------------------------ the walk over this CTA's range
+        if (lane == 0) {
+            for (uint32_t k = 0;; ++k) {
+                CtSeg c;
+                c.nb = 0;
+                if (walk.next(a, c.g)) {
+                    c.nb = c.g.b1 - c.g.b0;
+                    c.turns = c.g.tokens <= half_tokens;
+                    c.heads = chunk_heads(a, c.g.part);
+                    c.split = 0;
+                    if (c.g.slot >= 0) {
+                        c.share = chunk_share(a, c.g, unit);
+                        c.split = c.share.first < c.share.last;
+                    }
+                }
+                if (k >= kCtSegs) ct_wait_seg(&sh.seg_empty[k % kCtSegs], ((k / kCtSegs) - 1) & 1, a.err);
+                sh.seg[k % kCtSegs] = c;
+                mbar_arrive(&sh.seg_full[k % kCtSegs]);
+                if (c.nb == 0) break;
+            }
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ------------------------------------------------ K/V producer
+        uint32_t n = 0;
+        const int R = maps.box_rows;
+        for (uint32_t seg = 0;; ++seg) {
+            const CtSeg &c = seg_get(seg);
+            const int nb = c.nb;
+            if (nb == 0) break;
+            const bool turns = c.turns;
+            const int kv = c.heads.kv, b0 = c.g.b0, len = c.g.len, seq = c.g.seq;
+            __syncwarp();
+            if (lane == 0) seg_done(seg);
+            for (int i = 0; i < 2 * nb; ++i, ++n) {
+                int j;
+                bool is_v;
+                if (!turns) {
+                    is_v = i & 1;
+                    j = i >> 1;
+                } else if (i < 2 && nb > 1) {
+                    is_v = false;
+                    j = i;
+                } else if (nb == 1) {
+                    is_v = i == 1;
+                    j = 0;
+                } else {
+                    const int m = i - 2;
+                    is_v = !(m & 1) || m / 2 + 2 >= nb;
+                    j = !is_v ? m / 2 + 2 : (m + 1) / 2;
+                }
+                const int t0 = (b0 + j) * kCtStep;
+                const int boxes = (min(kCtStep, len - t0) + R - 1) / R;
+                // lane l: box l / halves, half l % halves (32 boxes at most); its
+                // block number is fetched before the stage is awaited
+                const int bx = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
+                int row = 0;
+                if (bx < boxes) {
+                    const int pos = t0 + bx * R;
+                    row = (int)(chunk_block_row(a, seq, pos / a.bt, flags) + pos % a.bt);
+                }
+                const int s = n % ST;
+                if (n >= ST) ct_wait(&sh.empty[s], ((n / ST) - 1) & 1, dead, a.err);
+                // one decision for the warp; a block that has given up fetches no more
+                if (__any_sync(0xffffffffu, *dead)) continue;
+                if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * R * 128 * Cfg::kHalves));
+                __syncwarp();
+                if (bx < boxes)
+                    ct_box(smem_u32(s_ring + (size_t)s * Cfg::kTileBytes) + hf * kCtHalf + bx * R * 128,
+                           is_v ? &maps.v : &maps.k, row, kv * Cfg::kHalves + hf, &sh.full[s]);
+            }
+        }
+        // every copy issued has landed before the block may end
+        if (lane == 0) {
+            int none = 0;
+            for (uint32_t f = n > ST ? n - ST : 0; f < n; ++f)
+                if (!mbar_wait(&sh.full[f % ST], (f / ST) & 1, *dead ? &none : a.err)) break;
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------ MMA issue
+        if (lane == 0) {
+            constexpr uint32_t kIdQk = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+            constexpr uint32_t kIdPv =
+                (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((128u >> 4) << 24);
+            uint32_t n0 = 0, pc0 = 0, pc1 = 0;
+            const uint64_t q0 = smem_desc(smem_u32(s_q), 16, 1024);
+            const uint32_t ring = smem_u32(s_ring);
+            auto wait_tile = [&](uint32_t n) { ct_wait(&sh.full[n % ST], (n / ST) & 1, dead, a.err); };
+            auto qk = [&](int w, uint32_t n) {
+                const uint64_t ad = q0 + (uint64_t)(w * (Cfg::kTileBytes >> 4));
+                const uint64_t bd = smem_desc(ring + (n % ST) * Cfg::kTileBytes, 16, 1024);
+                const uint32_t d = tmem + w * 128;
+#pragma unroll
+                for (int k = 0; k < HD / 16; ++k) {
+                    const uint64_t o = (uint64_t)((k / 4) * (kCtHalf >> 4) + (k % 4) * 2);
+                    tc_mma(d, ad + o, bd + o, kIdQk, k ? 1u : 0u);
+                }
+            };
+            auto pv = [&](int w, uint32_t n, bool first) {
+                const uint64_t bd = smem_desc(ring + (n % ST) * Cfg::kTileBytes, kCtHalf, 1024);
+                const uint32_t d = tmem + 256 + w * HD, p = tmem + w * 128;
+#pragma unroll
+                for (int k = 0; k < kCtStep / 16; ++k)
+                    ct_mma_ts(d, p + k * 8, bd + (uint64_t)(k * 128), kIdPv, (k || !first) ? 1u : 0u);
+            };
+            for (uint32_t seg = 0;; ++seg) {
+                const CtSeg &c = seg_get(seg);
+                const int nb = c.nb;
+                if (nb == 0) break;
+                const bool turns = c.turns;
+                seg_done(seg);
+                const int steps = turns ? (nb + 1) >> 1 : nb;
+                auto kn = [&](int j) { return n0 + (uint32_t)ct_k_place(turns, j); };
+                auto vn = [&](int j) { return n0 + (uint32_t)ct_v_place(turns, j, nb); };
+                for (int w = 0; w < 2; ++w) ct_wait(&sh.q_full[w], seg & 1, dead, a.err);
+                tc_fence_after();
+#pragma unroll 1
+                for (int w = 0; w < 2; ++w) {
+                    const int j = turns ? w : 0;
+                    if (j >= nb) continue;
+                    wait_tile(kn(j));
+                    tc_fence_after();
+                    qk(w, kn(j));
+                    if (turns || w == 1) tc_commit(&sh.empty[kn(j) % ST]);
+                    tc_commit(&sh.s_full[w]);
+                }
+                for (int i = 0; i < steps; ++i) {
+#pragma unroll 1
+                    for (int w = 0; w < 2; ++w) {
+                        const int j = turns ? 2 * i + w : i;
+                        if (j >= nb) continue;
+                        const int jn = turns ? j + 2 : j + 1;
+                        wait_tile(vn(j));
+                        ct_wait(&sh.p_full[w], (w ? pc1 : pc0) & 1, dead, a.err);
+                        w ? ++pc1 : ++pc0;
+                        tc_fence_after();
+                        pv(w, vn(j), i == 0);
+                        if (turns || w == 1) tc_commit(&sh.empty[vn(j) % ST]);
+                        if (jn < nb) {
+                            wait_tile(kn(jn));
+                            tc_fence_after();
+                            qk(w, kn(jn));
+                            if (turns || w == 1) tc_commit(&sh.empty[kn(jn) % ST]);
+                            tc_commit(&sh.s_full[w]);
+                        } else {
+                            tc_commit(&sh.o_full[w]);
+                        }
+                    }
+                }
+                n0 += 2 * nb;
+            }
+            // nothing of ours runs on the tensor cores when the block ends
+            tc_commit(&sh.done);
+            int none = 0;
+            mbar_wait(&sh.done, 0, *dead ? &none : a.err);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        // ------------------------------------------------ softmax, part w
+        const int w = warp >> 2, q4 = warp & 3, t = tid & 127;
+        const int r = PARTS == 1 ? t : q4 * RPW + lane % RPW;  // row of the part
+        const int piece = PARTS == 1 ? 0 : lane / RPW;         // hi, mid, lo (3: an unused lane)
+        const uint32_t lane_base = (uint32_t)(q4 * 32) << 16;
+        const uint32_t ts = tmem + lane_base + w * 128, to = tmem + lane_base + 256 + w * HD;
+        const float c = a.scale * kCtLog2e;
+        const int tok_r = r / a.part_heads, head_r = r % a.part_heads;
+        auto token_of = [&](const CtSeg &s) { return (s.turns ? 0 : w * half_tokens) + tok_r; };
+        // the part's 128 MMA rows of q, 16 bytes a thread, in the swizzled
+        // order the MMA reads; rows without a pair keep what is there (an MMA
+        // row reaches no other row)
+        auto load_q = [&](const CtSeg &s) {
+            const ChunkHeads hh = s.heads;
+            unsigned char *dst = s_q + w * Cfg::kTileBytes;
+            const int first = s.turns ? 0 : w * half_tokens, r0 = s.g.r0 + first;
+            const int tokens = min(half_tokens, s.g.tokens - first);
+            int base = t;
+            asm volatile("" : "+r"(base));  // the addresses below are formed here, not kept through the steps
+#pragma unroll 1
+            for (int i0 = 0; i0 < HD / 8; i0 += 4) {
+                uint4 v[4];
+                int at[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int idx = base + 128 * (i0 + i);
+                    const int m = idx / (HD / 8), ch = idx % (HD / 8);
+                    const int pr = PARTS == 1 ? m : (m >> 5) * RPW + (m & 31) % RPW;
+                    const int pc = PARTS == 1 ? 0 : (m & 31) / RPW;
+                    const int tk = pr / a.part_heads, h = pr % a.part_heads;
+                    at[i] = -1;
+                    if (tk < tokens && h < hh.count && (PARTS == 1 || pc < PARTS)) {
+                        at[i] = (ch >> 3) * kCtHalf + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
+                        const long long e = ((long long)(r0 + tk) * a.n_qh + hh.first + h) * HD + ch * 8;
+                        if (PARTS == 1) {
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + e));
+                        } else {
+                            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + e);
+                            const float4 x0 = __ldg(p), x1 = __ldg(p + 1);
+                            float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                if (pc > 0) x[k] -= ct_bf16(x[k]);
+                                if (pc > 1) x[k] -= ct_bf16(x[k]);
+                            }
+                            v[i] = make_uint4(ct_pack(x[0], x[1]), ct_pack(x[2], x[3]), ct_pack(x[4], x[5]),
+                                              ct_pack(x[6], x[7]));
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (at[i] >= 0) *reinterpret_cast<uint4 *>(dst + at[i]) = v[i];
+            }
+            ct_fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[w]);
+        };
+
+        uint32_t n0 = 0, sc = 0, oc0 = 0, oc1 = 0;
+        bool turns_before = true;
+        const CtSeg *cur = &seg_get(0);
+        if (cur->nb) load_q(*cur);
+        for (uint32_t seg = 0; cur->nb; ++seg) {
+            const ChunkSeg &g = cur->g;
+            const bool turns = cur->turns;
+            const int nb = cur->nb;
+            const int steps = turns ? (nb + 1 - w) >> 1 : nb;
+            const int rel = token_of(*cur);  // this row attends positions up to pos0 + rel
+            const bool valid = tok_r < half_tokens && rel < g.tokens && head_r < cur->heads.count &&
+                               (PARTS == 1 || piece < PARTS);
+            const bool busy = __any_sync(0xffffffffu, valid);
+            float m_ref = -INFINITY, sum = 0.0f;
+            if (turns && !turns_before) named_sync(1, 256);  // the shared notes of the tile before are read
+            turns_before = turns;
+            for (int i = 0; i < steps; ++i, ++sc) {
+                const int j = turns ? 2 * i + w : i;
+                const int t0 = (g.b0 + j) * kCtStep;
+                const bool masked = t0 + kCtStep - 1 > g.pos0;
+                if (masked) {
+                    // both parts write and read one set of notes when they share
+                    // the steps: neither begins before the other is done with
+                    // the tile before
+                    if (!turns) named_sync(1, 256);
+                    // this thread: position t0 + t of V; both halves of the dims
+                    // (turns), or the part's half of them
+                    const uint32_t n = n0 + (uint32_t)ct_v_place(turns, j, nb);
+                    ct_wait(&sh.full[n % ST], (n / ST) & 1, dead, a.err);
+                    unsigned char *row = s_ring + (size_t)(n % ST) * Cfg::kTileBytes + t * 128;
+                    const int c0 = turns ? 0 : w * (HD / 16), c1 = turns ? HD / 8 : c0 + HD / 16;
+                    const int behind = t0 + t - g.pos0;
+                    if (t0 + t >= g.len) {
+                        for (int ch = c0; ch < c1; ++ch)
+                            *reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + (((ch & 7) ^ (t & 7)) << 4)) =
+                                make_uint4(0, 0, 0, 0);
+                    } else if (behind > 0) {
+                        for (int ch = c0; ch < c1; ++ch) {
+                            uint4 *p = reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + (((ch & 7) ^ (t & 7)) << 4));
+                            const uint4 x = *p;
+                            uint32_t u[4] = {x.x, x.y, x.z, x.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                bad |= (u[e] & 0x7f80u) == 0x7f80u || (u[e] & 0x7f800000u) == 0x7f800000u;
+                            if (bad) {
+#pragma unroll
+                                for (int e = 0; e < 8; ++e) {
+                                    const uint32_t b = (u[e >> 1] >> (16 * (e & 1))) & 0xffffu;
+                                    if ((b & 0x7f80u) != 0x7f80u) continue;
+                                    ct_note(&sh.note[turns ? w : 0][ch * 8 + e], behind, __uint_as_float(b << 16));
+                                    u[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
+                                }
+                                *p = make_uint4(u[0], u[1], u[2], u[3]);
+                                sh.noted[turns ? w : 0] = 1;
+                            }
+                        }
+                    }
+                    ct_fence_async();
+                    __syncwarp();
+                    if (turns)
+                        named_sync(2 + w, 128);
+                    else
+                        named_sync(1, 256);
+                }
+                ct_wait(&sh.s_full[w], sc & 1, dead, a.err);
+                __syncwarp();  // tensor memory is read by whole warps
+                tc_fence_after();
+                if (busy) {
+                    // 64 scores at a time (128 would not leave registers to work
+                    // with): the upper half once for the maximum, the lower half
+                    // kept, the upper half read again for its weights
+                    float s[64];
+                    const int lim = masked ? g.pos0 + rel - t0 : kCtStep;
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int hf = 1; hf >= 0; --hf) {
+                        ct_ld32(ts + hf * 64, s);
+                        ct_ld32(ts + hf * 64 + 32, s + 32);
+                        ct_wait_ld();
+                        if (PARTS == 3) {
+                            const int l0 = lane % RPW;
+#pragma unroll
+                            for (int k = 0; k < 64; ++k) {
+                                const float hi = __shfl_sync(0xffffffffu, s[k], l0);
+                                const float mid = __shfl_sync(0xffffffffu, s[k], l0 + RPW);
+                                const float lo = __shfl_sync(0xffffffffu, s[k], l0 + 2 * RPW);
+                                s[k] = (lo + mid) + hi;
+                            }
+                            if (hf == 1) {
+                                ct_st32f(ts + 64, s);
+                                ct_st32f(ts + 96, s + 32);
+                            }
+                        }
+                        if (masked) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k) s[k] = hf * 64 + k <= lim ? s[k] : -INFINITY;
+                        }
+                        float t4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+                        for (int k = 4; k < 64; ++k) t4[k & 3] = fmaxf(t4[k & 3], s[k]);
+                        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
+                    }
+                    const float m_new = fmaxf(m_ref, top);
+                    if (i == 0) {
+                        m_ref = m_new;
+                    } else if (__any_sync(0xffffffffu, valid && (m_new - m_ref) * c > kCtLag)) {
+                        const float f = m_new == -INFINITY ? 1.0f : ct_exp2((m_ref - m_new) * c);
+                        m_ref = m_new;
+                        sum *= f;
+#pragma unroll 1
+                        for (int k = 0; k < HD; k += 16) {
+                            float o[16];
+                            ct_ld16(to + k, o);
+                            ct_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] *= f;
+                            ct_st16(to + k, o);
+                        }
+                    }
+                    const float mc = m_ref == -INFINITY ? 0.0f : m_ref * c;
+                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf) {
+                        if (hf == 1) {
+                            if (PARTS == 3) ct_wait_st();
+                            ct_ld32(ts + 64, s);
+                            ct_ld32(ts + 96, s + 32);
+                            ct_wait_ld();
+                            if (masked) {
+#pragma unroll
+                                for (int k = 0; k < 64; ++k) s[k] = 64 + k <= lim ? s[k] : -INFINITY;
+                            }
+                        }
+                        uint32_t p[32];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            float x = ct_exp2(fmaf(s[2 * k], c, -mc)), y = ct_exp2(fmaf(s[2 * k + 1], c, -mc));
+                            add[(2 * k) & 3] += x;
+                            add[(2 * k + 1) & 3] += y;
+                            if (PARTS == 3) {
+                                if (piece > 0) {
+                                    x -= ct_bf16(x);
+                                    y -= ct_bf16(y);
+                                }
+                                if (piece > 1) {
+                                    x -= ct_bf16(x);
+                                    y -= ct_bf16(y);
+                                }
+                            }
+                            p[k] = ct_pack(x, y);
+                        }
+                        ct_st32(ts + hf * 32, p);
+                    }
+                    sum += (add[0] + add[1]) + (add[2] + add[3]);
+                    ct_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[w]);
+            }
+            n0 += 2 * nb;
+
+            // the next tile's q goes in while this one's last PV runs
+            const CtSeg *next = &seg_get(seg + 1);
+            if (turns) {
+                if (w == 1 && t < 128) sh.ml[t] = make_float2(m_ref, sum);
+                named_sync(1, 256);  // part 1's maxima and notes are written, both parts' q is read
+            }
+            if (next->nb) load_q(*next);
+
+            const int steps0 = turns ? (nb + 1) >> 1 : nb, steps1 = turns ? nb >> 1 : nb;
+            if (w == 0 || !turns) {
+                ct_wait(&sh.o_full[w], (w ? oc1 : oc0) & 1, dead, a.err);
+                if (turns && steps1) ct_wait(&sh.o_full[1], oc1 & 1, dead, a.err);
+                __syncwarp();
+                tc_fence_after();
+                const bool notes = sh.noted[0] || (turns && sh.noted[1]);
+                const bool split = cur->split;
+                float f0 = 1.0f, f1 = 0.0f;
+                if (turns && steps1) {  // join the two parts' turns
+                    const float2 o = sh.ml[t];
+                    const float top = fmaxf(m_ref, o.x);
+                    f0 = m_ref == top ? 1.0f : ct_exp2((m_ref - top) * c);
+                    f1 = o.x == top ? 1.0f : ct_exp2((o.x - top) * c);
+                    m_ref = top;
+                    sum = sum * f0 + o.y * f1;
+                }
+                if (busy) {
+                    const int m = (turns ? 0 : w * half_tokens * a.part_heads) + r;  // pair in the tile's record
+                    float *rec = split ? chunk_record(a, blockIdx.x, g.slot) : nullptr;
+                    const long long o = ((long long)(g.r0 + rel) * a.n_qh + cur->heads.first + head_r) * HD;
+                    const float inv = split ? 1.0f : 1.0f / sum;
+                    const bool writes = valid && piece == 0;
+                    if (split && writes) {
+                        rec[2 * m] = m_ref * c;
+                        rec[2 * m + 1] = sum;
+                    }
+#pragma unroll 1
+                    for (int k = 0; k < HD; k += 32) {
+                        float v[32], v1[32];
+                        ct_ld32(to + k, v);
+                        if (turns && steps1) ct_ld32(to + HD + k, v1);
+                        ct_wait_ld();
+                        if (turns && steps1) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] = v[e] * f0 + v1[e] * f1;
+                        }
+                        if (PARTS == 3) {
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float mid = __shfl_down_sync(0xffffffffu, v[e], RPW);
+                                const float lo = __shfl_down_sync(0xffffffffu, v[e], 2 * RPW);
+                                v[e] = (lo + mid) + v[e];
+                            }
+                        }
+                        unsigned nans = 0;
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) nans |= (v[e] != v[e] ? 1u : 0u) << e;
+                        if (writes && sum == sum) {
+                            while (nans) {
+                                const int d = __ffs(nans) - 1;
+                                nans &= nans - 1;
+                                const float x = ct_infinite(a, g.seq, cur->heads.kv, k + d, g.b0 * kCtStep,
+                                                            min(g.b1 * kCtStep, g.pos0 + rel + 1));
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) v[e] = e == d ? x : v[e];
+                            }
+                        }
+                        __syncwarp();
+                        if (notes) {
+                            for (int e = 0; e < 32; ++e) {
+                                v[e] += ct_noted(sh.note[0][k + e], rel);
+                                if (turns) v[e] += ct_noted(sh.note[1][k + e], rel);
+                            }
+                        }
+                        if (!writes) {
+                        } else if (split) {
+                            float4 *d = reinterpret_cast<float4 *>(rec + 2 * a.rec_rows + (size_t)m * HD + k);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                __stcg(d + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
+                        } else if (PARTS == 3) {
+                            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o + k);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e)
+                                d[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
+                                                   v[4 * e + 3] * inv);
+                        } else {
+                            uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + o + k);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                d[e] = make_uint4(ct_pack(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                  ct_pack(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                  ct_pack(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                  ct_pack(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                        }
+                        __syncwarp();
+                    }
+                }
+                if (split) {
+                    __threadfence();
+                    named_sync(2 + w, 128);
+                    if (t == 0) {
+                        int *ctr = a.counters + cur->share.counter * 2 + (turns ? 0 : w);
+                        const int last = atomicAdd(ctr, 1) == cur->share.last - cur->share.first;
+                        if (last) *ctr = 0;  // ready for the next launch
+                        sh.last[w] = last;
+                    }
+                    named_sync(2 + w, 128);
+                    if (sh.last[w]) {
+                        __threadfence();
+                        const int per = half_tokens * a.part_heads, all = g.tokens * a.part_heads;
+                        chunk_join(a, g, cur->share, unit, turns || w == 0 ? 0 : per,
+                                   turns || w == 1 ? all : per, q4, 4);
+                    }
+                    named_sync(2 + w, 128);  // sh.last is read
+                }
+                if (notes && !turns) {  // both parts have read the notes: each clears what it wrote
+                    named_sync(1, 256);
+                    for (int d = t; d < HD / 2; d += 128) sh.note[0][w * (HD / 2) + d] = kCtNoNote;
+                    if (t == 0) sh.noted[0] = 0;
+                    named_sync(1, 256);
+                }
+                if (notes && turns) {
+                    named_sync(2, 128);
+                    for (int d = t; d < HD; d += 128) sh.note[0][d] = sh.note[1][d] = kCtNoNote;
+                    if (t < 2) sh.noted[t] = 0;
+                }
+            }
+            if (turns) named_sync(1, 256);  // part 0 has read part 1's accumulator and notes
+            if (steps0) ++oc0;
+            if (steps1) ++oc1;
+            __syncwarp();
+            if (lane == 0) seg_done(seg);
+            cur = next;
+        }
+    }
+    if (flags) flag_error(a.err, flags);
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+bool chunk_tc_supported(const ChunkArgs &a) {
+    return a.kv_dtype == DS_BF16 && (a.hd == 64 || a.hd == 128) && a.bt % 8 == 0;
+}
+
+int chunk_tc_grid() { return sm_count(); }
+
+template <int HD, int PARTS>
+static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, cudaStream_t stream) {
+    static std::atomic<unsigned long long> ready{0};  // one bit per device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load() & bit)) {
+        e = cudaFuncSetAttribute((const void *)chunk_tc_kernel<HD, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)CtCfg<HD>::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) ready.fetch_or(bit);
+    }
+    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(chunk_tc_grid()), dim3(kCtThreads), CtCfg<HD>::kSmem, stream, false,
+                     a, maps);
+}
+
+cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
+    static_assert(CtCfg<128>::kSmem <= kCtSmemLimit && CtCfg<64>::kSmem <= kCtSmemLimit, "shared memory");
+    chunk_tile_shape(a, a.q_dtype == DS_BF16 ? 128 : 40, 2);
+    a.step = kCtStep;
+    a.min_cost = kCtMinCost;
+    CtMaps maps;
+    maps.box_rows = 8;
+    while (maps.box_rows < 128 && a.bt % (2 * maps.box_rows) == 0) maps.box_rows *= 2;
+    const long long dims[3] = {64, a.cache_rows, (long long)a.n_kvh * a.hd / 64};
+    const long long strides[2] = {(long long)a.n_kvh * a.hd * 2, 128};
+    const int box[3] = {64, maps.box_rows, 1};
+    if (!encode_tiled_3d(&maps.k, a.k_cache, DS_BF16, dims, strides, box, true) ||
+        !encode_tiled_3d(&maps.v, a.v_cache, DS_BF16, dims, strides, box, true))
+        return cudaErrorInvalidValue;
+    if (a.hd == 128)
+        return a.q_dtype == DS_BF16 ? launch_ct<128, 1>(a, maps, stream) : launch_ct<128, 3>(a, maps, stream);
+    return a.q_dtype == DS_BF16 ? launch_ct<64, 1>(a, maps, stream) : launch_ct<64, 3>(a, maps, stream);
+}
+
+}  // namespace ds
