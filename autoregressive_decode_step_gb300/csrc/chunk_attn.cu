@@ -37,7 +37,7 @@ __device__ __forceinline__ float4 cs_load4(const void *base, long long i, int dt
 }
 
 template <int HD>
-__global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kernel(const ChunkArgs a) {
+__global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) float sm[];
     constexpr int KS = HD + 4;  // K rows padded: sixteen rows read at once fall into different banks
     constexpr int PS = kCsStep + 4;

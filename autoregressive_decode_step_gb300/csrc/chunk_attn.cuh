@@ -286,44 +286,100 @@ __device__ inline void chunk_zero_empty_rows(const ChunkArgs &a) {
 // Join the records of a split tile's (row, head) pairs [m0, m1) in CTA order
 // and write their outputs; warp w of n_warps.
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
-__device__ inline void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h, long long unit, int m0,
-                                  int m1, int w, int n_warps) {
+// The records come from L2, so the loads in flight bound it: a warp takes
+// four pairs at a time (lane l: four dims of each) and four records of each,
+// 16 x 512 bytes; a tile of few pairs has one pair a warp and more records of
+// it.  The weights of a batch of 32 pairs are formed lane by lane first.
+template <int PAIRS, int RECS>
+__device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
+                                                 const ChunkHeads &hh, long long unit, int m0, int m1, int w,
+                                                 int n_warps) {
     const int lane = threadIdx.x & 31;
-    const ChunkHeads hh = chunk_heads(a, g.part);
-    for (int m = m0 + w; m < m1; m += n_warps) {
-        const int tok = m / a.part_heads, head = m % a.part_heads;
-        if (head >= hh.count) continue;
-        float M = -INFINITY;
-        for (int c = h.first + lane; c <= h.last; c += 32)
-            M = fmaxf(M, __ldcg(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m));
-        M = warp_max(M);
-        const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd;
-        for (int d = lane * 4; d < a.hd; d += 128) {
-            float L = 0.0f, A[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            for (int c0 = h.first; c0 <= h.last; c0 += 4) {  // four records' loads in flight
-                float2 ml[4];
-                float v[4][4];
+    // pair i of the warp: m0 + w + i * n_warps; lane l keeps pair i0 + l's sums
+    const int mine = (m1 - m0 - w + n_warps - 1) / n_warps;
+    for (int i0 = 0; i0 < mine; i0 += 32) {
+        const int m_l = min(m0 + w + (i0 + lane) * n_warps, m1 - 1);
+        float M = -INFINITY, L = 0.0f;
+        for (int c0 = h.first; c0 <= h.last; c0 += 8) {
+            float v[8];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c0 + k > h.last) break;
-                    const float *rec = chunk_record(a, c0 + k, chunk_slot(g, unit, c0 + k));
-                    ml[k] = make_float2(__ldcg(rec + 2 * m), __ldcg(rec + 2 * m + 1));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[k][e] = __ldcg(rec + 2 * a.rec_rows + (size_t)m * a.hd + d + e);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c0 + k > h.last) break;
-                    const float f = exp2f(ml[k].x - M);
-                    L = fmaf(ml[k].y, f, L);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) A[e] = fmaf(v[k][e], f, A[e]);
-                }
+            for (int k = 0; k < 8; ++k) {
+                const int c = min(c0 + k, h.last);
+                v[k] = __ldcg(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m_l);
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) store_as(a.out, o + d + e, a.q_dtype, A[e] / L);
+            for (int k = 0; k < 8; ++k) M = fmaxf(M, v[k]);
+        }
+        for (int c0 = h.first; c0 <= h.last; c0 += 8) {
+            float2 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = min(c0 + k, h.last);
+                v[k] = __ldcg(reinterpret_cast<const float2 *>(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m_l));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c0 + k <= h.last) L = fmaf(v[k].y, exp2f(v[k].x - M), L);
+        }
+        for (int i = i0; i < min(mine, i0 + 32); i += PAIRS) {
+            for (int d0 = 0; d0 < a.hd; d0 += 128) {
+                const int d = min(d0 + lane * 4, a.hd - 4);
+                float4 acc[PAIRS];
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int c0 = h.first; c0 <= h.last; c0 += RECS) {
+                    float4 v[PAIRS][RECS];
+                    float f[PAIRS][RECS];
+#pragma unroll
+                    for (int k = 0; k < RECS; ++k) {
+                        const int c = min(c0 + k, h.last);
+                        const float *rec = chunk_record(a, c, chunk_slot(g, unit, c));
+#pragma unroll
+                        for (int j = 0; j < PAIRS; ++j) {
+                            const int m = min(m0 + w + (i + j) * n_warps, m1 - 1);
+                            f[j][k] = __ldcg(rec + 2 * m);
+                            v[j][k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < PAIRS; ++j) {
+                        const float Mj = __shfl_sync(0xffffffffu, M, (i + j - i0) & 31);
+#pragma unroll
+                        for (int k = 0; k < RECS; ++k) {
+                            if (c0 + k > h.last) continue;
+                            const float e = exp2f(f[j][k] - Mj);
+                            acc[j].x = fmaf(v[j][k].x, e, acc[j].x);
+                            acc[j].y = fmaf(v[j][k].y, e, acc[j].y);
+                            acc[j].z = fmaf(v[j][k].z, e, acc[j].z);
+                            acc[j].w = fmaf(v[j][k].w, e, acc[j].w);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < PAIRS; ++j) {
+                    const float Lj = __shfl_sync(0xffffffffu, L, (i + j - i0) & 31);
+                    const int m = m0 + w + (i + j) * n_warps;
+                    const int tok = m / a.part_heads, head = m % a.part_heads;
+                    if (i + j >= mine || head >= hh.count || d0 + lane * 4 >= a.hd) continue;
+                    const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
+                    store_as(a.out, o, a.q_dtype, acc[j].x / Lj);
+                    store_as(a.out, o + 1, a.q_dtype, acc[j].y / Lj);
+                    store_as(a.out, o + 2, a.q_dtype, acc[j].z / Lj);
+                    store_as(a.out, o + 3, a.q_dtype, acc[j].w / Lj);
+                }
+                __syncwarp();
+            }
         }
     }
+}
+
+static __device__ __noinline__ void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h, long long unit,
+                                        int m0, int m1, int w, int n_warps) {
+    const ChunkHeads hh = chunk_heads(a, g.part);
+    if (m1 - m0 <= 2 * n_warps)
+        chunk_join_pairs<1, 8>(a, g, h, hh, unit, m0, m1, w, n_warps);
+    else
+        chunk_join_pairs<4, 2>(a, g, h, hh, unit, m0, m1, w, n_warps);
 }
 
 }  // namespace ds

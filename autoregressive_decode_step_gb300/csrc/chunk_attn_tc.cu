@@ -51,6 +51,9 @@ namespace ds {
 
 constexpr int kCtStep = 128;
 constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, the producer and the walking warp
+// Registers a thread: 168 at launch (384 x 168), moved to the softmax
+// warpgroups, whose thread holds a row's 128 scores: 2 x 216 + 72 = 3 x 168.
+constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 constexpr int kCtMinCost = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
@@ -105,35 +108,15 @@ __device__ __forceinline__ void ct_ld16(uint32_t taddr, float *v) {
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void ct_st16(uint32_t taddr, const float *v) {
+__device__ __forceinline__ void ct_st16(uint32_t taddr, const uint32_t *v) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
         "%14, %15, %16};" ::"r"(taddr),
-        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]), "f"(v[9]),
-        "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
 __device__ __forceinline__ void ct_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void ct_st32(uint32_t taddr, const uint32_t *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-__device__ __forceinline__ void ct_st32f(uint32_t taddr, const float *r) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
-        "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(taddr),
-        "f"(r[0]), "f"(r[1]), "f"(r[2]), "f"(r[3]), "f"(r[4]), "f"(r[5]), "f"(r[6]), "f"(r[7]), "f"(r[8]), "f"(r[9]),
-        "f"(r[10]), "f"(r[11]), "f"(r[12]), "f"(r[13]), "f"(r[14]), "f"(r[15]), "f"(r[16]), "f"(r[17]), "f"(r[18]),
-        "f"(r[19]), "f"(r[20]), "f"(r[21]), "f"(r[22]), "f"(r[23]), "f"(r[24]), "f"(r[25]), "f"(r[26]), "f"(r[27]),
-        "f"(r[28]), "f"(r[29]), "f"(r[30]), "f"(r[31])
-        : "memory");
-}
 __device__ __forceinline__ void ct_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void ct_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
@@ -141,6 +124,24 @@ __device__ __forceinline__ float ct_exp2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// a * b + c and a + b, two numbers at a time.
+__device__ __forceinline__ float2 ct_fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 ct_add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
 }
 // bf16 pair, a in the low half.
 __device__ __forceinline__ uint32_t ct_pack(float a, float b) {
@@ -250,8 +251,7 @@ __device__ __noinline__ float ct_infinite(const ChunkArgs &a, int seq, int kv, i
 // up by them) and outlast it by far: every role then runs through.
 __device__ __forceinline__ void ct_wait_seg(uint64_t *bar, uint32_t parity, int *err) {
     for (int k = 0; k < 8; ++k) {
-        int none = 0;
-        if (mbar_wait(bar, parity, k == 7 ? err : &none)) return;
+        if (mbar_wait(bar, parity, k == 7 ? err : nullptr)) return;
     }
 }
 
@@ -309,6 +309,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     };
     auto seg_done = [&](uint32_t k) { mbar_arrive(&sh.seg_empty[k % kCtSegs]); };  // one thread of the warp
 
+    if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
     if (warp == 10) {
         // ------------------------------------------------ the walk over this CTA's range
         if (lane == 0) {
@@ -384,9 +386,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         // every copy issued has landed before the block may end
         if (lane == 0) {
-            int none = 0;
             for (uint32_t f = n > ST ? n - ST : 0; f < n; ++f)
-                if (!mbar_wait(&sh.full[f % ST], (f / ST) & 1, *dead ? &none : a.err)) break;
+                if (!mbar_wait(&sh.full[f % ST], (f / ST) & 1, *dead ? nullptr : a.err)) break;
         }
         __syncwarp();
     } else if (warp == 8) {
@@ -464,11 +465,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
             // nothing of ours runs on the tensor cores when the block ends
             tc_commit(&sh.done);
-            int none = 0;
-            mbar_wait(&sh.done, 0, *dead ? &none : a.err);
+            mbar_wait(&sh.done, 0, *dead ? nullptr : a.err);
         }
         __syncwarp();
-    } else if (warp < 8) {
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kCtRegsSoftmax));
         // ------------------------------------------------ softmax, part w
         const int w = warp >> 2, q4 = warp & 3, t = tid & 127;
         const int r = PARTS == 1 ? t : q4 * RPW + lane % RPW;  // row of the part
@@ -597,40 +599,30 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 __syncwarp();  // tensor memory is read by whole warps
                 tc_fence_after();
                 if (busy) {
-                    // 64 scores at a time (128 would not leave registers to work
-                    // with): the upper half once for the maximum, the lower half
-                    // kept, the upper half read again for its weights
-                    float s[64];
-                    const int lim = masked ? g.pos0 + rel - t0 : kCtStep;
-                    float top = -INFINITY;
+                    float s[kCtStep];
 #pragma unroll
-                    for (int hf = 1; hf >= 0; --hf) {
-                        ct_ld32(ts + hf * 64, s);
-                        ct_ld32(ts + hf * 64 + 32, s + 32);
-                        ct_wait_ld();
-                        if (PARTS == 3) {
-                            const int l0 = lane % RPW;
+                    for (int k = 0; k < kCtStep; k += 32) ct_ld32(ts + k, s + k);
+                    ct_wait_ld();
+                    if (PARTS == 3) {
+                        const int l0 = lane % RPW;
 #pragma unroll
-                            for (int k = 0; k < 64; ++k) {
-                                const float hi = __shfl_sync(0xffffffffu, s[k], l0);
-                                const float mid = __shfl_sync(0xffffffffu, s[k], l0 + RPW);
-                                const float lo = __shfl_sync(0xffffffffu, s[k], l0 + 2 * RPW);
-                                s[k] = (lo + mid) + hi;
-                            }
-                            if (hf == 1) {
-                                ct_st32f(ts + 64, s);
-                                ct_st32f(ts + 96, s + 32);
-                            }
+                        for (int k = 0; k < kCtStep; ++k) {
+                            const float hi = __shfl_sync(0xffffffffu, s[k], l0);
+                            const float mid = __shfl_sync(0xffffffffu, s[k], l0 + RPW);
+                            const float lo = __shfl_sync(0xffffffffu, s[k], l0 + 2 * RPW);
+                            s[k] = (lo + mid) + hi;
                         }
-                        if (masked) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) s[k] = hf * 64 + k <= lim ? s[k] : -INFINITY;
-                        }
-                        float t4[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-                        for (int k = 4; k < 64; ++k) t4[k & 3] = fmaxf(t4[k & 3], s[k]);
-                        top = fmaxf(top, fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])));
                     }
+                    if (masked) {
+                        const int lim = g.pos0 + rel - t0;
+#pragma unroll
+                        for (int k = 0; k < kCtStep; ++k) s[k] = k <= lim ? s[k] : -INFINITY;
+                    }
+                    float t4[4] = {s[0], s[1], s[2], s[3]};  // chains of three-input maxima
+#pragma unroll
+                    for (int k = 4; k + 1 < kCtStep; k += 2)
+                        t4[(k >> 1) & 3] = fmaxf(fmaxf(t4[(k >> 1) & 3], s[k]), s[k + 1]);
+                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     const float m_new = fmaxf(m_ref, top);
                     if (i == 0) {
                         m_ref = m_new;
@@ -641,48 +633,42 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll 1
                         for (int k = 0; k < HD; k += 16) {
                             float o[16];
+                            uint32_t u[16];
                             ct_ld16(to + k, o);
                             ct_wait_ld();
 #pragma unroll
-                            for (int e = 0; e < 16; ++e) o[e] *= f;
-                            ct_st16(to + k, o);
+                            for (int e = 0; e < 16; ++e) u[e] = __float_as_uint(o[e] * f);
+                            ct_st16(to + k, u);
                         }
                     }
                     const float mc = m_ref == -INFINITY ? 0.0f : m_ref * c;
-                    float add[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    // two scores an instruction where the machine has the pair form
+                    const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                    float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        if (hf == 1) {
-                            if (PARTS == 3) ct_wait_st();
-                            ct_ld32(ts + 64, s);
-                            ct_ld32(ts + 96, s + 32);
-                            ct_wait_ld();
-                            if (masked) {
+                    for (int k0 = 0; k0 < kCtStep; k0 += 32) {
+                        uint32_t p[16];
 #pragma unroll
-                                for (int k = 0; k < 64; ++k) s[k] = 64 + k <= lim ? s[k] : -INFINITY;
-                            }
-                        }
-                        uint32_t p[32];
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) {
-                            float x = ct_exp2(fmaf(s[2 * k], c, -mc)), y = ct_exp2(fmaf(s[2 * k + 1], c, -mc));
-                            add[(2 * k) & 3] += x;
-                            add[(2 * k + 1) & 3] += y;
+                        for (int k = 0; k < 16; ++k) {
+                            float2 x = ct_fma2(make_float2(s[k0 + 2 * k], s[k0 + 2 * k + 1]), c2, mc2);
+                            x.x = ct_exp2(x.x);
+                            x.y = ct_exp2(x.y);
+                            add[k & 1] = ct_add2(add[k & 1], x);
                             if (PARTS == 3) {
                                 if (piece > 0) {
-                                    x -= ct_bf16(x);
-                                    y -= ct_bf16(y);
+                                    x.x -= ct_bf16(x.x);
+                                    x.y -= ct_bf16(x.y);
                                 }
                                 if (piece > 1) {
-                                    x -= ct_bf16(x);
-                                    y -= ct_bf16(y);
+                                    x.x -= ct_bf16(x.x);
+                                    x.y -= ct_bf16(x.y);
                                 }
                             }
-                            p[k] = ct_pack(x, y);
+                            p[k] = ct_pack(x.x, x.y);
                         }
-                        ct_st32(ts + hf * 32, p);
+                        ct_st16(ts + k0 / 2, p);
                     }
-                    sum += (add[0] + add[1]) + (add[2] + add[3]);
+                    sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     ct_wait_st();
                     tc_fence_before();
                 }
