@@ -50,7 +50,7 @@
 namespace ds {
 
 constexpr int kCtStep = 128;
-constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, the producer and the walking warp
+constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, walking, K/V and q warps
 // Registers a thread: 168 at launch (384 x 168), moved to the softmax
 // warpgroups, whose thread holds a row's 128 scores: 2 x 216 + 72 = 3 x 168.
 constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
@@ -75,6 +75,7 @@ struct CtCfg {
 
 struct CtMaps {
     CUtensorMap k, v;  // {64, cache_rows, n_kvh * hd / 64}, boxes {64, box_rows, 1}, 128-byte swizzle
+    CUtensorMap q;     // bf16 q: {hd, n_qh, n_rows}, boxes {64, heads of a part, rows of a part}, the same swizzle
     int box_rows;
 };
 
@@ -151,11 +152,11 @@ __device__ __forceinline__ uint32_t ct_pack(float a, float b) {
 }
 __device__ __forceinline__ float ct_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
-__device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int row, int half, uint64_t *bar) {
+__device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
             dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(half), "r"(smem_u32(bar))
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
 
@@ -198,7 +199,7 @@ struct CtShared {
     CtSeg seg[kCtSegs];
     uint64_t seg_full[kCtSegs], seg_empty[kCtSegs];
     uint64_t full[kCtMaxStages], empty[kCtMaxStages];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done;
     uint32_t tmem;
     int dead;
     int noted[2];   // a part's notes hold something
@@ -276,7 +277,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_init(&sh.empty[i], 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(&sh.q_full[w], 4);
+            mbar_init(&sh.q_full[w], 1);
+            mbar_init(&sh.q_empty[w], 1);
             mbar_init(&sh.s_full[w], 1);
             mbar_init(&sh.p_full[w], 4);
             mbar_init(&sh.o_full[w], 1);
@@ -284,7 +286,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         for (int i = 0; i < kCtSegs; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 10);  // producer, MMA, eight softmax warps
+            mbar_init(&sh.seg_empty[i], 11);  // producers, MMA, eight softmax warps
         }
         mbar_init(&sh.done, 1);
         sh.dead = 0;
@@ -334,6 +336,73 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
         }
         __syncwarp();
+    } else if (warp == 11) {
+        // ------------------------------------------------ q of both parts
+        // A part's q is free once the tensor core is through with its last QK.
+        // MMA rows without a (row, head) pair hold anything: no row reaches
+        // another.
+        uint32_t issued = 0;
+        for (uint32_t seg = 0;; ++seg) {
+            const CtSeg &c = seg_get(seg);
+            if (c.nb == 0) break;
+            const bool turns = c.turns;
+            const int r0 = c.g.r0, tokens = c.g.tokens, first = c.heads.first, heads = c.heads.count;
+            __syncwarp();
+            if (lane == 0) seg_done(seg);
+            if (PARTS == 1) {
+                for (int w = 0; w < 2; ++w)
+                    if (seg) ct_wait(&sh.q_empty[w], (seg - 1) & 1, dead, a.err);
+                if (__any_sync(0xffffffffu, *dead)) continue;
+                ++issued;
+                for (int w = 0; w < 2; ++w) {
+                    if (lane == 0) {
+                        mbar_arrive_expect_tx(&sh.q_full[w], (uint32_t)(Cfg::kHalves * 128 * a.part_heads * half_tokens));
+                        for (int h = 0; h < Cfg::kHalves; ++h)
+                            ct_box(smem_u32(s_q) + w * Cfg::kTileBytes + h * kCtHalf, &maps.q, h * 64, first,
+                                   r0 + (turns ? 0 : w * half_tokens), &sh.q_full[w]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // eight values of a pair an item; pair p is row 32 (p / 10) + p % 10
+                // of its part, the mid and lo parts 10 and 20 rows further
+                for (int w = 0; w < (turns ? 1 : 2); ++w) {
+                    const int n_pairs = min(half_tokens, tokens - w * half_tokens) * a.part_heads;
+                    for (int u = w; u < (turns ? 2 : w + 1); ++u)
+                        if (seg) ct_wait(&sh.q_empty[u], (seg - 1) & 1, dead, a.err);
+                    for (int i = lane; i < n_pairs * (HD / 8); i += 32) {
+                        const int p = i / (HD / 8), ch = i % (HD / 8);
+                        const int tk = p / a.part_heads, h = p % a.part_heads;
+                        if (h >= heads) continue;
+                        const float4 *src = reinterpret_cast<const float4 *>(
+                            static_cast<const float *>(a.q) +
+                            ((long long)(r0 + w * half_tokens + tk) * a.n_qh + first + h) * HD + ch * 8);
+                        const float4 x0 = __ldg(src), x1 = __ldg(src + 1);
+                        float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
+#pragma unroll
+                        for (int z = 0; z < PARTS; ++z) {
+                            const uint4 v = make_uint4(ct_pack(x[0], x[1]), ct_pack(x[2], x[3]), ct_pack(x[4], x[5]),
+                                                       ct_pack(x[6], x[7]));
+                            const int m = (p / RPW) * 32 + p % RPW + z * RPW;
+                            unsigned char *dst = s_q + (ch >> 3) * kCtHalf + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
+                            for (int u = w; u < (turns ? 2 : w + 1); ++u)
+                                *reinterpret_cast<uint4 *>(dst + u * Cfg::kTileBytes) = v;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) x[k] -= ct_bf16(x[k]);
+                        }
+                    }
+                    ct_fence_async();
+                    __syncwarp();
+                    if (lane == 0)
+                        for (int u = w; u < (turns ? 2 : w + 1); ++u) mbar_arrive(&sh.q_full[u]);
+                }
+            }
+        }
+        // every copy issued has landed before the block may end
+        if (PARTS == 1 && lane == 0)
+            for (int w = 0; w < 2; ++w)
+                if (issued) mbar_wait(&sh.q_full[w], (issued - 1) & 1, *dead ? nullptr : a.err);
+        __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------ K/V producer
         uint32_t n = 0;
@@ -381,7 +450,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 __syncwarp();
                 if (bx < boxes)
                     ct_box(smem_u32(s_ring + (size_t)s * Cfg::kTileBytes) + hf * kCtHalf + bx * R * 128,
-                           is_v ? &maps.v : &maps.k, row, kv * Cfg::kHalves + hf, &sh.full[s]);
+                           is_v ? &maps.v : &maps.k, 0, row, kv * Cfg::kHalves + hf, &sh.full[s]);
             }
         }
         // every copy issued has landed before the block may end
@@ -431,12 +500,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll 1
                 for (int w = 0; w < 2; ++w) {
                     const int j = turns ? w : 0;
-                    if (j >= nb) continue;
-                    wait_tile(kn(j));
-                    tc_fence_after();
-                    qk(w, kn(j));
-                    if (turns || w == 1) tc_commit(&sh.empty[kn(j) % ST]);
-                    tc_commit(&sh.s_full[w]);
+                    if (j < nb) {
+                        wait_tile(kn(j));
+                        tc_fence_after();
+                        qk(w, kn(j));
+                        if (turns || w == 1) tc_commit(&sh.empty[kn(j) % ST]);
+                        tc_commit(&sh.s_full[w]);
+                    }
+                    if (j + (turns ? 2 : 1) >= nb) tc_commit(&sh.q_empty[w]);  // no further use of this tile's q
                 }
                 for (int i = 0; i < steps; ++i) {
 #pragma unroll 1
@@ -456,6 +527,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                             qk(w, kn(jn));
                             if (turns || w == 1) tc_commit(&sh.empty[kn(jn) % ST]);
                             tc_commit(&sh.s_full[w]);
+                            if (jn + (turns ? 2 : 1) >= nb) tc_commit(&sh.q_empty[w]);
                         } else {
                             tc_commit(&sh.o_full[w]);
                         }
@@ -480,61 +552,11 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         const float c = a.scale * kCtLog2e;
         const int tok_r = r / a.part_heads, head_r = r % a.part_heads;
         auto token_of = [&](const CtSeg &s) { return (s.turns ? 0 : w * half_tokens) + tok_r; };
-        // the part's 128 MMA rows of q, 16 bytes a thread, in the swizzled
-        // order the MMA reads; rows without a pair keep what is there (an MMA
-        // row reaches no other row)
-        auto load_q = [&](const CtSeg &s) {
-            const ChunkHeads hh = s.heads;
-            unsigned char *dst = s_q + w * Cfg::kTileBytes;
-            const int first = s.turns ? 0 : w * half_tokens, r0 = s.g.r0 + first;
-            const int tokens = min(half_tokens, s.g.tokens - first);
-            int base = t;
-            asm volatile("" : "+r"(base));  // the addresses below are formed here, not kept through the steps
-#pragma unroll 1
-            for (int i0 = 0; i0 < HD / 8; i0 += 4) {
-                uint4 v[4];
-                int at[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int idx = base + 128 * (i0 + i);
-                    const int m = idx / (HD / 8), ch = idx % (HD / 8);
-                    const int pr = PARTS == 1 ? m : (m >> 5) * RPW + (m & 31) % RPW;
-                    const int pc = PARTS == 1 ? 0 : (m & 31) / RPW;
-                    const int tk = pr / a.part_heads, h = pr % a.part_heads;
-                    at[i] = -1;
-                    if (tk < tokens && h < hh.count && (PARTS == 1 || pc < PARTS)) {
-                        at[i] = (ch >> 3) * kCtHalf + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
-                        const long long e = ((long long)(r0 + tk) * a.n_qh + hh.first + h) * HD + ch * 8;
-                        if (PARTS == 1) {
-                            v[i] = __ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(a.q) + e));
-                        } else {
-                            const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(a.q) + e);
-                            const float4 x0 = __ldg(p), x1 = __ldg(p + 1);
-                            float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                if (pc > 0) x[k] -= ct_bf16(x[k]);
-                                if (pc > 1) x[k] -= ct_bf16(x[k]);
-                            }
-                            v[i] = make_uint4(ct_pack(x[0], x[1]), ct_pack(x[2], x[3]), ct_pack(x[4], x[5]),
-                                              ct_pack(x[6], x[7]));
-                        }
-                    }
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (at[i] >= 0) *reinterpret_cast<uint4 *>(dst + at[i]) = v[i];
-            }
-            ct_fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[w]);
-        };
-
         uint32_t n0 = 0, sc = 0, oc0 = 0, oc1 = 0;
         bool turns_before = true;
-        const CtSeg *cur = &seg_get(0);
-        if (cur->nb) load_q(*cur);
-        for (uint32_t seg = 0; cur->nb; ++seg) {
+        for (uint32_t seg = 0;; ++seg) {
+            const CtSeg *cur = &seg_get(seg);
+            if (cur->nb == 0) break;
             const ChunkSeg &g = cur->g;
             const bool turns = cur->turns;
             const int nb = cur->nb;
@@ -677,14 +699,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
             n0 += 2 * nb;
 
-            // the next tile's q goes in while this one's last PV runs
-            const CtSeg *next = &seg_get(seg + 1);
             if (turns) {
                 if (w == 1 && t < 128) sh.ml[t] = make_float2(m_ref, sum);
-                named_sync(1, 256);  // part 1's maxima and notes are written, both parts' q is read
+                named_sync(1, 256);  // part 1's maxima and notes are written
             }
-            if (next->nb) load_q(*next);
-
             const int steps0 = turns ? (nb + 1) >> 1 : nb, steps1 = turns ? nb >> 1 : nb;
             if (w == 0 || !turns) {
                 ct_wait(&sh.o_full[w], (w ? oc1 : oc0) & 1, dead, a.err);
@@ -809,7 +827,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             if (steps1) ++oc1;
             __syncwarp();
             if (lane == 0) seg_done(seg);
-            cur = next;
         }
     }
     if (flags) flag_error(a.err, flags);
@@ -845,7 +862,7 @@ cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
     chunk_tile_shape(a, a.q_dtype == DS_BF16 ? 128 : 40, 2);
     a.step = kCtStep;
     a.min_cost = kCtMinCost;
-    CtMaps maps;
+    CtMaps maps = {};
     maps.box_rows = 8;
     while (maps.box_rows < 128 && a.bt % (2 * maps.box_rows) == 0) maps.box_rows *= 2;
     const long long dims[3] = {64, a.cache_rows, (long long)a.n_kvh * a.hd / 64};
@@ -854,6 +871,12 @@ cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
     if (!encode_tiled_3d(&maps.k, a.k_cache, DS_BF16, dims, strides, box, true) ||
         !encode_tiled_3d(&maps.v, a.v_cache, DS_BF16, dims, strides, box, true))
         return cudaErrorInvalidValue;
+    if (a.q_dtype == DS_BF16) {
+        const long long qdims[3] = {a.hd, a.n_qh, a.n_rows};
+        const long long qstrides[2] = {(long long)a.hd * 2, (long long)a.n_qh * a.hd * 2};
+        const int qbox[3] = {64, a.part_heads, a.tile_tokens / 2};
+        if (!encode_tiled_3d(&maps.q, a.q, DS_BF16, qdims, qstrides, qbox, true)) return cudaErrorInvalidValue;
+    }
     if (a.hd == 128)
         return a.q_dtype == DS_BF16 ? launch_ct<128, 1>(a, maps, stream) : launch_ct<128, 3>(a, maps, stream);
     return a.q_dtype == DS_BF16 ? launch_ct<64, 1>(a, maps, stream) : launch_ct<64, 3>(a, maps, stream);
