@@ -239,16 +239,21 @@ __device__ __forceinline__ int chunk_slot(const ChunkSeg &g, long long unit, int
     return g.start < (long long)c * unit ? 0 : 1;
 }
 
-// First cache row of the sequence's position `pos` block; a block number
-// outside the pool reads block 0 and flags.
-__device__ __forceinline__ long long chunk_block_row(const ChunkArgs &a, int seq, int blk, int &flags) {
-    long long id = a.block_table ? (long long)__ldg(a.block_table + (long long)seq * a.max_blocks + blk)
-                                 : (long long)seq * a.max_blocks + blk;
+// A sequence's block number as the table has it, and the block's first cache
+// row; a number outside the pool reads block 0 and flags.  (Two calls, so that
+// a caller can fetch ahead.)
+__device__ __forceinline__ int chunk_block_id(const ChunkArgs &a, int seq, int blk) {
+    return a.block_table ? __ldg(a.block_table + (long long)seq * a.max_blocks + blk) : seq * a.max_blocks + blk;
+}
+__device__ __forceinline__ long long chunk_id_row(const ChunkArgs &a, int id, int &flags) {
     if (id < 0 || id >= a.pool_blocks) {
         flags |= DS_ERR_POSITION;
         id = 0;
     }
-    return id * a.bt;
+    return (long long)id * a.bt;
+}
+__device__ __forceinline__ long long chunk_block_row(const ChunkArgs &a, int seq, int blk, int &flags) {
+    return chunk_id_row(a, chunk_block_id(a, seq, blk), flags);
 }
 
 // Query heads of a head part: count heads from `first` on, of KV head kv.
@@ -287,99 +292,86 @@ __device__ inline void chunk_zero_empty_rows(const ChunkArgs &a) {
 // and write their outputs; warp w of n_warps.
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
 // The records come from L2, so the loads in flight bound it: a warp takes
-// four pairs at a time (lane l: four dims of each) and four records of each,
-// 16 x 512 bytes; a tile of few pairs has one pair a warp and more records of
-// it.  The weights of a batch of 32 pairs are formed lane by lane first.
+// PAIRS pairs at a time (lane l: four dims of each) and RECS records of each,
+// all loads before the first use.
 template <int PAIRS, int RECS>
 __device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
                                                  const ChunkHeads &hh, long long unit, int m0, int m1, int w,
                                                  int n_warps) {
     const int lane = threadIdx.x & 31;
-    // pair i of the warp: m0 + w + i * n_warps; lane l keeps pair i0 + l's sums
-    const int mine = (m1 - m0 - w + n_warps - 1) / n_warps;
-    for (int i0 = 0; i0 < mine; i0 += 32) {
-        const int m_l = min(m0 + w + (i0 + lane) * n_warps, m1 - 1);
-        float M = -INFINITY, L = 0.0f;
-        for (int c0 = h.first; c0 <= h.last; c0 += 8) {
-            float v[8];
+    for (int i0 = m0 + w; i0 < m1; i0 += PAIRS * n_warps) {
+        for (int d0 = 0; d0 < a.hd; d0 += 128) {
+            const int d = min(d0 + lane * 4, a.hd - 4);
+            float4 acc[PAIRS];
+            float M[PAIRS], L[PAIRS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = min(c0 + k, h.last);
-                v[k] = __ldcg(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m_l);
+            for (int j = 0; j < PAIRS; ++j) {
+                acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                M[j] = -INFINITY;
+                L[j] = 0.0f;
             }
+            for (int c0 = h.first; c0 <= h.last; c0 += RECS) {
+                float4 v[PAIRS][RECS];
+                float2 ml[PAIRS][RECS];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) M = fmaxf(M, v[k]);
-        }
-        for (int c0 = h.first; c0 <= h.last; c0 += 8) {
-            float2 v[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = min(c0 + k, h.last);
-                v[k] = __ldcg(reinterpret_cast<const float2 *>(chunk_record(a, c, chunk_slot(g, unit, c)) + 2 * m_l));
-            }
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (c0 + k <= h.last) L = fmaf(v[k].y, exp2f(v[k].x - M), L);
-        }
-        for (int i = i0; i < min(mine, i0 + 32); i += PAIRS) {
-            for (int d0 = 0; d0 < a.hd; d0 += 128) {
-                const int d = min(d0 + lane * 4, a.hd - 4);
-                float4 acc[PAIRS];
-#pragma unroll
-                for (int j = 0; j < PAIRS; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                for (int c0 = h.first; c0 <= h.last; c0 += RECS) {
-                    float4 v[PAIRS][RECS];
-                    float f[PAIRS][RECS];
-#pragma unroll
-                    for (int k = 0; k < RECS; ++k) {
-                        const int c = min(c0 + k, h.last);
-                        const float *rec = chunk_record(a, c, chunk_slot(g, unit, c));
-#pragma unroll
-                        for (int j = 0; j < PAIRS; ++j) {
-                            const int m = min(m0 + w + (i + j) * n_warps, m1 - 1);
-                            f[j][k] = __ldcg(rec + 2 * m);
-                            v[j][k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
-                        }
-                    }
+                for (int k = 0; k < RECS; ++k) {
+                    const int c = min(c0 + k, h.last);
+                    const float *rec = chunk_record(a, c, chunk_slot(g, unit, c));
 #pragma unroll
                     for (int j = 0; j < PAIRS; ++j) {
-                        const float Mj = __shfl_sync(0xffffffffu, M, (i + j - i0) & 31);
-#pragma unroll
-                        for (int k = 0; k < RECS; ++k) {
-                            if (c0 + k > h.last) continue;
-                            const float e = exp2f(f[j][k] - Mj);
-                            acc[j].x = fmaf(v[j][k].x, e, acc[j].x);
-                            acc[j].y = fmaf(v[j][k].y, e, acc[j].y);
-                            acc[j].z = fmaf(v[j][k].z, e, acc[j].z);
-                            acc[j].w = fmaf(v[j][k].w, e, acc[j].w);
-                        }
+                        const int m = min(i0 + j * n_warps, m1 - 1);
+                        ml[j][k] = __ldcg(reinterpret_cast<const float2 *>(rec + 2 * m));
+                        v[j][k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
                     }
                 }
 #pragma unroll
                 for (int j = 0; j < PAIRS; ++j) {
-                    const float Lj = __shfl_sync(0xffffffffu, L, (i + j - i0) & 31);
-                    const int m = m0 + w + (i + j) * n_warps;
-                    const int tok = m / a.part_heads, head = m % a.part_heads;
-                    if (i + j >= mine || head >= hh.count || d0 + lane * 4 >= a.hd) continue;
-                    const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
-                    store_as(a.out, o, a.q_dtype, acc[j].x / Lj);
-                    store_as(a.out, o + 1, a.q_dtype, acc[j].y / Lj);
-                    store_as(a.out, o + 2, a.q_dtype, acc[j].z / Lj);
-                    store_as(a.out, o + 3, a.q_dtype, acc[j].w / Lj);
+                    float top = M[j];
+#pragma unroll
+                    for (int k = 0; k < RECS; ++k) top = fmaxf(top, ml[j][k].x);
+                    // a pair that has met no finite maximum yet has nothing to keep
+                    const float keep = M[j] == top ? 1.0f : exp2f(M[j] - top);
+                    M[j] = top;
+                    L[j] *= keep;
+                    acc[j].x *= keep;
+                    acc[j].y *= keep;
+                    acc[j].z *= keep;
+                    acc[j].w *= keep;
+#pragma unroll
+                    for (int k = 0; k < RECS; ++k) {
+                        if (c0 + k > h.last) continue;
+                        const float e = ml[j][k].x == top ? 1.0f : exp2f(ml[j][k].x - top);
+                        L[j] = fmaf(ml[j][k].y, e, L[j]);
+                        acc[j].x = fmaf(v[j][k].x, e, acc[j].x);
+                        acc[j].y = fmaf(v[j][k].y, e, acc[j].y);
+                        acc[j].z = fmaf(v[j][k].z, e, acc[j].z);
+                        acc[j].w = fmaf(v[j][k].w, e, acc[j].w);
+                    }
                 }
-                __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < PAIRS; ++j) {
+                const int m = i0 + j * n_warps;
+                const int tok = m / a.part_heads, head = m % a.part_heads;
+                if (m >= m1 || head >= hh.count || d0 + lane * 4 >= a.hd) continue;
+                const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
+                const float inv = 1.0f / L[j];
+                store_as(a.out, o, a.q_dtype, acc[j].x * inv);
+                store_as(a.out, o + 1, a.q_dtype, acc[j].y * inv);
+                store_as(a.out, o + 2, a.q_dtype, acc[j].z * inv);
+                store_as(a.out, o + 3, a.q_dtype, acc[j].w * inv);
             }
         }
     }
 }
 
-static __device__ __noinline__ void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h, long long unit,
-                                        int m0, int m1, int w, int n_warps) {
+static __device__ __noinline__ void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
+                                               long long unit, int m0, int m1, int w, int n_warps) {
     const ChunkHeads hh = chunk_heads(a, g.part);
     if (m1 - m0 <= 2 * n_warps)
         chunk_join_pairs<1, 8>(a, g, h, hh, unit, m0, m1, w, n_warps);
     else
-        chunk_join_pairs<4, 2>(a, g, h, hh, unit, m0, m1, w, n_warps);
+        chunk_join_pairs<4, 4>(a, g, h, hh, unit, m0, m1, w, n_warps);
 }
 
 }  // namespace ds

@@ -58,7 +58,7 @@ constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 constexpr int kCtMinCost = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
-constexpr int kCtSmall = 3072;      // barriers, exchange words, notes
+constexpr int kCtSmall = 3072;      // barriers, segments, notes
 constexpr size_t kCtSmemLimit = 227 * 1024;
 constexpr float kCtLog2e = 1.4426950408889634f;
 constexpr float kCtLag = 8.0f;      // log2 of the growth that moves the reference maximum
@@ -67,10 +67,10 @@ template <int HD>
 struct CtCfg {
     static constexpr int kHalves = HD / 64;
     static constexpr int kTileBytes = kHalves * kCtHalf;  // 128 rows of one head
-    static constexpr int kStages = (int)((kCtSmemLimit - kCtSmall - 2 * kTileBytes) / kTileBytes) < kCtMaxStages
-                                       ? (int)((kCtSmemLimit - kCtSmall - 2 * kTileBytes) / kTileBytes)
-                                       : kCtMaxStages;
-    static constexpr size_t kSmem = kCtSmall + (size_t)(2 + kStages) * kTileBytes;
+    static constexpr int kFixed = kCtSmall + 2 * kTileBytes;
+    static constexpr int kFit = (int)((kCtSmemLimit - kFixed) / kTileBytes);
+    static constexpr int kStages = kFit < kCtMaxStages ? kFit : kCtMaxStages;
+    static constexpr size_t kSmem = kFixed + (size_t)kStages * kTileBytes;
 };
 
 struct CtMaps {
@@ -79,13 +79,46 @@ struct CtMaps {
     int box_rows;
 };
 
-// D[tmem] (+)= A[tmem] x B[smem].
-__device__ __forceinline__ void ct_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The MMA warp runs its loop with all its lanes and one of them issues, by a
+// predicate: addresses and descriptors then stay in uniform registers, where
+// the instruction wants them.  (From a branch of one lane each of them has to
+// be moved there first: about 100 cycles an MMA against the 64 it runs.)
+__device__ __forceinline__ uint32_t ct_elect() {
+    uint32_t one;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one;
+}
+// D[tmem] (+)= A[smem] x B[smem], and A[tmem] x B[smem].
+__device__ __forceinline__ void ct_mma_ss(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void ct_mma_ts(uint32_t one, uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void ct_commit(uint32_t one, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(one)
         : "memory");
 }
 // 32 columns of this thread's lane; complete only after ct_wait_ld().
@@ -150,6 +183,9 @@ __device__ __forceinline__ uint32_t ct_pack(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
+__device__ __forceinline__ float2 ct_unpack(uint32_t u) {
+    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ float ct_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
 
 __device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
@@ -177,10 +213,9 @@ __device__ __forceinline__ void ct_wait(uint64_t *bar, uint32_t parity, volatile
     }
 }
 
-// Order of the 2 nb tiles of a segment in the ring, the order the MMA thread
-// needs them in.  Shared steps: K0 V0 K1 V1 ...  Steps taken in turns:
+// Order of the 2 nb tiles of a segment in the ring, the order they are first
+// needed in.  Shared steps: K0 V0 K1 V1 ...  Steps taken in turns:
 // K0 K1 V0 K2 V1 K3 ... V(nb-2) V(nb-1).
-__device__ __forceinline__ int ct_k_place(bool turns, int j) { return !turns ? 2 * j : j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int ct_v_place(bool turns, int j, int nb) {
     return !turns ? 2 * j + 1 : j == nb - 1 ? 2 * nb - 1 : 2 * j + 2;
 }
@@ -199,16 +234,18 @@ struct CtShared {
     CtSeg seg[kCtSegs];
     uint64_t seg_full[kCtSegs], seg_empty[kCtSegs];
     uint64_t full[kCtMaxStages], empty[kCtMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], done;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clean[2], done;
     uint32_t tmem;
     int dead;
-    int noted[2];   // a part's notes hold something
     int last[2];
     union {
-        long long red[34];   // ChunkWalk::init
-        float2 ml[128];      // part 1's (max, sum) per row, for part 0 to join
+        long long red[34];  // ChunkWalk::init
+        float2 ml[128];     // turns: a row's (max, sum) of part 1, for part 0
     };
-    unsigned note[2][128];  // non-finite V per dim: 10-bit first positions of NaN, +inf, -inf behind the tile's pos0
+    // non-finite V per dim, by the segment's parity: 10-bit first positions of
+    // NaN, +inf, -inf behind the tile's pos0; noted: there are some
+    int noted[2];
+    unsigned note[2][128];
 };
 static_assert(sizeof(CtShared) <= kCtSmall, "shared words");
 
@@ -262,6 +299,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     using Cfg = CtCfg<HD>;
     constexpr int ST = Cfg::kStages;
     constexpr int RPW = PARTS == 1 ? 32 : 10;  // rows a warp
+    constexpr int SUB = 4 * RPW;               // rows of a part
     extern __shared__ __align__(1024) unsigned char ct_smem[];
     CtShared &sh = *reinterpret_cast<CtShared *>(ct_smem);
     unsigned char *s_q = ct_smem + kCtSmall, *s_ring = s_q + 2 * Cfg::kTileBytes;
@@ -277,7 +315,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_init(&sh.empty[i], 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(&sh.q_full[w], 1);
+            mbar_init(&sh.q_full[w], PARTS == 1 ? 1 : 4);
             mbar_init(&sh.q_empty[w], 1);
             mbar_init(&sh.s_full[w], 1);
             mbar_init(&sh.p_full[w], 4);
@@ -286,8 +324,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
         for (int i = 0; i < kCtSegs; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], 11);  // producers, MMA, eight softmax warps
+            mbar_init(&sh.seg_empty[i], PARTS == 1 ? 11 : 10);  // producers, MMA, eight softmax warps
         }
+        mbar_init(&sh.v_clean[0], 4);
+        mbar_init(&sh.v_clean[1], 4);
         mbar_init(&sh.done, 1);
         sh.dead = 0;
         fence_mbarrier_init();
@@ -336,7 +376,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
         }
         __syncwarp();
-    } else if (warp == 11) {
+    } else if (warp == 11 && PARTS == 1) {
         // ------------------------------------------------ q of both parts
         // A part's q is free once the tensor core is through with its last QK.
         // MMA rows without a (row, head) pair hold anything: no row reaches
@@ -345,61 +385,25 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         for (uint32_t seg = 0;; ++seg) {
             const CtSeg &c = seg_get(seg);
             if (c.nb == 0) break;
-            const bool turns = c.turns;
-            const int r0 = c.g.r0, tokens = c.g.tokens, first = c.heads.first, heads = c.heads.count;
+            const int r0 = c.g.r0, first = c.heads.first, r1 = c.turns ? r0 : r0 + half_tokens;
             __syncwarp();
             if (lane == 0) seg_done(seg);
-            if (PARTS == 1) {
-                for (int w = 0; w < 2; ++w)
-                    if (seg) ct_wait(&sh.q_empty[w], (seg - 1) & 1, dead, a.err);
-                if (__any_sync(0xffffffffu, *dead)) continue;
-                ++issued;
+            for (int w = 0; w < 2; ++w)
+                if (seg) ct_wait(&sh.q_empty[w], (seg - 1) & 1, dead, a.err);
+            if (__any_sync(0xffffffffu, *dead)) continue;
+            ++issued;
+            if (lane == 0) {
                 for (int w = 0; w < 2; ++w) {
-                    if (lane == 0) {
-                        mbar_arrive_expect_tx(&sh.q_full[w], (uint32_t)(Cfg::kHalves * 128 * a.part_heads * half_tokens));
-                        for (int h = 0; h < Cfg::kHalves; ++h)
-                            ct_box(smem_u32(s_q) + w * Cfg::kTileBytes + h * kCtHalf, &maps.q, h * 64, first,
-                                   r0 + (turns ? 0 : w * half_tokens), &sh.q_full[w]);
-                    }
-                    __syncwarp();
-                }
-            } else {
-                // eight values of a pair an item; pair p is row 32 (p / 10) + p % 10
-                // of its part, the mid and lo parts 10 and 20 rows further
-                for (int w = 0; w < (turns ? 1 : 2); ++w) {
-                    const int n_pairs = min(half_tokens, tokens - w * half_tokens) * a.part_heads;
-                    for (int u = w; u < (turns ? 2 : w + 1); ++u)
-                        if (seg) ct_wait(&sh.q_empty[u], (seg - 1) & 1, dead, a.err);
-                    for (int i = lane; i < n_pairs * (HD / 8); i += 32) {
-                        const int p = i / (HD / 8), ch = i % (HD / 8);
-                        const int tk = p / a.part_heads, h = p % a.part_heads;
-                        if (h >= heads) continue;
-                        const float4 *src = reinterpret_cast<const float4 *>(
-                            static_cast<const float *>(a.q) +
-                            ((long long)(r0 + w * half_tokens + tk) * a.n_qh + first + h) * HD + ch * 8);
-                        const float4 x0 = __ldg(src), x1 = __ldg(src + 1);
-                        float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
-#pragma unroll
-                        for (int z = 0; z < PARTS; ++z) {
-                            const uint4 v = make_uint4(ct_pack(x[0], x[1]), ct_pack(x[2], x[3]), ct_pack(x[4], x[5]),
-                                                       ct_pack(x[6], x[7]));
-                            const int m = (p / RPW) * 32 + p % RPW + z * RPW;
-                            unsigned char *dst = s_q + (ch >> 3) * kCtHalf + m * 128 + (((ch & 7) ^ (m & 7)) << 4);
-                            for (int u = w; u < (turns ? 2 : w + 1); ++u)
-                                *reinterpret_cast<uint4 *>(dst + u * Cfg::kTileBytes) = v;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) x[k] -= ct_bf16(x[k]);
-                        }
-                    }
-                    ct_fence_async();
-                    __syncwarp();
-                    if (lane == 0)
-                        for (int u = w; u < (turns ? 2 : w + 1); ++u) mbar_arrive(&sh.q_full[u]);
+                    mbar_arrive_expect_tx(&sh.q_full[w], (uint32_t)(Cfg::kHalves * 128 * a.part_heads * half_tokens));
+                    for (int h = 0; h < Cfg::kHalves; ++h)
+                        ct_box(smem_u32(s_q) + w * Cfg::kTileBytes + h * kCtHalf, &maps.q, h * 64, first, w ? r1 : r0,
+                               &sh.q_full[w]);
                 }
             }
+            __syncwarp();
         }
         // every copy issued has landed before the block may end
-        if (PARTS == 1 && lane == 0)
+        if (lane == 0)
             for (int w = 0; w < 2; ++w)
                 if (issued) mbar_wait(&sh.q_full[w], (issued - 1) & 1, *dead ? nullptr : a.err);
         __syncwarp();
@@ -415,33 +419,39 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             const int kv = c.heads.kv, b0 = c.g.b0, len = c.g.len, seq = c.g.seq;
             __syncwarp();
             if (lane == 0) seg_done(seg);
-            for (int i = 0; i < 2 * nb; ++i, ++n) {
-                int j;
-                bool is_v;
+            // lane l: box l / halves, half l % halves of a tile (32 at most).
+            // The block number of the next tile's box is fetched before the stage
+            // of this one is awaited: the table is a trip to L2 away.
+            const int bx = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
+            auto tile_of = [&](int i, int &j, bool &is_v) {
                 if (!turns) {
                     is_v = i & 1;
                     j = i >> 1;
-                } else if (i < 2 && nb > 1) {
-                    is_v = false;
-                    j = i;
-                } else if (nb == 1) {
-                    is_v = i == 1;
-                    j = 0;
+                } else if (i < 2) {
+                    is_v = i == nb;  // one step: K0 V0
+                    j = is_v ? 0 : i;
                 } else {
                     const int m = i - 2;
                     is_v = !(m & 1) || m / 2 + 2 >= nb;
                     j = !is_v ? m / 2 + 2 : (m + 1) / 2;
                 }
-                const int t0 = (b0 + j) * kCtStep;
-                const int boxes = (min(kCtStep, len - t0) + R - 1) / R;
-                // lane l: box l / halves, half l % halves (32 boxes at most); its
-                // block number is fetched before the stage is awaited
-                const int bx = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
-                int row = 0;
-                if (bx < boxes) {
-                    const int pos = t0 + bx * R;
-                    row = (int)(chunk_block_row(a, seq, pos / a.bt, flags) + pos % a.bt);
-                }
+            };
+            auto id_of = [&](int i) {
+                int j;
+                bool is_v;
+                tile_of(i, j, is_v);
+                const int pos = (b0 + j) * kCtStep + bx * R;
+                return pos < len && bx * R < kCtStep ? chunk_block_id(a, seq, pos / a.bt) : 0;
+            };
+            int id = id_of(0);
+            for (int i = 0; i < 2 * nb; ++i, ++n) {
+                int j;
+                bool is_v;
+                tile_of(i, j, is_v);
+                const int boxes = (min(kCtStep, len - (b0 + j) * kCtStep) + R - 1) / R;
+                const int id_next = i + 1 < 2 * nb ? id_of(i + 1) : 0;
+                const int row = (int)chunk_id_row(a, id, flags) + ((b0 + j) * kCtStep + bx * R) % a.bt;
+                id = id_next;
                 const int s = n % ST;
                 if (n >= ST) ct_wait(&sh.empty[s], ((n / ST) - 1) & 1, dead, a.err);
                 // one decision for the warp; a block that has given up fetches no more
@@ -461,82 +471,118 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         __syncwarp();
     } else if (warp == 8) {
         // ------------------------------------------------ MMA issue
-        if (lane == 0) {
+        {
             constexpr uint32_t kIdQk = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdPv =
                 (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((128u >> 4) << 24);
-            uint32_t n0 = 0, pc0 = 0, pc1 = 0;
+            const uint32_t one = ct_elect();
+            const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);  // the same in all lanes, for the compiler too
+            // Everything the next MMA needs is at hand before its wait is over:
+            // this warp's own instructions are on the critical path.
             const uint64_t q0 = smem_desc(smem_u32(s_q), 16, 1024);
-            const uint32_t ring = smem_u32(s_ring);
-            auto wait_tile = [&](uint32_t n) { ct_wait(&sh.full[n % ST], (n / ST) & 1, dead, a.err); };
-            auto qk = [&](int w, uint32_t n) {
+            const uint64_t k0 = smem_desc(smem_u32(s_ring), 16, 1024), v0 = smem_desc(smem_u32(s_ring), kCtHalf, 1024);
+            uint32_t at = 0, at_par = 0, p_par = 0;
+            auto take = [&]() {  // the next tile of the ring is there
+                ct_wait(&sh.full[at], at_par, dead, a.err);
+                const uint32_t s = at;
+                if (++at == ST) {
+                    at = 0;
+                    at_par ^= 1;
+                }
+                return s;
+            };
+            auto wait_p = [&](uint32_t w) {
+                ct_wait(&sh.p_full[w], (p_par >> w) & 1, dead, a.err);
+                p_par ^= 1u << w;
+                tc_fence_after();
+            };
+            auto qk = [&](uint32_t w, uint32_t s) {
                 const uint64_t ad = q0 + (uint64_t)(w * (Cfg::kTileBytes >> 4));
-                const uint64_t bd = smem_desc(ring + (n % ST) * Cfg::kTileBytes, 16, 1024);
-                const uint32_t d = tmem + w * 128;
+                const uint64_t bd = k0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
+                const uint32_t d = tm + w * 128;
 #pragma unroll
                 for (int k = 0; k < HD / 16; ++k) {
                     const uint64_t o = (uint64_t)((k / 4) * (kCtHalf >> 4) + (k % 4) * 2);
-                    tc_mma(d, ad + o, bd + o, kIdQk, k ? 1u : 0u);
+                    ct_mma_ss(one, d, ad + o, bd + o, kIdQk, k ? 1u : 0u);
                 }
             };
-            auto pv = [&](int w, uint32_t n, bool first) {
-                const uint64_t bd = smem_desc(ring + (n % ST) * Cfg::kTileBytes, kCtHalf, 1024);
-                const uint32_t d = tmem + 256 + w * HD, p = tmem + w * 128;
+            auto pv = [&](uint32_t w, uint32_t s, bool first) {
+                const uint64_t bd = v0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
+                const uint32_t d = tm + 256 + w * HD, p = tm + w * 128;
 #pragma unroll
                 for (int k = 0; k < kCtStep / 16; ++k)
-                    ct_mma_ts(d, p + k * 8, bd + (uint64_t)(k * 128), kIdPv, (k || !first) ? 1u : 0u);
+                    ct_mma_ts(one, d, p + k * 8, bd + (uint64_t)(k * 128), kIdPv, (k || !first) ? 1u : 0u);
             };
             for (uint32_t seg = 0;; ++seg) {
                 const CtSeg &c = seg_get(seg);
-                const int nb = c.nb;
+                const int nb = __shfl_sync(0xffffffffu, c.nb, 0);
                 if (nb == 0) break;
-                const bool turns = c.turns;
-                seg_done(seg);
-                const int steps = turns ? (nb + 1) >> 1 : nb;
-                auto kn = [&](int j) { return n0 + (uint32_t)ct_k_place(turns, j); };
-                auto vn = [&](int j) { return n0 + (uint32_t)ct_v_place(turns, j, nb); };
-                for (int w = 0; w < 2; ++w) ct_wait(&sh.q_full[w], seg & 1, dead, a.err);
+                const int turns = __shfl_sync(0xffffffffu, c.turns, 0);
+                if (one) seg_done(seg);
+                uint32_t ks = take(), vs;
+                ct_wait(&sh.q_full[0], seg & 1, dead, a.err);
+                ct_wait(&sh.q_full[1], seg & 1, dead, a.err);
                 tc_fence_after();
-#pragma unroll 1
-                for (int w = 0; w < 2; ++w) {
-                    const int j = turns ? w : 0;
-                    if (j < nb) {
-                        wait_tile(kn(j));
-                        tc_fence_after();
-                        qk(w, kn(j));
-                        if (turns || w == 1) tc_commit(&sh.empty[kn(j) % ST]);
-                        tc_commit(&sh.s_full[w]);
-                    }
-                    if (j + (turns ? 2 : 1) >= nb) tc_commit(&sh.q_empty[w]);  // no further use of this tile's q
-                }
-                for (int i = 0; i < steps; ++i) {
-#pragma unroll 1
-                    for (int w = 0; w < 2; ++w) {
-                        const int j = turns ? 2 * i + w : i;
-                        if (j >= nb) continue;
-                        const int jn = turns ? j + 2 : j + 1;
-                        wait_tile(vn(j));
-                        ct_wait(&sh.p_full[w], (w ? pc1 : pc0) & 1, dead, a.err);
-                        w ? ++pc1 : ++pc0;
-                        tc_fence_after();
-                        pv(w, vn(j), i == 0);
-                        if (turns || w == 1) tc_commit(&sh.empty[vn(j) % ST]);
-                        if (jn < nb) {
-                            wait_tile(kn(jn));
-                            tc_fence_after();
-                            qk(w, kn(jn));
-                            if (turns || w == 1) tc_commit(&sh.empty[kn(jn) % ST]);
-                            tc_commit(&sh.s_full[w]);
-                            if (jn + (turns ? 2 : 1) >= nb) tc_commit(&sh.q_empty[w]);
-                        } else {
-                            tc_commit(&sh.o_full[w]);
+                qk(0, ks);
+                if (!turns) {
+                    ct_commit(one, &sh.s_full[0]);
+                    if (nb == 1) ct_commit(one, &sh.q_empty[0]);
+                    qk(1, ks);
+                    ct_commit(one, &sh.s_full[1]);
+                    ct_commit(one, &sh.empty[ks]);
+                    if (nb == 1) ct_commit(one, &sh.q_empty[1]);
+                    for (int i = 0; i < nb; ++i) {
+                        const bool more = i + 1 < nb, last_qk = i + 2 >= nb;
+                        vs = take();
+                        if (more) ks = take();
+#pragma unroll
+                        for (uint32_t w = 0; w < 2; ++w) {
+                            wait_p(w);
+                            pv(w, vs, i == 0);
+                            if (more) {
+                                qk(w, ks);
+                                ct_commit(one, &sh.s_full[w]);
+                                if (last_qk) ct_commit(one, &sh.q_empty[w]);
+                            } else {
+                                ct_commit(one, &sh.o_full[w]);
+                            }
                         }
+                        ct_commit(one, &sh.empty[vs]);
+                        if (more) ct_commit(one, &sh.empty[ks]);
+                    }
+                } else {
+                    ct_commit(one, &sh.s_full[0]);
+                    ct_commit(one, &sh.empty[ks]);
+                    if (nb <= 2) ct_commit(one, &sh.q_empty[0]);
+                    if (nb > 1) {
+                        ks = take();
+                        tc_fence_after();
+                        qk(1, ks);
+                        ct_commit(one, &sh.s_full[1]);
+                        ct_commit(one, &sh.empty[ks]);
+                    }
+                    if (nb <= 3) ct_commit(one, &sh.q_empty[1]);
+                    for (int j = 0; j < nb; ++j) {
+                        const uint32_t w = j & 1;
+                        const bool more = j + 2 < nb;
+                        vs = take();
+                        if (more) ks = take();
+                        wait_p(w);
+                        pv(w, vs, j < 2);
+                        if (more) {
+                            qk(w, ks);
+                            ct_commit(one, &sh.s_full[w]);
+                            if (j + 4 >= nb) ct_commit(one, &sh.q_empty[w]);
+                            ct_commit(one, &sh.empty[ks]);
+                        } else {
+                            ct_commit(one, &sh.o_full[w]);
+                        }
+                        ct_commit(one, &sh.empty[vs]);
                     }
                 }
-                n0 += 2 * nb;
             }
             // nothing of ours runs on the tensor cores when the block ends
-            tc_commit(&sh.done);
+            ct_commit(one, &sh.done);
             mbar_wait(&sh.done, 0, *dead ? nullptr : a.err);
         }
         __syncwarp();
@@ -551,9 +597,51 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         const uint32_t ts = tmem + lane_base + w * 128, to = tmem + lane_base + 256 + w * HD;
         const float c = a.scale * kCtLog2e;
         const int tok_r = r / a.part_heads, head_r = r % a.part_heads;
-        auto token_of = [&](const CtSeg &s) { return (s.turns ? 0 : w * half_tokens) + tok_r; };
-        uint32_t n0 = 0, sc = 0, oc0 = 0, oc1 = 0;
-        bool turns_before = true;
+        uint32_t n0 = 0, sc = 0, oc0 = 0, oc1 = 0, vc = 0;
+        // fp32 q: the part's pairs, eight values a thread and item, as three
+        // bf16 numbers each; pair p is row 32 (p / 10) + p % 10, the mid and lo
+        // parts 10 and 20 rows further
+        auto load_q = [&](const CtSeg &c) {
+            const int first = c.turns ? 0 : w * half_tokens;
+            const int n_items = min(half_tokens, c.g.tokens - first) * a.part_heads * (HD / 8);
+            constexpr int kItems = (SUB * (HD / 8) + 127) / 128;
+            float4 x[kItems][2];
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int it = t + 128 * i, p = it / (HD / 8), ch = it % (HD / 8);
+                const int tk = p / a.part_heads, h = p - tk * a.part_heads;
+                x[i][0] = x[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (it < n_items && h < c.heads.count) {
+                    const float4 *src = reinterpret_cast<const float4 *>(
+                        static_cast<const float *>(a.q) +
+                        ((long long)(c.g.r0 + first + tk) * a.n_qh + c.heads.first + h) * HD + ch * 8);
+                    x[i][0] = __ldg(src);
+                    x[i][1] = __ldg(src + 1);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kItems; ++i) {
+                const int it = t + 128 * i, p = it / (HD / 8), ch = it % (HD / 8);
+                if (it >= n_items) break;
+                float y[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+#pragma unroll
+                for (int z = 0; z < PARTS; ++z) {
+                    const int m = (p / RPW) * 32 + p % RPW + z * RPW;
+                    *reinterpret_cast<uint4 *>(s_q + w * Cfg::kTileBytes + (ch >> 3) * kCtHalf + m * 128 +
+                                               (((ch & 7) ^ (m & 7)) << 4)) =
+                        make_uint4(ct_pack(y[0], y[1]), ct_pack(y[2], y[3]), ct_pack(y[4], y[5]), ct_pack(y[6], y[7]));
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] -= ct_bf16(y[k]);
+                }
+            }
+            ct_fence_async();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.q_full[w]);
+        };
+        if (PARTS == 3) {
+            const CtSeg &c = seg_get(0);
+            if (c.nb) load_q(c);
+        }
         for (uint32_t seg = 0;; ++seg) {
             const CtSeg *cur = &seg_get(seg);
             if (cur->nb == 0) break;
@@ -561,65 +649,62 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             const bool turns = cur->turns;
             const int nb = cur->nb;
             const int steps = turns ? (nb + 1 - w) >> 1 : nb;
-            const int rel = token_of(*cur);  // this row attends positions up to pos0 + rel
+            const int rel = (turns ? 0 : w * half_tokens) + tok_r;  // this row attends positions up to pos0 + rel
             const bool valid = tok_r < half_tokens && rel < g.tokens && head_r < cur->heads.count &&
                                (PARTS == 1 || piece < PARTS);
             const bool busy = __any_sync(0xffffffffu, valid);
+            const int par = seg & 1;
             float m_ref = -INFINITY, sum = 0.0f;
-            if (turns && !turns_before) named_sync(1, 256);  // the shared notes of the tile before are read
-            turns_before = turns;
             for (int i = 0; i < steps; ++i, ++sc) {
                 const int j = turns ? 2 * i + w : i;
                 const int t0 = (g.b0 + j) * kCtStep;
                 const bool masked = t0 + kCtStep - 1 > g.pos0;
-                if (masked) {
-                    // both parts write and read one set of notes when they share
-                    // the steps: neither begins before the other is done with
-                    // the tile before
-                    if (!turns) named_sync(1, 256);
-                    // this thread: position t0 + t of V; both halves of the dims
-                    // (turns), or the part's half of them
-                    const uint32_t n = n0 + (uint32_t)ct_v_place(turns, j, nb);
-                    ct_wait(&sh.full[n % ST], (n / ST) & 1, dead, a.err);
-                    unsigned char *row = s_ring + (size_t)(n % ST) * Cfg::kTileBytes + t * 128;
-                    const int c0 = turns ? 0 : w * (HD / 16), c1 = turns ? HD / 8 : c0 + HD / 16;
+                ct_wait(&sh.s_full[w], sc & 1, dead, a.err);
+                __syncwarp();  // tensor memory is read by whole warps
+                tc_fence_after();
+                if (masked && (turns || w == 0)) {
+                    // Check the step's V: this thread position t0 + t.  Part 0
+                    // does it for both where they share the step.  (Its S is
+                    // there, so part 1 has given up its last P of the segment
+                    // before, and is done with the one before that, which had
+                    // these notes.)
+                    const uint32_t place = n0 + (uint32_t)ct_v_place(turns, j, nb);
+                    ct_wait(&sh.full[place % ST], (place / ST) & 1, dead, a.err);
+                    unsigned char *row = s_ring + (size_t)(place % ST) * Cfg::kTileBytes + t * 128;
                     const int behind = t0 + t - g.pos0;
                     if (t0 + t >= g.len) {
-                        for (int ch = c0; ch < c1; ++ch)
-                            *reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + (((ch & 7) ^ (t & 7)) << 4)) =
-                                make_uint4(0, 0, 0, 0);
+#pragma unroll
+                        for (int ch = 0; ch < HD / 8; ++ch)
+                            *reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
                     } else if (behind > 0) {
-                        for (int ch = c0; ch < c1; ++ch) {
-                            uint4 *p = reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + (((ch & 7) ^ (t & 7)) << 4));
-                            const uint4 x = *p;
-                            uint32_t u[4] = {x.x, x.y, x.z, x.w};
-                            bool bad = false;
+                        // an exponent of all ones carries into the sign's place
+                        uint32_t bad = 0;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                bad |= (u[e] & 0x7f80u) == 0x7f80u || (u[e] & 0x7f800000u) == 0x7f800000u;
-                            if (bad) {
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const uint32_t b = (u[e >> 1] >> (16 * (e & 1))) & 0xffffu;
-                                    if ((b & 0x7f80u) != 0x7f80u) continue;
-                                    ct_note(&sh.note[turns ? w : 0][ch * 8 + e], behind, __uint_as_float(b << 16));
-                                    u[e >> 1] &= ~(0xffffu << (16 * (e & 1)));
-                                }
-                                *p = make_uint4(u[0], u[1], u[2], u[3]);
-                                sh.noted[turns ? w : 0] = 1;
+                        for (int ch = 0; ch < HD / 8; ++ch) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(row + (ch >> 3) * kCtHalf +
+                                                                             (((ch & 7) ^ (t & 7)) << 4));
+                            bad |= ((x.x & 0x7f807f80u) + 0x00800080u) | ((x.y & 0x7f807f80u) + 0x00800080u) |
+                                   ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
+                        }
+                        if (bad & 0x80008000u) {
+                            for (int d = 0; d < HD; ++d) {
+                                __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(
+                                    row + (d >> 6) * kCtHalf + ((((d >> 3) & 7) ^ (t & 7)) << 4) + (d & 7) * 2);
+                                const float x = __bfloat162float(*p);
+                                if (fabsf(x) < INFINITY) continue;
+                                ct_note(&sh.note[par][d], behind, x);
+                                *p = __float2bfloat16_rn(0.0f);
                             }
+                            sh.noted[par] = 1;
                         }
                     }
                     ct_fence_async();
                     __syncwarp();
                     if (turns)
                         named_sync(2 + w, 128);
-                    else
-                        named_sync(1, 256);
+                    else if (lane == 0)
+                        mbar_arrive(&sh.v_clean[vc & 1]);
                 }
-                ct_wait(&sh.s_full[w], sc & 1, dead, a.err);
-                __syncwarp();  // tensor memory is read by whole warps
-                tc_fence_after();
                 if (busy) {
                     float s[kCtStep];
 #pragma unroll
@@ -666,6 +751,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     const float mc = m_ref == -INFINITY ? 0.0f : m_ref * c;
                     // two scores an instruction where the machine has the pair form
                     const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
+                    const float k1 = piece > 0 ? -1.0f : 0.0f, k2 = piece > 1 ? -1.0f : 0.0f;
+                    const float2 minus1 = make_float2(k1, k1), minus2 = make_float2(k2, k2);
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                     for (int k0 = 0; k0 < kCtStep; k0 += 32) {
@@ -676,17 +763,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                             x.x = ct_exp2(x.x);
                             x.y = ct_exp2(x.y);
                             add[k & 1] = ct_add2(add[k & 1], x);
-                            if (PARTS == 3) {
-                                if (piece > 0) {
-                                    x.x -= ct_bf16(x.x);
-                                    x.y -= ct_bf16(x.y);
-                                }
-                                if (piece > 1) {
-                                    x.x -= ct_bf16(x.x);
-                                    x.y -= ct_bf16(x.y);
-                                }
-                            }
                             p[k] = ct_pack(x.x, x.y);
+                            if (PARTS == 3) {  // hi, mid or lo of it: subtract what the pieces before hold
+                                x = ct_fma2(ct_unpack(p[k]), minus1, x);
+                                p[k] = ct_pack(x.x, x.y);
+                                x = ct_fma2(ct_unpack(p[k]), minus2, x);
+                                p[k] = ct_pack(x.x, x.y);
+                            }
                         }
                         ct_st16(ts + k0 / 2, p);
                     }
@@ -694,22 +777,33 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     ct_wait_st();
                     tc_fence_before();
                 }
+                if (masked && !turns) {
+                    // part 0 has checked this V; it may be a step ahead, so the
+                    // checked steps alternate between two barriers
+                    if (w == 1) ct_wait(&sh.v_clean[vc & 1], (vc >> 1) & 1, dead, a.err);
+                    ++vc;
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.p_full[w]);
             }
             n0 += 2 * nb;
 
             if (turns) {
-                if (w == 1 && t < 128) sh.ml[t] = make_float2(m_ref, sum);
+                if (w == 1) sh.ml[t] = make_float2(m_ref, sum);
                 named_sync(1, 256);  // part 1's maxima and notes are written
             }
+            if (PARTS == 3) {  // this tile's S are all there: its q is free
+                const CtSeg &next = seg_get(seg + 1);
+                if (next.nb) load_q(next);
+            }
+
             const int steps0 = turns ? (nb + 1) >> 1 : nb, steps1 = turns ? nb >> 1 : nb;
             if (w == 0 || !turns) {
                 ct_wait(&sh.o_full[w], (w ? oc1 : oc0) & 1, dead, a.err);
                 if (turns && steps1) ct_wait(&sh.o_full[1], oc1 & 1, dead, a.err);
                 __syncwarp();
                 tc_fence_after();
-                const bool notes = sh.noted[0] || (turns && sh.noted[1]);
+                const bool notes = sh.noted[par];
                 const bool split = cur->split;
                 float f0 = 1.0f, f1 = 0.0f;
                 if (turns && steps1) {  // join the two parts' turns
@@ -723,20 +817,25 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (busy) {
                     const int m = (turns ? 0 : w * half_tokens * a.part_heads) + r;  // pair in the tile's record
                     float *rec = split ? chunk_record(a, blockIdx.x, g.slot) : nullptr;
-                    const long long o = ((long long)(g.r0 + rel) * a.n_qh + cur->heads.first + head_r) * HD;
+                    // where the row goes, in elements; -1: nowhere
+                    const long long row_at =
+                        !valid || piece != 0 ? -1
+                        : split ? 2 * a.rec_rows + (long long)m * HD
+                                : ((long long)(g.r0 + rel) * a.n_qh + cur->heads.first + head_r) * HD;
                     const float inv = split ? 1.0f : 1.0f / sum;
-                    const bool writes = valid && piece == 0;
-                    if (split && writes) {
+                    if (split && row_at >= 0) {
                         rec[2 * m] = m_ref * c;
                         rec[2 * m + 1] = sum;
                     }
 #pragma unroll 1
                     for (int k = 0; k < HD; k += 32) {
-                        float v[32], v1[32];
+                        float v[32];
                         ct_ld32(to + k, v);
-                        if (turns && steps1) ct_ld32(to + HD + k, v1);
                         ct_wait_ld();
                         if (turns && steps1) {
+                            float v1[32];
+                            ct_ld32(to + HD + k, v1);
+                            ct_wait_ld();
 #pragma unroll
                             for (int e = 0; e < 32; ++e) v[e] = v[e] * f0 + v1[e] * f1;
                         }
@@ -748,49 +847,47 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                                 v[e] = (lo + mid) + v[e];
                             }
                         }
-                        unsigned nans = 0;
+                        float any = 0.0f;  // NaN if one of them is NaN or infinite
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) nans |= (v[e] != v[e] ? 1u : 0u) << e;
-                        if (writes && sum == sum) {
-                            while (nans) {
-                                const int d = __ffs(nans) - 1;
-                                nans &= nans - 1;
-                                const float x = ct_infinite(a, g.seq, cur->heads.kv, k + d, g.b0 * kCtStep,
-                                                            min(g.b1 * kCtStep, g.pos0 + rel + 1));
+                        for (int e = 0; e < 32; ++e) any = fmaf(v[e], 0.0f, any);
+                        if (any != any && row_at >= 0 && sum == sum) {
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) v[e] = e == d ? x : v[e];
-                            }
+                            for (int e = 0; e < 32; ++e)
+                                if (v[e] != v[e])
+                                    v[e] = ct_infinite(a, g.seq, cur->heads.kv, k + e, g.b0 * kCtStep,
+                                                       min(g.b1 * kCtStep, g.pos0 + rel + 1));
                         }
-                        __syncwarp();
                         if (notes) {
-                            for (int e = 0; e < 32; ++e) {
-                                v[e] += ct_noted(sh.note[0][k + e], rel);
-                                if (turns) v[e] += ct_noted(sh.note[1][k + e], rel);
-                            }
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) v[e] += ct_noted(sh.note[par][k + e], rel);
                         }
-                        if (!writes) {
-                        } else if (split) {
-                            float4 *d = reinterpret_cast<float4 *>(rec + 2 * a.rec_rows + (size_t)m * HD + k);
+                        if (row_at >= 0) {
+                            if (PARTS == 3 || split) {
+                                float4 *d = reinterpret_cast<float4 *>((split ? rec : static_cast<float *>(a.out)) + row_at + k);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                __stcg(d + e, make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]));
-                        } else if (PARTS == 3) {
-                            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(a.out) + o + k);
+                                for (int e = 0; e < 8; ++e)
+                                    d[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
+                                                       v[4 * e + 3] * inv);
+                            } else {
+                                uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + row_at + k);
 #pragma unroll
-                            for (int e = 0; e < 8; ++e)
-                                d[e] = make_float4(v[4 * e] * inv, v[4 * e + 1] * inv, v[4 * e + 2] * inv,
-                                                   v[4 * e + 3] * inv);
-                        } else {
-                            uint4 *d = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) + o + k);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                d[e] = make_uint4(ct_pack(v[8 * e] * inv, v[8 * e + 1] * inv),
-                                                  ct_pack(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
-                                                  ct_pack(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
-                                                  ct_pack(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                                for (int e = 0; e < 4; ++e)
+                                    d[e] = make_uint4(ct_pack(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                      ct_pack(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                      ct_pack(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                      ct_pack(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                            }
                         }
                         __syncwarp();
                     }
+                }
+                if (notes) {  // read: clear them for the segment after the next
+                    turns ? named_sync(2 + w, 128) : named_sync(1, 256);
+                    if (w == 0) {
+                        for (int d = t; d < HD; d += 128) sh.note[par][d] = kCtNoNote;
+                        if (t == 0) sh.noted[par] = 0;
+                    }
+                    turns ? named_sync(2 + w, 128) : named_sync(1, 256);
                 }
                 if (split) {
                     __threadfence();
@@ -810,19 +907,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     }
                     named_sync(2 + w, 128);  // sh.last is read
                 }
-                if (notes && !turns) {  // both parts have read the notes: each clears what it wrote
-                    named_sync(1, 256);
-                    for (int d = t; d < HD / 2; d += 128) sh.note[0][w * (HD / 2) + d] = kCtNoNote;
-                    if (t == 0) sh.noted[0] = 0;
-                    named_sync(1, 256);
-                }
-                if (notes && turns) {
-                    named_sync(2, 128);
-                    for (int d = t; d < HD; d += 128) sh.note[0][d] = sh.note[1][d] = kCtNoNote;
-                    if (t < 2) sh.noted[t] = 0;
-                }
             }
-            if (turns) named_sync(1, 256);  // part 0 has read part 1's accumulator and notes
+            if (turns) named_sync(1, 256);  // part 0 has read part 1's accumulator, maxima and notes
             if (steps0) ++oc0;
             if (steps1) ++oc1;
             __syncwarp();
