@@ -196,6 +196,17 @@ __device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int
         : "memory");
 }
 
+// The same from the one lane of the warp that `one` marks.
+__device__ __forceinline__ void ct_box_one(uint32_t one, uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(y), "r"(z), "r"(bar), "r"(one)
+        : "memory");
+}
+
 // Wait for a phase; once any wait of the block has given up, at once.
 __device__ __forceinline__ void ct_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
     if (mbar_try_wait(bar, parity)) return;
@@ -411,18 +422,19 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         // ------------------------------------------------ K/V producer
         uint32_t n = 0;
         const int R = maps.box_rows;
+        const uint32_t one = ct_elect(), ring = smem_u32(s_ring);
         for (uint32_t seg = 0;; ++seg) {
             const CtSeg &c = seg_get(seg);
-            const int nb = c.nb;
+            const int nb = __shfl_sync(0xffffffffu, c.nb, 0);
             if (nb == 0) break;
-            const bool turns = c.turns;
-            const int kv = c.heads.kv, b0 = c.g.b0, len = c.g.len, seq = c.g.seq;
+            const bool turns = __shfl_sync(0xffffffffu, c.turns, 0);
+            const int kv = __shfl_sync(0xffffffffu, c.heads.kv, 0), b0 = __shfl_sync(0xffffffffu, c.g.b0, 0);
+            const int len = __shfl_sync(0xffffffffu, c.g.len, 0), seq = c.g.seq;
             __syncwarp();
-            if (lane == 0) seg_done(seg);
-            // lane l: box l / halves, half l % halves of a tile (32 at most).
-            // The block number of the next tile's box is fetched before the stage
-            // of this one is awaited: the table is a trip to L2 away.
-            const int bx = lane / Cfg::kHalves, hf = lane % Cfg::kHalves;
+            if (one) seg_done(seg);
+            // Lane l holds box l's block number (16 boxes at most); the next
+            // tile's is fetched before the stage of this one is awaited: the
+            // table is a trip to L2 away.
             auto tile_of = [&](int i, int &j, bool &is_v) {
                 if (!turns) {
                     is_v = i & 1;
@@ -440,8 +452,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 int j;
                 bool is_v;
                 tile_of(i, j, is_v);
-                const int pos = (b0 + j) * kCtStep + bx * R;
-                return pos < len && bx * R < kCtStep ? chunk_block_id(a, seq, pos / a.bt) : 0;
+                const int pos = (b0 + j) * kCtStep + lane * R;
+                return pos < len && lane * R < kCtStep ? chunk_block_id(a, seq, pos / a.bt) : 0;
             };
             int id = id_of(0);
             for (int i = 0; i < 2 * nb; ++i, ++n) {
@@ -450,17 +462,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 tile_of(i, j, is_v);
                 const int boxes = (min(kCtStep, len - (b0 + j) * kCtStep) + R - 1) / R;
                 const int id_next = i + 1 < 2 * nb ? id_of(i + 1) : 0;
-                const int row = (int)chunk_id_row(a, id, flags) + ((b0 + j) * kCtStep + bx * R) % a.bt;
+                const int row = (int)chunk_id_row(a, id, flags) + ((b0 + j) * kCtStep + lane * R) % a.bt;
                 id = id_next;
                 const int s = n % ST;
                 if (n >= ST) ct_wait(&sh.empty[s], ((n / ST) - 1) & 1, dead, a.err);
                 // one decision for the warp; a block that has given up fetches no more
                 if (__any_sync(0xffffffffu, *dead)) continue;
-                if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * R * 128 * Cfg::kHalves));
+                if (one) mbar_arrive_expect_tx(&sh.full[s], (uint32_t)(boxes * R * 128 * Cfg::kHalves));
                 __syncwarp();
-                if (bx < boxes)
-                    ct_box(smem_u32(s_ring + (size_t)s * Cfg::kTileBytes) + hf * kCtHalf + bx * R * 128,
-                           is_v ? &maps.v : &maps.k, 0, row, kv * Cfg::kHalves + hf, &sh.full[s]);
+                const uint32_t dst = ring + (uint32_t)s * Cfg::kTileBytes, bar = smem_u32(&sh.full[s]);
+                const CUtensorMap *map = is_v ? &maps.v : &maps.k;
+                for (int b = 0; b < boxes; ++b) {
+                    const int y = __shfl_sync(0xffffffffu, row, b);
+#pragma unroll
+                    for (int h = 0; h < Cfg::kHalves; ++h)
+                        ct_box_one(one, dst + h * kCtHalf + b * R * 128, map, y, kv * Cfg::kHalves + h, bar);
+                }
             }
         }
         // every copy issued has landed before the block may end
