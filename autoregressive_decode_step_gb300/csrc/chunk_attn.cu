@@ -227,6 +227,7 @@ int chunk_simt_grid() { return 2 * sm_count(); }
 cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream) {
     chunk_tile_shape(a, kCsRows, 1);
     a.step = kCsStep;
+    a.tile_cost = 0;
     a.min_cost = kCsMinCost;
     const int HD = cs_hd(a.hd);
     const size_t smem = cs_smem(HD);

@@ -4,7 +4,8 @@
 // A tile is up to `tile_tokens` consecutive new rows of one sequence times the
 // query heads that share one KV head (a group of more than `sub_heads` heads
 // is cut into equal parts, each with tiles of its own).  Its cost is the
-// number of positions its last row attends.  The costs of all tiles, ordered
+// number of positions its last row attends and a constant for its beginning
+// and end (tile_cost, in positions).  The costs of all tiles, ordered
 // by sequence, head and row, form one line that is cut into equal ranges, one
 // per CTA, so the load is even whatever the mix of chunks and single tokens.
 // A tile that a cut falls into is worked on by several CTAs, the cut rounded
@@ -43,7 +44,8 @@ struct ChunkArgs {
     int part_heads;   // query heads of a part (the last may have fewer)
     int tile_tokens;  // rows of a sequence per tile
     int step;         // positions of one K/V step
-    int min_cost;     // smallest range a CTA is given, at least `step`
+    int tile_cost;    // what beginning and ending a tile costs, in positions
+    int min_cost;     // smallest range a CTA is given, at least tile_cost + step
     int rec_rows;     // rows of a partial record
     int *counters;    // [grid][2], zero between launches
     float *partials;  // [grid][2] records of rec_rows * (hd + 2) floats (max, sum, then the accumulators)
@@ -84,13 +86,13 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int s, int &fl
     q.ctx = L - q.n;
     q.tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens;
     const long long T = q.tiles;
-    q.cost = T ? T * q.ctx + (long long)a.tile_tokens * (T * (T - 1) / 2) + q.n : 0;
+    q.cost = T ? T * (q.ctx + a.tile_cost) + (long long)a.tile_tokens * (T * (T - 1) / 2) + q.n : 0;
     return q;
 }
 
 // Cost of a sequence's tiles before tile t < tiles.
 __device__ __forceinline__ long long chunk_cost_before(const ChunkArgs &a, const ChunkSeq &q, long long t) {
-    return t * q.ctx + (long long)a.tile_tokens * (t * (t + 1) / 2);
+    return t * (q.ctx + a.tile_cost) + (long long)a.tile_tokens * (t * (t + 1) / 2);
 }
 
 // One piece of work: a tile's K/V steps [b0, b1).
@@ -206,11 +208,13 @@ struct ChunkWalk {
             g.len = q.ctx + j0 + g.tokens;
             g.seq = q.s;
             g.part = part;
-            g.cost = g.len;
+            g.cost = g.len + a.tile_cost;
             g.start = seq_start + (long long)part * q.cost + chunk_cost_before(a, q, tile);
             const long long end = min(u1, g.start + g.cost);
-            g.b0 = (int)((u - g.start) / a.step);
-            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : (int)((end - g.start) / a.step);
+            // the constant comes first: a cut inside it is one at position 0
+            const int p0 = max(0, (int)(u - g.start) - a.tile_cost), p1 = max(0, (int)(end - g.start) - a.tile_cost);
+            g.b0 = p0 / a.step;
+            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : p1 / a.step;
             const long long u0 = (long long)blockIdx.x * unit;
             g.slot = g.start < u0 ? 0 : g.start + g.cost > u1 ? 1 : -1;
             ++tile;
@@ -222,7 +226,7 @@ struct ChunkWalk {
 };
 
 // The CTAs that share a split tile, in order.  The first CTA the tile reaches
-// into may have been left less than one step of it, which rounds to nothing.
+// into may have been left less than its first step, which rounds to nothing.
 struct ChunkShare {
     int first, last;  // contributors
     int counter;      // the tile's counter: the CTA its cost starts in
@@ -231,7 +235,7 @@ __device__ __forceinline__ ChunkShare chunk_share(const ChunkArgs &a, const Chun
     ChunkShare h;
     h.counter = (int)(g.start / unit);
     h.last = (int)((g.start + g.cost - 1) / unit);
-    h.first = (h.counter + 1) * unit - g.start < a.step ? h.counter + 1 : h.counter;
+    h.first = (h.counter + 1) * unit - g.start < a.tile_cost + a.step ? h.counter + 1 : h.counter;
     return h;
 }
 // Is the tile's record in CTA c its slot 0 (it began before c's range) or 1?

@@ -21,9 +21,13 @@
 // running maximum and sum each, joined at the end: the same overlap.
 //
 // fp32 q (PARTS 3): q and P each go to the tensor core as three bf16 numbers
-// hi + mid + lo, 24 significant bits.  The three take the place of three rows
-// of the same warp (10 rows a warp instead of 32), so one MMA multiplies all
-// of them; S and O are added up over the three lanes.
+// that add up to them (24 bits cut in three).  The pieces of q are three MMAs
+// into one S.  The pieces of P are rows of one MMA: a part has 40 pairs, each
+// in three rows of a warp with the same S (10 pairs a warp), and row by row
+// the warp writes the high, the middle and the low piece; O is the sum of the
+// three rows.  (q in rows too costs half the MMAs, but S then is a sum over
+// lanes: 384 shuffles a step, which took longer than everything else.)  Both
+// parts work on the one tile, in turns.
 //
 // The running maximum that P is taken relative to is moved (and O rescaled)
 // only when a row's maximum has grown by more than 2^8: P then stays below
@@ -55,7 +59,8 @@ constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, wa
 // warpgroups, whose thread holds a row's 128 scores: 2 x 216 + 72 = 3 x 168.
 constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
-constexpr int kCtMinCost = 256;
+constexpr int kCtMinCost = 512;
+constexpr int kCtTileCost = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
 constexpr int kCtSmall = 3072;      // barriers, segments, notes
@@ -63,11 +68,12 @@ constexpr size_t kCtSmemLimit = 227 * 1024;
 constexpr float kCtLog2e = 1.4426950408889634f;
 constexpr float kCtLag = 8.0f;      // log2 of the growth that moves the reference maximum
 
-template <int HD>
+template <int HD, int PARTS>
 struct CtCfg {
     static constexpr int kHalves = HD / 64;
     static constexpr int kTileBytes = kHalves * kCtHalf;  // 128 rows of one head
-    static constexpr int kFixed = kCtSmall + 2 * kTileBytes;
+    static constexpr int kQTiles = PARTS == 1 ? 2 : 3;    // both parts' q, or the three pieces of one
+    static constexpr int kFixed = kCtSmall + kQTiles * kTileBytes;
     static constexpr int kFit = (int)((kCtSmemLimit - kFixed) / kTileBytes);
     static constexpr int kStages = kFit < kCtMaxStages ? kFit : kCtMaxStages;
     static constexpr size_t kSmem = kFixed + (size_t)kStages * kTileBytes;
@@ -183,10 +189,11 @@ __device__ __forceinline__ uint32_t ct_pack(float a, float b) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
     return r;
 }
-__device__ __forceinline__ float2 ct_unpack(uint32_t u) {
-    return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+// The leading 8 bits of two numbers (cut off, not rounded) as a bf16 pair.
+__device__ __forceinline__ uint32_t ct_top2(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
 }
-__device__ __forceinline__ float ct_bf16(float x) { return __bfloat162float(__float2bfloat16_rn(x)); }
+__device__ __forceinline__ float ct_top(float a, uint32_t mask) { return __uint_as_float(__float_as_uint(a) & mask); }
 
 __device__ __forceinline__ void ct_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar) {
     asm volatile(
@@ -307,13 +314,13 @@ __device__ __forceinline__ void ct_wait_seg(uint64_t *bar, uint32_t parity, int 
 template <int HD, int PARTS>
 __global__ void __launch_bounds__(kCtThreads, 1)
     chunk_tc_kernel(const __grid_constant__ ChunkArgs a, const __grid_constant__ CtMaps maps) {
-    using Cfg = CtCfg<HD>;
+    using Cfg = CtCfg<HD, PARTS>;
     constexpr int ST = Cfg::kStages;
     constexpr int RPW = PARTS == 1 ? 32 : 10;  // rows a warp
     constexpr int SUB = 4 * RPW;               // rows of a part
     extern __shared__ __align__(1024) unsigned char ct_smem[];
     CtShared &sh = *reinterpret_cast<CtShared *>(ct_smem);
-    unsigned char *s_q = ct_smem + kCtSmall, *s_ring = s_q + 2 * Cfg::kTileBytes;
+    unsigned char *s_q = ct_smem + kCtSmall, *s_ring = s_q + Cfg::kQTiles * Cfg::kTileBytes;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     volatile int *dead = &sh.dead;
     if (smem_u32(ct_smem) & 1023u) {  // swizzled tiles start on 1 KB; the same answer in every thread
@@ -326,7 +333,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_init(&sh.empty[i], 1);
         }
         for (int w = 0; w < 2; ++w) {
-            mbar_init(&sh.q_full[w], PARTS == 1 ? 1 : 4);
+            mbar_init(&sh.q_full[w], PARTS == 1 ? 1 : 8);
             mbar_init(&sh.q_empty[w], 1);
             mbar_init(&sh.s_full[w], 1);
             mbar_init(&sh.p_full[w], 4);
@@ -353,7 +360,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     walk.init(a, sh.red);  // synchronises the block
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int half_tokens = a.tile_tokens >> 1;  // rows of the sequence in one part
+    const int half_tokens = PARTS == 1 ? a.tile_tokens >> 1 : a.tile_tokens;  // rows of the sequence in one part
     int flags = walk.flags;
     const long long unit = walk.unit;
     auto seg_get = [&](uint32_t k) -> const CtSeg & {
@@ -514,14 +521,17 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 tc_fence_after();
             };
             auto qk = [&](uint32_t w, uint32_t s) {
-                const uint64_t ad = q0 + (uint64_t)(w * (Cfg::kTileBytes >> 4));
+                const uint64_t ad = q0 + (uint64_t)(PARTS == 1 ? w * (Cfg::kTileBytes >> 4) : 0);
                 const uint64_t bd = k0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
                 const uint32_t d = tm + w * 128;
 #pragma unroll
-                for (int k = 0; k < HD / 16; ++k) {
-                    const uint64_t o = (uint64_t)((k / 4) * (kCtHalf >> 4) + (k % 4) * 2);
-                    ct_mma_ss(one, d, ad + o, bd + o, kIdQk, k ? 1u : 0u);
-                }
+                for (int z = PARTS - 1; z >= 0; --z)  // the smallest piece first
+#pragma unroll
+                    for (int k = 0; k < HD / 16; ++k) {
+                        const uint64_t o = (uint64_t)((k / 4) * (kCtHalf >> 4) + (k % 4) * 2);
+                        ct_mma_ss(one, d, ad + (uint64_t)(z * (Cfg::kTileBytes >> 4)) + o, bd + o, kIdQk,
+                                  k || z < PARTS - 1 ? 1u : 0u);
+                    }
             };
             auto pv = [&](uint32_t w, uint32_t s, bool first) {
                 const uint64_t bd = v0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
@@ -538,7 +548,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (one) seg_done(seg);
                 uint32_t ks = take(), vs;
                 ct_wait(&sh.q_full[0], seg & 1, dead, a.err);
-                ct_wait(&sh.q_full[1], seg & 1, dead, a.err);
+                if (PARTS == 1) ct_wait(&sh.q_full[1], seg & 1, dead, a.err);
                 tc_fence_after();
                 qk(0, ks);
                 if (!turns) {
@@ -615,45 +625,48 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         const float c = a.scale * kCtLog2e;
         const int tok_r = r / a.part_heads, head_r = r % a.part_heads;
         uint32_t n0 = 0, sc = 0, oc0 = 0, oc1 = 0, vc = 0;
-        // fp32 q: the part's pairs, eight values a thread and item, as three
-        // bf16 numbers each; pair p is row 32 (p / 10) + p % 10, the mid and lo
-        // parts 10 and 20 rows further
+        // fp32 q: eight values of a pair an item, as three bf16 numbers each
+        // (cut, not rounded: 8 bits of the 24 a piece), one MMA operand per
+        // piece; pair p is rows 32 (p / 10) + p % 10 and 10 and 20 further of
+        // each.  Both warpgroups load.
         auto load_q = [&](const CtSeg &c) {
-            const int first = c.turns ? 0 : w * half_tokens;
-            const int n_items = min(half_tokens, c.g.tokens - first) * a.part_heads * (HD / 8);
-            constexpr int kItems = (SUB * (HD / 8) + 127) / 128;
+            const int n_items = c.g.tokens * a.part_heads * (HD / 8);
+            constexpr int kItems = (SUB * (HD / 8) + 255) / 256;
             float4 x[kItems][2];
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int it = t + 128 * i, p = it / (HD / 8), ch = it % (HD / 8);
+                const int it = tid + 256 * i, p = it / (HD / 8), ch = it % (HD / 8);
                 const int tk = p / a.part_heads, h = p - tk * a.part_heads;
                 x[i][0] = x[i][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 if (it < n_items && h < c.heads.count) {
                     const float4 *src = reinterpret_cast<const float4 *>(
                         static_cast<const float *>(a.q) +
-                        ((long long)(c.g.r0 + first + tk) * a.n_qh + c.heads.first + h) * HD + ch * 8);
+                        ((long long)(c.g.r0 + tk) * a.n_qh + c.heads.first + h) * HD + ch * 8);
                     x[i][0] = __ldg(src);
                     x[i][1] = __ldg(src + 1);
                 }
             }
 #pragma unroll
             for (int i = 0; i < kItems; ++i) {
-                const int it = t + 128 * i, p = it / (HD / 8), ch = it % (HD / 8);
+                const int it = tid + 256 * i, p = it / (HD / 8), ch = it % (HD / 8);
                 if (it >= n_items) break;
                 float y[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+                const int m0 = (p / RPW) * 32 + p % RPW;
+                unsigned char *dst = s_q + (ch >> 3) * kCtHalf;
 #pragma unroll
-                for (int z = 0; z < PARTS; ++z) {
-                    const int m = (p / RPW) * 32 + p % RPW + z * RPW;
-                    *reinterpret_cast<uint4 *>(s_q + w * Cfg::kTileBytes + (ch >> 3) * kCtHalf + m * 128 +
-                                               (((ch & 7) ^ (m & 7)) << 4)) =
-                        make_uint4(ct_pack(y[0], y[1]), ct_pack(y[2], y[3]), ct_pack(y[4], y[5]), ct_pack(y[6], y[7]));
+                for (int z = 0; z < 3; ++z) {
+                    const uint4 v = make_uint4(ct_top2(y[0], y[1]), ct_top2(y[2], y[3]), ct_top2(y[4], y[5]),
+                                               ct_top2(y[6], y[7]));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] -= ct_bf16(y[k]);
+                    for (int m = m0; m < m0 + 3 * RPW; m += RPW)
+                        *reinterpret_cast<uint4 *>(dst + z * Cfg::kTileBytes + m * 128 + (((ch & 7) ^ (m & 7)) << 4)) = v;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
                 }
             }
             ct_fence_async();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.q_full[w]);
+            if (lane == 0) mbar_arrive(&sh.q_full[0]);
         };
         if (PARTS == 3) {
             const CtSeg &c = seg_get(0);
@@ -727,16 +740,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kCtStep; k += 32) ct_ld32(ts + k, s + k);
                     ct_wait_ld();
-                    if (PARTS == 3) {
-                        const int l0 = lane % RPW;
-#pragma unroll
-                        for (int k = 0; k < kCtStep; ++k) {
-                            const float hi = __shfl_sync(0xffffffffu, s[k], l0);
-                            const float mid = __shfl_sync(0xffffffffu, s[k], l0 + RPW);
-                            const float lo = __shfl_sync(0xffffffffu, s[k], l0 + 2 * RPW);
-                            s[k] = (lo + mid) + hi;
-                        }
-                    }
                     if (masked) {
                         const int lim = g.pos0 + rel - t0;
 #pragma unroll
@@ -768,8 +771,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     const float mc = m_ref == -INFINITY ? 0.0f : m_ref * c;
                     // two scores an instruction where the machine has the pair form
                     const float2 c2 = make_float2(c, c), mc2 = make_float2(-mc, -mc);
-                    const float k1 = piece > 0 ? -1.0f : 0.0f, k2 = piece > 1 ? -1.0f : 0.0f;
-                    const float2 minus1 = make_float2(k1, k1), minus2 = make_float2(k2, k2);
+                    // this lane's piece: what the pieces before it hold is taken off
+                    const uint32_t cut1 = piece > 0 ? 0xffff0000u : 0u, cut2 = piece > 1 ? 0xffff0000u : 0u;
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
                     for (int k0 = 0; k0 < kCtStep; k0 += 32) {
@@ -780,12 +783,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                             x.x = ct_exp2(x.x);
                             x.y = ct_exp2(x.y);
                             add[k & 1] = ct_add2(add[k & 1], x);
-                            p[k] = ct_pack(x.x, x.y);
-                            if (PARTS == 3) {  // hi, mid or lo of it: subtract what the pieces before hold
-                                x = ct_fma2(ct_unpack(p[k]), minus1, x);
+                            if (PARTS == 1) {
                                 p[k] = ct_pack(x.x, x.y);
-                                x = ct_fma2(ct_unpack(p[k]), minus2, x);
-                                p[k] = ct_pack(x.x, x.y);
+                            } else {
+                                x = ct_add2(x, make_float2(-ct_top(x.x, cut1), -ct_top(x.y, cut1)));
+                                x = ct_add2(x, make_float2(-ct_top(x.x, cut2), -ct_top(x.y, cut2)));
+                                p[k] = ct_top2(x.x, x.y);
                             }
                         }
                         ct_st16(ts + k0 / 2, p);
@@ -844,6 +847,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         rec[2 * m] = m_ref * c;
                         rec[2 * m + 1] = sum;
                     }
+                    float any = 0.0f;  // NaN once a value is NaN or infinite
 #pragma unroll 1
                     for (int k = 0; k < HD; k += 32) {
                         float v[32];
@@ -864,20 +868,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                                 v[e] = (lo + mid) + v[e];
                             }
                         }
-                        float any = 0.0f;  // NaN if one of them is NaN or infinite
 #pragma unroll
                         for (int e = 0; e < 32; ++e) any = fmaf(v[e], 0.0f, any);
-                        if (any != any && row_at >= 0 && sum == sum) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e)
-                                if (v[e] != v[e])
-                                    v[e] = ct_infinite(a, g.seq, cur->heads.kv, k + e, g.b0 * kCtStep,
-                                                       min(g.b1 * kCtStep, g.pos0 + rel + 1));
-                        }
-                        if (notes) {
-#pragma unroll
-                            for (int e = 0; e < 32; ++e) v[e] += ct_noted(sh.note[par][k + e], rel);
-                        }
                         if (row_at >= 0) {
                             if (PARTS == 3 || split) {
                                 float4 *d = reinterpret_cast<float4 *>((split ? rec : static_cast<float *>(a.out)) + row_at + k);
@@ -897,6 +889,20 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         }
                         __syncwarp();
                     }
+                    if (row_at >= 0 && ((any != any && sum == sum) || notes)) {
+                        // rare: columns with infinities or NaN, put right where they went
+                        void *to_mem = split ? static_cast<void *>(rec) : a.out;
+                        const int dt = split ? DS_F32 : a.q_dtype;
+                        for (int d = 0; d < HD; ++d) {
+                            float x = load_as(to_mem, row_at + d, dt);
+                            if (x != x && sum == sum)
+                                x = ct_infinite(a, g.seq, cur->heads.kv, d, g.b0 * kCtStep,
+                                                min(g.b1 * kCtStep, g.pos0 + rel + 1));
+                            if (notes) x += ct_noted(sh.note[par][d], rel);
+                            store_as(to_mem, row_at + d, dt, x);
+                        }
+                    }
+                    __syncwarp();
                 }
                 if (notes) {  // read: clear them for the segment after the next
                     turns ? named_sync(2 + w, 128) : named_sync(1, 256);
@@ -952,18 +958,19 @@ static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, cudaStream_
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(ready.load() & bit)) {
         e = cudaFuncSetAttribute((const void *)chunk_tc_kernel<HD, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)CtCfg<HD>::kSmem);
+                                 (int)CtCfg<HD, PARTS>::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(bit);
     }
-    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(chunk_tc_grid()), dim3(kCtThreads), CtCfg<HD>::kSmem, stream, false,
+    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(chunk_tc_grid()), dim3(kCtThreads), CtCfg<HD, PARTS>::kSmem, stream, false,
                      a, maps);
 }
 
 cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
-    static_assert(CtCfg<128>::kSmem <= kCtSmemLimit && CtCfg<64>::kSmem <= kCtSmemLimit, "shared memory");
-    chunk_tile_shape(a, a.q_dtype == DS_BF16 ? 128 : 40, 2);
+    static_assert(CtCfg<128, 1>::kSmem <= kCtSmemLimit && CtCfg<128, 3>::kSmem <= kCtSmemLimit, "shared memory");
+    a.q_dtype == DS_BF16 ? chunk_tile_shape(a, 128, 2) : chunk_tile_shape(a, 40, 1);
     a.step = kCtStep;
+    a.tile_cost = kCtTileCost;
     a.min_cost = kCtMinCost;
     CtMaps maps = {};
     maps.box_rows = 8;
