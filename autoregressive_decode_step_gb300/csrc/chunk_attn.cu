@@ -25,7 +25,7 @@ namespace ds {
 constexpr int kCsThreads = 256;
 constexpr int kCsRows = 64;
 constexpr int kCsStep = 64;
-constexpr int kCsMinCost = 256;
+constexpr int kCsPiece = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // Four consecutive elements as fp32 (the row starts on 4 elements).
@@ -227,8 +227,10 @@ int chunk_simt_grid() { return 2 * sm_count(); }
 cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream) {
     chunk_tile_shape(a, kCsRows, 1);
     a.step = kCsStep;
+    a.half_tokens = 0;
+    a.w_half = a.w_full = 1;
     a.tile_cost = 0;
-    a.min_cost = kCsMinCost;
+    a.piece = kCsPiece;
     const int HD = cs_hd(a.hd);
     const size_t smem = cs_smem(HD);
     const int grid = HD == 256 ? sm_count() : chunk_simt_grid();

@@ -4,14 +4,16 @@
 // A tile is up to `tile_tokens` consecutive new rows of one sequence times the
 // query heads that share one KV head (a group of more than `sub_heads` heads
 // is cut into equal parts, each with tiles of its own).  Its cost is the
-// number of positions its last row attends and a constant for its beginning
-// and end (tile_cost, in positions).  The costs of all tiles, ordered
-// by sequence, head and row, form one line that is cut into equal ranges, one
-// per CTA, so the load is even whatever the mix of chunks and single tokens.
-// A tile that a cut falls into is worked on by several CTAs, the cut rounded
-// down to a whole K/V step of `step` positions; their (max, sum, accumulator)
-// records are joined in CTA order by whichever contributor arrives last (a
-// counter, never a wait), so results do not depend on timing.
+// number of positions its last row attends, times a weight, and a constant
+// for its beginning and end.  The costs of all tiles, ordered by sequence,
+// head and row, form one line that is cut into equal ranges, one per CTA, so
+// the load is even whatever the mix of chunks and single tokens.  A cut inside
+// a tile is rounded down to a whole K/V step of `step` positions, or to the
+// tile's beginning or end where it would leave a piece of fewer than `piece`
+// positions: joining the pieces' (max, sum, accumulator) records costs more
+// than the uneven load then.  The records are joined in CTA order by whichever
+// contributor arrives last (a counter, never a wait), so results do not depend
+// on timing.
 //
 // Costs have a closed form (a sum over a sequence's tiles is a quadratic in
 // their number), so no plan is kept in memory: a CTA finds its range by one
@@ -44,8 +46,10 @@ struct ChunkArgs {
     int part_heads;   // query heads of a part (the last may have fewer)
     int tile_tokens;  // rows of a sequence per tile
     int step;         // positions of one K/V step
-    int tile_cost;    // what beginning and ending a tile costs, in positions
-    int min_cost;     // smallest range a CTA is given, at least tile_cost + step
+    int half_tokens;  // tiles of at most so many rows weigh w_half a position, others w_full
+    int w_half, w_full;
+    int tile_cost;    // what beginning and ending a tile costs
+    int piece;        // fewest positions of a tile worth a record, at least one step
     int rec_rows;     // rows of a partial record
     int *counters;    // [grid][2], zero between launches
     float *partials;  // [grid][2] records of rec_rows * (hd + 2) floats (max, sum, then the accumulators)
@@ -65,6 +69,7 @@ void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs);
 struct ChunkSeq {
     int s, r0, n, ctx;
     int tiles;
+    int w_last;      // weight of the last tile's positions (the others': w_full)
     long long cost;  // of one head part
 };
 
@@ -86,13 +91,16 @@ __device__ __forceinline__ ChunkSeq chunk_seq(const ChunkArgs &a, int s, int &fl
     q.ctx = L - q.n;
     q.tiles = (q.n + a.tile_tokens - 1) / a.tile_tokens;
     const long long T = q.tiles;
-    q.cost = T ? T * (q.ctx + a.tile_cost) + (long long)a.tile_tokens * (T * (T - 1) / 2) + q.n : 0;
+    q.w_last = q.n - (q.tiles - 1) * a.tile_tokens <= a.half_tokens ? a.w_half : a.w_full;
+    q.cost = T ? a.w_full * ((T - 1) * q.ctx + (long long)a.tile_tokens * (T * (T - 1) / 2)) +
+                     (long long)q.w_last * (q.ctx + q.n) + T * a.tile_cost
+               : 0;
     return q;
 }
 
 // Cost of a sequence's tiles before tile t < tiles.
 __device__ __forceinline__ long long chunk_cost_before(const ChunkArgs &a, const ChunkSeq &q, long long t) {
-    return t * (q.ctx + a.tile_cost) + (long long)a.tile_tokens * (t * (t + 1) / 2);
+    return a.w_full * (t * q.ctx + (long long)a.tile_tokens * (t * (t + 1) / 2)) + t * a.tile_cost;
 }
 
 // One piece of work: a tile's K/V steps [b0, b1).
@@ -104,8 +112,18 @@ struct ChunkSeg {
     int seq, part;   // sequence; head part (kv head * head_parts + part)
     int b0, b1;      // K/V steps of this CTA
     int slot;        // partial record of this CTA (0 / 1), -1: the tile is all its own
+    int weight;      // of its positions
     long long start, cost;  // place of the tile on the line of costs
 };
+
+// The K/V step that a cut at x behind the tile's start falls to.  (The
+// constant comes first: a cut inside it is one at position 0.)
+__device__ __forceinline__ int chunk_cut(const ChunkArgs &a, const ChunkSeg &g, long long x) {
+    const int pos = (int)max(0ll, x - a.tile_cost) / g.weight;
+    if (pos < a.piece) return 0;
+    if (g.len - pos < a.piece) return (g.len + a.step - 1) / a.step;
+    return pos / a.step;
+}
 
 // The walk of one CTA over its range.  init() is called by every thread of
 // the block (it synchronises the block); then each role walks its own copy.
@@ -131,7 +149,8 @@ struct ChunkWalk {
         for (int w = 0; w < nw; ++w) total += s_red[w];
         total *= parts;
         unit = (total + gridDim.x - 1) / gridDim.x;
-        unit = max(unit, (long long)a.min_cost);
+        // two cuts never round to the same step (and never both to one end)
+        unit = max(unit, (long long)(a.piece + a.step) * a.w_full + a.tile_cost);
         u = min((long long)blockIdx.x * unit, total);
         u1 = min(u + unit, total);
         // the sequence that holds u
@@ -208,13 +227,12 @@ struct ChunkWalk {
             g.len = q.ctx + j0 + g.tokens;
             g.seq = q.s;
             g.part = part;
-            g.cost = g.len + a.tile_cost;
+            g.weight = tile == q.tiles - 1 ? q.w_last : a.w_full;
+            g.cost = (long long)g.weight * g.len + a.tile_cost;
             g.start = seq_start + (long long)part * q.cost + chunk_cost_before(a, q, tile);
             const long long end = min(u1, g.start + g.cost);
-            // the constant comes first: a cut inside it is one at position 0
-            const int p0 = max(0, (int)(u - g.start) - a.tile_cost), p1 = max(0, (int)(end - g.start) - a.tile_cost);
-            g.b0 = p0 / a.step;
-            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : p1 / a.step;
+            g.b0 = u == g.start ? 0 : chunk_cut(a, g, u - g.start);
+            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : chunk_cut(a, g, end - g.start);
             const long long u0 = (long long)blockIdx.x * unit;
             g.slot = g.start < u0 ? 0 : g.start + g.cost > u1 ? 1 : -1;
             ++tile;
@@ -225,17 +243,20 @@ struct ChunkWalk {
     }
 };
 
-// The CTAs that share a split tile, in order.  The first CTA the tile reaches
-// into may have been left less than its first step, which rounds to nothing.
+// The CTAs that share a split tile, in order.  The first and the last CTA the
+// tile reaches into may have been left nothing by the rounding of the cuts.
 struct ChunkShare {
     int first, last;  // contributors
     int counter;      // the tile's counter: the CTA its cost starts in
 };
 __device__ __forceinline__ ChunkShare chunk_share(const ChunkArgs &a, const ChunkSeg &g, long long unit) {
     ChunkShare h;
-    h.counter = (int)(g.start / unit);
+    h.counter = h.first = (int)(g.start / unit);
     h.last = (int)((g.start + g.cost - 1) / unit);
-    h.first = (h.counter + 1) * unit - g.start < a.tile_cost + a.step ? h.counter + 1 : h.counter;
+    if (h.first < h.last) {
+        if (chunk_cut(a, g, (h.first + 1) * unit - g.start) == 0) ++h.first;
+        if (chunk_cut(a, g, h.last * unit - g.start) == (g.len + a.step - 1) / a.step) --h.last;
+    }
     return h;
 }
 // Is the tile's record in CTA c its slot 0 (it began before c's range) or 1?
@@ -292,6 +313,12 @@ __device__ inline void chunk_zero_empty_rows(const ChunkArgs &a) {
     }
 }
 
+__device__ __forceinline__ float chunk_exp2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Join the records of a split tile's (row, head) pairs [m0, m1) in CTA order
 // and write their outputs; warp w of n_warps.
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
@@ -334,7 +361,7 @@ __device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const Chunk
 #pragma unroll
                     for (int k = 0; k < RECS; ++k) top = fmaxf(top, ml[j][k].x);
                     // a pair that has met no finite maximum yet has nothing to keep
-                    const float keep = M[j] == top ? 1.0f : exp2f(M[j] - top);
+                    const float keep = M[j] == top ? 1.0f : chunk_exp2(M[j] - top);
                     M[j] = top;
                     L[j] *= keep;
                     acc[j].x *= keep;
@@ -344,7 +371,7 @@ __device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const Chunk
 #pragma unroll
                     for (int k = 0; k < RECS; ++k) {
                         if (c0 + k > h.last) continue;
-                        const float e = ml[j][k].x == top ? 1.0f : exp2f(ml[j][k].x - top);
+                        const float e = ml[j][k].x == top ? 1.0f : chunk_exp2(ml[j][k].x - top);
                         L[j] = fmaf(ml[j][k].y, e, L[j]);
                         acc[j].x = fmaf(v[j][k].x, e, acc[j].x);
                         acc[j].y = fmaf(v[j][k].y, e, acc[j].y);
@@ -372,10 +399,10 @@ __device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const Chunk
 static __device__ __noinline__ void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
                                                long long unit, int m0, int m1, int w, int n_warps) {
     const ChunkHeads hh = chunk_heads(a, g.part);
-    if (m1 - m0 <= 2 * n_warps)
-        chunk_join_pairs<1, 8>(a, g, h, hh, unit, m0, m1, w, n_warps);
+    if (m1 - m0 <= n_warps)
+        chunk_join_pairs<1, 4>(a, g, h, hh, unit, m0, m1, w, n_warps);
     else
-        chunk_join_pairs<4, 4>(a, g, h, hh, unit, m0, m1, w, n_warps);
+        chunk_join_pairs<4, 2>(a, g, h, hh, unit, m0, m1, w, n_warps);
 }
 
 }  // namespace ds

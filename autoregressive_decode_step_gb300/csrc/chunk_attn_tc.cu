@@ -59,8 +59,11 @@ constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, wa
 // warpgroups, whose thread holds a row's 128 scores: 2 x 216 + 72 = 3 x 168.
 constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
-constexpr int kCtMinCost = 512;
-constexpr int kCtTileCost = 256;
+// Weights of the work split (chunk_attn.cuh): a K/V step of both parts takes
+// about 1.5 times as long as one of a tile that takes turns; beginning and
+// ending a tile takes about as long as two steps, joining a tile's records as
+// four.
+constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kCtPiece = 512;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
 constexpr int kCtSmall = 3072;      // barriers, segments, notes
@@ -360,7 +363,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     walk.init(a, sh.red);  // synchronises the block
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    const int half_tokens = PARTS == 1 ? a.tile_tokens >> 1 : a.tile_tokens;  // rows of the sequence in one part
+    const int half_tokens = a.half_tokens;  // rows of the sequence in one part
     int flags = walk.flags;
     const long long unit = walk.unit;
     auto seg_get = [&](uint32_t k) -> const CtSeg & {
@@ -970,8 +973,11 @@ cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
     static_assert(CtCfg<128, 1>::kSmem <= kCtSmemLimit && CtCfg<128, 3>::kSmem <= kCtSmemLimit, "shared memory");
     a.q_dtype == DS_BF16 ? chunk_tile_shape(a, 128, 2) : chunk_tile_shape(a, 40, 1);
     a.step = kCtStep;
+    a.half_tokens = a.q_dtype == DS_BF16 ? a.tile_tokens / 2 : a.tile_tokens;
+    a.w_half = kCtWeightTurns;
+    a.w_full = kCtWeightShared;
     a.tile_cost = kCtTileCost;
-    a.min_cost = kCtMinCost;
+    a.piece = kCtPiece;
     CtMaps maps = {};
     maps.box_rows = 8;
     while (maps.box_rows < 128 && a.bt % (2 * maps.box_rows) == 0) maps.box_rows *= 2;
