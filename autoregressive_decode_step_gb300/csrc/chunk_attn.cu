@@ -13,7 +13,7 @@
 // than a bf16 product keeps): 64 (row, head) pairs by 64 positions a step,
 // 256 threads of 4 x 4 scores and 4 x hd/16 outputs in registers, Q, K and V
 // in shared memory.  The fp32 FMA rate bounds it (chunks); work split as in
-// chunk_attn.h.
+// chunk_attn.cuh.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -45,7 +45,6 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
     float *sQ = sm, *sK = sQ + kCsRows * HD, *sV = sK + kCsStep * KS;
     float *sP = sK;  // the weights take K's place once the scores are formed
     __shared__ long long s_red[34];
-    __shared__ int s_last;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int flags = 0;
 
@@ -53,10 +52,10 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
     ChunkWalk walk;
     walk.init(a, s_red);
     flags |= walk.flags;
+    if (tid == 0) a.joins[blockIdx.x].pairs = 0;
     ChunkSeg g;
     while (walk.next(a, g)) {
         const ChunkHeads hh = chunk_heads(a, g.part);
-        const int rows = g.tokens * a.part_heads;
         for (int i = tid; i < kCsRows * (HD / 4); i += kCsThreads) {
             const int m = i / (HD / 4), d = (i % (HD / 4)) * 4;
             const int tok = m / a.part_heads, h = m % a.part_heads;
@@ -167,12 +166,8 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 }
             }
         }
-        ChunkShare share = {};
-        bool split = g.slot >= 0;
-        if (split) {
-            share = chunk_share(a, g, walk.unit);
-            split = share.first < share.last;
-        }
+        const bool split = g.split;
+        if (split && g.b0 == 0 && tid == 0) a.joins[blockIdx.x] = walk.join(a, g);
         float *rec = split ? chunk_record(a, blockIdx.x, g.slot) : nullptr;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -201,22 +196,69 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 }
             }
         }
-        if (split) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                int *ctr = a.counters + share.counter * 2;
-                s_last = atomicAdd(ctr, 1) == share.last - share.first;
-                if (s_last) *ctr = 0;  // ready for the next launch
+    }
+    allow_dependent_launch();
+    if (flags) flag_error(a.err, flags);
+}
+
+// Join the records of the split tiles: block (c, y) takes its share of the
+// pairs of the tile whose first contributor CTA c was.
+//   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
+// A warp takes a pair at a time (lane l: four dims), four records' loads in
+// flight; the latency of L2 bounds it, so the pairs are spread over the grid.
+constexpr int kCjThreads = 256;
+constexpr int kCjShares = 8;
+__global__ void __launch_bounds__(kCjThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
+    grid_dependency_wait();
+    const ChunkJoin t = a.joins[blockIdx.x];
+    const int lane = threadIdx.x & 31;
+    const ChunkHeads hh = chunk_heads(a, t.part);
+    const size_t rec_floats = (size_t)a.rec_rows * (a.hd + 2);
+    const float *rec0 = a.partials + ((size_t)t.first * 2 + t.first_slot) * rec_floats;
+    for (int m = blockIdx.y * (kCjThreads / 32) + (threadIdx.x >> 5); m < t.pairs; m += gridDim.y * (kCjThreads / 32)) {
+        const int tok = m / a.part_heads, head = m % a.part_heads;
+        if (head >= hh.count) continue;
+        for (int d = lane * 4; d < a.hd; d += 128) {
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            float M = -INFINITY, L = 0.0f;
+            for (int c0 = t.first; c0 <= t.last; c0 += 4) {
+                float2 ml[4];
+                float4 v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int c = min(c0 + k, t.last);
+                    const float *rec = c == t.first ? rec0 : a.partials + (size_t)c * 2 * rec_floats;
+                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(rec + 2 * m));
+                    v[k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
+                }
+                float top = M;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+                const float keep = M == top ? 1.0f : exp2f(M - top);  // (equal: both may be -inf)
+                M = top;
+                L *= keep;
+                acc.x *= keep;
+                acc.y *= keep;
+                acc.z *= keep;
+                acc.w *= keep;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (c0 + k > t.last) break;
+                    const float e = ml[k].x == top ? 1.0f : exp2f(ml[k].x - top);
+                    L = fmaf(ml[k].y, e, L);
+                    acc.x = fmaf(v[k].x, e, acc.x);
+                    acc.y = fmaf(v[k].y, e, acc.y);
+                    acc.z = fmaf(v[k].z, e, acc.z);
+                    acc.w = fmaf(v[k].w, e, acc.w);
+                }
             }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                chunk_join(a, g, share, walk.unit, 0, rows, tid >> 5, kCsThreads / 32);
-            }
+            const long long o = ((long long)(t.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
+            store_as(a.out, o, a.q_dtype, acc.x / L);
+            store_as(a.out, o + 1, a.q_dtype, acc.y / L);
+            store_as(a.out, o + 2, a.q_dtype, acc.z / L);
+            store_as(a.out, o + 3, a.q_dtype, acc.w / L);
         }
     }
-    if (flags) flag_error(a.err, flags);
 }
 
 static size_t cs_smem(int HD) { return (size_t)(kCsRows * HD + kCsStep * (HD + 4) + kCsStep * HD) * sizeof(float); }
@@ -224,7 +266,7 @@ static int cs_hd(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
 int chunk_simt_grid() { return 2 * sm_count(); }
 
-cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream) {
+cudaError_t launch_chunk_simt(ChunkArgs &a, int *grid, cudaStream_t stream) {
     chunk_tile_shape(a, kCsRows, 1);
     a.step = kCsStep;
     a.half_tokens = 0;
@@ -233,11 +275,11 @@ cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream) {
     a.piece = kCsPiece;
     const int HD = cs_hd(a.hd);
     const size_t smem = cs_smem(HD);
-    const int grid = HD == 256 ? sm_count() : chunk_simt_grid();
+    *grid = HD == 256 ? sm_count() : chunk_simt_grid();
     void (*fn)(ChunkArgs) = HD == 64 ? chunk_simt_kernel<64> : HD == 128 ? chunk_simt_kernel<128> : chunk_simt_kernel<256>;
     const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    return launch_ex(fn, dim3(grid), dim3(kCsThreads), smem, stream, false, a);
+    return launch_ex(fn, dim3(*grid), dim3(kCsThreads), smem, stream, false, a);
 }
 
 void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs) {
@@ -262,7 +304,7 @@ extern "C" DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t 
         n_rows > DS_MAX_DIM || n_qh > DS_MAX_DIM)
         return 0;
     const size_t grid = chunk_simt_grid();
-    return kWsHeader + align_up(grid * 2 * sizeof(int), 256) +
+    return kWsHeader + align_up(grid * sizeof(ChunkJoin), 256) +
            grid * 2 * (size_t)chunk_rec_rows(n_rows, n_qh / n_kvh) * (head_dim + 2) * sizeof(float);
 }
 
@@ -317,9 +359,12 @@ extern "C" DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtyp
     a.rec_rows = chunk_rec_rows(n_rows, a.gq);
     char *ws = static_cast<char *>(workspace);
     a.err = reinterpret_cast<int *>(ws);
-    a.counters = reinterpret_cast<int *>(ws + kWsHeader);
-    a.partials = reinterpret_cast<float *>(ws + kWsHeader + align_up((size_t)chunk_simt_grid() * 2 * sizeof(int), 256));
+    a.joins = reinterpret_cast<ChunkJoin *>(ws + kWsHeader);
+    a.partials = reinterpret_cast<float *>(ws + kWsHeader + align_up((size_t)chunk_simt_grid() * sizeof(ChunkJoin), 256));
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = chunk_tc_supported(a) ? launch_chunk_tc(a, s) : launch_chunk_simt(a, s);
+    int grid = 0;
+    cudaError_t e = chunk_tc_supported(a) ? launch_chunk_tc(a, &grid, s) : launch_chunk_simt(a, &grid, s);
+    if (e == cudaSuccess)
+        e = launch_ex(chunk_join_kernel, dim3(grid, kCjShares), dim3(kCjThreads), 0, s, true, a);
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
 }

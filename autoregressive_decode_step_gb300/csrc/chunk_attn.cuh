@@ -10,10 +10,13 @@
 // the load is even whatever the mix of chunks and single tokens.  A cut inside
 // a tile is rounded down to a whole K/V step of `step` positions, or to the
 // tile's beginning or end where it would leave a piece of fewer than `piece`
-// positions: joining the pieces' (max, sum, accumulator) records costs more
-// than the uneven load then.  The records are joined in CTA order by whichever
-// contributor arrives last (a counter, never a wait), so results do not depend
-// on timing.
+// positions (an eighth of a CTA's range, within bounds): a record is not worth
+// that.  Each contributor leaves its (max, sum, accumulator) record in the
+// workspace and a second launch joins them in CTA order, so results do not
+// depend on timing.  (The last contributor to arrive joining them inside the
+// first launch was measured and dropped: one CTA reading up to 128 pairs'
+// records took 15 to 28 us at the end of the launch when the others had left;
+// in the second every SM reads a few.)
 //
 // Costs have a closed form (a sum over a sequence's tiles is a quadratic in
 // their number), so no plan is kept in memory: a CTA finds its range by one
@@ -49,17 +52,27 @@ struct ChunkArgs {
     int half_tokens;  // tiles of at most so many rows weigh w_half a position, others w_full
     int w_half, w_full;
     int tile_cost;    // what beginning and ending a tile costs
-    int piece;        // fewest positions of a tile worth a record, at least one step
+    int piece;        // most positions a piece may need to be worth a record, at least one step
     int rec_rows;     // rows of a partial record
-    int *counters;    // [grid][2], zero between launches
+    struct ChunkJoin *joins;  // [grid]: the split tile whose first contributor the CTA is
     float *partials;  // [grid][2] records of rec_rows * (hd + 2) floats (max, sum, then the accumulators)
     int *err;
 };
 
+// A split tile, for the joining launch.  pairs 0: the CTA has none.
+struct ChunkJoin {
+    int pairs;       // rows x part_heads
+    int r0, part;    // first row; head part
+    int first, last; // contributing CTAs
+    int first_slot;  // record of the first of them (the others': 0)
+};
+
 int chunk_simt_grid();  // the largest grid of any of the kernels
-cudaError_t launch_chunk_simt(ChunkArgs a, cudaStream_t stream);
+// The first launch; *grid gets its CTA count and `a` the tile shape that the
+// joining launch needs too.
+cudaError_t launch_chunk_simt(ChunkArgs &a, int *grid, cudaStream_t stream);
 bool chunk_tc_supported(const ChunkArgs &a);
-cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream);
+cudaError_t launch_chunk_tc(ChunkArgs &a, int *grid, cudaStream_t stream);
 // Set head_parts, part_heads and tile_tokens for tiles of `subs` parts of
 // sub_rows (row, head) pairs, each part holding whole rows.
 void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs);
@@ -111,17 +124,18 @@ struct ChunkSeg {
     int len;         // positions the tile attends
     int seq, part;   // sequence; head part (kv head * head_parts + part)
     int b0, b1;      // K/V steps of this CTA
-    int slot;        // partial record of this CTA (0 / 1), -1: the tile is all its own
+    int slot;        // partial record of this CTA (0 / 1) if others contribute
+    int split;       // they do
     int weight;      // of its positions
     long long start, cost;  // place of the tile on the line of costs
 };
 
 // The K/V step that a cut at x behind the tile's start falls to.  (The
 // constant comes first: a cut inside it is one at position 0.)
-__device__ __forceinline__ int chunk_cut(const ChunkArgs &a, const ChunkSeg &g, long long x) {
+__device__ __forceinline__ int chunk_cut(const ChunkArgs &a, const ChunkSeg &g, int piece, long long x) {
     const int pos = (int)max(0ll, x - a.tile_cost) / g.weight;
-    if (pos < a.piece) return 0;
-    if (g.len - pos < a.piece) return (g.len + a.step - 1) / a.step;
+    if (pos < piece) return 0;
+    if (g.len - pos < piece) return (g.len + a.step - 1) / a.step;
     return pos / a.step;
 }
 
@@ -132,6 +146,7 @@ struct ChunkWalk {
     long long seq_start;    // of the current sequence
     ChunkSeq q;
     int part, tile;
+    int piece;
     int flags;
 
     // s_red: 34 long longs of shared memory
@@ -149,8 +164,8 @@ struct ChunkWalk {
         for (int w = 0; w < nw; ++w) total += s_red[w];
         total *= parts;
         unit = (total + gridDim.x - 1) / gridDim.x;
-        // two cuts never round to the same step (and never both to one end)
-        unit = max(unit, (long long)(a.piece + a.step) * a.w_full + a.tile_cost);
+        piece = (int)min((long long)a.piece, max((long long)a.step, unit / (8 * a.w_full)));
+        unit = max(unit, (long long)a.step * a.w_full);  // no two cuts inside one step
         u = min((long long)blockIdx.x * unit, total);
         u1 = min(u + unit, total);
         // the sequence that holds u
@@ -231,38 +246,34 @@ struct ChunkWalk {
             g.cost = (long long)g.weight * g.len + a.tile_cost;
             g.start = seq_start + (long long)part * q.cost + chunk_cost_before(a, q, tile);
             const long long end = min(u1, g.start + g.cost);
-            g.b0 = u == g.start ? 0 : chunk_cut(a, g, u - g.start);
-            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : chunk_cut(a, g, end - g.start);
+            g.b0 = u == g.start ? 0 : chunk_cut(a, g, piece, u - g.start);
+            g.b1 = end == g.start + g.cost ? (g.len + a.step - 1) / a.step : chunk_cut(a, g, piece, end - g.start);
             const long long u0 = (long long)blockIdx.x * unit;
-            g.slot = g.start < u0 ? 0 : g.start + g.cost > u1 ? 1 : -1;
+            g.slot = g.start < u0 ? 0 : 1;
             ++tile;
             u = end;
-            if (g.b0 < g.b1) return true;
+            if (g.b0 >= g.b1) continue;
+            g.split = g.b0 > 0 || g.b1 < (g.len + a.step - 1) / a.step;
+            return true;
         }
         return false;
     }
-};
 
-// The CTAs that share a split tile, in order.  The first and the last CTA the
-// tile reaches into may have been left nothing by the rounding of the cuts.
-struct ChunkShare {
-    int first, last;  // contributors
-    int counter;      // the tile's counter: the CTA its cost starts in
-};
-__device__ __forceinline__ ChunkShare chunk_share(const ChunkArgs &a, const ChunkSeg &g, long long unit) {
-    ChunkShare h;
-    h.counter = h.first = (int)(g.start / unit);
-    h.last = (int)((g.start + g.cost - 1) / unit);
-    if (h.first < h.last) {
-        if (chunk_cut(a, g, (h.first + 1) * unit - g.start) == 0) ++h.first;
-        if (chunk_cut(a, g, h.last * unit - g.start) == (g.len + a.step - 1) / a.step) --h.last;
+    // The joining launch's word of a split tile whose first contributor this
+    // CTA is.  CTAs that the rounding of the cuts left nothing of it do not
+    // count; those in between have a step at least.
+    __device__ ChunkJoin join(const ChunkArgs &a, const ChunkSeg &g) const {
+        ChunkJoin j;
+        j.pairs = g.tokens * a.part_heads;
+        j.r0 = g.r0;
+        j.part = g.part;
+        j.first = blockIdx.x;
+        j.first_slot = g.slot;
+        j.last = (int)((g.start + g.cost - 1) / unit);
+        while (chunk_cut(a, g, piece, j.last * unit - g.start) == (g.len + a.step - 1) / a.step) --j.last;
+        return j;
     }
-    return h;
-}
-// Is the tile's record in CTA c its slot 0 (it began before c's range) or 1?
-__device__ __forceinline__ int chunk_slot(const ChunkSeg &g, long long unit, int c) {
-    return g.start < (long long)c * unit ? 0 : 1;
-}
+};
 
 // A sequence's block number as the table has it, and the block's first cache
 // row; a number outside the pool reads block 0 and flags.  (Two calls, so that
@@ -311,98 +322,6 @@ __device__ inline void chunk_zero_empty_rows(const ChunkArgs &a) {
         const long long w = (long long)a.n_qh * a.hd;
         for (long long i = r0 * w + threadIdx.x; i < (r1 - L) * w; i += blockDim.x) store_as(a.out, i, a.q_dtype, 0.0f);
     }
-}
-
-__device__ __forceinline__ float chunk_exp2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Join the records of a split tile's (row, head) pairs [m0, m1) in CTA order
-// and write their outputs; warp w of n_warps.
-//   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
-// The records come from L2, so the loads in flight bound it: a warp takes
-// PAIRS pairs at a time (lane l: four dims of each) and RECS records of each,
-// all loads before the first use.
-template <int PAIRS, int RECS>
-__device__ __forceinline__ void chunk_join_pairs(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
-                                                 const ChunkHeads &hh, long long unit, int m0, int m1, int w,
-                                                 int n_warps) {
-    const int lane = threadIdx.x & 31;
-    for (int i0 = m0 + w; i0 < m1; i0 += PAIRS * n_warps) {
-        for (int d0 = 0; d0 < a.hd; d0 += 128) {
-            const int d = min(d0 + lane * 4, a.hd - 4);
-            float4 acc[PAIRS];
-            float M[PAIRS], L[PAIRS];
-#pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                M[j] = -INFINITY;
-                L[j] = 0.0f;
-            }
-            for (int c0 = h.first; c0 <= h.last; c0 += RECS) {
-                float4 v[PAIRS][RECS];
-                float2 ml[PAIRS][RECS];
-#pragma unroll
-                for (int k = 0; k < RECS; ++k) {
-                    const int c = min(c0 + k, h.last);
-                    const float *rec = chunk_record(a, c, chunk_slot(g, unit, c));
-#pragma unroll
-                    for (int j = 0; j < PAIRS; ++j) {
-                        const int m = min(i0 + j * n_warps, m1 - 1);
-                        ml[j][k] = __ldcg(reinterpret_cast<const float2 *>(rec + 2 * m));
-                        v[j][k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < PAIRS; ++j) {
-                    float top = M[j];
-#pragma unroll
-                    for (int k = 0; k < RECS; ++k) top = fmaxf(top, ml[j][k].x);
-                    // a pair that has met no finite maximum yet has nothing to keep
-                    const float keep = M[j] == top ? 1.0f : chunk_exp2(M[j] - top);
-                    M[j] = top;
-                    L[j] *= keep;
-                    acc[j].x *= keep;
-                    acc[j].y *= keep;
-                    acc[j].z *= keep;
-                    acc[j].w *= keep;
-#pragma unroll
-                    for (int k = 0; k < RECS; ++k) {
-                        if (c0 + k > h.last) continue;
-                        const float e = ml[j][k].x == top ? 1.0f : chunk_exp2(ml[j][k].x - top);
-                        L[j] = fmaf(ml[j][k].y, e, L[j]);
-                        acc[j].x = fmaf(v[j][k].x, e, acc[j].x);
-                        acc[j].y = fmaf(v[j][k].y, e, acc[j].y);
-                        acc[j].z = fmaf(v[j][k].z, e, acc[j].z);
-                        acc[j].w = fmaf(v[j][k].w, e, acc[j].w);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < PAIRS; ++j) {
-                const int m = i0 + j * n_warps;
-                const int tok = m / a.part_heads, head = m % a.part_heads;
-                if (m >= m1 || head >= hh.count || d0 + lane * 4 >= a.hd) continue;
-                const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
-                const float inv = 1.0f / L[j];
-                store_as(a.out, o, a.q_dtype, acc[j].x * inv);
-                store_as(a.out, o + 1, a.q_dtype, acc[j].y * inv);
-                store_as(a.out, o + 2, a.q_dtype, acc[j].z * inv);
-                store_as(a.out, o + 3, a.q_dtype, acc[j].w * inv);
-            }
-        }
-    }
-}
-
-static __device__ __noinline__ void chunk_join(const ChunkArgs &a, const ChunkSeg &g, const ChunkShare &h,
-                                               long long unit, int m0, int m1, int w, int n_warps) {
-    const ChunkHeads hh = chunk_heads(a, g.part);
-    if (m1 - m0 <= n_warps)
-        chunk_join_pairs<1, 4>(a, g, h, hh, unit, m0, m1, w, n_warps);
-    else
-        chunk_join_pairs<4, 2>(a, g, h, hh, unit, m0, m1, w, n_warps);
 }
 
 }  // namespace ds

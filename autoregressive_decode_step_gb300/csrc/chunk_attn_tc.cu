@@ -61,8 +61,7 @@ constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 // Weights of the work split (chunk_attn.cuh): a K/V step of both parts takes
 // about 1.5 times as long as one of a tile that takes turns; beginning and
-// ending a tile takes about as long as two steps, joining a tile's records as
-// four.
+// ending a tile takes about as long as two steps.
 constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kCtPiece = 512;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
@@ -244,11 +243,9 @@ __device__ __forceinline__ int ct_v_place(bool turns, int j, int nb) {
 // A segment as the walking warp hands it to the other roles.
 struct CtSeg {
     ChunkSeg g;
-    ChunkShare share;
     ChunkHeads heads;
     int nb;     // K/V steps; 0: the walk is over
     int turns;  // the parts take turns at the steps
-    int split;  // other CTAs contribute to the tile
 };
 
 struct CtShared {
@@ -258,7 +255,6 @@ struct CtShared {
     uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clean[2], done;
     uint32_t tmem;
     int dead;
-    int last[2];
     union {
         long long red[34];  // ChunkWalk::init
         float2 ml[128];     // turns: a row's (max, sum) of part 1, for part 0
@@ -365,7 +361,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     const uint32_t tmem = sh.tmem;
     const int half_tokens = a.half_tokens;  // rows of the sequence in one part
     int flags = walk.flags;
-    const long long unit = walk.unit;
     auto seg_get = [&](uint32_t k) -> const CtSeg & {
         ct_wait_seg(&sh.seg_full[k % kCtSegs], (k / kCtSegs) & 1, a.err);
         return sh.seg[k % kCtSegs];
@@ -377,6 +372,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (warp == 10) {
         // ------------------------------------------------ the walk over this CTA's range
         if (lane == 0) {
+            a.joins[blockIdx.x].pairs = 0;
             for (uint32_t k = 0;; ++k) {
                 CtSeg c;
                 c.nb = 0;
@@ -384,11 +380,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     c.nb = c.g.b1 - c.g.b0;
                     c.turns = c.g.tokens <= half_tokens;
                     c.heads = chunk_heads(a, c.g.part);
-                    c.split = 0;
-                    if (c.g.slot >= 0) {
-                        c.share = chunk_share(a, c.g, unit);
-                        c.split = c.share.first < c.share.last;
-                    }
+                    if (c.g.split && c.g.b0 == 0) a.joins[blockIdx.x] = walk.join(a, c.g);
                 }
                 if (k >= kCtSegs) ct_wait_seg(&sh.seg_empty[k % kCtSegs], ((k / kCtSegs) - 1) & 1, a.err);
                 sh.seg[k % kCtSegs] = c;
@@ -827,7 +819,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 __syncwarp();
                 tc_fence_after();
                 const bool notes = sh.noted[par];
-                const bool split = cur->split;
+                const bool split = g.split;
                 float f0 = 1.0f, f1 = 0.0f;
                 if (turns && steps1) {  // join the two parts' turns
                     const float2 o = sh.ml[t];
@@ -915,24 +907,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     }
                     turns ? named_sync(2 + w, 128) : named_sync(1, 256);
                 }
-                if (split) {
-                    __threadfence();
-                    named_sync(2 + w, 128);
-                    if (t == 0) {
-                        int *ctr = a.counters + cur->share.counter * 2 + (turns ? 0 : w);
-                        const int last = atomicAdd(ctr, 1) == cur->share.last - cur->share.first;
-                        if (last) *ctr = 0;  // ready for the next launch
-                        sh.last[w] = last;
-                    }
-                    named_sync(2 + w, 128);
-                    if (sh.last[w]) {
-                        __threadfence();
-                        const int per = half_tokens * a.part_heads, all = g.tokens * a.part_heads;
-                        chunk_join(a, g, cur->share, unit, turns || w == 0 ? 0 : per,
-                                   turns || w == 1 ? all : per, q4, 4);
-                    }
-                    named_sync(2 + w, 128);  // sh.last is read
-                }
             }
             if (turns) named_sync(1, 256);  // part 0 has read part 1's accumulator, maxima and notes
             if (steps0) ++oc0;
@@ -942,6 +916,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
     }
     if (flags) flag_error(a.err, flags);
+    allow_dependent_launch();  // the joining launch, which waits for the end of this one
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
@@ -950,10 +925,8 @@ bool chunk_tc_supported(const ChunkArgs &a) {
     return a.kv_dtype == DS_BF16 && (a.hd == 64 || a.hd == 128) && a.bt % 8 == 0;
 }
 
-int chunk_tc_grid() { return sm_count(); }
-
 template <int HD, int PARTS>
-static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, cudaStream_t stream) {
+static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, int grid, cudaStream_t stream) {
     static std::atomic<unsigned long long> ready{0};  // one bit per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -965,11 +938,11 @@ static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, cudaStream_
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(bit);
     }
-    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(chunk_tc_grid()), dim3(kCtThreads), CtCfg<HD, PARTS>::kSmem, stream, false,
+    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(grid), dim3(kCtThreads), CtCfg<HD, PARTS>::kSmem, stream, false,
                      a, maps);
 }
 
-cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
+cudaError_t launch_chunk_tc(ChunkArgs &a, int *grid, cudaStream_t stream) {
     static_assert(CtCfg<128, 1>::kSmem <= kCtSmemLimit && CtCfg<128, 3>::kSmem <= kCtSmemLimit, "shared memory");
     a.q_dtype == DS_BF16 ? chunk_tile_shape(a, 128, 2) : chunk_tile_shape(a, 40, 1);
     a.step = kCtStep;
@@ -978,6 +951,7 @@ cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
     a.w_full = kCtWeightShared;
     a.tile_cost = kCtTileCost;
     a.piece = kCtPiece;
+    *grid = sm_count();
     CtMaps maps = {};
     maps.box_rows = 8;
     while (maps.box_rows < 128 && a.bt % (2 * maps.box_rows) == 0) maps.box_rows *= 2;
@@ -994,8 +968,8 @@ cudaError_t launch_chunk_tc(ChunkArgs a, cudaStream_t stream) {
         if (!encode_tiled_3d(&maps.q, a.q, DS_BF16, qdims, qstrides, qbox, true)) return cudaErrorInvalidValue;
     }
     if (a.hd == 128)
-        return a.q_dtype == DS_BF16 ? launch_ct<128, 1>(a, maps, stream) : launch_ct<128, 3>(a, maps, stream);
-    return a.q_dtype == DS_BF16 ? launch_ct<64, 1>(a, maps, stream) : launch_ct<64, 3>(a, maps, stream);
+        return a.q_dtype == DS_BF16 ? launch_ct<128, 1>(a, maps, *grid, stream) : launch_ct<128, 3>(a, maps, *grid, stream);
+    return a.q_dtype == DS_BF16 ? launch_ct<64, 1>(a, maps, *grid, stream) : launch_ct<64, 3>(a, maps, *grid, stream);
 }
 
 }  // namespace ds
