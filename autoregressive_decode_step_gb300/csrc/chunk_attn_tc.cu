@@ -8,11 +8,11 @@
 //   P = 2^(c S - c m)   by the part's warpgroup, thread r owning row r; P
 //       goes back to TMEM as bf16 over the columns S was in
 //   O += P V    (M 128, N hd, K 128): P from TMEM, V from shared memory
-// While one warpgroup turns its S into P the tensor core works for the other:
-// the MMA thread issues PV and the next QK of part 0, then those of part 1.
-// tcgen05.mma of one thread complete in issue order, so the S of a step being
-// complete means that the PV before it is, and S may overwrite the P it
-// follows.
+// While one warpgroup turns its S into P the tensor core works for the other.
+// Each part has a warp that issues its MMAs, a PV and the next QK at a time:
+// tcgen05.mma of one thread complete in issue order, so S may overwrite the P
+// it follows, and the two warps fill each other's waits (from one warp the
+// tensor core ran dry for some 900 of 4,400 cycles a step).
 //
 // Two parts share one stream of K and V (one fetch serves 256 MMA rows; at
 // 128 rows a step takes as long to fetch from L2 as to multiply).  A tile that
@@ -54,10 +54,11 @@
 namespace ds {
 
 constexpr int kCtStep = 128;
-constexpr int kCtThreads = 384;  // two softmax warpgroups; one with the MMA, walking, K/V and q warps
+constexpr int kCtThreads = 384;  // two softmax warpgroups; one with two MMA, the K/V and the walking warp
 // Registers a thread: 168 at launch (384 x 168), moved to the softmax
 // warpgroups, whose thread holds a row's 128 scores: 2 x 216 + 72 = 3 x 168.
 constexpr int kCtRegsSoftmax = 216, kCtRegsOther = 72;
+constexpr int kCtAhead = 8;      // steps one part may be ahead of the other, and more: half the ring's tiles
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 // Weights of the work split (chunk_attn.cuh): a K/V step of both parts takes
 // about 1.5 times as long as one of a tile that takes turns; beginning and
@@ -252,7 +253,7 @@ struct CtShared {
     CtSeg seg[kCtSegs];
     uint64_t seg_full[kCtSegs], seg_empty[kCtSegs];
     uint64_t full[kCtMaxStages], empty[kCtMaxStages];
-    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clean[2], done;
+    uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], v_clean[kCtAhead], done[2];
     uint32_t tmem;
     int dead;
     union {
@@ -262,6 +263,7 @@ struct CtShared {
     // non-finite V per dim, by the segment's parity: 10-bit first positions of
     // NaN, +inf, -inf behind the tile's pos0; noted: there are some
     int noted[2];
+    int left[2];  // segments a part's warps are done with, four counts each
     unsigned note[2][128];
 };
 static_assert(sizeof(CtShared) <= kCtSmall, "shared words");
@@ -329,7 +331,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < ST; ++i) {
             mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
+            mbar_init(&sh.empty[i], 2);  // both parts
         }
         for (int w = 0; w < 2; ++w) {
             mbar_init(&sh.q_full[w], PARTS == 1 ? 1 : 8);
@@ -337,15 +339,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_init(&sh.s_full[w], 1);
             mbar_init(&sh.p_full[w], 4);
             mbar_init(&sh.o_full[w], 1);
-            sh.noted[w] = 0;
+            mbar_init(&sh.done[w], 1);
+            sh.noted[w] = sh.left[w] = 0;
         }
         for (int i = 0; i < kCtSegs; ++i) {
             mbar_init(&sh.seg_full[i], 1);
-            mbar_init(&sh.seg_empty[i], PARTS == 1 ? 11 : 10);  // producers, MMA, eight softmax warps
+            mbar_init(&sh.seg_empty[i], 11);  // K/V producer, two MMA warps, eight softmax warps
         }
-        mbar_init(&sh.v_clean[0], 4);
-        mbar_init(&sh.v_clean[1], 4);
-        mbar_init(&sh.done, 1);
+        for (int i = 0; i < kCtAhead; ++i) mbar_init(&sh.v_clean[i], 4);
         sh.dead = 0;
         fence_mbarrier_init();
     }
@@ -370,9 +371,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCtRegsOther));
     if (warp == 10) {
-        // ------------------------------------------------ the walk over this CTA's range
+        // ------------------------------------------------ the walk over this CTA's range, and bf16 q
+        // A segment is handed out before the q of the one before it is waited
+        // for.  A part's q is free once the tensor core is through with its
+        // last QK; MMA rows without a (row, head) pair hold anything: no row
+        // reaches another.
         if (lane == 0) {
             a.joins[blockIdx.x].pairs = 0;
+            uint32_t issued = 0;
+            int q_first = 0, q_row[2] = {0, 0};
             for (uint32_t k = 0;; ++k) {
                 CtSeg c;
                 c.nb = 0;
@@ -385,40 +392,29 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (k >= kCtSegs) ct_wait_seg(&sh.seg_empty[k % kCtSegs], ((k / kCtSegs) - 1) & 1, a.err);
                 sh.seg[k % kCtSegs] = c;
                 mbar_arrive(&sh.seg_full[k % kCtSegs]);
-                if (c.nb == 0) break;
-            }
-        }
-        __syncwarp();
-    } else if (warp == 11 && PARTS == 1) {
-        // ------------------------------------------------ q of both parts
-        // A part's q is free once the tensor core is through with its last QK.
-        // MMA rows without a (row, head) pair hold anything: no row reaches
-        // another.
-        uint32_t issued = 0;
-        for (uint32_t seg = 0;; ++seg) {
-            const CtSeg &c = seg_get(seg);
-            if (c.nb == 0) break;
-            const int r0 = c.g.r0, first = c.heads.first, r1 = c.turns ? r0 : r0 + half_tokens;
-            __syncwarp();
-            if (lane == 0) seg_done(seg);
-            for (int w = 0; w < 2; ++w)
-                if (seg) ct_wait(&sh.q_empty[w], (seg - 1) & 1, dead, a.err);
-            if (__any_sync(0xffffffffu, *dead)) continue;
-            ++issued;
-            if (lane == 0) {
-                for (int w = 0; w < 2; ++w) {
-                    mbar_arrive_expect_tx(&sh.q_full[w], (uint32_t)(Cfg::kHalves * 128 * a.part_heads * half_tokens));
-                    for (int h = 0; h < Cfg::kHalves; ++h)
-                        ct_box(smem_u32(s_q) + w * Cfg::kTileBytes + h * kCtHalf, &maps.q, h * 64, first, w ? r1 : r0,
-                               &sh.q_full[w]);
+                if (PARTS == 1 && k > 0) {
+                    for (int w = 0; w < 2; ++w)
+                        if (k > 1) ct_wait(&sh.q_empty[w], k & 1, dead, a.err);  // the segment's before: k - 2
+                    if (!*dead) {
+                        ++issued;
+                        for (int w = 0; w < 2; ++w) {
+                            mbar_arrive_expect_tx(&sh.q_full[w],
+                                                  (uint32_t)(Cfg::kHalves * 128 * a.part_heads * half_tokens));
+                            for (int h = 0; h < Cfg::kHalves; ++h)
+                                ct_box(smem_u32(s_q) + w * Cfg::kTileBytes + h * kCtHalf, &maps.q, h * 64, q_first,
+                                       q_row[w], &sh.q_full[w]);
+                        }
+                    }
                 }
+                if (c.nb == 0) break;
+                q_first = c.heads.first;
+                q_row[0] = c.g.r0;
+                q_row[1] = c.turns ? c.g.r0 : c.g.r0 + half_tokens;
             }
-            __syncwarp();
-        }
-        // every copy issued has landed before the block may end
-        if (lane == 0)
+            // every copy issued has landed before the block may end
             for (int w = 0; w < 2; ++w)
                 if (issued) mbar_wait(&sh.q_full[w], (issued - 1) & 1, *dead ? nullptr : a.err);
+        }
         __syncwarp();
     } else if (warp == 9) {
         // ------------------------------------------------ K/V producer
@@ -488,9 +484,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (!mbar_wait(&sh.full[f % ST], (f / ST) & 1, *dead ? nullptr : a.err)) break;
         }
         __syncwarp();
-    } else if (warp == 8) {
-        // ------------------------------------------------ MMA issue
+    } else {
+        // ------------------------------------------------ MMA issue, a warp for each part
         {
+            const uint32_t w = warp == 8 ? 0 : 1;
             constexpr uint32_t kIdQk = (1u << 4) | (1u << 7) | (1u << 10) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
             constexpr uint32_t kIdPv =
                 (1u << 4) | (1u << 7) | (1u << 10) | (1u << 16) | ((uint32_t)(HD >> 3) << 17) | ((128u >> 4) << 24);
@@ -510,12 +507,16 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 }
                 return s;
             };
-            auto wait_p = [&](uint32_t w) {
-                ct_wait(&sh.p_full[w], (p_par >> w) & 1, dead, a.err);
-                p_par ^= 1u << w;
+            auto pass = [&]() {  // the next tile is the other part's alone
+                const uint32_t s = take();
+                if (one) mbar_arrive(&sh.empty[s]);
+            };
+            auto wait_p = [&]() {
+                ct_wait(&sh.p_full[w], p_par, dead, a.err);
+                p_par ^= 1;
                 tc_fence_after();
             };
-            auto qk = [&](uint32_t w, uint32_t s) {
+            auto qk = [&](uint32_t s) {
                 const uint64_t ad = q0 + (uint64_t)(PARTS == 1 ? w * (Cfg::kTileBytes >> 4) : 0);
                 const uint64_t bd = k0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
                 const uint32_t d = tm + w * 128;
@@ -528,7 +529,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                                   k || z < PARTS - 1 ? 1u : 0u);
                     }
             };
-            auto pv = [&](uint32_t w, uint32_t s, bool first) {
+            auto pv = [&](uint32_t s, bool first) {
                 const uint64_t bd = v0 + (uint64_t)(s * (Cfg::kTileBytes >> 4));
                 const uint32_t d = tm + 256 + w * HD, p = tm + w * 128;
 #pragma unroll
@@ -541,71 +542,48 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (nb == 0) break;
                 const int turns = __shfl_sync(0xffffffffu, c.turns, 0);
                 if (one) seg_done(seg);
-                uint32_t ks = take(), vs;
-                ct_wait(&sh.q_full[0], seg & 1, dead, a.err);
-                if (PARTS == 1) ct_wait(&sh.q_full[1], seg & 1, dead, a.err);
-                tc_fence_after();
-                qk(0, ks);
-                if (!turns) {
-                    ct_commit(one, &sh.s_full[0]);
-                    if (nb == 1) ct_commit(one, &sh.q_empty[0]);
-                    qk(1, ks);
-                    ct_commit(one, &sh.s_full[1]);
+                uint32_t ks, vs;
+                const int stride = turns ? 2 : 1, mine = turns ? (int)w : 0;  // steps mine, mine + stride, ...
+                // (fp32 q: one barrier for both parts, whose next phase only this
+                // part's S holds back; without a step here it may have passed)
+                if (PARTS == 1 || mine < nb) ct_wait(&sh.q_full[PARTS == 1 ? w : 0], seg & 1, dead, a.err);
+                for (int j = 0; j < min(stride, nb); ++j) {
+                    if (j != mine) {
+                        pass();
+                        continue;
+                    }
+                    ks = take();
+                    tc_fence_after();
+                    qk(ks);
+                    ct_commit(one, &sh.s_full[w]);
                     ct_commit(one, &sh.empty[ks]);
-                    if (nb == 1) ct_commit(one, &sh.q_empty[1]);
-                    for (int i = 0; i < nb; ++i) {
-                        const bool more = i + 1 < nb, last_qk = i + 2 >= nb;
-                        vs = take();
-                        if (more) ks = take();
-#pragma unroll
-                        for (uint32_t w = 0; w < 2; ++w) {
-                            wait_p(w);
-                            pv(w, vs, i == 0);
-                            if (more) {
-                                qk(w, ks);
-                                ct_commit(one, &sh.s_full[w]);
-                                if (last_qk) ct_commit(one, &sh.q_empty[w]);
-                            } else {
-                                ct_commit(one, &sh.o_full[w]);
-                            }
-                        }
-                        ct_commit(one, &sh.empty[vs]);
-                        if (more) ct_commit(one, &sh.empty[ks]);
+                }
+                if (mine + stride >= nb) ct_commit(one, &sh.q_empty[w]);  // no further use of this tile's q
+                for (int j = 0; j < nb; ++j) {
+                    const bool more = j + stride < nb;
+                    if (turns && (j & 1) != mine) {
+                        pass();
+                        if (more) pass();
+                        continue;
                     }
-                } else {
-                    ct_commit(one, &sh.s_full[0]);
-                    ct_commit(one, &sh.empty[ks]);
-                    if (nb <= 2) ct_commit(one, &sh.q_empty[0]);
-                    if (nb > 1) {
-                        ks = take();
-                        tc_fence_after();
-                        qk(1, ks);
-                        ct_commit(one, &sh.s_full[1]);
-                        ct_commit(one, &sh.empty[ks]);
+                    vs = take();
+                    if (more) ks = take();
+                    wait_p();
+                    pv(vs, j < stride);
+                    if (more) {
+                        qk(ks);
+                        ct_commit(one, &sh.s_full[w]);
+                        if (j + 2 * stride >= nb) ct_commit(one, &sh.q_empty[w]);
+                    } else {
+                        ct_commit(one, &sh.o_full[w]);
                     }
-                    if (nb <= 3) ct_commit(one, &sh.q_empty[1]);
-                    for (int j = 0; j < nb; ++j) {
-                        const uint32_t w = j & 1;
-                        const bool more = j + 2 < nb;
-                        vs = take();
-                        if (more) ks = take();
-                        wait_p(w);
-                        pv(w, vs, j < 2);
-                        if (more) {
-                            qk(w, ks);
-                            ct_commit(one, &sh.s_full[w]);
-                            if (j + 4 >= nb) ct_commit(one, &sh.q_empty[w]);
-                            ct_commit(one, &sh.empty[ks]);
-                        } else {
-                            ct_commit(one, &sh.o_full[w]);
-                        }
-                        ct_commit(one, &sh.empty[vs]);
-                    }
+                    ct_commit(one, &sh.empty[vs]);
+                    if (more) ct_commit(one, &sh.empty[ks]);
                 }
             }
             // nothing of ours runs on the tensor cores when the block ends
-            ct_commit(one, &sh.done);
-            mbar_wait(&sh.done, 0, *dead ? nullptr : a.err);
+            ct_commit(one, &sh.done[w]);
+            mbar_wait(&sh.done[w], 0, *dead ? nullptr : a.err);
         }
         __syncwarp();
     }
@@ -689,10 +667,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 tc_fence_after();
                 if (masked && (turns || w == 0)) {
                     // Check the step's V: this thread position t0 + t.  Part 0
-                    // does it for both where they share the step.  (Its S is
-                    // there, so part 1 has given up its last P of the segment
-                    // before, and is done with the one before that, which had
-                    // these notes.)
+                    // does it for both where they share the step.
                     const uint32_t place = n0 + (uint32_t)ct_v_place(turns, j, nb);
                     ct_wait(&sh.full[place % ST], (place / ST) & 1, dead, a.err);
                     unsigned char *row = s_ring + (size_t)(place % ST) * Cfg::kTileBytes + t * 128;
@@ -700,7 +675,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     if (t0 + t >= g.len) {
 #pragma unroll
                         for (int ch = 0; ch < HD / 8; ++ch)
-                            *reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + ((ch & 7) << 4)) = make_uint4(0, 0, 0, 0);
+                            *reinterpret_cast<uint4 *>(row + (ch >> 3) * kCtHalf + (((ch & 7) ^ (t & 7)) << 4)) =
+                                make_uint4(0, 0, 0, 0);
                     } else if (behind > 0) {
                         // an exponent of all ones carries into the sign's place
                         uint32_t bad = 0;
@@ -712,6 +688,14 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                                    ((x.z & 0x7f807f80u) + 0x00800080u) | ((x.w & 0x7f807f80u) + 0x00800080u);
                         }
                         if (bad & 0x80008000u) {
+                            // the notes were those of the segment before the last:
+                            // the other part is done with it before they change
+                            const uint64_t since = global_timer_ns();
+                            while (*reinterpret_cast<volatile int *>(&sh.left[1 - w]) < 4 * ((int)seg - 1) && !*dead)
+                                if (global_timer_ns() - since > kWaitLimitNs) {
+                                    flag_error(a.err, DS_ERR_WAIT_TIMEOUT);
+                                    *dead = 1;
+                                }
                             for (int d = 0; d < HD; ++d) {
                                 __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(
                                     row + (d >> 6) * kCtHalf + ((((d >> 3) & 7) ^ (t & 7)) << 4) + (d & 7) * 2);
@@ -728,7 +712,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     if (turns)
                         named_sync(2 + w, 128);
                     else if (lane == 0)
-                        mbar_arrive(&sh.v_clean[vc & 1]);
+                        mbar_arrive(&sh.v_clean[vc % kCtAhead]);
                 }
                 if (busy) {
                     float s[kCtStep];
@@ -793,9 +777,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     tc_fence_before();
                 }
                 if (masked && !turns) {
-                    // part 0 has checked this V; it may be a step ahead, so the
-                    // checked steps alternate between two barriers
-                    if (w == 1) ct_wait(&sh.v_clean[vc & 1], (vc >> 1) & 1, dead, a.err);
+                    // part 0 has checked this V; it may be as far ahead as the
+                    // ring reaches, so the checked steps go round several barriers
+                    if (w == 1) ct_wait(&sh.v_clean[vc % kCtAhead], (vc / kCtAhead) & 1, dead, a.err);
                     ++vc;
                 }
                 __syncwarp();
@@ -912,7 +896,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             if (steps0) ++oc0;
             if (steps1) ++oc1;
             __syncwarp();
-            if (lane == 0) seg_done(seg);
+            if (lane == 0) {
+                seg_done(seg);
+                atomicAdd(&sh.left[w], 1);
+            }
         }
     }
     if (flags) flag_error(a.err, flags);
