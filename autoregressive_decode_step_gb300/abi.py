@@ -182,17 +182,19 @@ def ptr(t):
     return ctypes.c_void_p(t.data_ptr())
 
 
+_DTYPE_CODES = {torch.float32: DS_F32, torch.bfloat16: DS_BF16}
+
+
 def dtype_code(t):
-    if t.dtype == torch.float32:
-        return DS_F32
-    if t.dtype == torch.bfloat16:
-        return DS_BF16
-    raise TypeError("unsupported dtype %s" % t.dtype)
+    code = _DTYPE_CODES.get(t.dtype)
+    if code is None:
+        raise TypeError("unsupported dtype %s" % t.dtype)
+    return code
 
 
 def stream_handle(stream=None):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: building a Stream object takes 3 us
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return ctypes.c_void_p(stream.cuda_stream)
 
 
@@ -323,9 +325,10 @@ def ds_rope_append(qkv, row_stride, n_rows, positions, n_axes, pair_axis, n_qh, 
                    q_out, k_cache, v_cache, cache_rows, slots, ws, stream=None):
     """Rotate a ragged step's q|k|v rows and write k and v to their slots.
     pair_axis: host uint8 numpy array of rot_dim / 2 axes, or None (one axis)."""
-    if pair_axis is not None and (pair_axis.dtype.str != "|u1" or not pair_axis.flags.c_contiguous or
-                                  pair_axis.size < rot_dim // 2):
-        raise ValueError("pair_axis: a contiguous uint8 array of rot_dim / 2 axes is needed")
+    if pair_axis is not None:
+        if pair_axis.dtype.char != "B" or pair_axis.size < rot_dim // 2:
+            raise ValueError("pair_axis: a uint8 array of rot_dim / 2 axes is needed")
+        pair_axis = pair_axis.tobytes()  # (the array's .ctypes takes 2 us to build)
     if v_cache.dtype != k_cache.dtype:
         raise ValueError("k_cache and v_cache: one dtype is needed")
     n_kv = cache_rows * n_kvh * head_dim
@@ -333,8 +336,7 @@ def ds_rope_append(qkv, row_stride, n_rows, positions, n_axes, pair_axis, n_qh, 
     reach = qkv.untyped_storage().nbytes() // qkv.element_size() - qkv.storage_offset()
     check(lib.ds_rope_append(qkv.data_ptr(), reach, dtype_code(qkv), row_stride, n_rows,
                              _i32(positions, n_axes * n_rows, "positions"), n_axes,
-                             None if pair_axis is None else pair_axis.ctypes.data, n_qh, n_kvh, head_dim, rot_dim,
-                             base, layout, _dense(q_out, q_out.numel(), "q_out"), q_out.numel(), dtype_code(q_out),
+                             pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout, _dense(q_out, q_out.numel(), "q_out"), q_out.numel(), dtype_code(q_out),
                              _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"), dtype_code(k_cache),
                              cache_rows, _i32(slots, n_rows, "slots"), ws.data_ptr(), nbytes(ws),
                              stream_handle(stream)), "ds_rope_append")
