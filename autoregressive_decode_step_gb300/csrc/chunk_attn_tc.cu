@@ -159,6 +159,17 @@ __device__ __forceinline__ void ct_st16(uint32_t taddr, const uint32_t *v) {
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
 }
+// The loads of this warp are complete, v's 32 among them (named, so that no
+// use of them is moved in front of the wait).
+__device__ __forceinline__ void ct_wait_ld32(float *v) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                   "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                   "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void ct_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void ct_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void ct_fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -715,20 +726,44 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         mbar_arrive(&sh.v_clean[vc % kCtAhead]);
                 }
                 if (busy) {
-                    float s[kCtStep];
+                    // bf16: the row's 128 scores stay in registers between their
+                    // maximum and their weights.  fp32: short loops that read S
+                    // twice, because a whole row's code, three pieces a weight,
+                    // is fetched more slowly than it runs (64 single tokens:
+                    // 165 -> 142 us; for bf16 the same costs 448 -> 485 us on a
+                    // prompt of 8192, where the tensor core waits for P).
+                    constexpr int kHeld = PARTS == 1 ? kCtStep : 64;
+                    const int lim = masked ? g.pos0 + rel - t0 : kCtStep;  // the row's last column
+                    float s[kHeld], top;
+                    auto hide = [&](float *v, int k0, int n) {
 #pragma unroll
-                    for (int k = 0; k < kCtStep; k += 32) ct_ld32(ts + k, s + k);
-                    ct_wait_ld();
-                    if (masked) {
-                        const int lim = g.pos0 + rel - t0;
+                        for (int k = 0; k < n; ++k) v[k] = k0 + k <= lim ? v[k] : -INFINITY;
+                    };
+                    auto highest = [&](const float *v, int n) {  // chains of three-input maxima
+                        float t4[4] = {v[0], v[1], v[2], v[3]};
 #pragma unroll
-                        for (int k = 0; k < kCtStep; ++k) s[k] = k <= lim ? s[k] : -INFINITY;
+                        for (int k = 4; k + 1 < n; k += 2)
+                            t4[(k >> 1) & 3] = fmaxf(fmaxf(t4[(k >> 1) & 3], v[k]), v[k + 1]);
+                        return fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    };
+                    if constexpr (PARTS == 1) {
+#pragma unroll
+                        for (int k = 0; k < kHeld; k += 32) ct_ld32(ts + k, s + k);
+                        ct_wait_ld();
+                        if (masked) hide(s, 0, kHeld);
+                        top = highest(s, kHeld);
+                    } else {
+                        top = -INFINITY;
+#pragma unroll 1
+                        for (int k0 = 0; k0 < kCtStep; k0 += 64) {
+                            ct_ld32(ts + k0, s);
+                            ct_ld32(ts + k0 + 32, s + 32);
+                            ct_wait_ld32(s);
+                            ct_wait_ld32(s + 32);
+                            if (masked) hide(s, k0, 64);
+                            top = fmaxf(top, highest(s, 64));
+                        }
                     }
-                    float t4[4] = {s[0], s[1], s[2], s[3]};  // chains of three-input maxima
-#pragma unroll
-                    for (int k = 4; k + 1 < kCtStep; k += 2)
-                        t4[(k >> 1) & 3] = fmaxf(fmaxf(t4[(k >> 1) & 3], s[k]), s[k + 1]);
-                    const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     const float m_new = fmaxf(m_ref, top);
                     if (i == 0) {
                         m_ref = m_new;
@@ -753,12 +788,12 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     // this lane's piece: what the pieces before it hold is taken off
                     const uint32_t cut1 = piece > 0 ? 0xffff0000u : 0u, cut2 = piece > 1 ? 0xffff0000u : 0u;
                     float2 add[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-                    for (int k0 = 0; k0 < kCtStep; k0 += 32) {
+                    auto weigh = [&](float *v, int k0) {  // 32 scores to weights, back to where S was
+                        if (PARTS == 3 && masked) hide(v, k0, 32);
                         uint32_t p[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            float2 x = ct_fma2(make_float2(s[k0 + 2 * k], s[k0 + 2 * k + 1]), c2, mc2);
+                            float2 x = ct_fma2(make_float2(v[2 * k], v[2 * k + 1]), c2, mc2);
                             x.x = ct_exp2(x.x);
                             x.y = ct_exp2(x.y);
                             add[k & 1] = ct_add2(add[k & 1], x);
@@ -770,7 +805,23 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                                 p[k] = ct_top2(x.x, x.y);
                             }
                         }
-                        ct_st16(ts + k0 / 2, p);
+                        ct_st16(ts + k0 / 2, p);  // (columns whose S has been read)
+                    };
+                    if constexpr (PARTS == 1) {
+#pragma unroll
+                        for (int k0 = 0; k0 < kHeld; k0 += 32) weigh(s + k0, k0);
+                    } else {
+                        float *s_a = s, *s_b = s + 32;  // the next 32 on their way while these are worked on
+                        ct_ld32(ts, s_a);
+#pragma unroll 1
+                        for (int k0 = 0; k0 < kCtStep; k0 += 64) {
+                            ct_wait_ld32(s_a);
+                            ct_ld32(ts + k0 + 32, s_b);
+                            weigh(s_a, k0);
+                            ct_wait_ld32(s_b);
+                            if (k0 + 64 < kCtStep) ct_ld32(ts + k0 + 64, s_a);
+                            weigh(s_b, k0 + 32);
+                        }
                     }
                     sum += (add[0].x + add[0].y) + (add[1].x + add[1].y);
                     ct_wait_st();
