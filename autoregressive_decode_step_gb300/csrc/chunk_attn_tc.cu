@@ -369,6 +369,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     chunk_zero_empty_rows(a);
     ChunkWalk walk;
     walk.init(a, sh.red);  // synchronises the block
+    // The joining launch may take its place as blocks of this one end; it
+    // waits for the end of all before it reads.
+    allow_dependent_launch();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     const int half_tokens = a.half_tokens;  // rows of the sequence in one part
@@ -954,7 +957,6 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         }
     }
     if (flags) flag_error(a.err, flags);
-    allow_dependent_launch();  // the joining launch, which waits for the end of this one
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
