@@ -17,6 +17,7 @@
 #include <algorithm>
 #include <atomic>
 #include <cmath>
+#include <type_traits>
 
 #include "chunk_attn.cuh"
 
@@ -45,6 +46,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
     float *sQ = sm, *sK = sQ + kCsRows * HD, *sV = sK + kCsStep * KS;
     float *sP = sK;  // the weights take K's place once the scores are formed
     __shared__ long long s_red[34];
+    __shared__ int s_row[2][kCsStep];
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     int flags = 0;
 
@@ -65,7 +67,8 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 v = cs_load4(a.q, ((long long)(g.r0 + tok) * a.n_qh + hh.first + h) * a.hd + d, a.q_dtype);
             *reinterpret_cast<float4 *>(sQ + m * HD + d) = v;
         }
-        float acc[4][HD / 16], mx[4], sum[4];
+        float2 acc[4][HD / 32];
+        float mx[4], sum[4];
         int lim[4];  // last position of each row
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -73,18 +76,24 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
             sum[i] = 0.0f;
             lim[i] = g.pos0 + (ty * 4 + i) / a.part_heads;
 #pragma unroll
-            for (int c = 0; c < HD / 16; ++c) acc[i][c] = 0.0f;
+            for (int c = 0; c < HD / 32; ++c) acc[i][c] = make_float2(0.0f, 0.0f);
         }
+        // a step's cache rows, worked out by 64 threads while the step before runs
+        auto find_rows = [&](int b) {
+            const int pos = b * kCsStep + tid;
+            if (tid < kCsStep && pos < g.len)
+                s_row[b & 1][tid] = (int)(chunk_block_row(a, g.seq, pos / a.bt, flags) + pos % a.bt);
+        };
+        find_rows(g.b0);
         for (int b = g.b0; b < g.b1; ++b) {
             const int t0 = b * kCsStep, nt = min(kCsStep, g.len - t0);
-            __syncthreads();  // the last step's weights and values are read
+            __syncthreads();  // the last step's weights and values are read, this one's rows found
+            if (b + 1 < g.b1) find_rows(b + 1);
             for (int i = tid; i < kCsStep * (HD / 4); i += kCsThreads) {
                 const int t = i / (HD / 4), d = (i % (HD / 4)) * 4;
                 float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
                 if (t < nt && d < a.hd) {
-                    const int pos = t0 + t;
-                    const long long row = chunk_block_row(a, g.seq, pos / a.bt, flags) + pos % a.bt;
-                    const long long e = (row * a.n_kvh + hh.kv) * a.hd + d;
+                    const long long e = ((long long)s_row[b & 1][t] * a.n_kvh + hh.kv) * a.hd + d;
                     k = cs_load4(a.k_cache, e, a.kv_dtype);
                     v = cs_load4(a.v_cache, e, a.kv_dtype);
                 }
@@ -92,7 +101,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 *reinterpret_cast<float4 *>(sV + t * HD + d) = v;
             }
             __syncthreads();
-            float s[4][4] = {};
+            float2 s2[4][4] = {};  // sums over even and odd dims
 #pragma unroll 4
             for (int d = 0; d < HD; d += 4) {
                 float4 qv[4], kv[4];
@@ -105,12 +114,15 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        s[i][j] = fmaf(qv[i].x, kv[j].x, s[i][j]);
-                        s[i][j] = fmaf(qv[i].y, kv[j].y, s[i][j]);
-                        s[i][j] = fmaf(qv[i].z, kv[j].z, s[i][j]);
-                        s[i][j] = fmaf(qv[i].w, kv[j].w, s[i][j]);
+                        s2[i][j] = chunk_fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), s2[i][j]);
+                        s2[i][j] = chunk_fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), s2[i][j]);
                     }
             }
+            float s[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
             __syncthreads();  // K is read
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -138,34 +150,39 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 sum[i] = sum[i] * keep + add;
                 mx[i] = m_new;
 #pragma unroll
-                for (int c = 0; c < HD / 16; ++c) acc[i][c] *= keep;
+                for (int c = 0; c < HD / 32; ++c) {
+                    acc[i][c].x *= keep;
+                    acc[i][c].y *= keep;
+                }
             }
             __syncwarp();  // a warp reads the weights of its own rows only
-            const bool masked = t0 + kCsStep - 1 > g.pos0;
-            for (int t = 0; t < nt; t += 4) {
-                float4 p4[4];
+            auto add_values = [&](auto masked) {
+                for (int t = 0; t < nt; t += 4) {
+                    float4 p4[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * PS + t);
+                    for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * PS + t);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float p[4];
+                    for (int k = 0; k < 4; ++k) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p[i] = k == 0 ? p4[i].x : k == 1 ? p4[i].y : k == 2 ? p4[i].z : p4[i].w;
+                        for (int c = 0; c < HD / 64; ++c) {
+                            const float4 v = *reinterpret_cast<const float4 *>(sV + (t + k) * HD + 64 * c + tx * 4);
 #pragma unroll
-                    for (int c = 0; c < HD / 64; ++c) {
-                        const float4 v = *reinterpret_cast<const float4 *>(sV + (t + k) * HD + 64 * c + tx * 4);
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            // a row skips what it does not attend: 0 x an infinity there would be NaN
-                            if (masked && t0 + t + k > lim[i]) continue;
-                            acc[i][4 * c] = fmaf(p[i], v.x, acc[i][4 * c]);
-                            acc[i][4 * c + 1] = fmaf(p[i], v.y, acc[i][4 * c + 1]);
-                            acc[i][4 * c + 2] = fmaf(p[i], v.z, acc[i][4 * c + 2]);
-                            acc[i][4 * c + 3] = fmaf(p[i], v.w, acc[i][4 * c + 3]);
+                            for (int i = 0; i < 4; ++i) {
+                                // a row skips what it does not attend: 0 x an infinity there would be NaN
+                                if (masked.value && t0 + t + k > lim[i]) continue;
+                                const float p = k == 0 ? p4[i].x : k == 1 ? p4[i].y : k == 2 ? p4[i].z : p4[i].w;
+                                const float2 p2 = make_float2(p, p);
+                                acc[i][2 * c] = chunk_fma2(p2, make_float2(v.x, v.y), acc[i][2 * c]);
+                                acc[i][2 * c + 1] = chunk_fma2(p2, make_float2(v.z, v.w), acc[i][2 * c + 1]);
+                            }
                         }
                     }
                 }
-            }
+            };
+            if (t0 + kCsStep - 1 > g.pos0)
+                add_values(std::true_type{});
+            else
+                add_values(std::false_type{});
         }
         const bool split = g.split;
         if (split && g.b0 == 0 && tid == 0) a.joins[blockIdx.x] = walk.join(a, g);
@@ -184,7 +201,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                     const int d = 64 * c + tx * 4;
                     if (d < a.hd)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) rec[2 * a.rec_rows + m * a.hd + d + e] = acc[i][4 * c + e];
+                        for (int e = 0; e < 4; ++e) rec[2 * a.rec_rows + m * a.hd + d + e] = (e & 1) ? acc[i][2 * c + e / 2].y : acc[i][2 * c + e / 2].x;
                 }
             } else {
                 const long long o = ((long long)(g.r0 + tok) * a.n_qh + hh.first + h) * a.hd;
@@ -193,7 +210,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                     const int d = 64 * c + tx * 4;
                     if (d < a.hd)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) store_as(a.out, o + d + e, a.q_dtype, acc[i][4 * c + e] / sum[i]);
+                        for (int e = 0; e < 4; ++e) store_as(a.out, o + d + e, a.q_dtype, ((e & 1) ? acc[i][2 * c + e / 2].y : acc[i][2 * c + e / 2].x) / sum[i]);
                 }
             }
         }
@@ -365,6 +382,7 @@ extern "C" DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtyp
     int grid = 0;
     cudaError_t e = chunk_tc_supported(a) ? launch_chunk_tc(a, &grid, s) : launch_chunk_simt(a, &grid, s);
     if (e == cudaSuccess)
-        e = launch_ex(chunk_join_kernel, dim3(grid, kCjShares), dim3(kCjThreads), 0, s, true, a);
+        e = launch_ex(chunk_join_kernel, dim3(grid, std::min(kCjShares, (a.rec_rows + kCjThreads / 32 - 1) / (kCjThreads / 32))),
+                      dim3(kCjThreads), 0, s, true, a);
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
 }

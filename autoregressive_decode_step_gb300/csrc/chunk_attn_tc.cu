@@ -179,24 +179,6 @@ __device__ __forceinline__ float ct_exp2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-// a * b + c and a + b, two numbers at a time.
-__device__ __forceinline__ float2 ct_fma2(float2 a, float2 b, float2 c) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y, z;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return r;
-}
-__device__ __forceinline__ float2 ct_add2(float2 a, float2 b) {
-    float2 r;
-    asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-        : "=f"(r.x), "=f"(r.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return r;
-}
 // bf16 pair, a in the low half.
 __device__ __forceinline__ uint32_t ct_pack(float a, float b) {
     uint32_t r;
@@ -558,9 +540,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (one) seg_done(seg);
                 uint32_t ks, vs;
                 const int stride = turns ? 2 : 1, mine = turns ? (int)w : 0;  // steps mine, mine + stride, ...
-                // (fp32 q: one barrier for both parts, whose next phase only this
-                // part's S holds back; without a step here it may have passed)
-                if (PARTS == 1 || mine < nb) ct_wait(&sh.q_full[PARTS == 1 ? w : 0], seg & 1, dead, a.err);
+                // (also where this part has no step: a barrier tells two phases
+                // apart, so each is awaited, and q_empty below lets the next come)
+                ct_wait(&sh.q_full[PARTS == 1 ? w : 0], seg & 1, dead, a.err);
                 for (int j = 0; j < min(stride, nb); ++j) {
                     if (j != mine) {
                         pass();
@@ -796,15 +778,15 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         uint32_t p[16];
 #pragma unroll
                         for (int k = 0; k < 16; ++k) {
-                            float2 x = ct_fma2(make_float2(v[2 * k], v[2 * k + 1]), c2, mc2);
+                            float2 x = chunk_fma2(make_float2(v[2 * k], v[2 * k + 1]), c2, mc2);
                             x.x = ct_exp2(x.x);
                             x.y = ct_exp2(x.y);
-                            add[k & 1] = ct_add2(add[k & 1], x);
+                            add[k & 1] = chunk_add2(add[k & 1], x);
                             if (PARTS == 1) {
                                 p[k] = ct_pack(x.x, x.y);
                             } else {
-                                x = ct_add2(x, make_float2(-ct_top(x.x, cut1), -ct_top(x.y, cut1)));
-                                x = ct_add2(x, make_float2(-ct_top(x.x, cut2), -ct_top(x.y, cut2)));
+                                x = chunk_add2(x, make_float2(-ct_top(x.x, cut1), -ct_top(x.y, cut1)));
+                                x = chunk_add2(x, make_float2(-ct_top(x.x, cut2), -ct_top(x.y, cut2)));
                                 p[k] = ct_top2(x.x, x.y);
                             }
                         }
@@ -847,6 +829,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             }
             if (PARTS == 3) {  // this tile's S are all there: its q is free
                 const CtSeg &next = seg_get(seg + 1);
+                for (int u = 0; u < 2; ++u) ct_wait(&sh.q_empty[u], seg & 1, dead, a.err);
                 if (next.nb) load_q(next);
             }
 

@@ -547,3 +547,146 @@ def test_a_serving_loop(A, cache, qt, graph):
                 assert np.sqrt(np.mean((got - ref) ** 2)) <= 4 * t * np.sqrt(np.mean(vv ** 2))
             r += m[s]
         cached += new
+
+
+# ------------------------------------------------- larger and longer batches
+def attn_reference_fast(q, k, v, table, starts, total, bt, nq, nkv, hd, scale):
+    """attn_reference in matrices on the GPU (still 64 bits), for batches too large for its loops."""
+    out = torch.zeros(q.shape[0], nq, hd, dtype=torch.float64, device="cuda")
+    d, vmax = torch.zeros(q.shape[0], nq, 1, dtype=torch.float64), torch.zeros(q.shape[0], nq, 1, dtype=torch.float64)
+    q, k, v, table = q.cuda(), k.cuda(), v.cuda(), table.cuda()
+    for s in range(len(total)):
+        n, L = starts[s + 1] - starts[s], total[s]
+        if n == 0:
+            continue
+        t = torch.arange(L, device="cuda")
+        at = table[s].long()[t // bt] * bt + t % bt
+        ks, vs = (x[at].double().view(L, nkv, hd).repeat_interleave(nq // nkv, 1) for x in (k, v))
+        qs = q[starts[s]:starts[s + 1]].double().view(n, nq, hd)
+        e = torch.einsum("jhd,thd->hjt", qs, ks) * scale
+        hidden = t[None, :] > (L - n + torch.arange(n, device="cuda"))[:, None]
+        w = torch.softmax(e.masked_fill(hidden, -math.inf), 2)
+        out[starts[s]:starts[s + 1]] = torch.einsum("hjt,thd->jhd", w, vs)
+        # bounds over all of the sequence's positions: no smaller than the row's own
+        mag = (qs.abs().sum(2) * ks.abs().amax()).cpu()
+        d[starts[s]:starts[s + 1], :, 0] = (hd + 4) * U * scale * mag
+        vmax[starts[s]:starts[s + 1]] = float(vs.abs().max())
+    return out.view(q.shape[0], -1).cpu(), d, vmax
+
+
+@pytest.mark.parametrize("qt", [BF16, F32])
+@pytest.mark.parametrize("kind", ["many short", "one long", "chunks", "narrow heads", "prompt"])
+def test_chunk_attention_on_larger_batches(A, kind, qt):
+    g = np.random.RandomState(7)
+    if kind == "many short":  # more sequences than a block has threads, some without rows
+        new = g.randint(0, 5, 900)
+        total, bt, nq, nkv, hd = new + g.randint(0, 200, 900), 8, 4, 2, 64
+        total = np.maximum(total, 1)
+    elif kind == "one long":  # a tile shared by most of the CTAs
+        new, total, bt, nq, nkv, hd = np.array([3]), np.array([30011]), 32, 8, 2, 128
+    elif kind == "chunks":
+        new = np.array([1, 257, 1, 64, 65, 1, 129, 0, 300, 1])
+        total, bt, nq, nkv, hd = new + np.array([2000, 700, 1, 0, 63, 128, 512, 9, 1111, 4095]), 16, 32, 8, 128
+    elif kind == "narrow heads":
+        new = g.randint(1, 90, 40)
+        total, bt, nq, nkv, hd = new + g.randint(0, 900, 40), 64, 14, 2, 64
+    else:
+        new, total, bt, nq, nkv, hd = np.array([1537]), np.array([1600]), 16, 8, 1, 128
+    new, total = new.tolist(), total.tolist()
+    starts = np.concatenate([[0], np.cumsum(new)]).tolist()
+    k, v, table, width, _ = pool(new, total, bt, nkv, hd, BF16, seed=3)
+    q = torch.randn(starts[-1], nq * hd, generator=torch.Generator().manual_seed(9)).to(qt)
+    scale = 1.0 / math.sqrt(hd)
+    got, ws = run_attn(A, q, k, v, table, starts, total, bt, nq, nkv, hd, scale, width)
+    assert A.ds_workspace_error(ws) == 0
+    want, d, vmax = attn_reference_fast(q, k, v, table, starts, total, bt, nq, nkv, hd, scale)
+    attn_near(got, want, d, vmax, max(total), nq, hd, qt == BF16)
+    for _ in range(3):  # the same bits from every run
+        again, _ = run_attn(A, q, k, v, table, starts, total, bt, nq, nkv, hd, scale, width, ws=ws)
+        assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("qt", [BF16, F32])
+def test_many_tiles_with_values_that_are_not_finite(A, qt):
+    """A non-finite value in the new rows of every sequence: tiles of both kinds, one after the other in every CTA, keep
+    theirs apart, and a clean batch through the same workspace afterwards is what it was before."""
+    g = np.random.RandomState(5)
+    n, bt, nq, nkv, hd = 60, 16, 8, 2, 128
+    new = g.randint(1, 120, n)
+    total = (new + g.randint(0, 300, n)).tolist()
+    new = new.tolist()
+    starts = np.concatenate([[0], np.cumsum(new)]).tolist()
+    k, v, table, width, _ = pool(new, total, bt, nkv, hd, BF16, seed=13)
+    q = torch.randn(starts[-1], nq * hd, generator=torch.Generator().manual_seed(2)).to(qt)
+    clean, ws = run_attn(A, q, k, v, table, starts, total, bt, nq, nkv, hd, 0.1, width)
+    v2 = v.clone()
+    at_row = [int(g.randint(0, m)) for m in new]
+    col = [int(g.randint(0, nkv * hd)) for _ in new]
+    bad = [(float("nan"), float("inf"), float("-inf"))[s % 3] for s in range(n)]
+    for s in range(n):
+        t = total[s] - new[s] + at_row[s]
+        v2[int(table[s, t // bt]) * bt + t % bt, col[s]] = bad[s]
+    got, _ = run_attn(A, q, k, v2, table, starts, total, bt, nq, nkv, hd, 0.1, width, ws=ws)
+    want = clean.clone().view(-1, nkv, nq // nkv, hd)
+    for s in range(n):
+        want[starts[s] + at_row[s]:starts[s + 1], col[s] // hd, :, col[s] % hd] = bad[s]
+    want = want.view_as(clean)
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    ok = ~torch.isnan(want)
+    assert torch.equal(got[ok], want[ok])
+    again, _ = run_attn(A, q, k, v, table, starts, total, bt, nq, nkv, hd, 0.1, width, ws=ws)
+    assert torch.equal(clean, again) and A.ds_workspace_error(ws) == 0
+
+
+def test_offsets_past_32_bits(A):
+    """A pool of more than 2^31 elements: rows at its end are written and read where they belong."""
+    nq, nkv, hd, bt = 16, 8, 128, 16
+    rows = (1 << 21) + 1024            # x 1,024 elements
+    k = torch.zeros(rows, nkv * hd, dtype=BF16, device="cuda")
+    v = torch.zeros(rows, nkv * hd, dtype=BF16, device="cuda")
+    T, width = 200, 13
+    blocks = rows // bt
+    table = torch.tensor([[blocks - 1 - i for i in range(width)]], dtype=torch.int32)
+    x = torch.randn(T, (nq + 2 * nkv) * hd, generator=torch.Generator().manual_seed(4))
+    t = torch.arange(T)
+    slots = (table[0].long()[t // bt] * bt + t % bt).to(torch.int32)
+    for qt in (BF16, F32):
+        q = torch.zeros(T, nq * hd, dtype=qt, device="cuda")
+        A.ds_rope_append(x.cuda(), x.shape[1], T, t.to(torch.int32).cuda(), 1, None, nq, nkv, hd, hd, 1e4, 0, q, k, v,
+                         rows, slots.cuda(), A.workspace(256))
+        at = slots.long().cuda()
+        assert torch.equal(v[at], x[:, (nq + nkv) * hd:].to(BF16).cuda())
+        assert not v[:rows - width * bt].any() and not k[:rows - width * bt].any()
+        out = torch.zeros_like(q)
+        ws = A.workspace(A.ds_chunk_attention_workspace_bytes(1, T, nq, nkv, hd))
+        A.ds_gqa_chunk_attn(q, T, i32([0, T]), i32([T]), 1, k, v, rows, table.cuda(), width, bt, nq, nkv, hd, 0.1, out, ws)
+        want, d, vmax = attn_reference_fast(q, k, v, table, [0, T], [T], bt, nq, nkv, hd, 0.1)
+        attn_near(out, want, d, vmax, T, nq, hd, qt == BF16)
+        assert A.ds_workspace_error(ws) == 0
+
+
+def test_two_captured_graphs_replayed_at_once(A):
+    """Two captured calls with a workspace each, replayed on two streams without waiting for one another."""
+    new, total, bt, nq, nkv, hd = [1, 90, 1, 1], [1500, 333, 4000, 17], 16, 32, 8, 128
+    starts = [0, 1, 91, 92, 93]
+    k, v, table, width, _ = pool(new, total, bt, nkv, hd, BF16, 31)
+    k, v, table = k.cuda(), v.cuda(), table.cuda()
+    st, ln = i32(starts), i32(total)
+    calls = []
+    for qt in (BF16, F32):
+        q = torch.randn(93, nq * hd, device="cuda").to(qt)
+        want, _ = run_attn(A, q, k, v, table, starts, total, bt, nq, nkv, hd, 0.09, width)
+        out, ws = torch.zeros_like(q), A.workspace(A.ds_chunk_attention_workspace_bytes(4, 93, nq, nkv, hd))
+        cg = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(cg):
+            for _ in range(5):
+                A.ds_gqa_chunk_attn(q, 93, st, ln, 4, k, v, k.shape[0], table, width, bt, nq, nkv, hd, 0.09, out, ws)
+        calls.append((cg, q, out, ws, want, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for cg, _, _, _, _, s in calls:
+            with torch.cuda.stream(s):
+                cg.replay()
+    torch.cuda.synchronize()
+    for _, _, out, ws, want, _ in calls:
+        assert torch.equal(out, want) and A.ds_workspace_error(ws) == 0
