@@ -62,8 +62,11 @@ constexpr int kCtAhead = 8;      // steps one part may be ahead of the other, an
 constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 // Weights of the work split (chunk_attn.cuh): a K/V step of both parts takes
 // about 1.5 times as long as one of a tile that takes turns; beginning and
-// ending a tile takes about as long as two steps.
-constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kCtPiece = 512;
+// ending a tile takes about as long as two steps, with fp32 q as four (swept
+// from 256 to 2048: 64 single fp32 tokens 158 us at 256, 148 at 512, 138 at
+// 1024, 146 at 2048; a bf16 prompt of 8192 464, 446, 452, 470).
+constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kCtTileCostF32 = 2 * 512;
+constexpr int kCtPiece = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
 constexpr int kCtSmall = 3072;      // barriers, segments, notes
@@ -972,7 +975,7 @@ cudaError_t launch_chunk_tc(ChunkArgs &a, int *grid, cudaStream_t stream) {
     a.half_tokens = a.q_dtype == DS_BF16 ? a.tile_tokens / 2 : a.tile_tokens;
     a.w_half = kCtWeightTurns;
     a.w_full = kCtWeightShared;
-    a.tile_cost = kCtTileCost;
+    a.tile_cost = a.q_dtype == DS_BF16 ? kCtTileCost : kCtTileCostF32;
     a.piece = kCtPiece;
     *grid = sm_count();
     CtMaps maps = {};
