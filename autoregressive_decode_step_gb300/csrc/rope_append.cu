@@ -12,12 +12,20 @@
 // before the rest is rounded to fp32, so sine and cosine are those of an
 // argument within an eighth of a turn.
 //
-// Bound by bytes (each element read once and written once).  A thread keeps
-// the same places of a row for all the rows of its block, so what an item is
-// is worked out once; the next row's elements, slot and position are requested
-// before this row's are used, and a row's angles are formed once, in shared
-// memory, for all its heads.  (One block per row, everything worked out and
-// requested anew: 60 us for 8,192 bf16 rows of 32 + 16 heads of 128, 3.4 TB/s.)
+// Bound by bytes (each element read once and written once).  Two kernels:
+//  - few rows: a thread keeps the same place of a row for all the rows of its
+//    block, so what it does there is worked out once, and the next row's
+//    element, slot and position are requested before this row's are used;
+//  - from kRaBulkRows on: whole rows come through a shared-memory ring by bulk
+//    copies, so the bytes in flight do not hang on the threads that wait for
+//    them.
+// A row's angles are formed once, in shared memory, for all its heads.
+// Measured, bf16 rows of 32 + 8 + 8 heads of 128 (24,576 bytes in and out):
+//   rows          512    1,001   2,048   4,096   8,192
+//   first        4.5 us  7.3    13.2    24.0    43.9
+//   second       4.8     6.6    11.2    18.0    35.2   (5.7 TB/s)
+// (fp32 rows 4.8 / 5.6 us at 512, 53.2 / 48.0 at 8,192; one block per row with
+// everything worked out anew, the first version: 60 us at 8,192.)
 #include <algorithm>
 #include <cmath>
 
@@ -29,6 +37,7 @@ namespace ds {
 
 constexpr int kRaThreads = 256;
 constexpr int kRaBlocksPerSm = 4;
+constexpr int kRaBulkRows = 2048;
 constexpr int kRaMaxHd = 256;
 constexpr int kRaMaxAxes = 8;
 
@@ -105,8 +114,41 @@ __device__ __forceinline__ void ra_store(__nv_bfloat16 *p, const float (&v)[8]) 
 __device__ __forceinline__ void ra_store(float *p, const float (&v)[1]) { *p = v[0]; }
 __device__ __forceinline__ void ra_store(__nv_bfloat16 *p, const float (&v)[1]) { *p = __float2bfloat16_rn(v[0]); }
 
+__device__ __forceinline__ void ra_get8(const float *p, float (&v)[8]) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void ra_get8(const __nv_bfloat16 *p, float (&v)[8]) {
+    widen16(*reinterpret_cast<const uint4 *>(p), v);
+}
+
+// Rotate W pairs.  Half-split: pair e is (u[e], w[e]).  Interleaved: u holds
+// pairs 0 .. W/2 - 1, w the others (W 1: the pair's two elements).
+template <int W>
+__device__ __forceinline__ void ra_rotate(const float (&u)[W], const float (&w)[W], const float (&c)[W],
+                                          const float (&s)[W], bool split, float (&y0)[W], float (&y1)[W]) {
+    if (split || W == 1) {
+#pragma unroll
+        for (int e = 0; e < W; ++e) {
+            y0[e] = u[e] * c[e] - w[e] * s[e];
+            y1[e] = w[e] * c[e] + u[e] * s[e];
+        }
+    } else {
+        constexpr int h = W / 2;
+#pragma unroll
+        for (int e = 0; e < h; ++e) {
+            y0[2 * e] = u[2 * e] * c[e] - u[2 * e + 1] * s[e];
+            y0[2 * e + 1] = u[2 * e + 1] * c[e] + u[2 * e] * s[e];
+            y1[2 * e] = w[2 * e] * c[h + e] - w[2 * e + 1] * s[h + e];
+            y1[2 * e + 1] = w[2 * e + 1] * c[h + e] + w[2 * e] * s[h + e];
+        }
+    }
+}
+
 // Items of a row that a thread has: W pairs of a q or k head (two chunks of W
 // elements), or W elements as they are (the tail of a q or k head, or v).
+// (Two a thread: half the blocks stay resident, 47 us against 44 at 8,192.)
 constexpr int kRaItems = 1;
 
 template <typename XT, typename QT, typename KT, int W, int P>
@@ -199,22 +241,7 @@ __global__ void __launch_bounds__(kRaThreads)
                 c[0] = cosine[buf][pair[k]];
                 s[0] = sine[buf][pair[k]];
             }
-            if (split || W == 1) {
-#pragma unroll
-                for (int e = 0; e < W; ++e) {
-                    y0[k][e] = u[e] * c[e] - w[e] * s[e];
-                    y1[k][e] = w[e] * c[e] + u[e] * s[e];
-                }
-            } else {
-#pragma unroll
-                for (int e = 0; e < W / 2; ++e) {  // pairs 0 .. 3 in the first chunk, 4 .. 7 in the second
-                    constexpr int h = W / 2;
-                    y0[k][2 * e] = u[2 * e] * c[e] - u[2 * e + 1] * s[e];
-                    y0[k][2 * e + 1] = u[2 * e + 1] * c[e] + u[2 * e] * s[e];
-                    y1[k][2 * e] = w[2 * e] * c[h + e] - w[2 * e + 1] * s[h + e];
-                    y1[k][2 * e + 1] = w[2 * e + 1] * c[h + e] + w[2 * e] * s[h + e];
-                }
-            }
+            ra_rotate(u, w, c, s, split, y0[k], y1[k]);
         }
         if (slot_n >= 0) fetch(next);
 #pragma unroll
@@ -235,11 +262,144 @@ __global__ void __launch_bounds__(kRaThreads)
     }
 }
 
+// Many rows: rows of x through a ring of bulk copies; what an item is stands in
+// a table in shared memory.  A row of padding is fetched and not looked at.
+struct RaItem {
+    int src, apart, pair, dst;  // dst: offset within its buffer's row, x 4, + 0 q, 1 k, 2 v
+};
+constexpr int kRaStages = 3;
+constexpr int kRaBulkBlocks = 4;         // blocks an SM, registers and shared memory permitting
+constexpr int kRaBulkSmem = 100 * 1024;  // most shared memory a block takes
+
+template <typename XT, typename QT, typename KT, int P>
+__global__ void __launch_bounds__(kRaThreads, 4)
+    rope_append_bulk_kernel(const __grid_constant__ RopeAppendArgs a, const __grid_constant__ RopeTurns<P> turns,
+                            int n_items, int row_bytes) {
+    extern __shared__ __align__(128) unsigned char ra_smem[];
+    __shared__ __align__(16) float cosine[2][P], sine[2][P];
+    __shared__ uint64_t full[kRaStages];
+    RaItem *items = reinterpret_cast<RaItem *>(ra_smem + (size_t)kRaStages * row_bytes);
+    const int half = a.rot >> 1, hd = a.hd, n_rot = a.n_qh + a.n_kvh, tid = threadIdx.x;
+    const bool split = a.layout == DS_ROPE_HALF_SPLIT;
+    const int step = gridDim.x, first = blockIdx.x;
+    const uint64_t policy = policy_evict_first();
+    auto fetch = [&](int n) {  // the block's n-th row, by one thread
+        const long long row = first + (long long)n * step;
+        if (row >= a.n_rows) return;
+        mbar_arrive_expect_tx(&full[n % kRaStages], (uint32_t)row_bytes);
+        bulk_g2s(ra_smem + (size_t)(n % kRaStages) * row_bytes, static_cast<const XT *>(a.x) + row * a.row_stride,
+                 (uint32_t)row_bytes, &full[n % kRaStages], policy);
+    };
+    if (tid == 0) {
+        for (int i = 0; i < kRaStages; ++i) mbar_init(&full[i], 1);
+        fence_mbarrier_init();
+        for (int i = 0; i < kRaStages - 1; ++i) fetch(i);
+    }
+    const int per_rot = half / 8, per_cp = (hd - a.rot) / 8, per_v = hd / 8;
+    const int n1 = n_rot * per_rot, n2 = n1 + n_rot * per_cp;
+    for (int i = tid; i < n_items; i += kRaThreads) {
+        RaItem it = {0, 0, 0, 0};
+        int head, d;
+        if (i < n1) {
+            head = i / per_rot;
+            it.pair = (i % per_rot) * 8;
+            d = split ? it.pair : 2 * it.pair;
+            it.apart = split ? half : 8;
+        } else if (i < n2) {
+            head = (i - n1) / per_cp;
+            d = a.rot + ((i - n1) % per_cp) * 8;
+        } else {
+            head = n_rot + (i - n2) / per_v;
+            d = ((i - n2) % per_v) * 8;
+        }
+        it.src = head * hd + d;
+        const int to = head < a.n_qh ? 0 : head < n_rot ? 1 : 2;
+        it.dst = ((head - (to == 0 ? 0 : to == 1 ? a.n_qh : n_rot)) * hd + d) * 4 + to;
+        items[i] = it;
+    }
+    const int axis_row = tid < half ? turns.axis[tid] : 0;
+    const unsigned long long turn = tid < half ? turns.turn[tid] : 0;
+    auto pos_of = [&](int row) { return tid < half ? __ldg(a.positions + (long long)axis_row * a.n_rows + row) : 0; };
+    int slot = __ldg(a.slots + first), pos = pos_of(first);
+    for (int n = 0, r = first; r < a.n_rows; r += step, ++n) {
+        const int buf = n & 1, next = r + step;
+        int slot_n = -1, pos_n = 0;
+        if (next < a.n_rows) {
+            slot_n = __ldg(a.slots + next);
+            pos_n = pos_of(next);
+        }
+        if (slot >= 0 && tid < half) {
+            const float2 t = ra_cos_sin((unsigned long long)(unsigned)pos * turn);
+            cosine[buf][tid] = t.x;
+            sine[buf][tid] = t.y;
+        }
+        // (also: every thread is done with the row before, whose stage is free)
+        const int bad = __syncthreads_or(slot >= 0 && (pos < 0 || slot >= a.cache_rows));
+        if (tid == 0) {
+            if (bad) flag_error(a.err, DS_ERR_POSITION);
+            fetch(n + kRaStages - 1);
+        }
+        const bool there = mbar_wait(&full[n % kRaStages], (n / kRaStages) & 1, a.err);
+        if (there && slot >= 0 && !bad) {
+            const XT *x = reinterpret_cast<const XT *>(ra_smem + (size_t)(n % kRaStages) * row_bytes);
+            for (int i = tid; i < n_items; i += kRaThreads) {
+                const int4 e4 = *reinterpret_cast<const int4 *>(items + i);
+                const RaItem it = {e4.x, e4.y, e4.z, e4.w};
+                float u[8], w[8];
+                ra_get8(x + it.src, u);
+                const int to = it.dst & 3, at = it.dst >> 2;
+                QT *q = static_cast<QT *>(a.q) + (long long)r * a.n_qh * hd + at;
+                KT *k = static_cast<KT *>(to == 1 ? a.k_cache : a.v_cache) + (long long)slot * a.n_kvh * hd + at;
+                if (it.apart) {
+                    ra_get8(x + it.src + it.apart, w);
+                    float c[8], s[8], y0[8], y1[8];
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        const float4 c4 = *reinterpret_cast<const float4 *>(&cosine[buf][it.pair + e]);
+                        const float4 s4 = *reinterpret_cast<const float4 *>(&sine[buf][it.pair + e]);
+                        c[e] = c4.x; c[e + 1] = c4.y; c[e + 2] = c4.z; c[e + 3] = c4.w;
+                        s[e] = s4.x; s[e + 1] = s4.y; s[e + 2] = s4.z; s[e + 3] = s4.w;
+                    }
+                    ra_rotate(u, w, c, s, split, y0, y1);
+                    if (to == 0) {
+                        ra_store(q, y0);
+                        ra_store(q + it.apart, y1);
+                    } else {
+                        ra_store(k, y0);
+                        ra_store(k + it.apart, y1);
+                    }
+                } else if (to == 0) {
+                    ra_store(q, u);
+                } else {
+                    ra_store(k, u);
+                }
+            }
+        }
+        slot = slot_n;
+        pos = pos_n;
+    }
+}
+
+template <typename XT, typename QT, typename KT, int P>
+static cudaError_t launch_ra_bulk(const RopeAppendArgs &a, const RopeTurns<P> &t, int items, int row_bytes, int smem,
+                                  cudaStream_t s) {
+    const cudaError_t e = cudaFuncSetAttribute((const void *)rope_append_bulk_kernel<XT, QT, KT, P>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int per_sm = std::min(kRaBulkBlocks, 220 * 1024 / (smem + 2 * 1024));
+    return launch_ex(rope_append_bulk_kernel<XT, QT, KT, P>, dim3(std::min(a.n_rows, per_sm * sm_count())),
+                     dim3(kRaThreads), smem, s, false, a, t, items, row_bytes);
+}
+
 template <typename XT, typename QT, typename KT, int P>
 static cudaError_t launch_ra(const RopeAppendArgs &a, const RopeTurns<P> &t, bool vec, cudaStream_t s) {
     const int w = vec ? 8 : 1;
     const int items = (a.n_qh + a.n_kvh) * (a.rot / 2 / w + (a.hd - a.rot) / w) + a.n_kvh * (a.hd / w);
     const int ny = (items + kRaItems * kRaThreads - 1) / (kRaItems * kRaThreads);
+    const int row_bytes = (a.n_qh + 2 * a.n_kvh) * a.hd * (int)sizeof(XT);
+    const long long smem = (long long)kRaStages * row_bytes + (long long)items * sizeof(RaItem);
+    if (vec && a.n_rows >= kRaBulkRows && smem <= kRaBulkSmem)
+        return launch_ra_bulk<XT, QT, KT, P>(a, t, items, row_bytes, (int)smem, s);
     // as many blocks as stay resident; a block with several rows keeps loads in flight
     const int nx = std::min(a.n_rows, std::max(1, kRaBlocksPerSm * sm_count() / ny));
     return vec ? launch_ex(rope_append_kernel<XT, QT, KT, 8, P>, dim3(nx, ny), dim3(kRaThreads), 0, s, false, a, t)

@@ -346,15 +346,15 @@ DS_API size_t ds_rope_append_workspace_bytes(void);
  *   positions: device int32 [n_axes][n_rows]; pair_axis: HOST bytes
  *   [rot_dim / 2], each < n_axes (NULL for one axis), read before the call
  *   returns; slots: device int32 [n_rows].
- * A row with a negative slot is padding: nothing of it is read or written
- * (its q_out stays).  A slot past the cache or a negative position skips the
+ * A row with a negative slot is padding: it may hold anything and nothing is
+ * written for it (its q_out stays).  A slot past the cache or a negative position skips the
  * row and flags DS_ERR_POSITION.  Two rows with one slot: either may stay.
  * qkv_len (562) must reach the last row's end and row_stride its width; q_len
  * must be n_rows * n_qh * head_dim (563).  head_dim <= 256, rot_dim even and
  * <= head_dim, n_axes <= 8, base finite and > 0, qkv and q_out not
  * overlapping (577).  Rows with 16-byte aligned buffers, row_stride and
- * head_dim multiples of 8 and rot_dim of 16 move 16 bytes at a time; others
- * one element. */
+ * head_dim multiples of 8 and rot_dim of 16 move 16 bytes at a time (whole
+ * rows by bulk copies from 2,048 rows on); others one element. */
 DS_API int ds_rope_append(const void *qkv, int64_t qkv_len, int qkv_dtype, int64_t row_stride,
                           int64_t n_rows, const int32_t *positions, int n_axes, const uint8_t *pair_axis,
                           int n_qh, int n_kvh, int head_dim, int rot_dim, double base, int layout,

@@ -187,6 +187,10 @@ def near(got, want, mag):
     (5, 2, 1, 6, 2, 0, 2, F32, F32, BF16, 3),          # odd strides
     (9, 2, 2, 256, 256, 0, 3, BF16, BF16, BF16, 0),
     (300, 8, 1, 128, 64, 0, 8, BF16, F32, BF16, 24),
+    (2100, 4, 2, 64, 64, 0, 3, BF16, BF16, BF16, 8),   # many rows: the shared-memory ring
+    (2500, 5, 1, 128, 96, 1, 2, F32, BF16, F32, 0),
+    (4001, 1, 1, 16, 16, 0, 1, F32, F32, BF16, 0),
+    (2048, 2, 1, 40, 24, 0, 1, BF16, F32, BF16, 0),    # many rows of single elements
 ])
 @pytest.mark.parametrize("maxpos", [64, 2 ** 31 - 1])
 def test_rope_append_matches_fp64(A, rows, nq, nkv, hd, rot, layout, axes, xt, qt, kt, extra, maxpos):
@@ -233,6 +237,24 @@ def test_rope_append_with_one_axis_is_the_token_rotation(A):
     bound = 16 * U * 2 * float(x.abs().max())
     assert (q[0] - q1).abs().max() <= bound and (k[0] - k1).abs().max() <= bound
     assert torch.equal(v[0], x[0, 5120:])
+
+
+def test_rope_append_flags_and_skips_bad_rows_among_many(A):
+    n = 3000
+    x = torch.randn(n, 6 * 64, device="cuda")
+    x[5] = float("nan")  # padding may hold anything
+    pos, slots = torch.arange(n, dtype=torch.int32), torch.arange(n, dtype=torch.int32)
+    slots[5], slots[700], pos[2999] = -1, n, -4
+    q, k = torch.full((n, 128), 7.0, device="cuda"), torch.full((n, 128), 7.0, device="cuda")
+    v, ws = k.clone(), A.workspace(256)
+    A.ds_rope_append(x, 6 * 64, n, pos.cuda(), 1, None, 2, 2, 64, 64, 1e4, 0, q, k, v, n, slots.cuda(), ws)
+    assert A.ds_workspace_error(ws) == A.DS_ERR_POSITION
+    out = [5, 700, 2999]
+    rest = torch.ones(n, dtype=torch.bool)
+    rest[out] = False
+    rest = rest.cuda()
+    assert (q[out] == 7).all() and (k[out] == 7).all() and (v[out] == 7).all()
+    assert torch.equal(v[rest], x[rest, 256:]) and not (q[rest] == 7).any()
 
 
 def test_rope_append_flags_and_skips_bad_rows(A):
