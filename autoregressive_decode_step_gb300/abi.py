@@ -290,6 +290,13 @@ def _i32(t, n, name):
     return t.data_ptr()
 
 
+def _here(ws):
+    """Address of a workspace, which has to be on the current device: the launch goes there."""
+    if not ws.is_cuda or ws.get_device() != torch._C._cuda_getDevice():
+        raise ValueError("the buffers have to be on the current CUDA device")
+    return ws.data_ptr()
+
+
 def _dense(t, n, name):
     """Address of a contiguous tensor of at least n elements."""
     if not t.is_contiguous() or t.numel() < n:
@@ -313,7 +320,7 @@ def ds_paged_plan(cached_lens, new_lens, n_seqs, free_blocks, block_tokens, cach
                             max_blocks_per_seq, _i32(row_starts, n_seqs + 1, "row_starts"),
                             _i32(seq_lens, n_seqs, "seq_lens"), _i32(row_seq, max_rows, "row_seq"),
                             _i32(positions, max_rows, "positions"), _i32(slots, max_rows, "slots"), max_rows,
-                            _i32(n_taken, 1, "n_taken"), ws.data_ptr(), nbytes(ws), stream_handle(stream)),
+                            _i32(n_taken, 1, "n_taken"), _here(ws), nbytes(ws), stream_handle(stream)),
           "ds_paged_plan")
 
 
@@ -329,16 +336,17 @@ def ds_rope_append(qkv, row_stride, n_rows, positions, n_axes, pair_axis, n_qh, 
         if pair_axis.dtype.char != "B" or pair_axis.size < rot_dim // 2:
             raise ValueError("pair_axis: a uint8 array of rot_dim / 2 axes is needed")
         pair_axis = pair_axis.tobytes()  # (the array's .ctypes takes 2 us to build)
-    if v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache: one dtype is needed")
+    if v_cache.dtype != k_cache.dtype or qkv.stride(-1) != 1:
+        raise ValueError("k_cache and v_cache need one dtype, qkv's rows no gaps between elements")
     n_kv = cache_rows * n_kvh * head_dim
     # qkv may be a view of wider rows: its reach is what the storage holds from its start on
     reach = qkv.untyped_storage().nbytes() // qkv.element_size() - qkv.storage_offset()
     check(lib.ds_rope_append(qkv.data_ptr(), reach, dtype_code(qkv), row_stride, n_rows,
                              _i32(positions, n_axes * n_rows, "positions"), n_axes,
-                             pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout, _dense(q_out, q_out.numel(), "q_out"), q_out.numel(), dtype_code(q_out),
+                             pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout, _dense(q_out, 0, "q_out"),
+                             q_out.numel(), dtype_code(q_out),
                              _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"), dtype_code(k_cache),
-                             cache_rows, _i32(slots, n_rows, "slots"), ws.data_ptr(), nbytes(ws),
+                             cache_rows, _i32(slots, n_rows, "slots"), _here(ws), nbytes(ws),
                              stream_handle(stream)), "ds_rope_append")
 
 
@@ -360,7 +368,7 @@ def ds_gqa_chunk_attn(q, n_rows, row_starts, seq_lens, n_seqs, k_cache, v_cache,
                                 None if block_table is None else _i32(block_table, n_seqs * max_blocks_per_seq,
                                                                       "block_table"), max_blocks_per_seq,
                                 block_tokens, n_qh, n_kvh, head_dim, scale, _dense(out, 0, "out"), out.numel(),
-                                ws.data_ptr(), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
+                                _here(ws), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
 
 
 def ds_argmax_workspace_bytes(n_rows, n):

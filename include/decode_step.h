@@ -351,8 +351,8 @@ DS_API size_t ds_rope_append_workspace_bytes(void);
  * row and flags DS_ERR_POSITION.  Two rows with one slot: either may stay.
  * qkv_len (562) must reach the last row's end and row_stride its width; q_len
  * must be n_rows * n_qh * head_dim (563).  head_dim <= 256, rot_dim even and
- * <= head_dim, n_axes <= 8, base finite and > 0, qkv and q_out not
- * overlapping (577).  Rows with 16-byte aligned buffers, row_stride and
+ * <= head_dim, n_axes <= 8, base finite and > 0 (577).  No output may overlap
+ * qkv or another output (qkv and q_out: 577).  Rows with 16-byte aligned buffers, row_stride and
  * head_dim multiples of 8 and rot_dim of 16 move 16 bytes at a time (whole
  * rows by bulk copies from 2,048 rows on); others one element. */
 DS_API int ds_rope_append(const void *qkv, int64_t qkv_len, int qkv_dtype, int64_t row_stride,

@@ -350,6 +350,7 @@ SHAPES = [
     ([6], [150], 64, 150, 1, 64),                      # 150 heads share one
     ([300], [1300], 128, 4, 1, 128),
     ([3, 4], [2, 4], 16, 8, 2, 128),                   # a row that attends nothing
+    ([2, 3, 150], [0, 3, 20], 16, 4, 2, 64),           # a sequence of length zero, most of a chunk in front of position 0
 ]
 
 

@@ -137,3 +137,10 @@ def test_the_binding_refuses_other_integer_types_and_strides(abi):
     with pytest.raises(ValueError):  # out of another type than q
         abi.ds_gqa_chunk_attn(q, 1, t32, t32, 1, kv, kv, 16, None, 1, 16, 8, 2, 64, 0.125, q.bfloat16(), ws, stream=0)
     assert ctypes.sizeof(ctypes.c_void_p) == 8
+
+
+def test_the_binding_refuses_a_workspace_that_is_not_on_the_device(abi):
+    t32 = torch.zeros(64, dtype=torch.int32)
+    with pytest.raises(ValueError):
+        abi.ds_paged_plan(t32, t32, 1, t32, 16, 128, t32, 8, t32, t32, t32, t32, t32, 8, t32,
+                          torch.zeros(256, dtype=torch.uint8), stream=None)
