@@ -221,60 +221,61 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
 // Join the records of the split tiles: block (c, y) takes its share of the
 // pairs of the tile whose first contributor CTA c was.
 //   M = max_c m_c,  out = sum_c 2^(m_c - M) acc_c / sum_c 2^(m_c - M) l_c
-// A warp takes a pair at a time (lane l: four dims), four records' loads in
-// flight; the latency of L2 bounds it, so the pairs are spread over the grid.
+// A thread takes four dims of a pair, four records' loads in flight; the
+// latency of L2 bounds it, so the items are spread over the grid.  (A warp per
+// pair, four pairs one after the other: 12 us behind the ragged chunks' first
+// launch, more than half of what that takes.)
 constexpr int kCjThreads = 256;
-constexpr int kCjShares = 8;
+constexpr int kCjShares = 16;
 __global__ void __launch_bounds__(kCjThreads) chunk_join_kernel(const __grid_constant__ ChunkArgs a) {
     grid_dependency_wait();
     const ChunkJoin t = a.joins[blockIdx.x];
-    const int lane = threadIdx.x & 31;
     const ChunkHeads hh = chunk_heads(a, t.part);
     const size_t rec_floats = (size_t)a.rec_rows * (a.hd + 2);
     const float *rec0 = a.partials + ((size_t)t.first * 2 + t.first_slot) * rec_floats;
-    for (int m = blockIdx.y * (kCjThreads / 32) + (threadIdx.x >> 5); m < t.pairs; m += gridDim.y * (kCjThreads / 32)) {
+    const int per = a.hd / 4;
+    for (int i = blockIdx.y * kCjThreads + threadIdx.x; i < t.pairs * per; i += gridDim.y * kCjThreads) {
+        const int m = i / per, d = (i % per) * 4;
         const int tok = m / a.part_heads, head = m % a.part_heads;
         if (head >= hh.count) continue;
-        for (int d = lane * 4; d < a.hd; d += 128) {
-            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float M = -INFINITY, L = 0.0f;
-            for (int c0 = t.first; c0 <= t.last; c0 += 4) {
-                float2 ml[4];
-                float4 v[4];
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        float M = -INFINITY, L = 0.0f;
+        for (int c0 = t.first; c0 <= t.last; c0 += 4) {
+            float2 ml[4];
+            float4 v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int c = min(c0 + k, t.last);
-                    const float *rec = c == t.first ? rec0 : a.partials + (size_t)c * 2 * rec_floats;
-                    ml[k] = __ldcg(reinterpret_cast<const float2 *>(rec + 2 * m));
-                    v[k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
-                }
-                float top = M;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
-                const float keep = M == top ? 1.0f : exp2f(M - top);  // (equal: both may be -inf)
-                M = top;
-                L *= keep;
-                acc.x *= keep;
-                acc.y *= keep;
-                acc.z *= keep;
-                acc.w *= keep;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    if (c0 + k > t.last) break;
-                    const float e = ml[k].x == top ? 1.0f : exp2f(ml[k].x - top);
-                    L = fmaf(ml[k].y, e, L);
-                    acc.x = fmaf(v[k].x, e, acc.x);
-                    acc.y = fmaf(v[k].y, e, acc.y);
-                    acc.z = fmaf(v[k].z, e, acc.z);
-                    acc.w = fmaf(v[k].w, e, acc.w);
-                }
+            for (int k = 0; k < 4; ++k) {
+                const int c = min(c0 + k, t.last);
+                const float *rec = c == t.first ? rec0 : a.partials + (size_t)c * 2 * rec_floats;
+                ml[k] = __ldcg(reinterpret_cast<const float2 *>(rec + 2 * m));
+                v[k] = __ldcg(reinterpret_cast<const float4 *>(rec + 2 * a.rec_rows + (size_t)m * a.hd + d));
             }
-            const long long o = ((long long)(t.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
-            store_as(a.out, o, a.q_dtype, acc.x / L);
-            store_as(a.out, o + 1, a.q_dtype, acc.y / L);
-            store_as(a.out, o + 2, a.q_dtype, acc.z / L);
-            store_as(a.out, o + 3, a.q_dtype, acc.w / L);
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, ml[k].x);
+            const float keep = M == top ? 1.0f : exp2f(M - top);  // (equal: both may be -inf)
+            M = top;
+            L *= keep;
+            acc.x *= keep;
+            acc.y *= keep;
+            acc.z *= keep;
+            acc.w *= keep;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (c0 + k > t.last) break;
+                const float e = ml[k].x == top ? 1.0f : exp2f(ml[k].x - top);
+                L = fmaf(ml[k].y, e, L);
+                acc.x = fmaf(v[k].x, e, acc.x);
+                acc.y = fmaf(v[k].y, e, acc.y);
+                acc.z = fmaf(v[k].z, e, acc.z);
+                acc.w = fmaf(v[k].w, e, acc.w);
+            }
         }
+        const long long o = ((long long)(t.r0 + tok) * a.n_qh + hh.first + head) * a.hd + d;
+        store_as(a.out, o, a.q_dtype, acc.x / L);
+        store_as(a.out, o + 1, a.q_dtype, acc.y / L);
+        store_as(a.out, o + 2, a.q_dtype, acc.z / L);
+        store_as(a.out, o + 3, a.q_dtype, acc.w / L);
     }
 }
 
@@ -382,7 +383,8 @@ extern "C" DS_API int ds_gqa_chunk_attn(const void *q, int64_t q_len, int q_dtyp
     int grid = 0;
     cudaError_t e = chunk_tc_supported(a) ? launch_chunk_tc(a, &grid, s) : launch_chunk_simt(a, &grid, s);
     if (e == cudaSuccess)
-        e = launch_ex(chunk_join_kernel, dim3(grid, std::min(kCjShares, (a.rec_rows + kCjThreads / 32 - 1) / (kCjThreads / 32))),
+        e = launch_ex(chunk_join_kernel,
+                      dim3(grid, std::min(kCjShares, (a.rec_rows * (a.hd / 4) + kCjThreads - 1) / kCjThreads)),
                       dim3(kCjThreads), 0, s, true, a);
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
 }
