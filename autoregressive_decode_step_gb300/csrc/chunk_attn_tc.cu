@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
+    grid_dependency_wait();  // everything up to here may run before the launch in front is through
     chunk_zero_empty_rows(a);
     ChunkWalk walk;
     walk.init(a, sh.red);  // synchronises the block
@@ -964,7 +965,7 @@ static cudaError_t launch_ct(const ChunkArgs &a, const CtMaps &maps, int grid, c
         if (e != cudaSuccess) return e;
         if (dev < 64) ready.fetch_or(bit);
     }
-    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(grid), dim3(kCtThreads), CtCfg<HD, PARTS>::kSmem, stream, false,
+    return launch_ex(chunk_tc_kernel<HD, PARTS>, dim3(grid), dim3(kCtThreads), CtCfg<HD, PARTS>::kSmem, stream, true,
                      a, maps);
 }
 
