@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
 
     chunk_zero_empty_rows(a);
     ChunkWalk walk;
-    walk.init(a, s_red);
+    walk.init<true>(a, s_red);
     allow_dependent_launch();
     flags |= walk.flags;
     if (tid == 0) a.joins[blockIdx.x].pairs = 0;

@@ -69,7 +69,7 @@ constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kC
 constexpr int kCtPiece = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
 constexpr int kCtMaxStages = 10;
-constexpr int kCtSmall = 3072;      // barriers, segments, notes
+constexpr int kCtSmall = 3 * 1024;     // barriers, segments, notes
 constexpr size_t kCtSmemLimit = 227 * 1024;
 constexpr float kCtLog2e = 1.4426950408889634f;
 constexpr float kCtLag = 8.0f;      // log2 of the growth that moves the reference maximum
@@ -91,7 +91,7 @@ struct CtMaps {
     int box_rows;
 };
 
-// The MMA warp runs its loop with all its lanes and one of them issues, by a
+// An MMA warp runs its loop with all its lanes and one of them issues, by a
 // predicate: addresses and descriptors then stay in uniform registers, where
 // the instruction wants them.  (From a branch of one lane each of them has to
 // be moved there first: about 100 cycles an MMA against the 64 it runs.)
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
     grid_dependency_wait();  // everything up to here may run before the launch in front is through
     chunk_zero_empty_rows(a);
     ChunkWalk walk;
-    walk.init(a, sh.red);  // synchronises the block
+    walk.init<false>(a, sh.red);  // synchronises the block
     // The joining launch may take its place as blocks of this one end; it
     // waits for the end of all before it reads.
     allow_dependent_launch();
