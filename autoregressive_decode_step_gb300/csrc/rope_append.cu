@@ -460,10 +460,18 @@ extern "C" DS_API int ds_rope_append(const void *qkv, int64_t qkv_len, int qkv_d
     for (int p = 0; pair_axis && p < rot_dim / 2; ++p)
         if (pair_axis[p] >= n_axes) return DS_BAD_ARGUMENT;
     const int xe = qkv_dtype == DS_BF16 ? 2 : 4, qe = q_dtype == DS_BF16 ? 2 : 4;
-    const uintptr_t x0 = (uintptr_t)qkv, x1 = x0 + (size_t)qkv_len * xe, q0 = (uintptr_t)q_out, q1 = q0 + (size_t)q_len * qe;
-    if (q0 < x1 && x0 < q1) return DS_BAD_ARGUMENT;  // blocks read a row while others write theirs
+    // Blocks read a row while others write theirs.  (To the last row's end:
+    // qkv_len may reach on, into a buffer that holds the outputs too.)
+    const uintptr_t x0 = (uintptr_t)qkv, x1 = x0 + (size_t)((n_rows - 1) * row_stride + cols) * xe;
+    const uintptr_t q0 = (uintptr_t)q_out, q1 = q0 + (size_t)q_len * qe;
+    if (q0 < x1 && x0 < q1) return DS_BAD_ARGUMENT;
     if (!workspace || workspace_bytes < kWsHeader) return DS_WORKSPACE_TOO_SMALL;
     if ((uintptr_t)workspace & 255) return DS_BAD_ARGUMENT;
+    const uintptr_t k0 = (uintptr_t)k_cache, v0 = (uintptr_t)v_cache;
+    const size_t cb = (size_t)cache_rows * n_kvh * head_dim * (kv_dtype == DS_BF16 ? 2 : 4);
+    if ((k0 < v0 + cb && v0 < k0 + cb) || (k0 < x1 && x0 < k0 + cb) || (v0 < x1 && x0 < v0 + cb) ||
+        (k0 < q1 && q0 < k0 + cb) || (v0 < q1 && q0 < v0 + cb))
+        return DS_BAD_ARGUMENT;
     RopeAppendArgs a = {};
     a.x = qkv;
     a.row_stride = row_stride;

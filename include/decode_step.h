@@ -309,7 +309,8 @@ DS_API size_t ds_paged_plan_workspace_bytes(void);
  *   [n_seqs]; row_seq, positions, slots: int32 [max_rows], all -1 behind the
  *   last row, so a batch padded to max_rows can be captured in a graph;
  *   n_taken: int32 [1], how many of free_blocks are used up.  No output may
- *   overlap an input or another output.
+ *   overlap an input or another output (577): cached_lens for the next step
+ *   is this one's seq_lens, in two buffers that take turns.
  * The lengths are not changed: the same call again gives the same answer.
  * A sequence with a negative length or one past its table row gets no rows
  * (DS_ERR_POSITION).  The first sequence whose rows pass max_rows or whose
@@ -348,11 +349,12 @@ DS_API size_t ds_rope_append_workspace_bytes(void);
  *   returns; slots: device int32 [n_rows].
  * A row with a negative slot is padding: it may hold anything and nothing is
  * written for it (its q_out stays).  A slot past the cache or a negative position skips the
- * row and flags DS_ERR_POSITION.  Two rows with one slot: either may stay.
+ * row and flags DS_ERR_POSITION.  Two rows with one slot: each element of the
+ * cache row is one's or the other's.
  * qkv_len (562) must reach the last row's end and row_stride its width; q_len
  * must be n_rows * n_qh * head_dim (563).  head_dim <= 256, rot_dim even and
  * <= head_dim, n_axes <= 8, base finite and > 0 (577).  No output may overlap
- * qkv or another output (qkv and q_out: 577).  Rows with 16-byte aligned buffers, row_stride and
+ * qkv or another output (577).  Rows with 16-byte aligned buffers, row_stride and
  * head_dim multiples of 8 and rot_dim of 16 move 16 bytes at a time (whole
  * rows by bulk copies from 2,048 rows on); others one element. */
 DS_API int ds_rope_append(const void *qkv, int64_t qkv_len, int qkv_dtype, int64_t row_stride,

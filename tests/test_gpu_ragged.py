@@ -239,6 +239,18 @@ def test_rope_append_with_one_axis_is_the_token_rotation(A):
     assert torch.equal(v[0], x[0, 5120:])
 
 
+def test_rope_append_with_all_buffers_in_one(A):
+    """The rows first, their outputs behind them in the same storage."""
+    rows = 5
+    buf = torch.randn(rows * (6 + 2) * 64 + 2 * 8 * 128, device="cuda")
+    x, rest = buf[:rows * 6 * 64].view(rows, 6 * 64), buf[rows * 6 * 64:]
+    q, k, v = rest[:rows * 128].view(rows, 128), rest[rows * 128:][:8 * 128].view(8, 128), rest[-8 * 128:].view(8, 128)
+    want, ws, args = [torch.zeros_like(t) for t in (q, k, v)], A.workspace(256), (i32([range(rows)]), 1, None, 2, 2, 64, 64, 1e4, 0)
+    A.ds_rope_append(x, 6 * 64, rows, *args, q, k, v, 8, i32(range(rows)), ws)
+    A.ds_rope_append(x.clone(), 6 * 64, rows, *args, *want, 8, i32(range(rows)), ws)
+    assert torch.equal(q, want[0]) and torch.equal(k[:rows], want[1][:rows]) and torch.equal(v[:rows], want[2][:rows])
+
+
 def test_rope_append_flags_and_skips_bad_rows_among_many(A):
     n = 3000
     x = torch.randn(n, 6 * 64, device="cuda")

@@ -144,3 +144,24 @@ def test_the_binding_refuses_a_workspace_that_is_not_on_the_device(abi):
     with pytest.raises(ValueError):
         abi.ds_paged_plan(t32, t32, 1, t32, 16, 128, t32, 8, t32, t32, t32, t32, t32, 8, t32,
                           torch.zeros(256, dtype=torch.uint8), stream=None)
+
+
+@pytest.mark.parametrize("out,other", [
+    ("lens", "cached"), ("lens", "new"), ("starts", "cached"), ("table", "free"), ("taken", "free"),
+    ("positions", "slots"), ("row_seq", "positions"), ("lens", "starts"),
+])
+def test_plan_refuses_outputs_that_overlap(abi, out, other):
+    names = ["cached", "new", "free", "table", "starts", "lens", "row_seq", "positions", "slots", "taken"]
+    at = {n: FAKE + 0x1000 * i for i, n in enumerate(names)}
+    at[out] = at[other] + 4  # (n_taken: the second free block; else all but the first element)
+    assert plan(abi, **at) == abi.DS_BAD_ARGUMENT
+
+
+@pytest.mark.parametrize("change", [
+    dict(v=0x50000000 + 64 * 2 * 64 * 2 - 16),             # the caches' ends
+    dict(k=FAKE + 4 * 10 * 6 * 64 - 16),                   # the last row's end
+    dict(v=FAR + 4 * 10 * 2 * 64 - 16),                    # q_out's end
+    dict(q=FAKE + 4 * 10 * 6 * 64 - 16, qkv_len=1 << 20),  # the rows' end, in a longer buffer
+])
+def test_rope_append_refuses_outputs_that_overlap(abi, change):
+    assert rope(abi, **dict(dict(k=0x50000000, v=0x60000000), **change)) == abi.DS_BAD_ARGUMENT
