@@ -10,10 +10,19 @@
 // in one pass over the positions with a running maximum and sum.
 //
 // chunk_simt_kernel keeps everything in fp32 (an fp32 cache has more digits
-// than a bf16 product keeps): 64 (row, head) pairs by 64 positions a step,
-// 256 threads of 4 x 4 scores and 4 x hd/16 outputs in registers, Q, K and V
-// in shared memory.  The fp32 FMA rate bounds it (chunks); work split as in
-// chunk_attn.cuh.
+// than a bf16 product keeps): 16 RT (row, head) pairs by 64 positions a step,
+// 256 threads of RT x 4 scores and RT x hd/16 outputs in registers, Q, K and V
+// in shared memory; work split as in chunk_attn.cuh.  Two sizes of tile:
+//  - RT 4, 64 pairs.  Bound by the fp32 FMA and the reads of shared memory:
+//    2,048 fp32 rows of 32 heads of 128 take 1,022 us, 34 TFLOP/s.  (Eight
+//    rows a thread, half the warps with fewer reads each: 1,190 against 1,074
+//    us then.)
+//  - RT 1, 16 pairs, for batches with 16 pairs a sequence or fewer on average
+//    (single tokens): 64 fp32 tokens over 1,024 to 4,096 positions 370 us
+//    against 640 with RT 4, one over 1,024 16.0 against 21.5, three rows each
+//    630 against 739.  A step's fetch and work in turns bound it: 3.6 TB/s.
+// Warps whose pairs are all behind the tile's last skip a step's work (without
+// that and with loads waited for one by one the 64 tokens took 1,210 us).
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -24,26 +33,34 @@
 namespace ds {
 
 constexpr int kCsThreads = 256;
-constexpr int kCsRows = 64;
 constexpr int kCsStep = 64;
 constexpr int kCsPiece = 128;
 constexpr float kLog2e = 1.4426950408889634f;
 
-// Four consecutive elements as fp32 (the row starts on 4 elements).
-__device__ __forceinline__ float4 cs_load4(const void *base, long long i, int dtype) {
-    if (dtype == DS_F32) return __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i));
-    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(base) + i));
+// Four consecutive elements (the row starts on 4 elements) as fp32.
+__device__ __forceinline__ float4 cs_load4(const float *base, long long i) {
+    return __ldg(reinterpret_cast<const float4 *>(base + i));
+}
+__device__ __forceinline__ float4 cs_load4(const __nv_bfloat16 *base, long long i) {
+    const uint2 w = __ldg(reinterpret_cast<const uint2 *>(base + i));
     return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
                        __uint_as_float(w.y & 0xffff0000u));
 }
+__device__ __forceinline__ float4 cs_load4(const void *base, long long i, int dtype) {
+    return dtype == DS_F32 ? cs_load4(static_cast<const float *>(base), i)
+                           : cs_load4(static_cast<const __nv_bfloat16 *>(base), i);
+}
 
-template <int HD>
+template <int HD, int RT>
 __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kernel(const __grid_constant__ ChunkArgs a) {
     extern __shared__ __align__(16) float sm[];
+    constexpr int rows = 16 * RT;  // (row, head) pairs of a tile
+    constexpr int kFetch = RT == 1 && HD >= 128 ? 8 : 4;
+    static_assert(kCsStep * (HD / 4) % (kFetch * kCsThreads) == 0, "");
     constexpr int KS = HD + 4;  // K rows padded: sixteen rows read at once fall into different banks
     constexpr int PS = kCsStep + 4;
     static_assert(PS <= KS || HD < 64, "");
-    float *sQ = sm, *sK = sQ + kCsRows * HD, *sV = sK + kCsStep * KS;
+    float *sQ = sm, *sK = sQ + rows * HD, *sV = sK + kCsStep * KS;
     float *sP = sK;  // the weights take K's place once the scores are formed
     __shared__ long long s_red[34];
     __shared__ int s_row[2][kCsStep];
@@ -59,7 +76,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
     ChunkSeg g;
     while (walk.next(a, g)) {
         const ChunkHeads hh = chunk_heads(a, g.part);
-        for (int i = tid; i < kCsRows * (HD / 4); i += kCsThreads) {
+        for (int i = tid; i < rows * (HD / 4); i += kCsThreads) {
             const int m = i / (HD / 4), d = (i % (HD / 4)) * 4;
             const int tok = m / a.part_heads, h = m % a.part_heads;
             float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -67,14 +84,14 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
                 v = cs_load4(a.q, ((long long)(g.r0 + tok) * a.n_qh + hh.first + h) * a.hd + d, a.q_dtype);
             *reinterpret_cast<float4 *>(sQ + m * HD + d) = v;
         }
-        float2 acc[4][HD / 32];
-        float mx[4], sum[4];
-        int lim[4];  // last position of each row
+        float2 acc[RT][HD / 32];
+        float mx[RT], sum[RT];
+        int lim[RT];  // last position of each row
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < RT; ++i) {
             mx[i] = -INFINITY;
             sum[i] = 0.0f;
-            lim[i] = g.pos0 + (ty * 4 + i) / a.part_heads;
+            lim[i] = g.pos0 + (ty * RT + i) / a.part_heads;
 #pragma unroll
             for (int c = 0; c < HD / 32; ++c) acc[i][c] = make_float2(0.0f, 0.0f);
         }
@@ -84,48 +101,65 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
             if (tid < kCsStep && pos < g.len)
                 s_row[b & 1][tid] = (int)(chunk_block_row(a, g.seq, pos / a.bt, flags) + pos % a.bt);
         };
+        // a step's K and V, several rows' loads on their way at a time
+        auto fetch = [&](const auto *k_cache, const auto *v_cache, int b, int nt) {
+            for (int i0 = tid; i0 < kCsStep * (HD / 4); i0 += kFetch * kCsThreads) {
+                float4 k[kFetch], v[kFetch];
+#pragma unroll
+                for (int u = 0; u < kFetch; ++u) {
+                    const int i = i0 + u * kCsThreads, t = i / (HD / 4), d = (i % (HD / 4)) * 4;
+                    k[u] = v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (t < nt && d < a.hd) {
+                        const long long e = ((long long)s_row[b & 1][t] * a.n_kvh + hh.kv) * a.hd + d;
+                        k[u] = cs_load4(k_cache, e);
+                        v[u] = cs_load4(v_cache, e);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kFetch; ++u) {
+                    const int i = i0 + u * kCsThreads, t = i / (HD / 4), d = (i % (HD / 4)) * 4;
+                    *reinterpret_cast<float4 *>(sK + t * KS + d) = k[u];
+                    *reinterpret_cast<float4 *>(sV + t * HD + d) = v[u];
+                }
+            }
+        };
+        // a warp whose rows are all behind the tile's last has nothing to work out
+        const bool busy = (ty & ~1) * RT < g.tokens * a.part_heads;
         find_rows(g.b0);
         for (int b = g.b0; b < g.b1; ++b) {
             const int t0 = b * kCsStep, nt = min(kCsStep, g.len - t0);
             __syncthreads();  // the last step's weights and values are read, this one's rows found
             if (b + 1 < g.b1) find_rows(b + 1);
-            for (int i = tid; i < kCsStep * (HD / 4); i += kCsThreads) {
-                const int t = i / (HD / 4), d = (i % (HD / 4)) * 4;
-                float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-                if (t < nt && d < a.hd) {
-                    const long long e = ((long long)s_row[b & 1][t] * a.n_kvh + hh.kv) * a.hd + d;
-                    k = cs_load4(a.k_cache, e, a.kv_dtype);
-                    v = cs_load4(a.v_cache, e, a.kv_dtype);
-                }
-                *reinterpret_cast<float4 *>(sK + t * KS + d) = k;
-                *reinterpret_cast<float4 *>(sV + t * HD + d) = v;
-            }
+            if (a.kv_dtype == DS_F32)
+                fetch(static_cast<const float *>(a.k_cache), static_cast<const float *>(a.v_cache), b, nt);
+            else
+                fetch(static_cast<const __nv_bfloat16 *>(a.k_cache), static_cast<const __nv_bfloat16 *>(a.v_cache), b, nt);
             __syncthreads();
-            float2 s2[4][4] = {};  // sums over even and odd dims
+            float2 s2[RT][4] = {};  // sums over even and odd dims
 #pragma unroll 4
-            for (int d = 0; d < HD; d += 4) {
-                float4 qv[4], kv[4];
+            for (int d = 0; d < (busy ? HD : 0); d += 4) {
+                float4 qv[RT], kv[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    qv[i] = *reinterpret_cast<const float4 *>(sQ + (ty * 4 + i) * HD + d);
-                    kv[i] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * i) * KS + d);
-                }
+                for (int i = 0; i < RT; ++i) qv[i] = *reinterpret_cast<const float4 *>(sQ + (ty * RT + i) * HD + d);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * KS + d);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         s2[i][j] = chunk_fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), s2[i][j]);
                         s2[i][j] = chunk_fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), s2[i][j]);
                     }
             }
-            float s[4][4];
+            float s[RT][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < RT; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[i][j] = s2[i][j].x + s2[i][j].y;
             __syncthreads();  // K is read
+            if (!busy) continue;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < RT; ++i) {
                 float top = -INFINITY;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
@@ -142,7 +176,7 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const float p = exp2f(s[i][j] - m_use);
-                    sP[(ty * 4 + i) * PS + tx + 16 * j] = p;
+                    sP[(ty * RT + i) * PS + tx + 16 * j] = p;
                     add += p;
                 }
 #pragma unroll
@@ -158,16 +192,16 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
             __syncwarp();  // a warp reads the weights of its own rows only
             auto add_values = [&](auto masked) {
                 for (int t = 0; t < nt; t += 4) {
-                    float4 p4[4];
+                    float4 p4[RT];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) p4[i] = *reinterpret_cast<const float4 *>(sP + (ty * 4 + i) * PS + t);
+                    for (int i = 0; i < RT; ++i) p4[i] = *reinterpret_cast<const float4 *>(sP + (ty * RT + i) * PS + t);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
 #pragma unroll
                         for (int c = 0; c < HD / 64; ++c) {
                             const float4 v = *reinterpret_cast<const float4 *>(sV + (t + k) * HD + 64 * c + tx * 4);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
+                            for (int i = 0; i < RT; ++i) {
                                 // a row skips what it does not attend: 0 x an infinity there would be NaN
                                 if (masked.value && t0 + t + k > lim[i]) continue;
                                 const float p = k == 0 ? p4[i].x : k == 1 ? p4[i].y : k == 2 ? p4[i].z : p4[i].w;
@@ -188,8 +222,8 @@ __global__ void __launch_bounds__(kCsThreads, HD <= 128 ? 2 : 1) chunk_simt_kern
         if (split && g.b0 == 0 && tid == 0) a.joins[blockIdx.x] = walk.join(a, g);
         float *rec = split ? chunk_record(a, blockIdx.x, g.slot) : nullptr;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int m = ty * 4 + i, tok = m / a.part_heads, h = m % a.part_heads;
+        for (int i = 0; i < RT; ++i) {
+            const int m = ty * RT + i, tok = m / a.part_heads, h = m % a.part_heads;
             if (tok >= g.tokens || h >= hh.count) continue;
             if (split) {
                 if (tx == 0) {
@@ -279,25 +313,35 @@ __global__ void __launch_bounds__(kCjThreads) chunk_join_kernel(const __grid_con
     }
 }
 
-static size_t cs_smem(int HD) { return (size_t)(kCsRows * HD + kCsStep * (HD + 4) + kCsStep * HD) * sizeof(float); }
+static size_t cs_smem(int HD, int rows) {
+    return (size_t)(rows * HD + kCsStep * (HD + 4) + kCsStep * HD) * sizeof(float);
+}
 static int cs_hd(int hd) { return hd <= 64 ? 64 : hd <= 128 ? 128 : 256; }
 
 int chunk_simt_grid() { return 2 * sm_count(); }
 
-cudaError_t launch_chunk_simt(ChunkArgs &a, int *grid, cudaStream_t stream) {
-    chunk_tile_shape(a, kCsRows, 1);
+template <int RT>
+static cudaError_t launch_cs(ChunkArgs &a, int *grid, cudaStream_t stream) {
+    chunk_tile_shape(a, 16 * RT, 1);
     a.step = kCsStep;
     a.half_tokens = 0;
     a.w_half = a.w_full = 1;
     a.tile_cost = 0;
     a.piece = kCsPiece;
     const int HD = cs_hd(a.hd);
-    const size_t smem = cs_smem(HD);
+    const size_t smem = cs_smem(HD, 16 * RT);
     *grid = HD == 256 ? sm_count() : chunk_simt_grid();
-    void (*fn)(ChunkArgs) = HD == 64 ? chunk_simt_kernel<64> : HD == 128 ? chunk_simt_kernel<128> : chunk_simt_kernel<256>;
+    void (*fn)(ChunkArgs) = HD == 64    ? chunk_simt_kernel<64, RT>
+                            : HD == 128 ? chunk_simt_kernel<128, RT>
+                                        : chunk_simt_kernel<256, RT>;
     const cudaError_t e = cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     return launch_ex(fn, dim3(*grid), dim3(kCsThreads), smem, stream, false, a);
+}
+
+cudaError_t launch_chunk_simt(ChunkArgs &a, int *grid, cudaStream_t stream) {
+    // (the lengths are on the device: the average decides, every tile size is right for every batch)
+    return (long long)a.n_rows * a.gq <= 16ll * a.n_seqs ? launch_cs<1>(a, grid, stream) : launch_cs<4>(a, grid, stream);
 }
 
 void chunk_tile_shape(ChunkArgs &a, int sub_rows, int subs) {

@@ -382,6 +382,22 @@ def test_chunk_attention_matches_fp64(A, new, total, bt, nq, nkv, hd, qt, kvt):
     assert torch.equal(got, again)  # the workspace is ready again, and the same bits come out
 
 
+@pytest.mark.parametrize("qt,kvt", [(F32, F32), (BF16, F32), (F32, BF16), (BF16, BF16)])
+@pytest.mark.parametrize("new,total,bt,nq,nkv,hd", [
+    ([1] * 6, [5, 64, 65, 129, 700, 1], 16, 16, 4, 128),
+    ([1, 2, 1], [300, 2, 64], 5, 4, 4, 64),
+    ([2, 1, 3, 1], [90, 513, 200, 128], 16, 6, 2, 80),
+    ([1, 1], [256, 77], 16, 8, 1, 256),
+    ([0] * 15 + [1] + [0] * 15, [3] * 15 + [140] + [9] * 15, 16, 24, 1, 64),   # groups of 24, most sequences without rows
+    ([1] * 30 + [61] + [1] * 30, [20] * 30 + [333] + [70] * 30, 16, 8, 4, 128),  # a chunk among single tokens
+    ([3, 1, 1], [2, 0, 9], 16, 4, 2, 4),                                        # rows that attend nothing
+])
+def test_chunk_attention_with_few_rows_a_sequence(A, new, total, bt, nq, nkv, hd, qt, kvt):
+    """16 (row, head) pairs a sequence or fewer on average: the plain cores' small tiles."""
+    assert (sum(new) + 2) * (nq // nkv) <= 16 * len(new)
+    test_chunk_attention_matches_fp64(A, new, total, bt, nq, nkv, hd, qt, kvt)
+
+
 def test_chunk_attention_contiguous_slots(A):
     new, total, bt, nq, nkv, hd = [5, 80], [100, 90], 16, 8, 2, 128
     k, v, table, width, _ = pool(new, total, bt, nkv, hd, BF16, 3, paged=False)
