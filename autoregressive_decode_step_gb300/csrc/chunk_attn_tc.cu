@@ -48,7 +48,7 @@
 // tokens with fp32 q over up to 4,096 positions in 136 us (3.8 TB/s; idle from
 // a tile's last step to the next one's first, 8,000 to 10,000 cycles); one
 // bf16 token over 1,024 in 13.7 us with the joining launch (latency); 256 fp32
-// rows behind 512 positions in 50 us.
+// rows behind 768 positions in 50 us.
 //
 // Every wait is bounded; after one gives up all others return at once and the
 // kernel runs to its end without them (its barriers still pair up), flagged.
