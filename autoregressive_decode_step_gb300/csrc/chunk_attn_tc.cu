@@ -609,7 +609,9 @@ __global__ void __launch_bounds__(kCtThreads, 1)
         // fp32 q: eight values of a pair an item, as three bf16 numbers each
         // (cut, not rounded: 8 bits of the 24 a piece), one MMA operand per
         // piece; pair p is rows 32 (p / 10) + p % 10 and 10 and 20 further of
-        // each.  Both warpgroups load.
+        // each.  Both warpgroups load.  A piece with nothing left in it is
+        // 2^-30 of the one before, below fp32's digits: zero times an infinite
+        // key would be NaN where q times it is an infinity.
         auto load_q = [&](const CtSeg &c) {
             const int n_items = c.g.tokens * a.part_heads * (HD / 8);
             constexpr int kItems = (SUB * (HD / 8) + 255) / 256;
@@ -642,7 +644,10 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     for (int m = m0; m < m0 + 3 * RPW; m += RPW)
                         *reinterpret_cast<uint4 *>(dst + z * Cfg::kTileBytes + m * 128 + (((ch & 7) ^ (m & 7)) << 4)) = v;
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) y[k] -= __uint_as_float(__float_as_uint(y[k]) & 0xffff0000u);
+                    for (int k = 0; k < 8; ++k) {
+                        const float t = ct_top(y[k], 0xffff0000u), rest = y[k] - t;
+                        y[k] = rest == 0.0f ? t * 0x1p-30f : rest;
+                    }
                 }
             }
             ct_fence_async();

@@ -1,0 +1,64 @@
+"""Edges of the ragged-step operators on the GPU."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+U, H = 2.0 ** -24, 2.0 ** -8  # half a step of fp32 and bf16, relative to the value
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def A():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from autoregressive_decode_step_gb300 import abi
+    return abi
+
+
+def i32(a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+@pytest.mark.parametrize("qt,kvt", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("new", [1, 3, 60])
+def test_an_infinite_key_that_a_row_attends(A, new, hd, qt, kvt):
+    """q . k is an infinity of q's sign times k's: minus infinity takes the
+    position out of the row's sum, plus infinity makes the row NaN, whatever
+    digits q has.
+
+    Tolerance: two scores' error d each and (T + 8) u over the sum, H for bf16
+    weights, and the output's rounding, as for finite keys."""
+    T, nq, nkv = new + 37, 4, 2
+    g = torch.Generator().manual_seed(new + hd)
+    q = torch.randn(new, nq, hd, generator=g).to(qt)
+    q[:, 0] = 1.0              # numbers of few digits, and of one sign
+    q[:, 1] = q[:, 1].abs()
+    q[:, 2] = -0.40625
+    q[:, 3] = -q[:, 3].abs()
+    k, v = (torch.randn(112, nkv, hd, generator=g).to(kvt) for _ in range(2))
+    k[5, :, 3], k[11, 0, hd - 1], k[20, 1, 7] = -math.inf, -math.inf, math.inf
+    scale = 1.0 / math.sqrt(hd)
+    out, ws = torch.full((new, nq * hd), 7.0, dtype=qt, device="cuda"), A.workspace(
+        A.ds_chunk_attention_workspace_bytes(1, new, nq, nkv, hd))
+    A.ds_gqa_chunk_attn(q.view(new, -1).cuda(), new, i32([0, new]), i32([T]), 1, k.view(112, -1).cuda(),
+                        v.view(112, -1).cuda(), 112, None, 7, 16, nq, nkv, hd, scale, out, ws)
+    kk, vv = (x[:T].double().repeat_interleave(nq // nkv, 1) for x in (k, v))
+    e = (q.double()[:, None] * kk[None]).sum(3).permute(2, 0, 1) * scale
+    e = e.masked_fill(torch.arange(T) > T - new + torch.arange(new)[:, None], -math.inf)
+    w = torch.softmax(e, 2)
+    want = torch.einsum("hjt,thd->jhd", w, vv)
+    finite = torch.where(torch.isfinite(kk), kk, 0.0).abs()
+    d = (hd + 4) * U * scale * torch.einsum("jhd,thd->jht", q.double().abs(), finite).amax(2)[:, :, None]
+    half = U if qt == F32 else H
+    slack = (2 * d + (T + 8) * U + (H if qt == BF16 else 0)) * vv.abs().max()
+    got = out.double().cpu().view(new, nq, hd)
+    assert not torch.isnan(want[:, :2]).any() and torch.isnan(want[:, 2:]).all()  # heads 2 and 3: plus infinity
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    err = (got - want).abs()[:, :2]
+    assert (err <= (slack + half * (want.abs() + slack))[:, :2]).all(), float(err.max())
+    assert A.ds_workspace_error(ws) == 0
