@@ -5,12 +5,13 @@
 //
 // Pair p of a head turns by pos[axis(p)] * f_p, f_p = base^(-2p / rot_dim).
 // Only the fraction of a full turn matters, so f_p / (2 pi) is held as a
-// 64-bit fixed-point fraction F_p of a turn and the product pos * F_p modulo
-// 2^64 is the angle, reduced exactly by integer overflow: a position of
-// 2^31 - 1 leaves an error under 2^-33 of a turn, where an fp32 angle of a far
-// position has lost whole digits.  The quadrant comes off the top two bits
-// before the rest is rounded to fp32, so sine and cosine are those of an
-// argument within an eighth of a turn.
+// 64-bit fixed-point fraction F_p of a turn, right to a unit (ra_turns), and
+// the product pos * F_p modulo 2^64 is the angle, reduced exactly by integer
+// overflow: a position of 2^31 - 1 leaves an error under 2^-33 of a turn (for
+// bases from 1e-8 up), where an fp32 angle of a far position has lost whole
+// digits.  The quadrant comes off the top two bits before the rest is rounded
+// to fp32, so sine and cosine are those of an argument within an eighth of a
+// turn.
 //
 // Bound by bytes (each element read once and written once).  Two kernels:
 //  - few rows: a thread keeps the same place of a row for all the rows of its
@@ -406,16 +407,56 @@ static cudaError_t launch_ra(const RopeAppendArgs &a, const RopeTurns<P> &t, boo
                : launch_ex(rope_append_kernel<XT, QT, KT, 1, P>, dim3(nx, ny), dim3(kRaThreads), 0, s, false, a, t);
 }
 
+// A number as the sum of two doubles, about 104 bits.
+struct Dd {
+    double hi, lo;
+};
+static Dd dd_mul(Dd a, Dd b) {
+    // (a fused multiply-add with zero: a plain product might be fused into the sum below)
+    const double p = std::fma(a.hi, b.hi, 0.0);
+    const double e = std::fma(a.hi, b.lo, std::fma(a.lo, b.hi, std::fma(a.hi, b.hi, -p)));
+    const double s = p + e;
+    return {s, e - (s - p)};
+}
+
+// x modulo 1 in units of 2^-64, to the nearest.
+static unsigned long long ra_fraction(Dd x) {
+    if (!std::isfinite(x.hi) || !std::isfinite(x.lo)) return 0;
+    unsigned long long sum = 0;
+    double rest = 0.0;
+    for (const double part : {x.hi, x.lo}) {
+        const double a = std::fabs(part), units = std::ldexp(a - std::floor(a), 64), whole = std::floor(units);
+        const unsigned long long u = (unsigned long long)whole;
+        sum += part < 0.0 ? 0ull - u : u;
+        rest += part < 0.0 ? whole - units : units - whole;
+    }
+    return sum + (unsigned long long)std::llrint(rest);
+}
+
+// F_p = base^(-2p / rot) / (2 pi) modulo 1 in units of 2^-64.  A double holds
+// 53 bits of it, which a far position would multiply into the angle (2^-25 of
+// a turn at 2^31), so: the root r = base^(-2 / rot) by one step of Newton's
+// method from the double's, r^(rot / 2) base = 1, and its powers by repeated
+// products.  An error of 2^-95 of the frequency remains, a unit of F_p while
+// that is below 2^30 turns a position (bases from 1e-8 up).
+static void ra_turns(unsigned long long *turn, int n, double base) {
+    const double r0 = std::pow(base, -1.0 / n);
+    Dd one = {base, 0.0};
+    for (int i = 0; i < n; ++i) one = dd_mul(one, {r0, 0.0});  // from base down to 1
+    const Dd r = {r0, -r0 * (((one.hi - 1.0) + one.lo) / n)};
+    Dd f = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / (2 pi)
+    for (int p = 0; p < n; ++p) {
+        turn[p] = ra_fraction(f);
+        f = dd_mul(f, r);
+    }
+}
+
 template <int P>
 static cudaError_t launch_ra_types(const RopeAppendArgs &a, const unsigned char *axes, double base, int xd, int qd,
                                    int kd, bool vec, cudaStream_t s) {
     RopeTurns<P> t = {};
-    for (int p = 0; p < a.rot / 2; ++p) {
-        const double turns = std::pow(base, -2.0 * p / a.rot) / 6.283185307179586476925286766559;
-        const double frac = turns - std::floor(turns);
-        t.turn[p] = frac < 1.0 ? (unsigned long long)std::ldexp(frac, 64) : 0ull;
-        t.axis[p] = axes ? axes[p] : 0;
-    }
+    ra_turns(t.turn, a.rot / 2, base);
+    for (int p = 0; p < a.rot / 2; ++p) t.axis[p] = axes ? axes[p] : 0;
     using B = __nv_bfloat16;
     switch ((xd == DS_BF16) * 4 + (qd == DS_BF16) * 2 + (kd == DS_BF16)) {
         case 0: return launch_ra<float, float, float>(a, t, vec, s);

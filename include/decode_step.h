@@ -339,8 +339,9 @@ DS_API size_t ds_rope_append_workspace_bytes(void);
  * them stay.  With one axis this is the rotation of ds_rope; with several
  * (time, height, width of an image's or a video's patches) each pair turns by
  * the axis it is given, in runs or interleaved, as pair_axis says.  The angle
- * is exact to 2^-33 of a turn at any position; the rotation is fp32, rounded
- * once to the output's type.
+ * is exact to 2^-33 of a turn at any position for bases from 1e-8 up (below,
+ * frequencies of billions of turns a position lose digits); the rotation is
+ * fp32, rounded once to the output's type.
  *   q_out: [n_rows][n_qh][head_dim]; the rotated k and v as it is go to row
  *   slots[r] of k_cache / v_cache (rows of n_kvh * head_dim elements).
  *   qkv, q_out and the caches are fp32 or bf16 each (572).

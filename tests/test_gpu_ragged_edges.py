@@ -1,5 +1,6 @@
 """Edges of the ragged-step operators on the GPU."""
 import math
+from decimal import Decimal, getcontext
 
 import numpy as np
 import pytest
@@ -62,3 +63,27 @@ def test_an_infinite_key_that_a_row_attends(A, new, hd, qt, kvt):
     err = (got - want).abs()[:, :2]
     assert (err <= (slack + half * (want.abs() + slack))[:, :2]).all(), float(err.max())
     assert A.ds_workspace_error(ws) == 0
+
+
+@pytest.mark.parametrize("base", [1e-3, 10000.0, 500000.0, 1e6])
+@pytest.mark.parametrize("hd,rot,layout", [(128, 128, 0), (256, 256, 1), (96, 80, 1), (6, 6, 0)])
+def test_angles_of_far_positions(A, hd, rot, layout, base):
+    """Pairs (1, 0) come out as cosine and sine of the angle, here worked out in 60 digits. Tolerance: 2^-33 of a turn,
+    and 4 u for the fp32 argument (an eighth of a turn at most) and the two functions; 1 c - 0 s is exact."""
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    pos = [2 ** 31 - 1, 2 ** 31 - 77, 2 ** 30 + 12345, 99999989, 6000000, 131071, 0]
+    n = len(pos)
+    x = torch.zeros(n, 3, hd, device="cuda")
+    first = slice(0, rot // 2) if layout == 0 else slice(0, rot, 2)
+    second = slice(rot // 2, rot) if layout == 0 else slice(1, rot, 2)
+    x[:, :, first] = 1.0
+    q, k, v = (torch.zeros(n, hd, device="cuda") for _ in range(3))
+    ws = A.workspace(A.ds_rope_append_workspace_bytes())
+    A.ds_rope_append(x.view(n, -1), 3 * hd, n, i32([pos]), 1, None, 1, 1, hd, rot, base, layout, q, k, v, n,
+                     i32(range(n)), ws)
+    angle = np.array([[float(i * (Decimal(base) ** (Decimal(-2 * p) / rot)) % (2 * pi)) for p in range(rot // 2)]
+                      for i in pos])
+    for got in (q.double().cpu().numpy(), k.double().cpu().numpy()):
+        assert np.abs(got[:, first] - np.cos(angle)).max() <= 4 * U + 2 * math.pi * 2.0 ** -33
+        assert np.abs(got[:, second] - np.sin(angle)).max() <= 4 * U + 2 * math.pi * 2.0 ** -33

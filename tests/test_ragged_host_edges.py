@@ -1,0 +1,28 @@
+"""Host side of the ragged-step operators without a GPU: what a call would
+launch, and refusals with a single reason each."""
+import struct
+from decimal import Decimal, getcontext
+
+import pytest
+
+from tests import fake_runtime
+
+PI = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+
+
+@pytest.mark.parametrize("base", [1e-8, 1e-3, 0.75, 1.0, 10000.0, 500000.0, 1e6, 1e30, 1.7e308])
+@pytest.mark.parametrize("hd,rot", [(128, 128), (256, 256), (80, 48), (6, 2), (4, 4)])
+def test_the_rotary_frequency_is_right_to_its_last_bit(tmp_path, base, hd, rot):
+    """The kernel multiplies positions by base^(-2p / rot) / 2 pi as a fraction of a turn in units of 2^-64: a unit at
+    most from 60 digits' answer, so a position below 2^31 leaves less than 2^-33 of a turn."""
+    getcontext().prec = 80
+    out = fake_runtime.run("""
+        arg_bytes = %d
+        assert rope(1, 1, 1, %d, %d, %r) == DS_OK
+        print(launches[0][3].hex())
+        """ % (4 * rot, hd, rot, base), str(tmp_path))
+    turns = struct.unpack("<%dQ" % (rot // 2), bytes.fromhex(out.strip())[:4 * rot])
+    for p, got in enumerate(turns):
+        want = Decimal(base) ** (Decimal(-2 * p) / rot) / (2 * PI) % 1 * 2 ** 64
+        off = abs(got - want)
+        assert min(off, 2 ** 64 - off) <= 1, (p, got, want)
