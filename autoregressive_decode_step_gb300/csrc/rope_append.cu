@@ -384,8 +384,10 @@ __global__ void __launch_bounds__(kRaThreads, 4)
 template <typename XT, typename QT, typename KT, int P>
 static cudaError_t launch_ra_bulk(const RopeAppendArgs &a, const RopeTurns<P> &t, int items, int row_bytes, int smem,
                                   cudaStream_t s) {
+    // (the most any call takes: the limit is the kernel's, and another thread's
+    // call may set it between this one's two lines)
     const cudaError_t e = cudaFuncSetAttribute((const void *)rope_append_bulk_kernel<XT, QT, KT, P>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kRaBulkSmem);
     if (e != cudaSuccess) return e;
     const int per_sm = std::min(kRaBulkBlocks, 220 * 1024 / (smem + 2 * 1024));
     return launch_ex(rope_append_bulk_kernel<XT, QT, KT, P>, dim3(std::min(a.n_rows, per_sm * sm_count())),

@@ -1,5 +1,6 @@
 """Edges of the ragged-step operators on the GPU."""
 import math
+import threading
 from decimal import Decimal, getcontext
 
 import numpy as np
@@ -87,3 +88,44 @@ def test_angles_of_far_positions(A, hd, rot, layout, base):
     for got in (q.double().cpu().numpy(), k.double().cpu().numpy()):
         assert np.abs(got[:, first] - np.cos(angle)).max() <= 4 * U + 2 * math.pi * 2.0 ** -33
         assert np.abs(got[:, second] - np.sin(angle)).max() <= 4 * U + 2 * math.pi * 2.0 ** -33
+
+
+def test_rope_append_of_two_widths_from_two_threads(A):
+    """Rows of two widths through one kernel (fp32 rows by bulk copies) from
+    two host threads at once: every call is accepted and does its own work."""
+    n, calls, errors = 2048, 500, []
+
+    def make(nq, nkv):
+        x = torch.randn(n, (nq + 2 * nkv) * 128, device="cuda")
+        q = torch.zeros(n, nq * 128, device="cuda")
+        k = torch.zeros(n, nkv * 128, device="cuda")
+        pos, ws, st = torch.arange(n, dtype=torch.int32, device="cuda")[None], A.workspace(256), torch.cuda.Stream()
+        return dict(x=x, q=q, k=k, v=torch.zeros_like(k), pos=pos, ws=ws, st=st, nq=nq, nkv=nkv)
+
+    def call(o, q, k, v, ws, st=None):
+        A.ds_rope_append(o["x"], o["x"].shape[1], n, o["pos"], 1, None, o["nq"], o["nkv"], 128, 128, 1e4, 0, q, k, v, n,
+                         o["pos"][0], ws, stream=st)
+
+    def work(o):
+        try:
+            for _ in range(calls):
+                call(o, o["q"], o["k"], o["v"], o["ws"], o["st"])
+        except Exception as e:
+            errors.append(e)
+
+    sets = [make(32, 8), make(4, 2)]
+    want = []
+    for o in sets:
+        alone = [torch.zeros_like(o[t]) for t in "qkv"]
+        call(o, *alone, A.workspace(256))
+        want.append(alone)
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(o,)) for o in sets]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors, errors[0]
+    for o, w in zip(sets, want):
+        assert all(torch.equal(o[t], w[i]) for i, t in enumerate("qkv")) and A.ds_workspace_error(o["ws"]) == 0

@@ -26,3 +26,18 @@ def test_the_rotary_frequency_is_right_to_its_last_bit(tmp_path, base, hd, rot):
         want = Decimal(base) ** (Decimal(-2 * p) / rot) / (2 * PI) % 1 * 2 ** 64
         off = abs(got - want)
         assert min(off, 2 ** 64 - off) <= 1, (p, got, want)
+
+
+@pytest.mark.parametrize("dtype,nq,nkv", [(0, 32, 8), (1, 64, 16)])
+def test_a_narrow_call_inside_a_wide_one_takes_no_shared_memory_from_it(tmp_path, dtype, nq, nkv):
+    """The limit of a kernel's shared memory belongs to the kernel, not to the call: another thread's call for narrower
+    rows that comes between a call's setting it and its launch must not lower it."""
+    out = fake_runtime.run("""
+        inner = []
+        on_set_limit.append(lambda: inner.append(rope(2048, 1, 1, 128, 128, 1e4, %d)))
+        shim.shim_hook(hook)
+        outer = rope(2048, %d, %d, 128, 128, 1e4, %d)
+        assert inner == [DS_OK] and len(launches) == 2 and launches[1][0] > 48 * 1024 > launches[0][0], launches
+        print(outer == DS_OK, [l[2] for l in launches])
+        """ % (dtype, nq, nkv, dtype), str(tmp_path))
+    assert out.strip() == "True [0, 0]"
