@@ -238,6 +238,16 @@ __device__ __forceinline__ void ct_wait(uint64_t *bar, uint32_t parity, volatile
     }
 }
 
+// The same for a counter in shared memory that reaches n.
+__device__ __forceinline__ void ct_wait_count(const int *count, int n, volatile int *dead, int *err) {
+    const uint64_t t0 = global_timer_ns();
+    while (*reinterpret_cast<const volatile int *>(count) < n && !*dead)
+        if (global_timer_ns() - t0 > kWaitLimitNs) {
+            flag_error(err, DS_ERR_WAIT_TIMEOUT);
+            *dead = 1;
+        }
+}
+
 // Order of the 2 nb tiles of a segment in the ring, the order they are first
 // needed in.  Shared steps: K0 V0 K1 V1 ...  Steps taken in turns:
 // K0 K1 V0 K2 V1 K3 ... V(nb-2) V(nb-1).
@@ -267,6 +277,7 @@ struct CtShared {
     // non-finite V per dim, by the segment's parity: 10-bit first positions of
     // NaN, +inf, -inf behind the tile's pos0; noted: there are some
     int noted[2];
+    int readers[2];  // warps that have read this segment's notes
     int left[2];  // segments a part's warps are done with, four counts each
     unsigned note[2][128];
 };
@@ -344,7 +355,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
             mbar_init(&sh.p_full[w], 4);
             mbar_init(&sh.o_full[w], 1);
             mbar_init(&sh.done[w], 1);
-            sh.noted[w] = sh.left[w] = 0;
+            sh.noted[w] = sh.readers[w] = sh.left[w] = 0;
         }
         for (int i = 0; i < kCtSegs; ++i) {
             mbar_init(&sh.seg_full[i], 1);
@@ -703,12 +714,7 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         if (bad & 0x80008000u) {
                             // the notes were those of the segment before the last:
                             // the other part is done with it before they change
-                            const uint64_t since = global_timer_ns();
-                            while (*reinterpret_cast<volatile int *>(&sh.left[1 - w]) < 4 * ((int)seg - 1) && !*dead)
-                                if (global_timer_ns() - since > kWaitLimitNs) {
-                                    flag_error(a.err, DS_ERR_WAIT_TIMEOUT);
-                                    *dead = 1;
-                                }
+                            ct_wait_count(&sh.left[1 - w], 4 * ((int)seg - 1), dead, a.err);
                             for (int d = 0; d < HD; ++d) {
                                 __nv_bfloat16 *p = reinterpret_cast<__nv_bfloat16 *>(
                                     row + (d >> 6) * kCtHalf + ((((d >> 3) & 7) ^ (t & 7)) << 4) + (d & 7) * 2);
@@ -856,7 +862,8 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                 if (turns && steps1) ct_wait(&sh.o_full[1], oc1 & 1, dead, a.err);
                 __syncwarp();
                 tc_fence_after();
-                const bool notes = sh.noted[par];
+                // (only a masked step notes, and only after one are they here to be read)
+                const bool notes = g.b1 * kCtStep - 1 > g.pos0 && sh.noted[par];
                 const bool split = g.split;
                 float f0 = 1.0f, f1 = 0.0f;
                 if (turns && steps1) {  // join the two parts' turns
@@ -937,13 +944,22 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                     }
                     __syncwarp();
                 }
-                if (notes) {  // read: clear them for the segment after the next
-                    turns ? named_sync(2 + w, 128) : named_sync(1, 256);
-                    if (w == 0) {
-                        for (int d = t; d < HD; d += 128) sh.note[par][d] = kCtNoNote;
-                        if (t == 0) sh.noted[par] = 0;
+                if (notes) {
+                    // Read: one warp clears them for the segment after the next
+                    // when all readers are through.  (Counted and with a limit,
+                    // not at a hardware barrier: after a wait has given up, the
+                    // warps may have read different answers.)
+                    __threadfence_block();
+                    __syncwarp();
+                    if (lane == 0) atomicAdd(&sh.readers[par], 1);
+                    if (warp == 0) {
+                        ct_wait_count(&sh.readers[par], turns ? 4 : 8, dead, a.err);
+                        __syncwarp();
+                        for (int d = lane; d < HD; d += 32) sh.note[par][d] = kCtNoNote;
+                        if (lane == 0) sh.noted[par] = sh.readers[par] = 0;
+                        __threadfence_block();
+                        __syncwarp();
                     }
-                    turns ? named_sync(2 + w, 128) : named_sync(1, 256);
                 }
             }
             if (turns) named_sync(1, 256);  // part 0 has read part 1's accumulator, maxima and notes

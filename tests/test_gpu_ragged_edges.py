@@ -129,3 +129,48 @@ def test_rope_append_of_two_widths_from_two_threads(A):
     assert not errors, errors[0]
     for o, w in zip(sets, want):
         assert all(torch.equal(o[t], w[i]) for i, t in enumerate("qkv")) and A.ds_workspace_error(o["ws"]) == 0
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("qt", [BF16, F32])
+def test_values_that_are_not_finite_in_tile_after_tile(A, hd, qt):
+    """Several non-finite values in the new rows of each of 500 sequences, so that every CTA has a run of tiles of both
+    kinds with values to set aside, split tiles among them: each comes out in its own column of the rows that attend it,
+    every other element as from the clean batch, time after time."""
+    g = np.random.RandomState(hd)
+    n, bt, nq, nkv = 500, 16, 8, 2
+    new = g.randint(1, 150, n)
+    total = new + g.randint(0, 200, n)
+    starts = np.concatenate([[0], np.cumsum(new)])
+    width = int(-(-total.max() // bt))
+    table = torch.from_numpy(g.permutation(n * width).astype(np.int32)).view(n, width)
+    gen = torch.Generator().manual_seed(hd + 1)
+    k, v = (torch.randn(n * width * bt, nkv * hd, generator=gen).to(BF16) for _ in range(2))
+    q = torch.randn(int(starts[-1]), nq * hd, generator=gen).to(qt).cuda()
+    bad_v, marks = v.clone(), []
+    for s in range(n):
+        for i in range(g.randint(0, 5)):
+            t = int(g.randint(total[s] - new[s], total[s]))
+            col, x = int(g.randint(0, nkv * hd)), (math.nan, math.inf, -math.inf)[g.randint(3)]
+            if all((s, col) != m[:2] for m in marks):
+                bad_v[int(table[s, t // bt]) * bt + t % bt, col] = x
+                marks.append((s, col, int(starts[s] + t - (total[s] - new[s])), x))
+    ws = A.workspace(A.ds_chunk_attention_workspace_bytes(n, q.shape[0], nq, nkv, hd))
+    args = i32(starts), i32(total), n, k.cuda()
+    vs, vb, tb = v.cuda(), bad_v.cuda(), table.cuda()
+
+    def call(values):
+        out = torch.full_like(q, 7.0)
+        A.ds_gqa_chunk_attn(q, q.shape[0], *args, values, k.shape[0], tb, width, bt, nq, nkv, hd, 0.1, out, ws)
+        return out
+
+    clean = call(vs)
+    want = clean.clone().view(-1, nkv, nq // nkv, hd)
+    for s, col, row, x in marks:
+        want[row:int(starts[s + 1]), col // hd, :, col % hd] = x
+    want = want.view_as(clean)
+    for _ in range(5):
+        got = call(vb)
+        assert torch.equal(torch.isnan(got), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(got, 0.0), torch.nan_to_num(want, 0.0))
+    assert torch.equal(call(vs), clean) and A.ds_workspace_error(ws) == 0

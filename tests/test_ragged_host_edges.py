@@ -41,3 +41,28 @@ def test_a_narrow_call_inside_a_wide_one_takes_no_shared_memory_from_it(tmp_path
         print(outer == DS_OK, [l[2] for l in launches])
         """ % (dtype, nq, nkv, dtype), str(tmp_path))
     assert out.strip() == "True [0, 0]"
+
+
+def test_the_chunk_attention_waits_at_no_barrier_by_what_it_read():
+    """A hardware barrier has no time limit, so whether a warp goes to one must not hang on data that its neighbours may
+    have read otherwise: once a bounded wait has given up, nothing orders the notes on non-finite values. Only what the
+    segment says (the same words in every warp) may decide."""
+    import os
+    import re
+    import autoregressive_decode_step_gb300 as pkg
+    with open(os.path.join(os.path.dirname(pkg.__file__), "csrc", "chunk_attn_tc.cu")) as f:
+        src = re.sub(r"//[^\n]*", "", f.read())
+    body = src[src.index("chunk_tc_kernel(const __grid_constant__"):src.index("bool chunk_tc_supported")]
+    conditions, at = [], []  # the open blocks' conditions where each barrier stands
+    i = 0
+    for m in re.finditer(r"[{}]|(?:named_sync|__syncthreads)\(", body):
+        if m.group() == "{":
+            at.append(body[i:m.start()].rsplit(";", 1)[-1])
+        elif m.group() == "}":
+            at.pop()
+        else:
+            conditions.append(" ".join(at + [body[i:m.start()].rsplit(";", 1)[-1]]))
+        i = m.end()
+    assert len(conditions) >= 4
+    for c in conditions:
+        assert not re.search(r"\b(notes|noted|bad|dead|any|busy|valid)\b", c.replace("*dead)", "")), c
