@@ -283,10 +283,16 @@ def ds_gqa_decode_attn(q, k_cache, v_cache, cache_rows, block_table, max_blocks_
           "ds_gqa_decode_attn")
 
 
-def _i32(t, n, name):
-    """Address of an int32 device tensor of at least n elements (contiguous)."""
+def _elsewhere(name):
+    return ValueError("%s: has to be on the workspace's device" % name)
+
+
+def _i32(t, n, name, dev):
+    """Address of a contiguous int32 tensor of at least n elements on device dev."""
     if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
         raise ValueError("%s: a contiguous int32 tensor of %d elements is needed" % (name, n))
+    if t.get_device() != dev:  # (-1 on the host)
+        raise _elsewhere(name)
     return t.data_ptr()
 
 
@@ -297,10 +303,12 @@ def _here(ws):
     return ws.data_ptr()
 
 
-def _dense(t, n, name):
-    """Address of a contiguous tensor of at least n elements."""
+def _dense(t, n, name, dev):
+    """Address of a contiguous tensor of at least n elements on device dev."""
     if not t.is_contiguous() or t.numel() < n:
         raise ValueError("%s: a contiguous tensor of %d elements is needed" % (name, n))
+    if t.get_device() != dev:
+        raise _elsewhere(name)
     return t.data_ptr()
 
 
@@ -313,14 +321,15 @@ def ds_paged_plan(cached_lens, new_lens, n_seqs, free_blocks, block_tokens, cach
                   stream=None):
     """Block table entries, row starts, positions and cache slots of a ragged
     step from its lengths; free_blocks may be None (no block left)."""
+    dev = ws.get_device()
     n_free = 0 if free_blocks is None else free_blocks.numel()
-    check(lib.ds_paged_plan(_i32(cached_lens, n_seqs, "cached_lens"), _i32(new_lens, n_seqs, "new_lens"), n_seqs,
-                            _i32(free_blocks, n_free, "free_blocks") if n_free else None, n_free, block_tokens,
-                            cache_rows, _i32(block_table, n_seqs * max_blocks_per_seq, "block_table"),
-                            max_blocks_per_seq, _i32(row_starts, n_seqs + 1, "row_starts"),
-                            _i32(seq_lens, n_seqs, "seq_lens"), _i32(row_seq, max_rows, "row_seq"),
-                            _i32(positions, max_rows, "positions"), _i32(slots, max_rows, "slots"), max_rows,
-                            _i32(n_taken, 1, "n_taken"), _here(ws), nbytes(ws), stream_handle(stream)),
+    check(lib.ds_paged_plan(_i32(cached_lens, n_seqs, "cached_lens", dev), _i32(new_lens, n_seqs, "new_lens", dev),
+                            n_seqs, _i32(free_blocks, n_free, "free_blocks", dev) if n_free else None, n_free,
+                            block_tokens, cache_rows,
+                            _i32(block_table, n_seqs * max_blocks_per_seq, "block_table", dev), max_blocks_per_seq, _i32(row_starts, n_seqs + 1, "row_starts", dev),
+                            _i32(seq_lens, n_seqs, "seq_lens", dev), _i32(row_seq, max_rows, "row_seq", dev),
+                            _i32(positions, max_rows, "positions", dev), _i32(slots, max_rows, "slots", dev), max_rows,
+                            _i32(n_taken, 1, "n_taken", dev), _here(ws), nbytes(ws), stream_handle(stream)),
           "ds_paged_plan")
 
 
@@ -338,15 +347,18 @@ def ds_rope_append(qkv, row_stride, n_rows, positions, n_axes, pair_axis, n_qh, 
         pair_axis = pair_axis.tobytes()  # (the array's .ctypes takes 2 us to build)
     if v_cache.dtype != k_cache.dtype or qkv.stride(-1) != 1:
         raise ValueError("k_cache and v_cache need one dtype, qkv's rows no gaps between elements")
-    n_kv = cache_rows * n_kvh * head_dim
+    n_kv, dev = cache_rows * n_kvh * head_dim, ws.get_device()
+    if qkv.get_device() != dev:
+        raise _elsewhere("qkv")
     # qkv may be a view of wider rows: its reach is what the storage holds from its start on
     reach = qkv.untyped_storage().nbytes() // qkv.element_size() - qkv.storage_offset()
     check(lib.ds_rope_append(qkv.data_ptr(), reach, dtype_code(qkv), row_stride, n_rows,
-                             _i32(positions, n_axes * n_rows, "positions"), n_axes,
-                             pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout, _dense(q_out, 0, "q_out"),
-                             q_out.numel(), dtype_code(q_out),
-                             _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"), dtype_code(k_cache),
-                             cache_rows, _i32(slots, n_rows, "slots"), _here(ws), nbytes(ws),
+                             _i32(positions, n_axes * n_rows, "positions", dev), n_axes,
+                             pair_axis, n_qh, n_kvh, head_dim, rot_dim, base, layout,
+                             _dense(q_out, 0, "q_out", dev), q_out.numel(), dtype_code(q_out),
+                             _dense(k_cache, n_kv, "k_cache", dev), _dense(v_cache, n_kv, "v_cache", dev),
+                             dtype_code(k_cache),
+                             cache_rows, _i32(slots, n_rows, "slots", dev), _here(ws), nbytes(ws),
                              stream_handle(stream)), "ds_rope_append")
 
 
@@ -360,14 +372,15 @@ def ds_gqa_chunk_attn(q, n_rows, row_starts, seq_lens, n_seqs, k_cache, v_cache,
     block_table None: contiguous slots."""
     if out.dtype != q.dtype or v_cache.dtype != k_cache.dtype:
         raise ValueError("q and out, and k_cache and v_cache, need one dtype each")
-    n_kv = cache_rows * n_kvh * head_dim
-    check(lib.ds_gqa_chunk_attn(_dense(q, 0, "q"), q.numel(), dtype_code(q), n_rows,
-                                _i32(row_starts, n_seqs + 1, "row_starts"), _i32(seq_lens, n_seqs, "seq_lens"), n_seqs,
-                                _dense(k_cache, n_kv, "k_cache"), _dense(v_cache, n_kv, "v_cache"),
+    n_kv, dev = cache_rows * n_kvh * head_dim, ws.get_device()
+    check(lib.ds_gqa_chunk_attn(_dense(q, 0, "q", dev), q.numel(), dtype_code(q), n_rows,
+                                _i32(row_starts, n_seqs + 1, "row_starts", dev),
+                                _i32(seq_lens, n_seqs, "seq_lens", dev), n_seqs,
+                                _dense(k_cache, n_kv, "k_cache", dev), _dense(v_cache, n_kv, "v_cache", dev),
                                 dtype_code(k_cache), cache_rows,
                                 None if block_table is None else _i32(block_table, n_seqs * max_blocks_per_seq,
-                                                                      "block_table"), max_blocks_per_seq,
-                                block_tokens, n_qh, n_kvh, head_dim, scale, _dense(out, 0, "out"), out.numel(),
+                                                                      "block_table", dev), max_blocks_per_seq,
+                                block_tokens, n_qh, n_kvh, head_dim, scale, _dense(out, 0, "out", dev), out.numel(),
                                 _here(ws), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
 
 

@@ -66,3 +66,90 @@ def test_the_chunk_attention_waits_at_no_barrier_by_what_it_read():
     assert len(conditions) >= 4
     for c in conditions:
         assert not re.search(r"\b(notes|noted|bad|dead|any|busy|valid)\b", c.replace("*dead)", "")), c
+
+
+class Placed:
+    """What the binding looks at of a tensor, on a device of choice."""
+
+    def __init__(self, dtype, n, device=0, width=None):
+        self.dtype, self.n, self.device, self.width = dtype, n, device, width
+        self.is_cuda = device >= 0
+
+    def get_device(self):
+        return self.device
+
+    def is_contiguous(self):
+        return True
+
+    def numel(self):
+        return self.n
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def data_ptr(self):
+        return 0x1000
+
+    def stride(self, dim):
+        return 1 if dim == -1 else self.width
+
+    def storage_offset(self):
+        return 0
+
+    def untyped_storage(self):
+        return self
+
+    def nbytes(self):
+        return self.n * self.element_size()
+
+
+def _calls(abi):
+    """Per operator: the tensors of a call by name, and the call."""
+    import torch
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    names = "cached new free table starts lens row_seq pos slots taken"
+    plan = {k: (i32, 64) for k in names.split()}
+    rope = dict(qkv=(f32, 4 * 384), pos=(i32, 4), q=(f32, 4 * 128), k=(f32, 8 * 128), v=(f32, 8 * 128), slots=(i32, 4))
+    attn = dict(q=(f32, 4 * 512), starts=(i32, 3), lens=(i32, 2), k=(f32, 256 * 128), v=(f32, 256 * 128),
+                table=(i32, 16), out=(f32, 4 * 512))
+    return {
+        "ds_paged_plan": (plan, lambda t, ws: abi.ds_paged_plan(
+            t["cached"], t["new"], 2, t["free"], 16, 1024, t["table"], 8, t["starts"], t["lens"], t["row_seq"],
+            t["pos"], t["slots"], 16, t["taken"], ws)),
+        "ds_rope_append": (rope, lambda t, ws: abi.ds_rope_append(
+            t["qkv"], 384, 4, t["pos"], 1, None, 2, 2, 64, 64, 1e4, 0, t["q"], t["k"], t["v"], 8, t["slots"], ws)),
+        "ds_gqa_chunk_attn": (attn, lambda t, ws: abi.ds_gqa_chunk_attn(
+            t["q"], 4, t["starts"], t["lens"], 2, t["k"], t["v"], 256, t["table"], 8, 16, 8, 2, 64, 0.125, t["out"],
+            ws)),
+    }
+
+
+@pytest.mark.parametrize("op", ["ds_paged_plan", "ds_rope_append", "ds_gqa_chunk_attn"])
+def test_the_binding_refuses_tensors_that_are_not_on_the_current_device(monkeypatch, op):
+    """Lengths, slots, tables or rows left on the host or on another GPU would be read by the kernel as addresses of the
+    current one."""
+    import torch
+    from autoregressive_decode_step_gb300 import build
+    build.build()
+    from autoregressive_decode_step_gb300 import abi
+    reached = []
+    monkeypatch.setattr(abi.lib, op, lambda *a: reached.append(a) or abi.DS_OK)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    kinds, call = _calls(abi)[op]
+    good = {k: Placed(*v) for k, v in kinds.items()}
+    ws = Placed(torch.uint8, 1 << 20)
+    call(good, ws)
+    assert len(reached) == 1
+    for name in list(kinds) + ["ws"]:
+        for device in (-1, 1):
+            moved = dict(good)
+            there = Placed(torch.uint8, 1 << 20, device) if name == "ws" else Placed(*kinds[name], device)
+            if name != "ws":
+                moved[name] = there
+            with pytest.raises(ValueError, match="device"):
+                call(moved, there if name == "ws" else ws)
+    everything = {k: Placed(*v, 1) for k, v in kinds.items()}  # together, but elsewhere
+    with pytest.raises(ValueError, match="device"):
+        call(everything, Placed(torch.uint8, 1 << 20, 1))
+    assert len(reached) == 1
