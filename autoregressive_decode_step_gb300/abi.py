@@ -326,7 +326,8 @@ def ds_paged_plan(cached_lens, new_lens, n_seqs, free_blocks, block_tokens, cach
     check(lib.ds_paged_plan(_i32(cached_lens, n_seqs, "cached_lens", dev), _i32(new_lens, n_seqs, "new_lens", dev),
                             n_seqs, _i32(free_blocks, n_free, "free_blocks", dev) if n_free else None, n_free,
                             block_tokens, cache_rows,
-                            _i32(block_table, n_seqs * max_blocks_per_seq, "block_table", dev), max_blocks_per_seq, _i32(row_starts, n_seqs + 1, "row_starts", dev),
+                            _i32(block_table, n_seqs * max_blocks_per_seq, "block_table", dev), max_blocks_per_seq,
+                            _i32(row_starts, n_seqs + 1, "row_starts", dev),
                             _i32(seq_lens, n_seqs, "seq_lens", dev), _i32(row_seq, max_rows, "row_seq", dev),
                             _i32(positions, max_rows, "positions", dev), _i32(slots, max_rows, "slots", dev), max_rows,
                             _i32(n_taken, 1, "n_taken", dev), _here(ws), nbytes(ws), stream_handle(stream)),

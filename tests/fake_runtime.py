@@ -20,9 +20,9 @@ typedef struct { unsigned g[3], b[3]; size_t smem; } config;
 static const void *fn[64];
 static int limit[64], n_fn;
 static void (*hook)(void);
-static int (*seen)(size_t, int, int, const void *);
+static int (*seen)(size_t, int, int, void **);
 void shim_hook(void (*h)(void)) { hook = h; }
-void shim_seen(int (*s)(size_t, int, int, const void *)) { seen = s; }
+void shim_seen(int (*s)(size_t, int, int, void **)) { seen = s; }
 static int *of(const void *f) {
     for (int i = 0; i < n_fn; ++i) if (fn[i] == f) return &limit[i];
     fn[n_fn] = f; limit[n_fn] = 48 * 1024; return &limit[n_fn++];
@@ -36,7 +36,7 @@ int cudaFuncSetAttribute(const void *f, int a, int v) {
 }
 int cudaLaunchKernelExC(const config *c, const void *f, void **args) {
     int status = c->smem > (size_t)*of(f) ? 1 : 0;
-    if (seen) seen(c->smem, *of(f), status, args[1]);
+    if (seen) seen(c->smem, *of(f), status, args);
     return status;
 }
 """
@@ -46,11 +46,12 @@ import ctypes, sys
 shim = ctypes.CDLL(sys.argv[1], mode=ctypes.RTLD_GLOBAL)  # found before the real runtime
 lib = ctypes.CDLL(sys.argv[2])
 launches, on_set_limit = [], []
-arg_bytes = 512
-HOOK, SEEN = ctypes.CFUNCTYPE(None), ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_size_t, ctypes.c_int, ctypes.c_int, ctypes.c_void_p)
+arg_bytes = 0
+P, I64, I, F64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_size_t
+HOOK, SEEN = ctypes.CFUNCTYPE(None), ctypes.CFUNCTYPE(I, SZ, I, I, ctypes.POINTER(P))
 @SEEN
-def seen(smem, limit, status, arg):
-    launches.append((smem, limit, status, ctypes.string_at(arg, arg_bytes)))
+def seen(smem, limit, status, args):
+    launches.append((smem, limit, status, ctypes.string_at(args[1], arg_bytes) if arg_bytes else b""))
     return 0
 @HOOK
 def hook():
@@ -59,7 +60,7 @@ def hook():
 shim.shim_seen(seen)
 shim.shim_hook(hook)
 DS_OK = 560
-P, I64, I, F64, SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_double, ctypes.c_size_t
+lib.ds_paged_plan.argtypes = [P, P, I, P, I64, I, I64, P, I, P, P, P, P, P, I64, P, P, SZ, P]
 lib.ds_rope_append.argtypes = [P, I64, I, I64, I64, P, I, P, I, I, I, I, F64, I, P, I64, I, P, P, I, I64, P, P, SZ, P]
 def rope(rows, nq, nkv, hd, rot, base, dtype=0):
     # addresses that nothing reads, far apart
@@ -77,6 +78,7 @@ def run(body, tmp_path):
     with open(src, "w") as f:
         f.write(SHIM)
     subprocess.run(["gcc", "-shared", "-fPIC", "-O1", "-o", shim, src], check=True)
-    r = subprocess.run([sys.executable, "-c", PRELUDE + textwrap.dedent(body), shim, lib], capture_output=True, text=True)
+    r = subprocess.run([sys.executable, "-c", PRELUDE + textwrap.dedent(body), shim, lib], capture_output=True,
+                       text=True)
     assert r.returncode == 0, r.stdout + r.stderr
     return r.stdout

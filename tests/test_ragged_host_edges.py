@@ -153,3 +153,72 @@ def test_the_binding_refuses_tensors_that_are_not_on_the_current_device(monkeypa
     with pytest.raises(ValueError, match="device"):
         call(everything, Placed(torch.uint8, 1 << 20, 1))
     assert len(reached) == 1
+
+
+# Buffers of their own for every argument, so that what a case changes is its only reason; the fake runtime takes the
+# place of a launch, so a check that is missing shows as a call that is accepted, with or without a GPU.
+REFUSALS = """
+import numpy as np
+AT = {n: 0x100000000 * (i + 1) for i, n in enumerate(
+    "cached new free table starts lens row_seq positions slots taken ws qkv pos q k v".split())}
+NAN, INF = float("nan"), float("inf")
+def plan(**kw):
+    a = dict(AT, n_seqs=4, n_free=8, bt=16, cache_rows=1024, width=8, rows=64, ws_bytes=256)
+    a.update(kw)
+    return lib.ds_paged_plan(a["cached"], a["new"], a["n_seqs"], a["free"], a["n_free"], a["bt"], a["cache_rows"],
+                             a["table"], a["width"], a["starts"], a["lens"], a["row_seq"], a["positions"], a["slots"],
+                             a["rows"], a["taken"], a["ws"], a["ws_bytes"], None)
+def rope(**kw):
+    hd = kw.get("hd", 64)
+    a = dict(AT, qkv_len=10 * 6 * hd, xd=0, stride=6 * hd, rows=10, axes=1, pair=None, nq=2, nkv=2, hd=hd,
+             rot=min(hd, 256), base=1e4, layout=0, q_len=10 * 2 * hd, qd=0, kd=1, cache_rows=64, ws_bytes=256)
+    a.update(kw)
+    pair = None if a["pair"] is None else np.asarray(a["pair"], np.uint8)
+    return lib.ds_rope_append(a["qkv"], a["qkv_len"], a["xd"], a["stride"], a["rows"], a["pos"], a["axes"],
+                              None if pair is None else pair.ctypes.data, a["nq"], a["nkv"], a["hd"], a["rot"],
+                              a["base"], a["layout"], a["q"], a["q_len"], a["qd"], a["k"], a["v"], a["kd"],
+                              a["cache_rows"], a["slots"], a["ws"], a["ws_bytes"], None)
+for op, change in CASES:
+    before = len(launches)
+    print(eval(op)(**eval(change)), len(launches) - before)
+"""
+
+PLAN_CASES = [
+    ("dict()", 560), ("dict(n_free=0, free=None)", 560),
+    ("dict(n_seqs=0)", 561), ("dict(bt=0)", 561), ("dict(rows=0)", 561), ("dict(n_free=-1)", 561),
+    ("dict(width=0)", 561), ("dict(cache_rows=0)", 561), ("dict(n_seqs=4097)", 564), ("dict(rows=(1 << 24) + 1)", 564),
+    ("dict(width=1 << 21)", 564), ("dict(cache_rows=(1 << 24) + 1)", 564), ("dict(n_free=(1 << 24) + 1)", 564),
+    ("dict(ws=None)", "DS_WORKSPACE_TOO_SMALL"), ("dict(ws_bytes=255)", "DS_WORKSPACE_TOO_SMALL"),
+    ("dict(ws=AT['ws'] + 8)", 577), ("dict(slots=AT['positions'] + 4 * 63)", 577),
+    ("dict(slots=AT['positions'] + 4 * 64)", 560),  # side by side
+] + [("dict(%s=None)" % n, 577) for n in
+     "cached new free table starts lens row_seq positions slots taken".split()]
+
+ROPE_CASES = [
+    ("dict()", 560), ("dict(axes=3, pair=[0] * 31 + [2])", 560), ("dict(rot=62)", 560), ("dict(hd=256)", 560),
+    ("dict(rows=0)", 561), ("dict(axes=0)", 561), ("dict(nkv=0)", 561), ("dict(rot=0)", 561),
+    ("dict(cache_rows=0)", 561),
+    ("dict(rows=(1 << 24) + 1)", 564), ("dict(cache_rows=(1 << 24) + 1)", 564),
+    ("dict(stride=6 * 64 - 1)", 562), ("dict(qkv_len=10 * 6 * 64 - 1)", 562), ("dict(q_len=10 * 2 * 64 + 1)", 563),
+    ("dict(xd=2)", 572), ("dict(qd=7)", 572), ("dict(kd=-1)", 572), ("dict(layout=2)", 572),
+    ("dict(rot=63)", 577), ("dict(rot=66)", 577), ("dict(axes=9, pair=[0] * 32)", 577), ("dict(hd=260)", 577),
+    ("dict(base=0.0)", 577), ("dict(base=-1.0)", 577), ("dict(base=NAN)", 577), ("dict(base=INF)", 577),
+    ("dict(axes=3)", 577), ("dict(axes=3, pair=[0] * 31 + [3])", 577),
+    ("dict(q=AT['qkv'] + 4 * 10 * 6 * 64 - 4)", 577), ("dict(q=AT['qkv'] + 4 * 10 * 6 * 64)", 560),
+    ("dict(v=AT['k'] + 64 * 2 * 64 * 2 - 2)", 577), ("dict(v=AT['k'] + 64 * 2 * 64 * 2)", 560),
+    ("dict(ws=None)", "DS_WORKSPACE_TOO_SMALL"), ("dict(ws_bytes=8)", "DS_WORKSPACE_TOO_SMALL"),
+    ("dict(ws=AT['ws'] + 16)", 577),
+] + [("dict(%s=None)" % n, 577) for n in "qkv pos q k v slots".split()]
+
+
+@pytest.mark.parametrize("op,cases", [("plan", PLAN_CASES), ("rope", ROPE_CASES)])
+def test_refusals_with_one_reason_each(tmp_path, op, cases):
+    from autoregressive_decode_step_gb300 import build
+    build.build()
+    from autoregressive_decode_step_gb300 import abi
+    want = [getattr(abi, c) if isinstance(c, str) else c for _, c in cases]
+    out = fake_runtime.run("CASES = %r\n" % [(op, c) for c, _ in cases] + REFUSALS, str(tmp_path))
+    got = [tuple(int(x) for x in line.split()) for line in out.splitlines()]
+    assert len(got) == len(cases)
+    for (change, _), code, (status, launched) in zip(cases, want, got):
+        assert (status, launched) == (code, int(code == abi.DS_OK)), change
