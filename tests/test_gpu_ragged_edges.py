@@ -72,7 +72,7 @@ def test_angles_of_far_positions(A, hd, rot, layout, base):
     """Pairs (1, 0) come out as cosine and sine of the angle, here worked out in 60 digits. Tolerance: 2^-33 of a turn,
     and 4 u for the fp32 argument (an eighth of a turn at most) and the two functions; 1 c - 0 s is exact."""
     getcontext().prec = 60
-    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899862803482534211706798")
+    pi = Decimal("3.141592653589793238462643383279502884197169399375105820974944592307816406286209")
     pos = [2 ** 31 - 1, 2 ** 31 - 77, 2 ** 30 + 12345, 99999989, 6000000, 131071, 0]
     n = len(pos)
     x = torch.zeros(n, 3, hd, device="cuda")
@@ -174,3 +174,64 @@ def test_values_that_are_not_finite_in_tile_after_tile(A, hd, qt):
         assert torch.equal(torch.isnan(got), torch.isnan(want))
         assert torch.equal(torch.nan_to_num(got, 0.0), torch.nan_to_num(want, 0.0))
     assert torch.equal(call(vs), clean) and A.ds_workspace_error(ws) == 0
+
+
+# ------------------------------------------------------- the digits of fp32 q
+PIECE_CASES = [(0.25, 4), (2.0, 2), (4.0, 8)]  # largest score, positions
+
+
+def piece_data(smax, T, n_seqs, nq, nkv, hd):
+    """q with one element a head that is not zero, so that a score is one product and its error a few roundings;
+    values 1 and -1, so that an output's error is that of the weights."""
+    g = torch.Generator().manual_seed(T + hd)
+    q = torch.zeros(n_seqs, nq, hd)
+    q[:, :, 5] = torch.rand(n_seqs, nq, generator=g) * 0.5 + 0.5
+    k = torch.randn(n_seqs * T, nkv, hd, generator=g)
+    k[:, :, 5] = (torch.rand(n_seqs * T, nkv, generator=g) * 2 - 1) * smax
+    v = torch.where(torch.rand(n_seqs * T, nkv, hd, generator=g) < 0.5, -1.0, 1.0)
+    return q, k.to(BF16), v.to(BF16)
+
+
+def piece_bound(smax, T):
+    """A score of three exact products: two sums, 2 u each if they are cut off, 4 u smax; times scale log2 e and from
+    the maximum, 3 u of a difference of at most 2 smax; ex2.approx 4 u and a piece's cut u. Weights off by e move the
+    mean of values +-1 by e at most. Then sums over T terms: products cut off (2 u), weights (u), three rows added, the
+    reciprocal and its product, 8 u."""
+    return (10 * smax + 5 + 3 * T + 8) * U
+
+
+def pieces(x, n):
+    """The first n of the bf16 numbers that add up to fp32 x, added."""
+    total = torch.zeros_like(x, dtype=torch.float64)
+    for _ in range(n):
+        top = (x.view(torch.int32) & -65536).view(F32)
+        total += top.double()
+        x = x - top
+    return total
+
+
+def piece_reference(q, k, v, T, q_pieces=None, p_pieces=None):
+    """fp64 attention of one row a sequence over its T positions (scale 1); with piece counts, what is left if the
+    others were lost."""
+    n, nq, hd = q.shape
+    kk, vv = (x.double().view(n, T, -1, hd).repeat_interleave(nq // x.shape[1], 2) for x in (k, v))
+    e = torch.einsum("nhd,nthd->nht", q.double() if q_pieces is None else pieces(q, q_pieces), kk)
+    p = torch.exp(e - e.amax(2, keepdim=True))
+    w = p if p_pieces is None else pieces(p.float(), p_pieces)
+    return torch.einsum("nht,nthd->nhd", w, vv) / p.sum(2)[..., None]
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("smax,T", PIECE_CASES)
+def test_fp32_attention_keeps_fp32_digits(A, smax, T, hd):
+    n, nq, nkv = 40, 8, 2
+    q, k, v = piece_data(smax, T, n, nq, nkv, hd)
+    bt = 8                                   # a block a sequence
+    kc, vc = (torch.full((n, bt, nkv * hd), float("nan")).to(BF16) for _ in range(2))
+    kc[:, :T], vc[:, :T] = k.view(n, T, -1), v.view(n, T, -1)
+    out = torch.zeros(n, nq * hd, device="cuda")
+    ws = A.workspace(A.ds_chunk_attention_workspace_bytes(n, n, nq, nkv, hd))
+    A.ds_gqa_chunk_attn(q.view(n, -1).cuda(), n, i32(range(n + 1)), i32([T] * n), n, kc.view(n * bt, -1).cuda(),
+                        vc.view(n * bt, -1).cuda(), n * bt, None, 1, bt, nq, nkv, hd, 1.0, out, ws)
+    err = (out.double().cpu().view(n, nq, hd) - piece_reference(q, k, v, T)).abs().max()
+    assert err <= piece_bound(smax, T), float(err) / U

@@ -222,3 +222,18 @@ def test_refusals_with_one_reason_each(tmp_path, op, cases):
     assert len(got) == len(cases)
     for (change, _), code, (status, launched) in zip(cases, want, got):
         assert (status, launched) == (code, int(code == abi.DS_OK)), change
+
+
+@pytest.mark.parametrize("hd", [64, 128])
+def test_a_lost_piece_of_fp32_attention_would_show(hd):
+    """The bound that the fp32 attention is held to on the GPU, on the CPU: attention with a piece of q or of the weights
+    left out breaks it in one case at least, with all of them it does not."""
+    from tests.test_gpu_ragged_edges import PIECE_CASES, piece_bound, piece_data, piece_reference
+    worst = {}
+    for smax, T in PIECE_CASES:
+        q, k, v = piece_data(smax, T, 40, 8, 2, hd)
+        want = piece_reference(q, k, v, T)
+        for kept in ((3, 3), (2, 3), (3, 2)):
+            err = (piece_reference(q, k, v, T, *kept) - want).abs().max()
+            worst[kept] = max(worst.get(kept, 0), float(err) / piece_bound(smax, T))
+    assert worst[3, 3] <= 0.25 and worst[2, 3] > 1.5 and worst[3, 2] > 1.5, worst
