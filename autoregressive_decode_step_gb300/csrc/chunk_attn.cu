@@ -24,7 +24,6 @@
 // Warps whose pairs are all behind the tile's last skip a step's work (without
 // that and with loads waited for one by one the 64 tokens took 1,210 us).
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <type_traits>
 

@@ -21,12 +21,20 @@
 //    copies, so the bytes in flight do not hang on the threads that wait for
 //    them.
 // A row's angles are formed once, in shared memory, for all its heads.
-// Measured, bf16 rows of 32 + 8 + 8 heads of 128 (24,576 bytes in and out):
-//   rows          512    1,001   2,048   4,096   8,192
-//   first        4.5 us  7.3    13.2    24.0    43.9
-//   second       4.8     6.6    11.2    18.0    35.2   (5.7 TB/s)
-// (fp32 rows 4.8 / 5.6 us at 512, 53.2 / 48.0 at 8,192; one block per row with
-// everything worked out anew, the first version: 60 us at 8,192.)
+// Measured in a graph, us, heads of 128; up to 2,048 rows stay in L2:
+//   rows                            512   1,001  1,500  2,048  4,096  8,192
+//   32 + 8 + 8 bf16          first  4.3    6.4    8.1   10.3   20.5   44.4
+//                            second 4.6    6.5    8.1    9.7   15.9   35.1  (5.7 TB/s)
+//   32 + 8 + 8 fp32 to bf16  first  4.9    7.3    9.2   11.9   25.0   53.7
+//                            second 5.6    8.2   10.1   12.9   23.7   48.9
+//   32 + 8 + 8 fp32 to fp32  first  6.2    9.7   12.9   16.8   35.9   67.6
+//                            second 6.7    9.7   12.4   15.6   35.6   69.3
+//   4 + 2 + 2 bf16           first  3.2    4.0    4.5    5.4    8.0   13.3
+//                            second 3.3    4.2    5.1    6.0    8.8   15.0
+// So kRaBulkRows suits wide bf16 rows; wide fp32 rows lose up to 8 % or win 9 %
+// by it and narrow rows lose 10 %.  Rows of single elements (see the entry
+// point) always take the first kernel: 1,001 rows of 14 + 2 + 2 fp32 heads of
+// 80, 40 dims of them rotated, 8.8 us, 8,192 rows 65.
 #include <algorithm>
 #include <cmath>
 
@@ -147,11 +155,9 @@ __device__ __forceinline__ void ra_rotate(const float (&u)[W], const float (&w)[
     }
 }
 
-// Items of a row that a thread has: W pairs of a q or k head (two chunks of W
+// A thread has one item of a row: W pairs of a q or k head (two chunks of W
 // elements), or W elements as they are (the tail of a q or k head, or v).
 // (Two a thread: half the blocks stay resident, 47 us against 44 at 8,192.)
-constexpr int kRaItems = 1;
-
 template <typename XT, typename QT, typename KT, int W, int P>
 __global__ void __launch_bounds__(kRaThreads)
     rope_append_kernel(const __grid_constant__ RopeAppendArgs a, const __grid_constant__ RopeTurns<P> turns) {
@@ -160,36 +166,31 @@ __global__ void __launch_bounds__(kRaThreads)
     const bool split = a.layout == DS_ROPE_HALF_SPLIT;
     const int tid = threadIdx.x;
 
-    // what this thread's items are
-    int src[kRaItems], apart[kRaItems], pair[kRaItems], dst[kRaItems], to[kRaItems];  // to: 0 q, 1 k, 2 v, -1 none
+    // what this thread's item is
+    int src = 0, apart = 0, pair = 0, dst = 0, to = -1;  // to: 0 q, 1 k, 2 v, -1 none
     {
         const int per_rot = half / W, per_cp = (hd - a.rot) / W, per_v = hd / W;
         const int n1 = n_rot * per_rot, n2 = n1 + n_rot * per_cp, n3 = n2 + a.n_kvh * per_v;
-#pragma unroll
-        for (int k = 0; k < kRaItems; ++k) {
-            const int i = (blockIdx.y * kRaItems + k) * kRaThreads + tid;
-            int head = 0, d = 0, d1 = -1;
-            pair[k] = 0;
-            if (i < n1) {
-                head = i / per_rot;
-                pair[k] = (i % per_rot) * W;
-                d = split ? pair[k] : 2 * pair[k];
-                d1 = split ? pair[k] + half : d + W;
-            } else if (i < n2) {
-                head = (i - n1) / per_cp;
-                d = a.rot + ((i - n1) % per_cp) * W;
-            } else if (i < n3) {
-                head = n_rot + (i - n2) / per_v;
-                d = ((i - n2) % per_v) * W;
-            }
-            to[k] = i >= n3 ? -1 : head < a.n_qh ? 0 : head < n_rot ? 1 : 2;
-            src[k] = head * hd + d;
-            apart[k] = d1 < 0 ? 0 : d1 - d;  // the second chunk is so far behind the first; 0: none
-            dst[k] = (to[k] <= 0 ? head : to[k] == 1 ? head - a.n_qh : head - n_rot) * hd + d;
+        const int i = blockIdx.y * kRaThreads + tid;
+        int head = 0, d = 0;
+        if (i < n1) {
+            head = i / per_rot;
+            pair = (i % per_rot) * W;
+            d = split ? pair : 2 * pair;
+            apart = split ? half : W;  // the second chunk is so far behind the first; 0: none
+        } else if (i < n2) {
+            head = (i - n1) / per_cp;
+            d = a.rot + ((i - n1) % per_cp) * W;
+        } else if (i < n3) {
+            head = n_rot + (i - n2) / per_v;
+            d = ((i - n2) % per_v) * W;
         }
+        to = i >= n3 ? -1 : head < a.n_qh ? 0 : head < n_rot ? 1 : 2;
+        src = head * hd + d;
+        dst = (to <= 0 ? head : to == 1 ? head - a.n_qh : head - n_rot) * hd + d;
     }
 
-    RaChunk<XT, W> x0[kRaItems], x1[kRaItems];
+    RaChunk<XT, W> x0, x1;
     const int step = gridDim.x;
     int r = blockIdx.x;
     const int axis_row = tid < half ? turns.axis[tid] : 0;
@@ -197,11 +198,8 @@ __global__ void __launch_bounds__(kRaThreads)
     auto pos_of = [&](int row) { return tid < half ? __ldg(a.positions + (long long)axis_row * a.n_rows + row) : 0; };
     auto fetch = [&](int row) {
         const XT *x = static_cast<const XT *>(a.x) + (long long)row * a.row_stride;
-#pragma unroll
-        for (int k = 0; k < kRaItems; ++k) {
-            if (to[k] >= 0) x0[k].load(x + src[k]);
-            if (apart[k]) x1[k].load(x + src[k] + apart[k]);
-        }
+        if (to >= 0) x0.load(x + src);
+        if (apart) x1.load(x + src + apart);
     };
     int slot = __ldg(a.slots + r), pos = pos_of(r);
     if (slot >= 0) fetch(r);  // a negative slot: a row of padding
@@ -220,43 +218,36 @@ __global__ void __launch_bounds__(kRaThreads)
         // (two sets of angles: a thread may be a row ahead, not two)
         const int bad = __syncthreads_or(slot >= 0 && (pos < 0 || slot >= a.cache_rows));
         if (bad && tid == 0) flag_error(a.err, DS_ERR_POSITION);
-        const bool ok = slot >= 0 && !bad;
-        float y0[kRaItems][W], y1[kRaItems][W];
-#pragma unroll
-        for (int k = 0; k < kRaItems; ++k) {
-            if (!ok || to[k] < 0) continue;
-            x0[k].get(y0[k]);
-            if (!apart[k]) continue;
+        const bool ok = slot >= 0 && !bad && to >= 0;
+        float y0[W], y1[W];
+        if (ok) x0.get(y0);
+        if (ok && apart) {
             float u[W], w[W], c[W], s[W];
-            x0[k].get(u);
-            x1[k].get(w);
+            x0.get(u);
+            x1.get(w);
             if constexpr (W == 8) {
 #pragma unroll
                 for (int e = 0; e < 8; e += 4) {
-                    const float4 c4 = *reinterpret_cast<const float4 *>(&cosine[buf][pair[k] + e]);
-                    const float4 s4 = *reinterpret_cast<const float4 *>(&sine[buf][pair[k] + e]);
+                    const float4 c4 = *reinterpret_cast<const float4 *>(&cosine[buf][pair + e]);
+                    const float4 s4 = *reinterpret_cast<const float4 *>(&sine[buf][pair + e]);
                     c[e] = c4.x; c[e + 1] = c4.y; c[e + 2] = c4.z; c[e + 3] = c4.w;
                     s[e] = s4.x; s[e + 1] = s4.y; s[e + 2] = s4.z; s[e + 3] = s4.w;
                 }
             } else {
-                c[0] = cosine[buf][pair[k]];
-                s[0] = sine[buf][pair[k]];
+                c[0] = cosine[buf][pair];
+                s[0] = sine[buf][pair];
             }
-            ra_rotate(u, w, c, s, split, y0[k], y1[k]);
+            ra_rotate(u, w, c, s, split, y0, y1);
         }
         if (slot_n >= 0) fetch(next);
-#pragma unroll
-        for (int k = 0; k < kRaItems; ++k) {
-            if (!ok || to[k] < 0) continue;
-            if (to[k] == 0) {
-                QT *q = static_cast<QT *>(a.q) + (long long)r * a.n_qh * hd + dst[k];
-                ra_store(q, y0[k]);
-                if (apart[k]) ra_store(q + apart[k], y1[k]);
-            } else {
-                KT *p = static_cast<KT *>(to[k] == 1 ? a.k_cache : a.v_cache) + (long long)slot * a.n_kvh * hd + dst[k];
-                ra_store(p, y0[k]);
-                if (apart[k]) ra_store(p + apart[k], y1[k]);
-            }
+        if (ok && to == 0) {
+            QT *q = static_cast<QT *>(a.q) + (long long)r * a.n_qh * hd + dst;
+            ra_store(q, y0);
+            if (apart) ra_store(q + apart, y1);
+        } else if (ok) {
+            KT *p = static_cast<KT *>(to == 1 ? a.k_cache : a.v_cache) + (long long)slot * a.n_kvh * hd + dst;
+            ra_store(p, y0);
+            if (apart) ra_store(p + apart, y1);
         }
         slot = slot_n;
         pos = pos_n;
@@ -398,7 +389,7 @@ template <typename XT, typename QT, typename KT, int P>
 static cudaError_t launch_ra(const RopeAppendArgs &a, const RopeTurns<P> &t, bool vec, cudaStream_t s) {
     const int w = vec ? 8 : 1;
     const int items = (a.n_qh + a.n_kvh) * (a.rot / 2 / w + (a.hd - a.rot) / w) + a.n_kvh * (a.hd / w);
-    const int ny = (items + kRaItems * kRaThreads - 1) / (kRaItems * kRaThreads);
+    const int ny = (items + kRaThreads - 1) / kRaThreads;
     const int row_bytes = (a.n_qh + 2 * a.n_kvh) * a.hd * (int)sizeof(XT);
     const long long smem = (long long)kRaStages * row_bytes + (long long)items * sizeof(RaItem);
     if (vec && a.n_rows >= kRaBulkRows && smem <= kRaBulkSmem)
