@@ -21,7 +21,8 @@
 // running maximum and sum each, joined at the end: the same overlap.
 //
 // fp32 q (PARTS 3): q and P each go to the tensor core as three bf16 numbers
-// that add up to them (24 bits cut in three).  The pieces of q are three MMAs
+// that add up to them (24 bits cut in three; where q has fewer bits its empty
+// pieces are 2^-30 and 2^-60 of it, see load_q).  The pieces of q are three MMAs
 // into one S.  The pieces of P are rows of one MMA: a part has 40 pairs, each
 // in three rows of a warp with the same S (10 pairs a warp), and row by row
 // the warp writes the high, the middle and the low piece; O is the sum of the
@@ -32,8 +33,10 @@
 // The running maximum that P is taken relative to is moved (and O rescaled)
 // only when a row's maximum has grown by more than 2^8: P then stays below
 // 2^8, which costs bf16 and fp32 no digits, and O is rescaled a few times in
-// a tile instead of every step.  P is rounded to bf16 (PARTS 1), the sum adds
-// the fp32 weights.
+// a tile instead of every step.  P is rounded to bf16 (PARTS 1), because a
+// second piece of it would double the second product: 2^-8 of a weight at most,
+// in the mean 1.3e-3 of the output beside the 1.6e-3 of its own rounding.  The
+// sum adds the fp32 weights.
 //
 // A step that reaches past the first row's position is masked per row.  V
 // there may hold anything (another row's NaN, the stale rest of a page), and
@@ -42,13 +45,16 @@
 // that only some of the rows attend is zeroed and noted, to be added to the
 // rows that do attend it at the end.
 //
-// Measured, heads of 128, 32 on 8, pages of 16: a bf16 prompt of 8,192 in 447
-// us (1,228 TFLOP/s; the tensor pipe is active 55 % of the cycles, the softmax
-// between a step's two products and the tiles' ends bound it); 64 single
-// tokens with fp32 q over up to 4,096 positions in 136 us (3.8 TB/s; idle from
-// a tile's last step to the next one's first, 8,000 to 10,000 cycles); one
-// bf16 token over 1,024 in 13.7 us with the joining launch (latency); 256 fp32
-// rows behind 768 positions in 50 us.
+// Measured in a graph, heads of 128, 32 on 8, pages of 16: a bf16 prompt of
+// 8,192 in 456 us (1,206 TFLOP/s; the tensor pipe is active 55 % of the cycles,
+// the softmax between a step's two products and the tiles' ends bound it); 64
+// single tokens over up to 4,096 positions with bf16 q in 110 us (4.7 TB/s),
+// with fp32 q in 137 (3.8 TB/s; idle from a tile's last step to the next one's
+// first, 8,000 to 10,000 cycles); one bf16 token over 1,024 in 13.9 us with the
+// joining launch (latency); 256 fp32 rows behind 768 positions in 51 us, 2,048
+// from position 0 in 306 (40 pairs a tile).
+// Registers: 168 a thread in every variant; spilled: none with bf16 q, 20 bytes
+// <64, 3>, 116 bytes <128, 3>.
 //
 // Every wait is bounded; after one gives up all others return at once and the
 // kernel runs to its end without them (its barriers still pair up), flagged.
@@ -72,7 +78,9 @@ constexpr int kCtSegs = 4;       // segments handed out and not yet done with
 // about 1.5 times as long as one of a tile that takes turns; beginning and
 // ending a tile takes about as long as two steps, with fp32 q as four (swept
 // from 256 to 2048: 64 single fp32 tokens 158 us at 256, 148 at 512, 138 at
-// 1024, 146 at 2048; a bf16 prompt of 8192 464, 446, 452, 470).
+// 1024, 146 at 2048; a bf16 prompt of 8192 464, 446, 452, 470).  With fp32 q
+// every tile takes turns, so the weights rate its whole tiles above the last
+// one of a sequence without cause; equal ones have not been measured.
 constexpr int kCtWeightTurns = 2, kCtWeightShared = 3, kCtTileCost = 2 * 256, kCtTileCostF32 = 2 * 512;
 constexpr int kCtPiece = 256;
 constexpr int kCtHalf = 128 * 128;  // bytes of 128 rows of one 64-element (128-byte) half
