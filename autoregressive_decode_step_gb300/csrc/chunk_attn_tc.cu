@@ -313,8 +313,8 @@ __device__ __forceinline__ float ct_noted(unsigned w, int rel) {
 
 // The sum of a row's weights times column d of V over positions [t0, t1), of
 // which the tensor core made NaN although the weights are finite: a weight (or
-// a part of it) that is zero or negative met an infinity.  Every weight is
-// positive, so the infinities decide.
+// a part of it) that is zero or negative met an infinity.  Weights are taken as
+// positive, so the infinities decide (also behind a key that is infinite).
 __device__ __noinline__ float ct_infinite(const ChunkArgs &a, int seq, int kv, int d, int t0, int t1) {
     float sum = 0.0f;
     int flags = 0;
@@ -937,13 +937,13 @@ __global__ void __launch_bounds__(kCtThreads, 1)
                         }
                         __syncwarp();
                     }
-                    if (row_at >= 0 && ((any != any && sum == sum) || notes)) {
+                    if (row_at >= 0 && ((any != any && sum > 0.0f) || notes)) {
                         // rare: columns with infinities or NaN, put right where they went
                         void *to_mem = split ? static_cast<void *>(rec) : a.out;
                         const int dt = split ? DS_F32 : a.q_dtype;
                         for (int d = 0; d < HD; ++d) {
                             float x = load_as(to_mem, row_at + d, dt);
-                            if (x != x && sum == sum)
+                            if (x != x && sum > 0.0f)  // (0: every score is -inf, the row is NaN)
                                 x = ct_infinite(a, g.seq, cur->heads.kv, d, g.b0 * kCtStep,
                                                 min(g.b1 * kCtStep, g.pos0 + rel + 1));
                             if (notes) x += ct_noted(sh.note[par][d], rel);

@@ -387,7 +387,8 @@ DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t n_rows, int
  * A row that attends nothing (L < n) is zero.  Rows of no sequence (in front
  * of row_starts[0], behind row_starts[n_seqs]) stay as they were.  What the
  * cache holds at positions a row does not attend, NaN and infinities
- * included, does not reach it; what it does attend counts as in the formula.
+ * included, does not reach it; what it does attend counts as in the formula
+ * (but an infinite value may show although its weight is zero).
  * Row starts that fall or pass n_rows and lengths outside the table row are
  * clamped (an element of a row that two sequences then claim is one's or the
  * other's), a block number outside the cache reads block 0; all flag

@@ -66,6 +66,23 @@ def test_an_infinite_key_that_a_row_attends(A, new, hd, qt, kvt):
     assert A.ds_workspace_error(ws) == 0
 
 
+@pytest.mark.parametrize("qt,kvt", [(F32, BF16), (BF16, BF16), (F32, F32)])
+@pytest.mark.parametrize("T", [1, 130, 700])
+def test_a_row_with_every_score_minus_infinity_is_nan(A, T, qt, kvt):
+    """No weight is left to divide by, whatever the values are: infinite ones do not show as infinities."""
+    nq, nkv, hd = 4, 2, 64
+    q = torch.ones(1, nq * hd, dtype=qt, device="cuda")
+    k, v = (torch.randn(704, nkv * hd, device="cuda").to(kvt) for _ in range(2))
+    k[:, 5] = -math.inf                     # every key of the first head
+    v[0, 3], v[T - 1, 9], v[0, hd + 3] = math.inf, -math.inf, math.inf
+    out = torch.zeros_like(q)
+    ws = A.workspace(A.ds_chunk_attention_workspace_bytes(1, 1, nq, nkv, hd))
+    A.ds_gqa_chunk_attn(q, 1, i32([0, 1]), i32([T]), 1, k, v, 704, None, 44, 16, nq, nkv, hd, 0.125, out, ws)
+    got = out.view(nq, hd)
+    assert torch.isnan(got[:2]).all()
+    assert (got[2:, 3] == math.inf).all() and torch.isfinite(got[2:, 4:]).all()
+
+
 @pytest.mark.parametrize("base", [1e-3, 10000.0, 500000.0, 1e6])
 @pytest.mark.parametrize("hd,rot,layout", [(128, 128, 0), (256, 256, 1), (96, 80, 1), (6, 6, 0)])
 def test_angles_of_far_positions(A, hd, rot, layout, base):
