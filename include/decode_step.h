@@ -396,8 +396,8 @@ DS_API size_t ds_chunk_attention_workspace_bytes(int n_seqs, int64_t n_rows, int
  * A bf16 cache with head_dim 64 or 128 and block_tokens a multiple of 8 runs
  * on the tensor cores.  There bf16 q has each weight of the softmax rounded to
  * bf16 before it meets v (2^-8 of the weight at most; sums stay fp32 and take
- * it unrounded): outputs are 2.0e-3 to 2.3e-3 from 64 bits in the mean, of which
- * their own rounding makes 1.5e-3 to 1.7e-3.  fp32 q keeps the digits of fp32
+ * it unrounded): on normal inputs outputs are 2.0e-3 to 2.3e-3 from 64 bits in
+ * the mean, of which their own rounding makes 1.5e-3 to 1.7e-3.  fp32 q keeps the digits of fp32
  * products.  fp32 caches, other heads and other pages run on the plain cores,
  * in fp32 throughout and slower the longer the chunks (2,048 bf16 rows of 32
  * heads: 62 us, with heads of 80 or pages of 7 positions 1,012); their tile

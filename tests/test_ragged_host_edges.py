@@ -226,8 +226,8 @@ def test_refusals_with_one_reason_each(tmp_path, op, cases):
 
 @pytest.mark.parametrize("hd", [64, 128])
 def test_a_lost_piece_of_fp32_attention_would_show(hd):
-    """The bound that the fp32 attention is held to on the GPU, on the CPU: attention with a piece of q or of the weights
-    left out breaks it in one case at least, with all of them it does not."""
+    """The bound that the fp32 attention is held to on the GPU, on the CPU: attention with a piece of q or of the
+    weights left out breaks it in one case at least, with all of them it does not."""
     from tests.test_gpu_ragged_edges import PIECE_CASES, piece_bound, piece_data, piece_reference
     worst = {}
     for smax, T in PIECE_CASES:
