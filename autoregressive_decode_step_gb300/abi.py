@@ -39,7 +39,7 @@ DS_BAD_SAMPLING_PARAM = 575
 DS_TOKEN_OUT_OF_RANGE = 576
 DS_BAD_ARGUMENT = 577
 DS_MAX_DIM = 1 << 24
-DS_F32, DS_BF16 = 0, 1
+DS_F32, DS_BF16, DS_E4M3 = 0, 1, 2
 DS_ROPE_HALF_SPLIT, DS_ROPE_INTERLEAVED = 0, 1
 DS_ERR_TOKEN_RANGE, DS_ERR_POSITION, DS_ERR_WAIT_TIMEOUT, DS_ERR_SAMPLING = 1, 2, 4, 8
 DS_ERR_NO_BLOCKS = 16
@@ -114,6 +114,10 @@ _sig("ds_sched_stats", ctypes.c_int, P, P)
 _sig("ds_sched_generated", I64, P, I64)
 _sig("ds_gemm_transposed", ctypes.c_int, P, I64, P, I64, I64, I64, I64, P, I64, P, SZ, P)
 _sig("ds_gemm", ctypes.c_int, P, I64, P, I64, I64, I64, I64, P, I64, P, SZ, P)
+_sig("ds_fp8_quantize", ctypes.c_int, P, I64, ctypes.c_int, I64, I64, I64, ctypes.c_int, P, I64, I64, P, I64, P)
+_sig("ds_gemm_fp8_workspace_bytes", SZ, I64, I64, I64)
+_sig("ds_gemm_fp8", ctypes.c_int, P, I64, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, P, I64, ctypes.c_int, I64, P,
+     SZ, P)
 _sig("ds_gemv_transposed_noalloc", ctypes.c_int, P, I64, ctypes.c_int, P, I64, I64, I64, P, I64, P)
 _sig("ds_gemv_transposed_noalloc_max_bytes", SZ)
 _sig("ds_gemv_transposed_noalloc_error", ctypes.c_int, P, P)
@@ -383,6 +387,63 @@ def ds_gqa_chunk_attn(q, n_rows, row_starts, seq_lens, n_seqs, k_cache, v_cache,
                                                                       "block_table", dev), max_blocks_per_seq,
                                 block_tokens, n_qh, n_kvh, head_dim, scale, _dense(out, 0, "out", dev), out.numel(),
                                 _here(ws), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
+
+
+def _rows(t, shape, dtypes, name, dev, unit=1):
+    """(address, elements, row stride) of a 2-D tensor of this shape and one of
+    these types whose rows have no gaps; a lone row's stride is its width in
+    whole units."""
+    if t.dtype not in dtypes or tuple(t.shape) != shape or (t.stride(1) != 1 and shape[1] > 1):
+        raise ValueError("%s: a tensor of shape %s with dense rows of %s is needed"
+                         % (name, shape, " or ".join(str(d) for d in dtypes)))
+    if t.get_device() != dev:
+        raise _elsewhere(name)
+    stride = t.stride(0) if shape[0] > 1 else -(-shape[1] // unit) * unit
+    return t.data_ptr(), (shape[0] - 1) * stride + shape[1], stride
+
+
+_E4M3, _FLOATS = (torch.float8_e4m3fn,), (torch.float32, torch.bfloat16)
+
+
+def _scales(t, shape, name, dev):
+    """Address and length of a contiguous fp32 tensor of block scales."""
+    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous fp32 tensor of shape %s is needed" % (name, shape))
+    if t.get_device() != dev:
+        raise _elsewhere(name)
+    return t.data_ptr(), t.numel()
+
+
+def ds_fp8_quantize(x, block_rows, q, scales, stream=None):
+    """x [rows][cols] as e4m3 codes in q with a scale for each block_rows x 128
+    (1: activations, 128: weights); the rows of x and q may be views of wider ones."""
+    dev = torch._C._cuda_getDevice()
+    rows, cols = x.shape
+    if block_rows not in (1, 128):
+        raise DecodeStepError(DS_BAD_ARGUMENT, "ds_fp8_quantize")
+    xp, xn, xs = _rows(x, (rows, cols), _FLOATS, "x", dev)
+    qp, qn, qs = _rows(q, (rows, cols), _E4M3, "q", dev)
+    sp, sn = _scales(scales, (-(-rows // block_rows), -(-cols // 128)), "scales", dev)
+    check(lib.ds_fp8_quantize(xp, xn, dtype_code(x), xs, rows, cols, block_rows, qp, qn, qs, sp, sn,
+                              stream_handle(stream)), "ds_fp8_quantize")
+
+
+def ds_gemm_fp8_workspace_bytes(n, rows, cols):
+    return lib.ds_gemm_fp8_workspace_bytes(n, rows, cols)
+
+
+def ds_gemm_fp8(W, w_scales, X, x_scales, Y, ws, stream=None):
+    """Y [n][rows] = X [n][cols] W [rows][cols]^T of e4m3 codes and their block scales."""
+    dev = ws.get_device()
+    (rows, cols), n = W.shape, X.shape[0]
+    kb = -(-cols // 128)
+    wp, wn, wst = _rows(W, (rows, cols), _E4M3, "W", dev, 16)
+    xp, xn, xst = _rows(X, (n, cols), _E4M3, "X", dev, 16)
+    yp, yn, yst = _rows(Y, (n, rows), _FLOATS, "Y", dev)
+    wsp, wsn = _scales(w_scales, (-(-rows // 128), kb), "w_scales", dev)
+    xsp, xsn = _scales(x_scales, (n, kb), "x_scales", dev)
+    check(lib.ds_gemm_fp8(wp, wn, wst, wsp, wsn, xp, xn, xst, xsp, xsn, n, rows, cols, yp, yn, dtype_code(Y), yst,
+                          _here(ws), nbytes(ws), stream_handle(stream)), "ds_gemm_fp8")
 
 
 def ds_argmax_workspace_bytes(n_rows, n):

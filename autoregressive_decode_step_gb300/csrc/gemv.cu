@@ -414,6 +414,11 @@ static bool encode_band_map(CUtensorMap *m, const void *base, int dtype, long lo
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+static CUtensorMapDataType tiled_type(int dtype) {
+    return dtype == DS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+           : dtype == DS_E4M3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+}
+
 bool encode_tiled_2d(CUtensorMap *m, const void *base, int dtype, long long cols, long long rows,
                      long long row_stride, int box_cols, int box_rows, bool swizzle128) {
     EncodeTiledFn fn = encode_fn();
@@ -422,7 +427,7 @@ bool encode_tiled_2d(CUtensorMap *m, const void *base, int dtype, long long cols
     const cuuint64_t strides[1] = {(cuuint64_t)row_stride};
     const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
     const cuuint32_t estr[2] = {1, 1};
-    const CUtensorMapDataType dt = dtype == DS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUtensorMapDataType dt = tiled_type(dtype);
     return fn(m, dt, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
@@ -436,7 +441,7 @@ bool encode_tiled_3d(CUtensorMap *m, const void *base, int dtype, const long lon
     const cuuint64_t st[2] = {(cuuint64_t)strides[0], (cuuint64_t)strides[1]};
     const cuuint32_t bx[3] = {(cuuint32_t)box[0], (cuuint32_t)box[1], (cuuint32_t)box[2]};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUtensorMapDataType dt = dtype == DS_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+    const CUtensorMapDataType dt = tiled_type(dtype);
     return fn(m, dt, 3, const_cast<void *>(base), d, st, bx, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               swizzle128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;

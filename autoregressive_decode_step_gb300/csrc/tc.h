@@ -8,7 +8,7 @@
 namespace ds {
 
 // Encode a 2-D tensor map over a row-major matrix of `rows` rows of `cols`
-// elements (dtype DS_F32 / DS_BF16) with rows `row_stride` bytes apart, boxes
+// elements (dtype DS_F32 / DS_BF16 / DS_E4M3) with rows `row_stride` bytes apart, boxes
 // of box_cols x box_rows elements, 128-byte swizzled or not.  False if the
 // driver refuses.
 bool encode_tiled_2d(CUtensorMap *map, const void *base, int dtype, long long cols, long long rows,

@@ -75,8 +75,9 @@ enum {
  * "LLM inference kernels" page ("Status vocabulary and the shape checks"). */
 #define DS_MAX_DIM (1LL << 24)
 
-/* Storage dtypes. */
-enum { DS_F32 = 0, DS_BF16 = 1 };
+/* Storage dtypes.  DS_E4M3 (8-bit floating point: sign, 4 bits of exponent, 3
+ * of mantissa, 0x7F and 0xFF NaN, no infinities) is taken where a call says so. */
+enum { DS_F32 = 0, DS_BF16 = 1, DS_E4M3 = 2 };
 
 /* RoPE layouts: pairs (p, p + head_dim/2) — the GPT-NeoX split-half
  * convention ("LLM inference kernels", "Two gaps, not three") — or pairs
@@ -203,6 +204,62 @@ DS_API int ds_gemm_transposed(const void *A, int64_t a_len, const void *X, int64
 DS_API int ds_gemm(const void *W, int64_t w_len, const void *X, int64_t x_len, int64_t n, int64_t rows,
                    int64_t cols, float *Y, int64_t y_len, void *workspace, size_t workspace_bytes,
                    ds_stream_t stream);
+
+/* ---------------------------------------------------------------------
+ * 8-bit projections
+ *
+ * Weights and activations in e4m3 with an fp32 scale for each block: a
+ * projection then streams half the bytes of bf16.  Weights are untransposed
+ * ([out][in], ds_gemm's form) with a scale for each 128 x 128 block,
+ * activations have one for each 128 values of a row.  A value stands for
+ * code x scale.
+ * ------------------------------------------------------------------- */
+
+/* Rows (block_rows 1: activations) or a matrix (block_rows 128: weights) in
+ * e4m3.  For each block of block_rows x 128 values (fewer at the ends):
+ *   top = max |x|, at least 2^-96;  scale = top / 448;
+ *   code = e4m3(x * (448 / top)), to nearest, ties to even;
+ * top, quotients and product in fp32.  A block that holds a NaN or an infinity
+ * has scale NaN and codes NaN.
+ *   x: `rows` rows of `cols` fp32 or bf16 elements, x_stride elements apart;
+ *   x_len counts the elements from x on ((rows - 1) * x_stride + cols at
+ *   least, else 562).  q: codes, rows q_stride bytes apart (563 likewise; the
+ *   bytes between rows stay as they were).  scales: fp32
+ *   [ceil(rows / block_rows)][ceil(cols / 128)] (563).  q and scales overlap
+ *   nothing (577).  561 / 564 for an empty / oversized dimension or stride,
+ *   572 for another x_dtype, 577 for another block_rows.
+ * Rows that start on 16 bytes (q on 8) are read 16 bytes at a time. */
+DS_API int ds_fp8_quantize(const void *x, int64_t x_len, int x_dtype, int64_t x_stride, int64_t rows,
+                           int64_t cols, int block_rows, void *q, int64_t q_len, int64_t q_stride,
+                           float *scales, int64_t scales_len, ds_stream_t stream);
+
+/* Workspace bytes ds_gemm_fp8 needs for these sizes (a workspace that several
+ * sizes share is as large as the largest of their answers; a larger n may need
+ * less); 0 for a dimension < 1 or past DS_MAX_DIM. */
+DS_API size_t ds_gemm_fp8_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
+
+/* Y[s][r] = sum_b x_scales[s][b] * w_scales[r / 128][b]
+ *           * sum_{c in [128 b, 128 b + 128), c < cols} X[s][c] * W[r][c]
+ * for s < n, r < rows: ds_gemm's untransposed product of e4m3 operands, the
+ * products of a block summed by the tensor cores in fp32, the blocks in fp32.
+ * n is any count from a single token to a whole prompt.
+ *   W: e4m3, rows w_stride bytes apart; w_scales: fp32 [ceil(rows / 128)]
+ *   [ceil(cols / 128)] (569).  X: e4m3 [n], rows x_stride bytes apart;
+ *   x_scales: fp32 [n][ceil(cols / 128)] (570).  Y: fp32 or bf16 (572), rows
+ *   y_stride elements apart (562).  w_len, x_len, y_len count the elements
+ *   from the pointer on, (count - 1) * stride + width at least.  W and X
+ *   16-byte aligned, w_stride and x_stride multiples of 16 (577); cols need
+ *   not be.  Y overlaps no input (577).  561 / 564 for an empty / oversized
+ *   dimension or stride.  A NaN code or scale reaches the outputs whose sums
+ *   it is part of and no other.
+ *   workspace: ds_gemm_fp8_workspace_bytes(n, rows, cols) bytes, 256-byte
+ *   aligned, zeroed before first use; calls whose GPU work may overlap need
+ *   one each. */
+DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride, const float *w_scales,
+                       int64_t w_scales_len, const void *X, int64_t x_len, int64_t x_stride,
+                       const float *x_scales, int64_t x_scales_len, int64_t n, int64_t rows, int64_t cols,
+                       void *Y, int64_t y_len, int y_dtype, int64_t y_stride, void *workspace,
+                       size_t workspace_bytes, ds_stream_t stream);
 
 /* ---------------------------------------------------------------------
  * Decode glue
