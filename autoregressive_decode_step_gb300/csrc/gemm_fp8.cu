@@ -166,13 +166,16 @@ struct F8Seg {
     int mt, nt, k0, k1;
     int split;  // number of the split tile, or -1 (a whole tile)
 };
+// CTAs that have a run of the split tiles' w steps, at least a step each.
+__device__ __forceinline__ int f8_runs(long long w, int grid) { return (int)max(1ll, min((long long)grid, w)); }
 struct F8Walk {
     int round = 0;
     long long u, u1;
     __device__ explicit F8Walk(const F8Args &p) {
         const long long w = (long long)p.split * p.kb;
-        u = w * blockIdx.x / gridDim.x;
-        u1 = w * (blockIdx.x + 1) / gridDim.x;
+        const int runs = f8_runs(w, gridDim.x);
+        u = w * min((int)blockIdx.x, runs) / runs;
+        u1 = w * min((int)blockIdx.x + 1, runs) / runs;
     }
     __device__ bool next(const F8Args &p, F8Seg &s) {
         int tile;
@@ -201,8 +204,9 @@ struct F8Walk {
 // The CTAs that hold a split tile's first and last step.
 __device__ __forceinline__ void f8_contributors(const F8Args &p, int grid, int split, int &first, int &last) {
     const long long w = (long long)p.split * p.kb, t = (long long)split * p.kb;
-    first = (int)(((t + 1) * grid - 1) / w);
-    last = (int)(((t + p.kb) * grid - 1) / w);
+    const int runs = f8_runs(w, grid);
+    first = (int)(((t + 1) * runs - 1) / w);
+    last = (int)(((t + p.kb) * runs - 1) / w);
 }
 
 __device__ __forceinline__ void f8_store(const F8Args &p, int row, int feature, float v) {

@@ -193,8 +193,9 @@ def test_product_not_a_number(abi):
 
 def test_product_rows_apart_and_neighbours(abi):
     """Y in a wider buffer; one workspace for calls of several sizes, in turn."""
-    space = abi.workspace(max(abi.ds_gemm_fp8_workspace_bytes(n, r, c) for n, r, c in SIZES))
-    for n, rows, cols in ((5, 300, 1000), (300, 500, 640), (1, 6144, 4096), (40, 1000, 2000), (5, 300, 1000)):
+    space = abi.workspace(max(abi.ds_gemm_fp8_workspace_bytes(n, r, c) for n, r, c in SIZES + [(1, 153 * 128, 384)]))
+    for n, rows, cols in ((256, 512, 2048), (5, 300, 1000), (300, 500, 640), (1, 6144, 4096), (2049, 2304, 512),
+                          (40, 1000, 2000), (1, 153 * 128, 384), (5, 300, 1000)):
         w, ws, x, xs = operands(n, rows, cols, 3)
         buf = torch.full((n, rows + 9), 7.0, device="cuda")
         y = buf[:, 4:4 + rows]
