@@ -118,6 +118,9 @@ _sig("ds_fp8_quantize", ctypes.c_int, P, I64, ctypes.c_int, I64, I64, I64, ctype
 _sig("ds_gemm_fp8_workspace_bytes", SZ, I64, I64, I64)
 _sig("ds_gemm_fp8", ctypes.c_int, P, I64, I64, P, I64, P, I64, I64, P, I64, I64, I64, I64, P, I64, ctypes.c_int, I64, P,
      SZ, P)
+_sig("ds_moe_layer_workspace_bytes", SZ, I64, I64, I64, ctypes.c_int, ctypes.c_int)
+_sig("ds_moe_layer", ctypes.c_int, P, I64, ctypes.c_int, I64, I64, P, I64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+     ctypes.c_int, P, I64, P, I64, P, I64, P, I64, ctypes.c_int, I64, P, P, I64, P, P, P, SZ, P)
 _sig("ds_gemv_transposed_noalloc", ctypes.c_int, P, I64, ctypes.c_int, P, I64, I64, I64, P, I64, P)
 _sig("ds_gemv_transposed_noalloc_max_bytes", SZ)
 _sig("ds_gemv_transposed_noalloc_error", ctypes.c_int, P, P)
@@ -444,6 +447,40 @@ def ds_gemm_fp8(W, w_scales, X, x_scales, Y, ws, stream=None):
     xsp, xsn = _scales(x_scales, (n, kb), "x_scales", dev)
     check(lib.ds_gemm_fp8(wp, wn, wst, wsp, wsn, xp, xn, xst, xsp, xsn, n, rows, cols, yp, yn, dtype_code(Y), yst,
                           _here(ws), nbytes(ws), stream_handle(stream)), "ds_gemm_fp8")
+
+
+def ds_moe_layer_workspace_bytes(n, d, ff, n_experts, top_k):
+    return lib.ds_moe_layer_workspace_bytes(n, d, ff, n_experts, top_k)
+
+
+def ds_moe_layer(x, w_router, top_k, renormalize, w_gate_up, gate_up_scales, w_down, down_scales, residual, y,
+                 expert_ids, expert_weights, ws, stream=None):
+    """y [n][d] = (residual +) the weighted sum of top_k experts' feed-forward of x [n][d].
+    w_router [experts][d], w_gate_up [experts][2][ff][d], w_down [experts][d][ff]; scales for e4m3 experts, else
+    None; residual, expert_ids and expert_weights may be None."""
+    dev = ws.get_device()
+    n, d = x.shape
+    experts, _, ff, _ = w_gate_up.shape
+    if (tuple(w_router.shape) != (experts, d) or tuple(w_gate_up.shape) != (experts, 2, ff, d)
+            or tuple(w_down.shape) != (experts, d, ff) or tuple(y.shape) != (n, d) or y.dtype != x.dtype
+            or w_down.dtype != w_gate_up.dtype):
+        raise ValueError("ds_moe_layer: shapes or types that do not go together")
+    if residual is not None and (tuple(residual.shape) != (n, d) or residual.dtype != x.dtype):
+        raise ValueError("residual: x's shape and type are needed")
+    e4m3 = w_gate_up.dtype == torch.float8_e4m3fn
+    kb, fb = -(-d // 128), -(-ff // 128)
+    gs, gn = _scales(gate_up_scales, (experts, 2, fb, kb), "gate_up_scales", dev) if e4m3 else (None, 0)
+    dns, dn = _scales(down_scales, (experts, kb, fb), "down_scales", dev) if e4m3 else (None, 0)
+    if expert_weights is not None and expert_weights.dtype != torch.float32:
+        raise ValueError("expert_weights: an fp32 tensor is needed")
+    check(lib.ds_moe_layer(_dense(x, 0, "x", dev), x.numel(), dtype_code(x), n, d, _dense(w_router, 0, "w_router", dev),
+                           w_router.numel(), dtype_code(w_router), experts, top_k, 1 if renormalize else 0,
+                           _dense(w_gate_up, 0, "w_gate_up", dev), w_gate_up.numel(), gs, gn,
+                           _dense(w_down, 0, "w_down", dev), w_down.numel(), dns, dn, DS_E4M3 if e4m3 else dtype_code(w_gate_up), ff,
+                           None if residual is None else _dense(residual, 0, "residual", dev), _dense(y, 0, "y", dev),
+                           y.numel(), None if expert_ids is None else _i32(expert_ids, n * top_k, "expert_ids", dev),
+                           None if expert_weights is None else _dense(expert_weights, n * top_k, "expert_weights", dev),
+                           _here(ws), nbytes(ws), stream_handle(stream)), "ds_moe_layer")
 
 
 def ds_argmax_workspace_bytes(n_rows, n):

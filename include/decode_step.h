@@ -262,6 +262,53 @@ DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride, const flo
                        size_t workspace_bytes, ds_stream_t stream);
 
 /* ---------------------------------------------------------------------
+ * Mixture of experts
+ *
+ * The feed-forward of a decoder whose tokens each go through a few of many
+ * experts, for a decode step's tokens: of the weights only the chosen
+ * experts' are read, each once.
+ * ------------------------------------------------------------------- */
+
+/* Workspace bytes ds_moe_layer needs; 0 for sizes that it refuses. */
+DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int n_experts, int top_k);
+
+/* The whole layer for n tokens in one launch.  For token t
+ *   l_e = sum_j x[t][j] * w_router[e][j], the top_k largest chosen (among
+ *   equals the lower index; NaN above every number), chosen i being e_i;
+ *   p_i = exp(l_{e_i}) / sum_e exp(l_e), over all experts, or with
+ *   renormalize != 0 over the chosen ones;
+ *   y[t] = (residual[t] +) sum_i p_i W_down[e_i] (silu(W_gate[e_i] x[t]) * (W_up[e_i] x[t])),
+ *   silu(z) = z / (1 + e^-z) as in ds_silu_mul.
+ *   x, residual (may be NULL) and y: [n][d] fp32 or bf16 (x_dtype; 570, 562).
+ *   w_router: [n_experts][d] fp32 or bf16 (router_dtype).  w_gate_up:
+ *   [n_experts][2][ff][d], an expert's gate rows and then its up rows; w_down:
+ *   [n_experts][d][ff]; both bf16, or e4m3 with a scale for each 128 x 128
+ *   block of every matrix (w_dtype): gate_up_scales [n_experts][2][ceil(ff /
+ *   128)][ceil(d / 128)], down_scales [n_experts][ceil(d / 128)][ceil(ff /
+ *   128)] (NULL and 0 with bf16).  569 for a weight's or scale's length.
+ *   expert_ids, expert_weights: e_i and p_i [n][top_k], either may be NULL.
+ * Logits are exact to some 45 bits, the choice of experts that of 64-bit
+ * arithmetic; everything else is fp32, rounded once.  A bf16 y sees an
+ * intermediate of 16 bits at least.  Weights are finite; a value of x that is
+ * not, or a product that overflows fp32, makes outputs of its own token (and
+ * of no other) NaN or infinite.
+ *   n <= 256, n_experts <= 512, top_k <= 16 (564), top_k <= n_experts (577);
+ *   d and ff multiples of 8 with bf16 weights, of 16 with e4m3 (577); x, the
+ *   router and the experts' matrices 16-byte aligned (577).  y may be x or
+ *   residual itself; otherwise no output overlaps an input or another output
+ *   (577).  workspace: ds_moe_layer_workspace_bytes(...) bytes, 256-byte
+ *   aligned, zeroed before first use; calls whose GPU work may overlap need
+ *   one each.  A cooperative launch: it starts when the whole GPU is free. */
+DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, int64_t n, int64_t d,
+                        const void *w_router, int64_t router_len, int router_dtype, int n_experts,
+                        int top_k, int renormalize, const void *w_gate_up, int64_t gate_up_len,
+                        const float *gate_up_scales, int64_t gate_up_scales_len, const void *w_down,
+                        int64_t down_len, const float *down_scales, int64_t down_scales_len, int w_dtype,
+                        int64_t ff, const void *residual, void *y, int64_t y_len, int32_t *expert_ids,
+                        float *expert_weights, void *workspace, size_t workspace_bytes,
+                        ds_stream_t stream);
+
+/* ---------------------------------------------------------------------
  * Decode glue
  * ------------------------------------------------------------------- */
 
