@@ -1,0 +1,74 @@
+// What ds_gemm_fp8's two kernels share: gemm_fp8.cu (up to 128 rows of X) and
+// gemm_fp8_wide.cu (more).
+#pragma once
+
+#include "internal.h"
+
+namespace ds {
+
+struct F8Args {
+    CUtensorMap tw, tx;  // bytes, boxes {128, 128} and {128, bn} (wide: {128, 128}), 128-byte swizzle
+    const float *ws, *xs;
+    int rows, n, kb;
+    int bn;              // columns of an MMA: rows of X, or features (wide)
+    int m_tiles, n_tiles;
+    int rounds, split;   // whole tiles a CTA (a pair) takes; tiles behind them that are cut
+    void *y;
+    int y_dtype;
+    long long ldy;
+    float *partials;
+    int *counters;       // a split tile's arrivals, zero between launches
+    int *err;
+};
+
+// The split tiles' w steps are cut into runs, one a CTA (a pair), a step at least.
+__host__ __device__ inline int f8_runs(long long w, int grid) { return w < 1 ? 1 : w < grid ? (int)w : grid; }
+// The first and last run that hold steps of a split tile.
+__device__ __forceinline__ void f8_contributors(const F8Args &p, int grid, int split, int &first, int &last) {
+    const long long w = (long long)p.split * p.kb, t = (long long)split * p.kb;
+    const int runs = f8_runs(w, grid);
+    first = (int)(((t + 1) * runs - 1) / w);
+    last = (int)(((t + p.kb) * runs - 1) / w);
+}
+
+// A run's segments: whole tiles in rounds, then its steps of the split tiles.
+struct F8Seg {
+    int tile, k0, k1;
+    int split;  // number of the split tile, or -1 (a whole tile)
+};
+struct F8Walk {
+    int id, grid, round = 0;
+    long long u, u1;
+    __device__ F8Walk(const F8Args &p, int id_, int grid_) : id(id_), grid(grid_) {
+        const long long w = (long long)p.split * p.kb;
+        const int runs = f8_runs(w, grid);
+        u = w * min(id, runs) / runs;
+        u1 = w * min(id + 1, runs) / runs;
+    }
+    __device__ bool next(const F8Args &p, F8Seg &s) {
+        if (round < p.rounds) {
+            s.tile = id + grid * round++;
+            s.k0 = 0;
+            s.k1 = p.kb;
+            s.split = -1;
+            return true;
+        }
+        if (u >= u1) return false;
+        s.split = (int)(u / p.kb);
+        s.tile = p.rounds * grid + s.split;
+        s.k0 = (int)(u - (long long)s.split * p.kb);
+        s.k1 = (int)min((long long)p.kb, s.k0 + u1 - u);
+        u += s.k1 - s.k0;
+        if (s.k0 == 0 && s.k1 == p.kb) s.split = -1;
+        return true;
+    }
+};
+
+constexpr int kF8WideRows = 256, kF8WideFeatures = 256;  // a pair's tile
+// More rows of X than this run on pairs of SMs.
+constexpr int kF8Narrow = 128;
+size_t f8_wide_partial_floats(int split);
+int f8_wide_pairs();
+cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream);
+
+}  // namespace ds

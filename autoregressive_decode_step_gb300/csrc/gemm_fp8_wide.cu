@@ -1,0 +1,447 @@
+// ds_gemm_fp8 for more than 128 rows of X: pairs of SMs on tiles of 256 rows by
+// 256 features.
+//
+// One tcgen05.mma of cta_group::2 spans both SMs of a pair: each holds 128 rows
+// of X and half of the tile's weights in shared memory and gets its own 128
+// rows of the product, lane r of its TMEM row r.  So an SM fetches 32 KB a step
+// (a block of 128 of the sum) for 128 x 256 x 128 products: 512 tensor cycles
+// against 64 bytes a cycle from L2; alone it would fetch 48 KB.
+//
+// A row's scale and its block of 128 features' make one factor a thread and
+// step, so the sums cost one packed multiply-add per two columns: four
+// warpgroups take 64 columns each out of TMEM, add them to registers and free
+// the buffer before they do, so that two buffers keep the tensor cores busy.
+// Rows are lanes, so a thread's outputs are 64 neighbours of one row, stored 32
+// bytes at a time.
+//
+// Tiles are dealt out whole, one a pair and round; what is left over is cut into
+// equal runs of steps whose partial sums a second launch adds in order.
+#include <algorithm>
+#include <atomic>
+
+#include "gemm_fp8.h"
+#include "mma_stream.cuh"
+
+namespace ds {
+
+constexpr int kFwThreads = 640;  // sixteen warps that add up; copies, products, scales, one idle
+// Registers a thread: 96 at launch (640 x 96), moved to the warps that add up:
+// 4 x 104 + 64 = 5 x 96.
+constexpr int kFwRegsSum = 104, kFwRegsOther = 64;
+constexpr int kFwStages = 5, kFwHalf = 128 * 128, kFwStageBytes = 2 * kFwHalf;
+constexpr int kFwSlots = 8;   // steps' factors ahead
+constexpr int kFwBufs = 4;    // TMEM buffers of 128 columns, two a step
+constexpr int kFwGroup = 8;   // row tiles that follow one another before the next features
+constexpr int kFwOutRow = 80;  // 64 bytes of a row and 16 that keep rows apart on the banks
+constexpr int kFwPart = 128 * kF8WideFeatures;  // floats of one SM's share of a tile
+
+struct FwShared {
+    uint64_t full[kFwStages], empty[kFwStages];
+    uint64_t s_full[kFwSlots], s_empty[kFwSlots];
+    uint64_t t_full[kFwBufs], t_empty[kFwBufs];
+    uint64_t done;
+    uint32_t tmem;
+    int dead;
+    alignas(16) float factor[kFwSlots][2][128];
+    alignas(16) unsigned char out[16][32 * kFwOutRow];  // a warp's outputs on their way
+};
+constexpr size_t kFwSmem = 1024 + (size_t)kFwStages * kFwStageBytes + sizeof(FwShared);
+static_assert(kFwSmem <= 227 * 1024, "shared memory");
+
+__device__ __forceinline__ uint32_t fw_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+// The address of the first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t fw_lead(const void *p) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+    return r;
+}
+__device__ __forceinline__ void fw_pair_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Both CTAs' copies count on the first one's barrier.
+__device__ __forceinline__ void fw_box(uint32_t one, uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], "
+        "[%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void fw_mma(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
+        : "memory");
+}
+// Arrive on both CTAs' barriers when the products issued so far are done.
+__device__ __forceinline__ void fw_commit(uint32_t one, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            smem_u32(bar)),
+        "h"((unsigned short)3), "r"(one)
+        : "memory");
+}
+// (Release at CTA scope: what it orders are TMEM loads, complete and fenced by
+// tcgen05.fence.  At cluster scope each arrival cost a memory barrier: 1.62 ms
+// for 8,192 rows by 28,672 x 4,096.)
+__device__ __forceinline__ void fw_arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool fw_try_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// stream_wait on a barrier that the other CTA arrives on too.
+__device__ __forceinline__ void fw_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
+    if (fw_try_wait(bar, parity)) return;
+    const long long t0 = clock64();
+    for (uint32_t it = 1;; ++it) {
+        if (fw_try_wait(bar, parity)) return;
+        if ((it & 63u) == 0) {
+            if (*dead) return;
+            if (clock64() - t0 > kStreamWaitCycles) {
+                flag_error(err, DS_ERR_WAIT_TIMEOUT);
+                *dead = 1;
+                return;
+            }
+        }
+    }
+}
+
+// Row and feature tile: kFwGroup row tiles for each feature tile, so that what
+// runs at one time shares both operands in L2.
+__device__ __forceinline__ void fw_tile(const F8Args &p, int tile, int &rt, int &ft) {
+    const int per = kFwGroup * p.m_tiles, g = tile / per, nn = min(kFwGroup, p.n_tiles - g * kFwGroup);
+    ft = (tile - g * per) / nn;
+    rt = g * kFwGroup + (tile - g * per) % nn;
+}
+
+// N neighbouring outputs of a row.
+template <int N>
+__device__ __forceinline__ void fw_store(const F8Args &p, int row, int f0, const float *v) {
+    if (row >= p.n || f0 >= p.rows) return;
+    const long long at = row * p.ldy + f0;
+    const int es = p.y_dtype == DS_BF16 ? 2 : 4;
+    char *to = static_cast<char *>(p.y) + at * es;
+    if (f0 + N <= p.rows && ((uintptr_t)to & 31) == 0) {
+        uint32_t w[8];
+        if (p.y_dtype == DS_BF16) {
+#pragma unroll
+            for (int i = 0; i < N; i += 16) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = stream_bf16x2(v[i + 2 * j], v[i + 2 * j + 1]);
+                stream_store32(to + i * 2, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; i += 8) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
+                stream_store32(to + i * 4, w);
+            }
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (f0 + i < p.rows) store_as(p.y, at + i, p.y_dtype, v[i]);
+}
+
+// A warp's 32 rows (lane r row row0 + r) by 64 outputs, through shared memory:
+// four lanes store 64 neighbouring bytes of a row, where a thread's own row at
+// a time took a quarter of the kernel (a line a lane).
+__device__ __forceinline__ void fw_store_tile(const F8Args &p, unsigned char *out, int row0, int f0, const float (&acc)[64]) {
+    const int lane = threadIdx.x & 31, es = p.y_dtype == DS_BF16 ? 2 : 4, per = 64 / es;
+    char *y = static_cast<char *>(p.y);
+    const bool dense = (((uintptr_t)y | (uintptr_t)(p.ldy * es)) & 15) == 0;
+#pragma unroll
+    for (int i = 0; i < 64; i += 16) {  // 16 values: 64 bytes of fp32, half of that of bf16
+        uint4 *to = reinterpret_cast<uint4 *>(out + lane * kFwOutRow);
+        if (es == 2) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const float *v = acc + i + 8 * j;
+                to[(i >> 3 & 2) + j] = make_uint4(stream_bf16x2(v[0], v[1]), stream_bf16x2(v[2], v[3]), stream_bf16x2(v[4], v[5]), stream_bf16x2(v[6], v[7]));
+            }
+            if ((i & 16) == 0) continue;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float *v = acc + i + 4 * j;
+                to[j] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            }
+        }
+        __syncwarp();
+        const int c0 = f0 + i / per * per;  // first column of these 64 bytes
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int at = j * 32 + lane, row = row0 + (at >> 2), col = c0 + (at & 3) * (16 / es);
+            if (row >= p.n || col >= p.rows) continue;
+            const uint4 v = *reinterpret_cast<const uint4 *>(out + (at >> 2) * kFwOutRow + (at & 3) * 16);
+            char *q = y + (row * p.ldy + col) * es;
+            if (dense && col + 16 / es <= p.rows) {
+                *reinterpret_cast<uint4 *>(q) = v;
+            } else {
+                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                if (es == 4) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (col + k < p.rows) reinterpret_cast<uint32_t *>(q)[k] = w[k];
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        if (col + k < p.rows) reinterpret_cast<unsigned short *>(q)[k] = (unsigned short)(w[k >> 1] >> (16 * (k & 1)));
+                }
+            }
+        }
+        __syncwarp();
+    }
+}
+
+__global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_gemm_wide_kernel(const __grid_constant__ F8Args p) {
+    extern __shared__ unsigned char smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    FwShared &sh = *reinterpret_cast<FwShared *>(smem_raw + (base - smem_u32(smem_raw)) + kFwStages * kFwStageBytes);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)fw_rank();
+    volatile int *dead = &sh.dead;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kFwStages; ++i) {
+            mbar_init(&sh.full[i], 1);
+            mbar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < kFwSlots; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_empty[i], 16);
+        }
+        for (int i = 0; i < kFwBufs; ++i) {
+            mbar_init(&sh.t_full[i], 1);
+            mbar_init(&sh.t_empty[i], 16);
+        }
+        mbar_init(&sh.done, 1);
+        sh.dead = 0;
+        fence_mbarrier_init();
+    }
+    if (warp == 19) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&sh.tmem)), "r"(512u) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    fw_pair_sync();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
+    allow_dependent_launch();
+
+    F8Walk walk(p, blockIdx.x >> 1, gridDim.x >> 1);
+    F8Seg sg;
+    int rt, ft;
+    if (warp >= 16) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFwRegsOther));
+        if (warp == 16) {
+            // copies: this CTA's rows of X and its half of the weights
+            const uint32_t one = stream_elect();
+            int s = 0;
+            uint32_t ph = 1;
+            long long issued = 0;
+            while (walk.next(p, sg)) {
+                fw_tile(p, sg.tile, rt, ft);
+                for (int k = sg.k0; k < sg.k1; ++k) {
+                    stream_wait(&sh.empty[s], ph, dead, p.err);
+                    if (*dead) break;
+                    if (one && rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kFwStageBytes);
+                    const uint32_t dst = base + s * kFwStageBytes, bar = fw_lead(&sh.full[s]);
+                    fw_box(one, dst, &p.tx, k * 128, rt * kF8WideRows + rank * 128, bar);
+                    fw_box(one, dst + kFwHalf, &p.tw, k * 128, ft * kF8WideFeatures + rank * 128, bar);
+                    ++issued;
+                    if (++s == kFwStages) s = 0, ph ^= 1;
+                }
+                if (*dead) break;
+            }
+            // the copies still under way land before either CTA ends
+            if (rank == 0)
+                for (long long i = max(0ll, issued - kFwStages); i < issued; ++i)
+                    mbar_wait(&sh.full[i % kFwStages], (uint32_t)(i / kFwStages) & 1, p.err);
+        } else if (warp == 17) {
+            // products, from the first CTA
+            const uint32_t one = stream_elect();
+            if (rank == 0) {
+                constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kF8WideRows >> 4) << 24);
+                int s = 0, b = 0;
+                uint32_t ph = 0, bph = 1;
+                while (walk.next(p, sg)) {
+                    for (int k = sg.k0; k < sg.k1; ++k) {
+                        fw_wait(&sh.full[s], ph, dead, p.err);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {  // 64 of either CTA's 128 features
+                            fw_wait(&sh.t_empty[b + h], bph, dead, p.err);
+                            tc_fence_after();
+                            const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
+                            const uint64_t bd = smem_desc(base + s * kFwStageBytes + kFwHalf + h * 64 * 128, 16, 1024);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
+                                fw_mma(one, tmem + (b + h) * 128, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+                            fw_commit(one, &sh.t_full[b + h]);
+                        }
+                        fw_commit(one, &sh.empty[s]);
+                        if (++s == kFwStages) s = 0, ph ^= 1;
+                        if ((b += 2) == kFwBufs) b = 0, bph ^= 1;
+                    }
+                }
+                fw_commit(one, &sh.done);
+            }
+            mbar_wait(&sh.done, 0, p.err);
+        } else if (warp == 18) {
+            // factors: four steps' scales requested together, so that a step's come before its product is done
+            int slot = 0;
+            uint32_t ph = 1;
+            while (walk.next(p, sg)) {
+                fw_tile(p, sg.tile, rt, ft);
+                const int row = rt * kF8WideRows + rank * 128 + lane, blocks = (p.rows + 127) / 128;
+                const float *xs = p.xs + (long long)row * p.kb;
+                const float *w0 = p.ws + (long long)(2 * ft) * p.kb, *w1 = p.ws + (long long)min(2 * ft + 1, blocks - 1) * p.kb;
+                for (int k = sg.k0; k < sg.k1; k += 4) {
+                    float v[4][4], a[4], b[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const bool in = k + j < sg.k1;
+                        a[j] = in ? __ldg(w0 + k + j) : 0.0f;
+                        b[j] = in ? __ldg(w1 + k + j) : 0.0f;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) v[j][i] = in && row + 32 * i < p.n ? __ldg(xs + (long long)(32 * i) * p.kb + k + j) : 0.0f;
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (k + j >= sg.k1) break;
+                        stream_wait(&sh.s_empty[slot], ph, dead, p.err);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            sh.factor[slot][0][32 * i + lane] = v[j][i] * a[j];
+                            sh.factor[slot][1][32 * i + lane] = v[j][i] * b[j];
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.s_full[slot]);
+                        if (++slot == kFwSlots) slot = 0, ph ^= 1;
+                    }
+                }
+            }
+        }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwRegsSum));
+        // sums: thread r of a warpgroup is row r; the warpgroup's 64 columns are
+        // features f0 on, half `half` of CTA `sub`'s
+        const int wg = warp >> 2, half = wg >> 1, sub = wg & 1, r = threadIdx.x & 127, f0 = sub * 128 + half * 64;
+        const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * 128 + sub * 64;
+        const uint32_t freed[2] = {fw_lead(&sh.t_empty[half]), fw_lead(&sh.t_empty[2 + half])};
+        int b = 0, slot = 0;
+        uint32_t bph = 0, ph = 0;
+        while (walk.next(p, sg)) {
+            float acc[64];
+#pragma unroll
+            for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
+            for (int k = sg.k0; k < sg.k1; ++k) {
+                stream_wait(&sh.s_full[slot], ph, dead, p.err);
+                const float f = sh.factor[slot][sub][r];
+                stream_wait(&sh.t_full[b + half], bph, dead, p.err);
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < 64; c += 32) {
+                    float v[32];
+                    stream_ld<32>(from + b * 128 + c, v);
+                    if (c == 32) {  // the buffer and the factors are read out
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) {
+                            fw_arrive(b ? freed[1] : freed[0]);
+                            mbar_arrive(&sh.s_empty[slot]);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f, f);
+                }
+                if ((b += 2) == kFwBufs) b = 0, bph ^= 1;
+                if (++slot == kFwSlots) slot = 0, ph ^= 1;
+            }
+            fw_tile(p, sg.tile, rt, ft);
+            if (sg.split < 0) {
+                fw_store_tile(p, sh.out[warp], rt * kF8WideRows + rank * 128 + (warp & 3) * 32, ft * kF8WideFeatures + f0, acc);
+            } else {
+                float *mine = p.partials + (((size_t)walk.id + sg.split) * 2 + rank) * kFwPart + (size_t)f0 * 128 + r;
+#pragma unroll
+                for (int i = 0; i < 64; ++i) __stcg(mine + i * 128, acc[i]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    fw_pair_sync();  // neither CTA ends while the other's products or arrivals may reach it
+    tc_fence_after();
+    if (warp == 19) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+}
+
+// Adds a split tile's partials, 16 columns of one SM's rows a block; thread r is row r.
+__global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constant__ F8Args p, int pairs) {
+    constexpr int C = 16;
+    grid_dependency_wait();
+    const int chunk = blockIdx.x % (kF8WideFeatures / C), rank = blockIdx.x / (kF8WideFeatures / C) % 2, split = blockIdx.x / (2 * kF8WideFeatures / C);
+    int first, last, rt, ft;
+    f8_contributors(p, pairs, split, first, last);
+    if (first == last) return;  // one pair had all of it
+    fw_tile(p, p.rounds * pairs + split, rt, ft);
+    const int row = rt * kF8WideRows + rank * 128 + threadIdx.x, f0 = ft * kF8WideFeatures + chunk * C;
+    if (row - (int)threadIdx.x >= p.n || f0 >= p.rows) return;
+    float acc[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+#pragma unroll 2
+    for (int c = first; c <= last; ++c) {
+        const float *from = p.partials + (((size_t)c + split) * 2 + rank) * kFwPart + (size_t)chunk * C * 128 + threadIdx.x;
+        float v[C];
+#pragma unroll
+        for (int i = 0; i < C; ++i) v[i] = __ldcg(from + i * 128);
+#pragma unroll
+        for (int i = 0; i < C; ++i) acc[i] += v[i];
+    }
+    fw_store<C>(p, row, f0, acc);
+}
+
+// ---------------------------------------------------------------- host
+int f8_wide_pairs() { return std::max(1, sm_count() / 2); }
+size_t f8_wide_partial_floats(int split) { return split ? ((size_t)f8_wide_pairs() + split) * 2 * kFwPart : 0; }
+
+cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream) {
+    static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised, a bit each
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (!(ready.load(std::memory_order_acquire) & bit)) {
+        e = cudaFuncSetAttribute(fp8_gemm_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwSmem);
+        if (e != cudaSuccess) return e;
+        ready.fetch_or(bit, std::memory_order_release);
+    }
+    const int pairs = f8_wide_pairs();
+    e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, false, a);
+    if (e != cudaSuccess || a.split == 0) return e;
+    return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / 16)), dim3(128), 0, stream, true, a, pairs);
+}
+
+}  // namespace ds

@@ -419,18 +419,27 @@ __device__ __forceinline__ void moe_stage_bf16(float (&acc)[8][4], uint32_t stag
         if (P > 2) b[P - 1][i] = moe_bf16x2(moe_rest(x), moe_rest(y));
     }
     const int lane = threadIdx.x & 31, t = lane & 3, r = moe_row(lane >> 2);
+    // The tensor core cuts its sums off rather than rounding them, so a stage's
+    // are kept short, small pieces first, and added outside.
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
+    for (int m = 0; m < 8; ++m) {
+        uint4 lo[2], hi[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const uint32_t at = stage + (m * 16 + r) * 128 + (((t + 4 * h) ^ r) << 4);
-            const uint4 lo = moe_lds(at), hi = moe_lds(at + 8 * 128);
-#pragma unroll
-            for (int q = P - 1; q >= 0; --q) {
-                moe_mma_bf16(acc[m], lo.x, hi.x, lo.y, hi.y, b[q][4 * h], b[q][4 * h + 1]);
-                moe_mma_bf16(acc[m], lo.z, hi.z, lo.w, hi.w, b[q][4 * h + 2], b[q][4 * h + 3]);
-            }
+            lo[h] = moe_lds(at), hi[h] = moe_lds(at + 8 * 128);
         }
+        float d[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int q = P - 1; q >= 0; --q)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                moe_mma_bf16(d, lo[h].x, hi[h].x, lo[h].y, hi[h].y, b[q][4 * h], b[q][4 * h + 1]);
+                moe_mma_bf16(d, lo[h].z, hi[h].z, lo[h].w, hi[h].w, b[q][4 * h + 2], b[q][4 * h + 3]);
+            }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] += d[i];
+    }
 }
 
 // The same with e4m3 weights; s0, s1: scales of rows 0 to 63 and 64 to 127.
