@@ -209,9 +209,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                             stream_ld<CH>(from + b * C::kCols + j * NB + c, v);
 #pragma unroll
                             for (int i = 0; i < CH; i += 4) {
-                                const float4 f = *reinterpret_cast<const float4 *>(scale + c + i);
-                                stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f.x, f.y);
-                                stream_fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f.z, f.w);
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(scale + c + i);
+                                stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f.x);
+                                stream_fma2(acc[c + i + 2], acc[c + i + 3], v[i + 2], v[i + 3], f.y);
                             }
                         }
                     }

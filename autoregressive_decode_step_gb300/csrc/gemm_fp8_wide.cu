@@ -91,38 +91,17 @@ __device__ __forceinline__ void fw_commit(uint32_t one, uint64_t *bar) {
         "h"((unsigned short)3), "r"(one)
         : "memory");
 }
-// (Release at CTA scope: what it orders are TMEM loads, complete and fenced by
-// tcgen05.fence.  At cluster scope each arrival cost a memory barrier: 1.62 ms
-// for 8,192 rows by 28,672 x 4,096.)
-__device__ __forceinline__ void fw_arrive(uint32_t bar) {
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-__device__ __forceinline__ bool fw_try_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
+// Arrive on a barrier of either CTA.  (Release at CTA scope: what it orders are
+// TMEM loads, complete and fenced by tcgen05.fence, and a CTA's own reads and
+// writes.  At cluster scope each arrival cost a memory barrier: 1.62 ms for
+// 8,192 rows by 28,672 x 4,096.)
+__device__ __forceinline__ void fw_arrive(uint32_t one, uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cluster.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(one)
         : "memory");
-    return ok != 0;
-}
-// stream_wait on a barrier that the other CTA arrives on too.
-__device__ __forceinline__ void fw_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
-    if (fw_try_wait(bar, parity)) return;
-    const long long t0 = clock64();
-    for (uint32_t it = 1;; ++it) {
-        if (fw_try_wait(bar, parity)) return;
-        if ((it & 63u) == 0) {
-            if (*dead) return;
-            if (clock64() - t0 > kStreamWaitCycles) {
-                flag_error(err, DS_ERR_WAIT_TIMEOUT);
-                *dead = 1;
-                return;
-            }
-        }
-    }
 }
 
 // Row and feature tile: kFwGroup row tiles for each feature tile, so that what
@@ -229,7 +208,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             mbar_init(&sh.empty[i], 1);
         }
         for (int i = 0; i < kFwSlots; ++i) {
-            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_full[i], 2);  // both CTAs' factors, on the first one's barrier
             mbar_init(&sh.s_empty[i], 16);
         }
         for (int i = 0; i < kFwBufs; ++i) {
@@ -285,25 +264,27 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             const uint32_t one = stream_elect();
             if (rank == 0) {
                 constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kF8WideRows >> 4) << 24);
-                int s = 0, b = 0;
-                uint32_t ph = 0, bph = 1;
+                int s = 0;
+                uint32_t ph = 0, n = 0;  // n: steps so far
                 while (walk.next(p, sg)) {
-                    for (int k = sg.k0; k < sg.k1; ++k) {
-                        fw_wait(&sh.full[s], ph, dead, p.err);
+                    for (int k = sg.k1 - sg.k0; k > 0; --k, ++n) {
+                        // a step's factors are there before its products start, so whoever sees these needs no other wait
+                        stream_wait(&sh.s_full[n % kFwSlots], n / kFwSlots & 1, dead, p.err);
+                        stream_wait(&sh.full[s], ph, dead, p.err);
+                        const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
+                        const uint64_t bd = smem_desc(base + s * kFwStageBytes + kFwHalf, 16, 1024);
+                        const uint32_t b = n & 1;
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {  // 64 of either CTA's 128 features
-                            fw_wait(&sh.t_empty[b + h], bph, dead, p.err);
+                            stream_wait(&sh.t_empty[2 * b + h], (n >> 1 & 1) ^ 1, dead, p.err);
                             tc_fence_after();
-                            const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
-                            const uint64_t bd = smem_desc(base + s * kFwStageBytes + kFwHalf + h * 64 * 128, 16, 1024);
 #pragma unroll
                             for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
-                                fw_mma(one, tmem + (b + h) * 128, ad + 2 * i, bd + 2 * i, idesc, i > 0);
-                            fw_commit(one, &sh.t_full[b + h]);
+                                fw_mma(one, tmem + b * 256 + h * 128, ad + 2 * i, bd + h * (64 * 128 / 16) + 2 * i, idesc, i > 0);
+                            fw_commit(one, &sh.t_full[2 * b + h]);
                         }
                         fw_commit(one, &sh.empty[s]);
                         if (++s == kFwStages) s = 0, ph ^= 1;
-                        if ((b += 2) == kFwBufs) b = 0, bph ^= 1;
                     }
                 }
                 fw_commit(one, &sh.done);
@@ -338,7 +319,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
                             sh.factor[slot][1][32 * i + lane] = v[j][i] * b[j];
                         }
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sh.s_full[slot]);
+                        fw_arrive(lane == 0, fw_lead(&sh.s_full[slot]));
                         if (++slot == kFwSlots) slot = 0, ph ^= 1;
                     }
                 }
@@ -350,35 +331,33 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
         // features f0 on, half `half` of CTA `sub`'s
         const int wg = warp >> 2, half = wg >> 1, sub = wg & 1, r = threadIdx.x & 127, f0 = sub * 128 + half * 64;
         const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * 128 + sub * 64;
-        const uint32_t freed[2] = {fw_lead(&sh.t_empty[half]), fw_lead(&sh.t_empty[2 + half])};
-        int b = 0, slot = 0;
-        uint32_t bph = 0, ph = 0;
+        const uint32_t full0 = smem_u32(&sh.t_full[half]), freed0 = fw_lead(&sh.t_empty[half]);
+        const uint32_t factor0 = smem_u32(&sh.factor[0][sub][r]), s_empty0 = smem_u32(&sh.s_empty[0]), one = stream_elect();
+        uint32_t n = 0;  // steps so far
         while (walk.next(p, sg)) {
             float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
-            for (int k = sg.k0; k < sg.k1; ++k) {
-                stream_wait(&sh.s_full[slot], ph, dead, p.err);
-                const float f = sh.factor[slot][sub][r];
-                stream_wait(&sh.t_full[b + half], bph, dead, p.err);
+            for (int k = sg.k1 - sg.k0; k > 0; --k, ++n) {
+                const uint32_t slot = n % kFwSlots, b = n & 1;
+                stream_wait(full0 + b * 16, n >> 1 & 1, dead, p.err);
                 tc_fence_after();
+                float factor;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(factor) : "r"(factor0 + slot * 1024));
+                const uint64_t f = stream_pair(factor, factor);
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
                     float v[32];
-                    stream_ld<32>(from + b * 128 + c, v);
+                    stream_ld<32>(from + b * 256 + c, v);
                     if (c == 32) {  // the buffer and the factors are read out
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) {
-                            fw_arrive(b ? freed[1] : freed[0]);
-                            mbar_arrive(&sh.s_empty[slot]);
-                        }
+                        fw_arrive(one, freed0 + b * 16);
+                        stream_arrive(one, s_empty0 + slot * 8);
                     }
 #pragma unroll
-                    for (int i = 0; i < 32; i += 2) stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f, f);
+                    for (int i = 0; i < 32; i += 2) stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
                 }
-                if ((b += 2) == kFwBufs) b = 0, bph ^= 1;
-                if (++slot == kFwSlots) slot = 0, ph ^= 1;
             }
             fw_tile(p, sg.tile, rt, ft);
             if (sg.split < 0) {

@@ -13,12 +13,24 @@ namespace ds {
 // Cycles after which a wait inside a kernel gives up (some two seconds).
 constexpr long long kStreamWaitCycles = 4000000000ll;
 
-// Wait for a phase; once any wait of the block has given up, at once.
-__device__ __forceinline__ void stream_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
-    if (mbar_try_wait(bar, parity)) return;
+__device__ __forceinline__ bool stream_try(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// Wait for a phase; once any wait of the block has given up, at once.  (Barriers
+// by their addresses in shared memory: inner loops then form few of them.)
+__device__ __forceinline__ void stream_wait(uint32_t bar, uint32_t parity, volatile int *dead, int *err) {
+    if (stream_try(bar, parity)) return;
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return;
+        if (stream_try(bar, parity)) return;
         if ((it & 63u) == 0) {
             if (*dead) return;
             if (clock64() - t0 > kStreamWaitCycles) {
@@ -28,6 +40,18 @@ __device__ __forceinline__ void stream_wait(uint64_t *bar, uint32_t parity, vola
             }
         }
     }
+}
+__device__ __forceinline__ void stream_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
+    stream_wait(smem_u32(bar), parity, dead, err);
+}
+// Arrive from the one lane of the warp that `one` marks.
+__device__ __forceinline__ void stream_arrive(uint32_t one, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %1, 0;\n\t"
+        "@q mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+        "r"(one)
+        : "memory");
 }
 
 // One lane of the warp: the others run the same code with 0, so that addresses
@@ -105,16 +129,21 @@ __device__ __forceinline__ void stream_ld<32>(uint32_t t, float *v) {
         : "r"(t)
         : "memory");
 }
-// (a0, a1) += (x0, x1) (s0, s1)
-__device__ __forceinline__ void stream_fma2(float &a0, float &a1, float x0, float x1, float s0, float s1) {
-    asm("{\n\t.reg .b64 a, x, s;\n\t"
+// A pair of fp32 for the packed instructions.
+__device__ __forceinline__ uint64_t stream_pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+// (a0, a1) += (x0, x1) s
+__device__ __forceinline__ void stream_fma2(float &a0, float &a1, float x0, float x1, uint64_t s) {
+    asm("{\n\t.reg .b64 a, x;\n\t"
         "mov.b64 a, {%0, %1};\n\t"
         "mov.b64 x, {%2, %3};\n\t"
-        "mov.b64 s, {%4, %5};\n\t"
-        "fma.rn.f32x2 a, x, s, a;\n\t"
+        "fma.rn.f32x2 a, x, %4, a;\n\t"
         "mov.b64 {%0, %1}, a;\n\t}"
         : "+f"(a0), "+f"(a1)
-        : "f"(x0), "f"(x1), "f"(s0), "f"(s1));
+        : "f"(x0), "f"(x1), "l"(s));
 }
 // 32 bytes at once.
 __device__ __forceinline__ void stream_store32(void *p, const uint32_t *v) {

@@ -5,51 +5,75 @@
 // or not.
 //
 // What bounds it is the chosen experts' weight bytes, each of which is wanted
-// by few tokens.  So the weights go through shared memory once, as 128 rows by
-// 128 bytes of the sum a stage (64 gate and 64 up rows, or 128 down rows), and
-// a stage belongs to one warp, which multiplies it with up to 32 tokens by
-// mma.sync: eight warps have eight stages in hand, none waits for another
-// until a tile of outputs is complete.  (tcgen05 would want 8-bit weights and
-// activations in one format; here fp32 activations meet e4m3 or bf16 weights.)
-// All tiles of a phase, expert after expert, are one line of stages cut into
-// equal runs, one a CTA; a tile that is cut is added up by the CTA that is last.
+// by few tokens.  A step takes 256 rows by 128 bytes of the sum (an expert's 128
+// gate and 128 up rows, or 256 down rows) through shared memory into two
+// tcgen05.mma whose N are the tokens; all tiles of a phase, expert after expert,
+// are one line of steps cut into equal runs, one a CTA, so that every SM streams
+// the same bytes.  A tile that is cut is added up by the CTA that is last.
 //
-// Four phases with a barrier of the whole grid between them (a cooperative
-// launch; waits are bounded): logits; gate and up; down; the weighted sum.
-// Every CTA draws up the tokens' choices for itself.  The copying warp goes on
-// to the next phase's weights while the others wait.
+// Phases with a barrier of the whole grid between them (a cooperative launch;
+// every wait is bounded): logits; for more than eight tokens their rows in the
+// order of the experts; gate and up; down; the weighted sum.  Every CTA draws up
+// the tokens' choices for itself.  The copying warp has the next phase's weights
+// under way while the others meet.
 //
-// Digits: fp32 activations meet bf16 weights as three bf16 pieces (24 bits,
-// exact), e4m3 weights as two f16 pieces behind a power of two per token and
-// 128 values that brings the largest below 2^15 (22 bits, and no value loses
-// more than 2^-40 of its block's largest; e4m3 is exact in f16).  Where
-// outputs are bf16 the intermediate has 16 bits or more.  Sums are fp32.  The
-// logits are sums of exact products with their rounding errors carried along
-// (two floats, added up in 64 bits): the choice of experts is that of 64 bits.
+// Digits: an activation goes to the tensor core in pieces of the weights' own
+// type, side by side as further columns, that add up to it: one bf16 piece for
+// bf16 activations, three (24 bits, exact) for fp32; e4m3 pieces of four bits
+// each, a sixteenth apart, behind a power of two per token and 128 values that
+// brings the largest below 2^8: six for fp32 (24 bits; no value loses more than
+// 2^-38 of its block's largest), two for bf16.  The intermediate is fp32 and
+// goes in three bf16 or six e4m3 pieces, before bf16 outputs in two or four (16
+// bits).  Sums leave the tensor core every 1,024 products (e4m3: every block of
+// 128, for its scale) and are fp32.  The logits are sums of exact products with
+// their rounding errors carried along (two floats, added up in 64 bits): the
+// choice of experts is that of 64 bits.
 #include <algorithm>
 #include <atomic>
 
 #include "common.cuh"
+#include "internal.h"
+#include "mma_stream.cuh"
 #include "tc.h"
-
-#include <cuda_fp16.h>
 
 namespace ds {
 
 constexpr int kMoeMaxTokens = 256, kMoeMaxExperts = 512, kMoeMaxK = 16;
 constexpr int kMoeMaxPairs = kMoeMaxTokens * kMoeMaxK;
-constexpr int kMoeGroup = 32;  // tokens a stage is multiplied with
-constexpr int kMoeMaxJobs = kMoeMaxExperts + kMoeMaxPairs / kMoeGroup;
-constexpr int kMoeWarps = 8;
-constexpr int kMoeThreads = 384;  // two warpgroups that multiply, one whose first warp copies
-// Registers a thread: 168 at launch (384 x 168), moved to the warps that hold
-// a tile's sums: 2 x 216 + 72 = 3 x 168.
-constexpr int kMoeRegsMain = 216, kMoeRegsOther = 72;
-constexpr int kMoeStages = 10, kMoeStageBytes = 128 * 128;
-constexpr int kMoeSums = kMoeGroup * 128;  // floats of a tile
+constexpr int kMoeGroup = 32;  // tokens a step is multiplied with at most
+constexpr int kMoeByToken = 8; // up to so many tokens every expert's columns are all the tokens
+constexpr int kMoeMaxJobs = kMoeMaxExperts + kMoeMaxPairs / 16;
+constexpr int kMoeThreads = 384;  // two warpgroups that add up; copies, products, scales, one idle
+// Registers a thread: 168 at launch (384 x 168), moved to the warps that add
+// up: 2 x 216 + 72 = 3 x 168.
+constexpr int kMoeRegsSum = 216, kMoeRegsOther = 72;
+constexpr int kMoeMaxStages = 5;
+constexpr int kMoeWeightBytes = 2 * 128 * 128;  // of a step
+constexpr int kMoeRing = 200 * 1024;  // four stages with 128 columns, five with 64 or 32
+constexpr int kMoeSlots = 8;  // steps' scales ahead
+constexpr int kMoeBatch = 16; // steps between two sums of bf16 products
+constexpr int kMoeSums = 2 * kMoeGroup * 128;  // floats of a tile
+
+// How many pieces an activation and the intermediate are cut into, and how many
+// tokens fit beside one another in 128 columns.
+template <bool W8, bool XB>
+struct MoeCfg {
+    static constexpr int kX = W8 ? (XB ? 2 : 6) : (XB ? 1 : 3);
+    static constexpr int kH = W8 ? (XB ? 4 : 6) : (XB ? 2 : 3);
+    static constexpr int kGroup = W8 && !XB ? 16 : 32;
+    static constexpr int kElem = W8 ? 1 : 2, kStep = 128 / kElem;  // values of a step
+    // Both phases share the ring and TMEM: columns of a half of the sums, buffers
+    // of two halves, stages.
+    static constexpr int kCols = kH * kGroup <= 32 ? 32 : kH * kGroup <= 64 ? 64 : 128;
+    static constexpr int kBufs = 256 / kCols < 4 ? 256 / kCols : 4;
+    static constexpr int kStageBytes = kMoeWeightBytes + kCols * 128;
+    static constexpr int kStages = kMoeRing / kStageBytes < kMoeMaxStages ? kMoeRing / kStageBytes : kMoeMaxStages;
+    static_assert(kX <= kH && kH * kGroup <= 128, "columns");
+};
 
 struct MoeArgs {
-    CUtensorMap tgu, td;  // {d, ff, 2 experts} boxes {128 B, 64, 1}; {ff, d, experts} boxes {128 B, 128, 1}; swizzled
+    CUtensorMap tgu, td;  // {d, ff, 2 experts}, {ff, d, experts}: boxes of 128 B x 128 rows; swizzled
+    CUtensorMap tx, th;   // the pieces: {d, rows, pieces}, {ff, pairs, pieces}: boxes of 128 B x 8 rows x all pieces
     const void *x, *router, *residual;
     const float *gu_scales, *d_scales;
     void *y;
@@ -61,51 +85,40 @@ struct MoeArgs {
     int *err, *bars, *counters;  // counters [2][grid]: arrivals at the tile that a CTA's run ends in
     double *logits;              // [n][experts]
     float *wts;                  // [n k]
-    float *h;                    // [n k][ff]
-    float *parts;                // [grid][2][32 x 128]
+    float *parts;                // [grid][2][2 x 32 x 128]
     float *out;                  // [n k][d]
+    unsigned char *xp, *hp;      // pieces of x (by token, or by pair in the experts' order) and of the intermediate
+    float *xs, *hs;              // e4m3: a scale for each 128 of their rows
 };
 
 struct MoeShared {
-    uint64_t full[kMoeStages], empty[kMoeStages];
-    int dead, last;
+    uint64_t full[kMoeMaxStages], empty[kMoeMaxStages];
+    uint64_t s_full[kMoeSlots], s_empty[kMoeSlots];
+    uint64_t t_full[2][4], t_empty[4];  // (a warpgroup sees every phase of its own t_full, and no other)
+    uint64_t go, done;
+    uint32_t tmem;
+    int dead, last[2];
+    alignas(16) float scale[kMoeSlots][2][kMoeGroup];
+    unsigned top[2][4][kMoeGroup];
     int offset[kMoeMaxExperts + 1], jobs[kMoeMaxExperts + 1];
     unsigned short job_expert[kMoeMaxJobs];
     unsigned short list[kMoeMaxPairs];  // pairs (token * k + slot) by expert
-    union {
-        unsigned short chosen[kMoeMaxPairs];
-        float sums[kMoeWarps][128 * 8];
-    };
 };
-constexpr size_t kMoeSmem = 1024 + (size_t)kMoeStages * kMoeStageBytes + sizeof(MoeShared);
+constexpr size_t kMoeSmem = 1024 + (size_t)kMoeRing + sizeof(MoeShared);
 static_assert(kMoeSmem <= 227 * 1024, "shared memory");
+static_assert(kMoeMaxPairs * 2 <= kMoeRing, "the choices lie in the ring until it is used");
 
 // ------------------------------------------------------------------ waits
-__device__ __forceinline__ bool moe_wait(uint64_t *bar, uint32_t parity, volatile int *dead, int *err) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 1;; ++it) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((it & 63u) == 0) {
-            if (*dead) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                flag_error(err, DS_ERR_WAIT_TIMEOUT);
-                *dead = 1;
-                return false;
-            }
-        }
-    }
-}
 // One thread of every CTA: all of them have arrived, and what they wrote is seen.
 __device__ __forceinline__ void moe_meet(int *bar, volatile int *dead, int *err) {
     __threadfence();
     atomicAdd(bar, 1);
-    const uint64_t t0 = global_timer_ns();
+    const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
         int v;
         asm volatile("ld.acquire.gpu.global.b32 %0, [%1];" : "=r"(v) : "l"(bar) : "memory");
         if (v >= (int)gridDim.x || *dead) break;
-        if ((it & 63u) == 0 && global_timer_ns() - t0 > kWaitLimitNs) {
+        if ((it & 63u) == 0 && clock64() - t0 > kStreamWaitCycles) {
             flag_error(err, DS_ERR_WAIT_TIMEOUT);
             *dead = 1;
             break;
@@ -225,27 +238,28 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &p, int t, unsigned sho
 }
 
 // Every token's choices, and from them each expert's pairs in order and the
-// jobs (an expert with up to 32 of its pairs).  All threads.
-__device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh) {
+// jobs (an expert with up to G of its pairs).  All threads.
+template <int G>
+__device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh, unsigned short *chosen) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.n * p.k;
     for (int t = warp; t < p.n; t += kMoeThreads / 32) {
         const bool tell = t % gridDim.x == blockIdx.x;
-        if (p.experts <= 64) moe_choose<2>(p, t, sh.chosen, tell);
-        else if (p.experts <= 128) moe_choose<4>(p, t, sh.chosen, tell);
-        else moe_choose<16>(p, t, sh.chosen, tell);
+        if (p.experts <= 64) moe_choose<2>(p, t, chosen, tell);
+        else if (p.experts <= 128) moe_choose<4>(p, t, chosen, tell);
+        else moe_choose<16>(p, t, chosen, tell);
     }
     for (int e = threadIdx.x; e <= p.experts; e += kMoeThreads) sh.offset[e] = 0;
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kMoeThreads) {
         int c = 0;
-        for (int i = 0; i < pairs; ++i) c += sh.chosen[i] == e;
+        for (int i = 0; i < pairs; ++i) c += chosen[i] == e;
         sh.offset[e + 1] = c;
     }
     __syncthreads();
     if (warp == 0) {  // running sums of the pairs and of the jobs
         int o = 0, j = 0;
         for (int e0 = 0; e0 < p.experts; e0 += 32) {
-            const int e = e0 + lane, c = e < p.experts ? sh.offset[e + 1] : 0, g = (c + kMoeGroup - 1) / kMoeGroup;
+            const int e = e0 + lane, c = e < p.experts ? sh.offset[e + 1] : 0, g = (c + G - 1) / G;
             int so = c, sj = g;
 #pragma unroll
             for (int d = 1; d < 32; d *= 2) {
@@ -267,16 +281,121 @@ __device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh) {
         int at = sh.offset[e];
         if (at == sh.offset[e + 1]) continue;
         for (int i = 0; i < pairs; ++i)
-            if (sh.chosen[i] == e) sh.list[at++] = (unsigned short)i;
+            if (chosen[i] == e) sh.list[at++] = (unsigned short)i;
     }
     __syncthreads();
 }
 
-// ------------------------------------------------------------------ stages
-// A phase's line of stages: jobs x tiles x steps of the sum, an expert's jobs
+// ------------------------------------------------------------------ pieces
+__device__ __forceinline__ uint32_t moe_e4m3x2(float a, float b) {  // a in the low byte
+    unsigned short r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
+    return r;
+}
+__device__ __forceinline__ float2 moe_from_e4m3x2(uint32_t v) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((unsigned short)v));
+    float2 f;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.f32.f16 %0, a;\n\tcvt.f32.f16 %1, b;\n\t}" : "=f"(f.x), "=f"(f.y) : "r"(h));
+    return f;
+}
+// The power of two that brings a block's largest (its bits) to [2^7, 2^8), by no
+// more than 2^107, and its inverse; NaN for a block that is not finite.
+__device__ __forceinline__ void moe_scale(unsigned top, float &up, float &back) {
+    if (top >= 0x7f800000u) {
+        up = back = __int_as_float(0x7fffffff);
+        return;
+    }
+    const int e = max((int)(top >> 23) - 127, -100);
+    up = __uint_as_float((unsigned)(127 + 7 - e) << 23);
+    back = __uint_as_float((unsigned)(127 - 7 + e) << 23);
+}
+// Two neighbouring values' pieces, `step` bytes from piece to piece.
+template <bool W8, int P>
+__device__ __forceinline__ void moe_put2(unsigned char *to, size_t step, float a, float b, float up) {
+    if (W8) {
+        a *= up, b *= up;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const uint32_t v = moe_e4m3x2(a, b);
+            *reinterpret_cast<unsigned short *>(to + q * step) = (unsigned short)v;
+            const float2 f = moe_from_e4m3x2(v);
+            a = (a - f.x) * 16.0f, b = (b - f.y) * 16.0f;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            // cut off but for the last, which is rounded
+            const float x = __uint_as_float(__float_as_uint(a) & 0xffff0000u), z = __uint_as_float(__float_as_uint(b) & 0xffff0000u);
+            *reinterpret_cast<uint32_t *>(to + q * step) = q < P - 1 ? __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632) : stream_bf16x2(a, b);
+            a -= x, b -= z;
+        }
+    }
+}
+// The same for one value.
+template <bool W8, int P>
+__device__ __forceinline__ void moe_put(unsigned char *to, size_t step, float a, float up) {
+    if (W8) {
+        a *= up;
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const uint32_t v = moe_e4m3x2(a, 0.0f);
+            to[q * step] = (unsigned char)v;
+            a = (a - moe_from_e4m3x2(v).x) * 16.0f;
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < P; ++q) {
+            const float x = __uint_as_float(__float_as_uint(a) & 0xffff0000u);
+            *reinterpret_cast<unsigned short *>(to + q * step) =
+                q < P - 1 ? (unsigned short)(__float_as_uint(a) >> 16) : __bfloat16_as_ushort(__float2bfloat16_rn(a));
+            a -= x;
+        }
+    }
+}
+// Rows of x in pieces, a warp for each 128 values: row r is token r, or that of
+// the pair at place r of the experts' order.
+template <bool W8, int P>
+__device__ __forceinline__ void moe_split_x(const MoeArgs &p, const unsigned short *list, int rows) {
+    const int lane = threadIdx.x & 31, blocks = (p.d + 127) / 128, warps = kMoeThreads / 32;
+    constexpr int E = W8 ? 1 : 2;
+    for (int i = blockIdx.x * warps + (threadIdx.x >> 5); i < rows * blocks; i += gridDim.x * warps) {
+        const int r = i / blocks, j = (i - r * blocks) * 128 + lane * 4, tok = list ? list[r] / p.k : r;
+        float v[4] = {0, 0, 0, 0};
+        if (j < p.d) {  // (d is a multiple of 8)
+            if (p.x_dtype == DS_BF16) {
+                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (size_t)tok * p.d + j));
+                v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
+                v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
+            } else {
+                const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + (size_t)tok * p.d + j));
+                v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
+            }
+        }
+        float up = 1.0f, back;
+        if (W8) {
+            unsigned top = 0;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) top = max(top, __float_as_uint(v[q]) & 0x7fffffffu);
+            moe_scale(__reduce_max_sync(0xffffffffu, top), up, back);
+            if (lane == 0) p.xs[(size_t)r * blocks + (j >> 7)] = back;
+        }
+        if (j < p.d) {
+            unsigned char *to = p.xp + ((size_t)r * p.d + j) * E;
+            const size_t step = (size_t)rows * p.d * E;
+            moe_put2<W8, P>(to, step, v[0], v[1], up);
+            moe_put2<W8, P>(to + 2 * E, step, v[2], v[3], up);
+        }
+    }
+}
+// What this thread wrote is seen by copies of whoever it meets next.
+__device__ __forceinline__ void moe_fence_copies() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
+// ------------------------------------------------------------------ steps
+// A phase's line of steps: jobs x tiles x steps of the sum, an expert's jobs
 // side by side for each tile (its weights are then still in L2).
 struct MoeLine {
-    int tiles, steps, runs;   // runs: CTAs that have one, at least a stage each
+    int tiles, steps, runs;   // runs: CTAs that have one, at least a step each
     long long total, s0, s1;  // this CTA's run
     __device__ MoeLine(int jobs, int tiles_, int steps_) : tiles(tiles_), steps(steps_) {
         total = (long long)jobs * tiles * steps;
@@ -289,342 +408,387 @@ struct MoeLine {
 struct MoeTile {
     int expert, tile, start, count;  // its pairs: list[start ...]
 };
+template <int G>
 __device__ __forceinline__ MoeTile moe_tile(const MoeShared &sh, const MoeLine &l, int unit) {
     MoeTile t;
     t.expert = sh.job_expert[unit / l.tiles];
     const int j0 = sh.jobs[t.expert], g = sh.jobs[t.expert + 1] - j0, in = unit - j0 * l.tiles;
     t.tile = in / g;
-    t.start = sh.offset[t.expert] + in % g * kMoeGroup;
-    t.count = min(kMoeGroup, sh.offset[t.expert + 1] - t.start);
+    t.start = sh.offset[t.expert] + in % g * G;
+    t.count = min(G, sh.offset[t.expert + 1] - t.start);
     return t;
 }
-
-__device__ __forceinline__ void moe_box(uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint64_t *bar, uint64_t policy) {
+// A run's segments: the part of a tile's steps that lies in it.
+struct MoeSeg {
+    int unit, k0, k1;
+};
+__device__ __forceinline__ bool moe_next(const MoeLine &l, long long &s, MoeSeg &g) {
+    if (s >= l.s1) return false;
+    g.unit = (int)(s / l.steps);
+    g.k0 = (int)(s - (long long)g.unit * l.steps);
+    g.k1 = (int)min((long long)l.steps, g.k0 + l.s1 - s);
+    s += g.k1 - g.k0;
+    return true;
+}
+// Eight-token groups of a tile and the MMA's columns (a multiple of 16): a
+// group's pieces one after the other, eight tokens each.
+template <int P>
+struct MoeCols {
+    int groups, n;
+    __device__ explicit MoeCols(int count) : groups((count + 7) / 8), n((8 * P * groups + 15) & ~15) {}
+};
+__device__ __forceinline__ void moe_box(uint32_t one, uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
-        "%4}], [%5], %6;" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void moe_box_once(uint32_t one, uint32_t dst, const CUtensorMap *map, int x, int y, int z, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, %4}], [%5], "
+        "%7;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(one), "l"(policy)
+        : "memory");
+}
+__device__ __forceinline__ void moe_expect(uint32_t one, uint32_t bar, uint32_t bytes) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(one)
+        : "memory");
+}
+__device__ __forceinline__ void moe_mma_bf16(uint32_t one, uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(one)
         : "memory");
 }
 
-// The copying thread's share of a phase; returns false once a wait gave up.
-__device__ __forceinline__ bool moe_fetch(const MoeArgs &p, MoeShared &sh, uint32_t ring, const MoeLine &l, bool down, int step,
-                                          long long &fill, uint64_t policy) {
-    int unit = (int)(l.s0 / l.steps), k = (int)(l.s0 - (long long)unit * l.steps);
-    MoeTile t;
-    if (l.s0 < l.s1) t = moe_tile(sh, l, unit);
-    for (long long s = l.s0; s < l.s1; ++s) {
-        const int slot = (int)(fill % kMoeStages);
-        if (!moe_wait(&sh.empty[slot], (uint32_t)(fill / kMoeStages + 1) & 1, &sh.dead, p.err)) return false;
-        mbar_arrive_expect_tx(&sh.full[slot], kMoeStageBytes);
-        const uint32_t dst = ring + slot * kMoeStageBytes;
-        if (down) {
-            moe_box(dst, &p.td, k * step, t.tile * 128, t.expert, &sh.full[slot], policy);
-        } else {
-            moe_box(dst, &p.tgu, k * step, t.tile * 64, 2 * t.expert, &sh.full[slot], policy);
-            moe_box(dst + kMoeStageBytes / 2, &p.tgu, k * step, t.tile * 64, 2 * t.expert + 1, &sh.full[slot], policy);
+// State of the ring and of the buffers that goes on from phase to phase.
+struct MoeRing {
+    int s = 0, b = 0, slot = 0;
+    uint32_t ph = 0, bph = 0, sph = 0;
+    __device__ void stage(int stages) {
+        if (++s == stages) s = 0, ph ^= 1;
+    }
+    __device__ void buffer(int bufs) {
+        if (++b == bufs) b = 0, bph ^= 1;
+    }
+    __device__ void scales() {
+        if (++slot == kMoeSlots) slot = 0, sph ^= 1;
+    }
+};
+__device__ __forceinline__ uint64_t moe_policy_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+// Copies of a step's weights, and of its tokens' pieces: two arrivals a stage.
+template <int STAGE, bool DOWN>
+__device__ __forceinline__ void moe_copy_weights(const MoeArgs &p, MoeShared &sh, uint32_t one, uint32_t ring, int s, const MoeTile &t, int x, uint64_t policy) {
+    const uint32_t dst = ring + s * STAGE, bar = smem_u32(&sh.full[s]);
+    moe_expect(one, bar, kMoeWeightBytes);
+    if (DOWN) {
+        moe_box_once(one, dst, &p.td, x, t.tile * 256, t.expert, bar, policy);
+        moe_box_once(one, dst + kMoeWeightBytes / 2, &p.td, x, t.tile * 256 + 128, t.expert, bar, policy);
+    } else {
+        moe_box_once(one, dst, &p.tgu, x, t.tile * 128, 2 * t.expert, bar, policy);
+        moe_box_once(one, dst + kMoeWeightBytes / 2, &p.tgu, x, t.tile * 128, 2 * t.expert + 1, bar, policy);
+    }
+}
+template <int STAGE, int P>
+__device__ __forceinline__ void moe_copy_tokens(const MoeArgs &p, MoeShared &sh, uint32_t one, uint32_t ring, int s, const CUtensorMap *map, int row, int count, int x) {
+    const uint32_t dst = ring + s * STAGE + kMoeWeightBytes, bar = smem_u32(&sh.full[s]);
+    const int groups = (count + 7) / 8;
+    moe_expect(one, bar, groups * P * 1024);
+    for (int j = 0; j < groups; ++j) moe_box(one, dst + j * P * 1024, map, x, row + 8 * j, 0, bar);
+}
+
+// The copying warp's share of a phase.  The tokens of the down products are there
+// when the CTAs have met (`go`); until then the ring fills with weights.
+template <typename C, bool DOWN, int P>
+__device__ __forceinline__ void moe_copies(const MoeArgs &p, MoeShared &sh, uint32_t ring, const MoeLine &l, MoeRing &r) {
+    constexpr int G = C::kGroup, step = C::kStep;
+    const uint32_t one = stream_elect();
+    const uint64_t once = policy_evict_first(), again = moe_policy_normal();  // an expert's weights are read for each of its jobs
+    const bool by_token = !DOWN && p.n <= kMoeByToken;
+    MoeSeg g;
+    long long at = l.s0;
+    int ahead = 0;
+    if (DOWN) {
+        MoeRing w = r;
+        while (ahead < C::kStages && moe_next(l, at, g)) {
+            const MoeTile t = moe_tile<G>(sh, l, g.unit);
+            for (int k = g.k0; k < g.k1 && ahead < C::kStages; ++k, ++ahead) {
+                stream_wait(&sh.empty[w.s], w.ph ^ 1, &sh.dead, p.err);
+                if (*(volatile int *)&sh.dead) return;
+                moe_copy_weights<C::kStageBytes, DOWN>(p, sh, one, ring, w.s, t, k * step, sh.jobs[t.expert + 1] - sh.jobs[t.expert] > 1 ? again : once);
+                w.stage(C::kStages);
+            }
         }
-        ++fill;
-        if (++k == l.steps) {
-            k = 0;
-            ++unit;
-            if (s + 1 < l.s1) t = moe_tile(sh, l, unit);
+        stream_wait(&sh.go, 0, &sh.dead, p.err);
+        moe_fence_copies();
+        at = l.s0;
+    }
+    while (moe_next(l, at, g)) {
+        const MoeTile t = moe_tile<G>(sh, l, g.unit);
+        for (int k = g.k0; k < g.k1; ++k) {
+            if (ahead > 0) {
+                --ahead;
+            } else {
+                stream_wait(&sh.empty[r.s], r.ph ^ 1, &sh.dead, p.err);
+                if (*(volatile int *)&sh.dead) return;
+                moe_copy_weights<C::kStageBytes, DOWN>(p, sh, one, ring, r.s, t, k * step, sh.jobs[t.expert + 1] - sh.jobs[t.expert] > 1 ? again : once);
+            }
+            moe_copy_tokens<C::kStageBytes, P>(p, sh, one, ring, r.s, DOWN ? &p.th : &p.tx, by_token ? 0 : t.start, by_token ? p.n : t.count, k * step);
+            r.stage(C::kStages);
         }
     }
-    return true;
 }
 
-__device__ __forceinline__ uint4 moe_lds(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-    return v;
-}
-__device__ __forceinline__ void moe_mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void moe_mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Four e4m3 values as two f16 pairs.
-__device__ __forceinline__ void moe_widen(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-}
-__device__ __forceinline__ uint32_t moe_top2(float a, float b) {  // leading 8 bits, cut off, a in the low half
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ float moe_rest(float a) { return a - __uint_as_float(__float_as_uint(a) & 0xffff0000u); }
-__device__ __forceinline__ uint32_t moe_bf16x2(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-__device__ __forceinline__ uint32_t moe_f16x2(float a, float b) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
-    return r;
-}
-
-// A lane's values of one token for a stage: runs t and t + 4 of eight (bf16
-// weights) or sixteen (e4m3); zeros behind the sum's end and for no token.
-template <typename SRC, int RUN>
-__device__ __forceinline__ void moe_values(const SRC *row, int k0, int len, float (&v)[2 * RUN]) {
-    const int t = threadIdx.x & 3;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int k = k0 + (t + 4 * h) * RUN;
-        const bool in = row != nullptr && k < len;
-#pragma unroll
-        for (int i = 0; i < RUN; i += 8) {
-            float w[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-            if (in) {
-                if (sizeof(SRC) == 2) {
-                    widen16(__ldcg(reinterpret_cast<const uint4 *>(row + k + i)), w);
-                } else {
-                    const float4 a = __ldcg(reinterpret_cast<const float4 *>(row + k + i));
-                    const float4 b = __ldcg(reinterpret_cast<const float4 *>(row + k + i) + 1);
-                    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+// The products.
+template <typename C, bool DOWN, int P>
+__device__ __forceinline__ void moe_products(const MoeArgs &p, MoeShared &sh, uint32_t ring, const MoeLine &l, MoeRing &r, uint32_t tmem, int &turn) {
+    constexpr int G = C::kGroup;
+    constexpr bool W8 = C::kElem == 1;
+    const uint32_t one = stream_elect();
+    const bool by_token = !DOWN && p.n <= kMoeByToken;
+    MoeSeg g;
+    long long at = l.s0;
+    for (; moe_next(l, at, g); turn ^= 1) {
+        const MoeTile t = moe_tile<G>(sh, l, g.unit);
+        const MoeCols<P> c(by_token ? p.n : t.count);
+        const uint32_t idesc = (1u << 4) | (W8 ? 0u : (1u << 7) | (1u << 10)) | ((uint32_t)(c.n >> 3) << 17) | (8u << 24);
+        for (int k = g.k0; k < g.k1;) {
+            stream_wait(&sh.t_empty[r.b], r.bph ^ 1, &sh.dead, p.err);
+            tc_fence_after();
+            const uint32_t d = tmem + r.b * 2 * C::kCols;
+            const int end = W8 ? k + 1 : min(g.k1, k + kMoeBatch);
+            for (uint32_t more = 0; k < end; ++k, more = 1) {
+                if (W8) {  // a step's scales are there before its products start
+                    stream_wait(&sh.s_full[r.slot], r.sph, &sh.dead, p.err);
+                    r.scales();
                 }
-            }
+                stream_wait(&sh.full[r.s], r.ph, &sh.dead, p.err);
+                tc_fence_after();
+                const uint32_t a = ring + r.s * C::kStageBytes;
+                const uint64_t a0 = smem_desc(a, 16, 1024), a1 = smem_desc(a + kMoeWeightBytes / 2, 16, 1024), bd = smem_desc(a + kMoeWeightBytes, 16, 1024);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) v[h * RUN + i + q] = w[q];
+                for (int i = 0; i < 4; ++i) {  // 32 bytes of every row a product
+                    if (W8) {
+                        stream_mma_f8(one, d, a0 + 2 * i, bd + 2 * i, idesc, i > 0 || more);
+                        stream_mma_f8(one, d + C::kCols, a1 + 2 * i, bd + 2 * i, idesc, i > 0 || more);
+                    } else {
+                        moe_mma_bf16(one, d, a0 + 2 * i, bd + 2 * i, idesc, i > 0 || more);
+                        moe_mma_bf16(one, d + C::kCols, a1 + 2 * i, bd + 2 * i, idesc, i > 0 || more);
+                    }
+                }
+                stream_commit(one, &sh.empty[r.s]);
+                r.stage(C::kStages);
+            }
+            stream_commit(one, &sh.t_full[turn][r.b]);
+            r.buffer(C::kBufs);
         }
     }
 }
 
-// The MMA's row g is row (g >> 1 | (g & 1) << 2) of eight, so that the eight
-// lanes of a shared-memory access meet all banks of the swizzled stage.
-__device__ __forceinline__ int moe_row(int g) { return g >> 1 | (g & 1) << 2; }
-
-// acc += (128 rows of the stage) x (8 tokens), bf16 weights: P pieces of the tokens' values.
-template <int P>
-__device__ __forceinline__ void moe_stage_bf16(float (&acc)[8][4], uint32_t stage, const float (&v)[16]) {
-    uint32_t b[P][8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        float x = v[2 * i], y = v[2 * i + 1];
-        b[0][i] = moe_top2(x, y);
-        if (P > 1) {
-            x = moe_rest(x), y = moe_rest(y);
-            b[P > 1 ? 1 : 0][i] = P == 2 ? moe_bf16x2(x, y) : moe_top2(x, y);
-        }
-        if (P > 2) b[P - 1][i] = moe_bf16x2(moe_rest(x), moe_rest(y));
-    }
-    const int lane = threadIdx.x & 31, t = lane & 3, r = moe_row(lane >> 2);
-    // The tensor core cuts its sums off rather than rounding them, so a stage's
-    // are kept short, small pieces first, and added outside.
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        uint4 lo[2], hi[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t at = stage + (m * 16 + r) * 128 + (((t + 4 * h) ^ r) << 4);
-            lo[h] = moe_lds(at), hi[h] = moe_lds(at + 8 * 128);
-        }
-        float d[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int q = P - 1; q >= 0; --q)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                moe_mma_bf16(d, lo[h].x, hi[h].x, lo[h].y, hi[h].y, b[q][4 * h], b[q][4 * h + 1]);
-                moe_mma_bf16(d, lo[h].z, hi[h].z, lo[h].w, hi[h].w, b[q][4 * h + 2], b[q][4 * h + 3]);
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] += d[i];
-    }
-}
-
-// The same with e4m3 weights; s0, s1: scales of rows 0 to 63 and 64 to 127.
-template <int P>
-__device__ __forceinline__ void moe_stage_e4m3(float (&acc)[8][4], uint32_t stage, const float (&v)[32], float s0, float s1) {
-    const int lane = threadIdx.x & 31, t = lane & 3, r = moe_row(lane >> 2);
-    unsigned top = 0;
-#pragma unroll
-    for (int i = 0; i < 32; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    // the largest to [2^14, 2^15), but by no more than 2^114; what is not finite stays so
-    const int e = top >= 0x7f800000u ? 14 : max((int)(top >> 23) - 127, -100);
-    const float up = __uint_as_float((unsigned)(127 + 14 - e) << 23), back = __uint_as_float((unsigned)(127 - 14 + e) << 23);
-    uint32_t b[P][16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float x = v[2 * i] * up, y = v[2 * i + 1] * up;
-        b[0][i] = moe_f16x2(x, y);
-        if (P > 1) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&b[0][i]));
-            b[P - 1][i] = moe_f16x2(x - f.x, y - f.y);
-        }
-    }
-    const float b0 = __shfl_sync(0xffffffffu, back, t * 8), b1 = __shfl_sync(0xffffffffu, back, t * 8 + 4);
-#pragma unroll
-    for (int m = 0; m < 8; ++m) {
-        float d[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t at = stage + (m * 16 + r) * 128 + (((t + 4 * h) ^ r) << 4);
-            const uint4 lo = moe_lds(at), hi = moe_lds(at + 8 * 128);
-            const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t a0, a1, a2, a3;
-                moe_widen(wl[i], a0, a2);
-                moe_widen(wh[i], a1, a3);
-#pragma unroll
-                for (int q = P - 1; q >= 0; --q) moe_mma_f16(d, a0, a1, a2, a3, b[q][8 * h + 2 * i], b[q][8 * h + 2 * i + 1]);
-            }
-        }
-        const float s = m < 4 ? s0 : s1;
-        acc[m][0] += d[0] * (s * b0);
-        acc[m][1] += d[1] * (s * b1);
-        acc[m][2] += d[2] * (s * b0);
-        acc[m][3] += d[3] * (s * b1);
-    }
-}
-
-// ------------------------------------------------------------------ phases
-// Two sums (rows f and f + 64) of two tokens of a tile, finished: the
-// intermediate's value, or two of the down product.
-template <bool DOWN>
-__device__ __forceinline__ void moe_finish(const MoeArgs &p, const MoeShared &sh, const MoeTile &t, int token, int f, float2 a, float2 b) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        if (token + i >= t.count) return;
-        const long long pair = sh.list[t.start + token + i];
-        const float x = i ? a.y : a.x, z = i ? b.y : b.x;
+// e4m3: a step's scales, of each token's block times those of the weights' two blocks.
+template <int G, bool DOWN>
+__device__ __forceinline__ void moe_scales(const MoeArgs &p, MoeShared &sh, const MoeLine &l, MoeRing &r) {
+    const int lane = threadIdx.x & 31, db = (p.d + 127) / 128, fb = (p.ff + 127) / 128;
+    const bool by_token = !DOWN && p.n <= kMoeByToken;
+    if (DOWN) stream_wait(&sh.go, 0, &sh.dead, p.err);
+    MoeSeg g;
+    long long at = l.s0;
+    while (moe_next(l, at, g)) {
+        const MoeTile t = moe_tile<G>(sh, l, g.unit);
+        const int cols = by_token ? p.n : t.count, blocks = DOWN ? fb : db;
+        const float *xs = (DOWN ? p.hs : p.xs) + (size_t)(by_token ? 0 : t.start) * blocks;
+        const float *w0, *w1;
         if (DOWN) {
-            const int r = t.tile * 128 + f;
-            if (r < p.d) __stcg(p.out + pair * p.d + r, x);
-            if (r + 64 < p.d) __stcg(p.out + pair * p.d + r + 64, z);
+            w0 = p.d_scales + ((size_t)t.expert * db + 2 * t.tile) * fb;
+            w1 = 2 * t.tile + 1 < db ? w0 + fb : w0;
         } else {
-            const int r = t.tile * 64 + f;
-            if (r < p.ff) __stcg(p.h + pair * p.ff + r, x / (1.0f + expf(-x)) * z);
+            w0 = p.gu_scales + ((size_t)t.expert * 2 * fb + t.tile) * db;
+            w1 = w0 + (size_t)fb * db;
+        }
+        for (int k = g.k0; k < g.k1; k += 4) {
+            float x[4], a[4], b[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const bool in = k + j < g.k1;
+                x[j] = in && lane < cols ? __ldcg(xs + (size_t)lane * blocks + k + j) : 0.0f;
+                a[j] = in ? __ldg(w0 + k + j) : 0.0f;
+                b[j] = in ? __ldg(w1 + k + j) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (k + j >= g.k1) break;
+                stream_wait(&sh.s_empty[r.slot], r.sph ^ 1, &sh.dead, p.err);
+                sh.scale[r.slot][0][lane] = x[j] * a[j];
+                sh.scale[r.slot][1][lane] = x[j] * b[j];
+                __syncwarp();
+                stream_arrive(lane == 0, smem_u32(&sh.s_full[r.slot]));
+                r.scales();
+            }
         }
     }
 }
 
-// The eight warps' share of a phase.
-template <bool W8, bool DOWN, typename SRC, int P>
-__device__ __forceinline__ void moe_phase(const MoeArgs &p, MoeShared &sh, uint32_t ring, const MoeLine &l, long long &fill) {
-    constexpr int RUN = W8 ? 16 : 8, STEP = 8 * RUN;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int len = DOWN ? p.ff : p.d, db = (p.d + 127) / 128, fb = (p.ff + 127) / 128;
-    const SRC *src = DOWN ? reinterpret_cast<const SRC *>(p.h) : static_cast<const SRC *>(p.x);
-    for (long long s = l.s0; s < l.s1;) {
-        const int unit = (int)(s / l.steps), k0 = (int)(s - (long long)unit * l.steps);
-        const int k1 = (int)min((long long)l.steps, k0 + l.s1 - s);
-        const MoeTile tile = moe_tile(sh, l, unit);
-        const int groups = (tile.count + 7) / 8;
-        const SRC *row[4];
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            const int i = n * 8 + g;
-            row[n] = nullptr;
-            if (i < tile.count) {
-                const int pair = sh.list[tile.start + i];
-                row[n] = src + (DOWN ? (long long)pair * p.ff : (long long)(pair / p.k) * p.d);
+template <int N>
+__device__ __forceinline__ void moe_ld(uint32_t t, float *v) {
+    if constexpr (N == 24) {
+        stream_ld<16>(t, v);
+        stream_ld<8>(t + 16, v + 16);
+    } else if constexpr (N == 48) {
+        stream_ld<32>(t, v);
+        stream_ld<16>(t + 32, v + 32);
+    } else {
+        stream_ld<N>(t, v);
+    }
+}
+
+// Two warpgroups add up, a segment each in turn: thread r is row r of either half.
+template <typename C, bool DOWN, int P>
+__device__ __forceinline__ void moe_sums(const MoeArgs &p, MoeShared &sh, const MoeLine &l, MoeRing &r, uint32_t tmem, int &turn, uint32_t &seen) {
+    constexpr int G = C::kGroup, NG = G / 8, PH = C::kH;
+    constexpr bool W8 = C::kElem == 1;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, wg = warp >> 2, f = threadIdx.x & 127;
+    const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21), one = lane == 0;
+    const bool by_token = !DOWN && p.n <= kMoeByToken;
+    MoeSeg g;
+    long long at = l.s0;
+    for (; moe_next(l, at, g); turn ^= 1) {
+        if (turn != wg) {  // the other's: its buffers and slots pass by
+            const int batches = W8 ? g.k1 - g.k0 : (g.k1 - g.k0 + kMoeBatch - 1) / kMoeBatch;
+            for (int i = 0; i < batches; ++i) {
+                r.buffer(C::kBufs);
+                if (W8) r.scales();
             }
+            continue;
         }
-        const float *scale = nullptr, *scale1 = nullptr;
-        if (W8) {
-            if (DOWN) {
-                scale = scale1 = p.d_scales + ((long long)tile.expert * db + tile.tile) * fb;
-            } else {
-                scale = p.gu_scales + ((long long)tile.expert * 2 * fb + tile.tile / 2) * db;
-                scale1 = scale + (long long)fb * db;
-            }
-        }
-        float acc[4][8][4];
+        const MoeTile t = moe_tile<G>(sh, l, g.unit);
+        const MoeCols<P> cols(by_token ? p.n : t.count);
+        float acc[2][G];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-            for (int m = 0; m < 8; ++m)
+            for (int i = 0; i < G; ++i) acc[h][i] = 0.0f;
+        for (int k = g.k0; k < g.k1; k += W8 ? 1 : kMoeBatch) {
+            stream_wait(&sh.t_full[wg][r.b], seen >> r.b & 1, &sh.dead, p.err);
+            seen ^= 1u << r.b;
+            tc_fence_after();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[n][m][i] = 0.0f;
-        // this warp's stages: every eighth
-        for (int k = k0 + (int)((warp - fill) & (kMoeWarps - 1)); k < k1; k += kMoeWarps) {
-            const long long f = fill + (k - k0);
-            const int slot = (int)(f % kMoeStages);
-            const uint32_t stage = ring + slot * kMoeStageBytes;
-            float s0 = 1.0f, s1 = 1.0f;
-            if (W8) s0 = __ldg(scale + k), s1 = __ldg(scale1 + k);
+            for (int j = 0; j < NG; ++j) {
+                if (j < cols.groups) {
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                if (n < groups) {
-                    float v[2 * RUN];
-                    moe_values<SRC, RUN>(row[n], k * STEP, len, v);
-                    if (n == 0) moe_wait(&sh.full[slot], (uint32_t)(f / kMoeStages) & 1, &sh.dead, p.err);
-                    if constexpr (W8) moe_stage_e4m3<P>(acc[n], stage, v, s0, s1);
-                    else moe_stage_bf16<P>(acc[n], stage, v);
+                    for (int h = 0; h < 2; ++h) {
+                        float v[8 * P];
+                        moe_ld<8 * P>(from + r.b * 2 * C::kCols + h * C::kCols + j * 8 * P, v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float x = v[8 * (P - 1) + i];
+#pragma unroll
+                            for (int q = P - 2; q >= 0; --q) x = W8 ? __fmaf_rn(x, 0.0625f, v[8 * q + i]) : x + v[8 * q + i];
+                            acc[h][8 * j + i] = W8 ? __fmaf_rn(x, sh.scale[r.slot][h][8 * j + i], acc[h][8 * j + i]) : acc[h][8 * j + i] + x;
+                        }
+                    }
                 }
             }
+            tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.empty[slot]);
+            stream_arrive(one, smem_u32(&sh.t_empty[r.b]));
+            if (W8) {
+                stream_arrive(one, smem_u32(&sh.s_empty[r.slot]));
+                r.scales();
+            }
+            r.buffer(C::kBufs);
         }
-        fill += k1 - k0;
-        // the eight warps' sums, eight tokens at a time, added in order
-        const bool whole = k0 == 0 && k1 == l.steps;
-        const int f = threadIdx.x >> 2;
-        float *mine = p.parts + ((long long)blockIdx.x * 2 + (k0 == 0)) * kMoeSums;
+        if (g.k0 != 0 || g.k1 != l.steps) {
+            // a cut tile: partial sums, added by whoever is last, in CTA order
+            float *mine = p.parts + ((size_t)blockIdx.x * 2 + (g.k0 == 0)) * kMoeSums + f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            if (n >= groups) break;
-            float *to = sh.sums[warp];
-#pragma unroll
-            for (int m = 0; m < 8; ++m) {
-                const int r = m * 16 + moe_row(g);
-                *reinterpret_cast<float2 *>(to + r * 8 + 2 * t) = make_float2(acc[n][m][0], acc[n][m][1]);
-                *reinterpret_cast<float2 *>(to + (r + 8) * 8 + 2 * t) = make_float2(acc[n][m][2], acc[n][m][3]);
-            }
-            named_sync(1, kMoeWarps * 32);
-            float2 a = make_float2(0, 0), b = make_float2(0, 0);
-#pragma unroll
-            for (int w = 0; w < kMoeWarps; ++w) {
-                const float2 x = *reinterpret_cast<const float2 *>(sh.sums[w] + f * 8 + 2 * t);
-                const float2 z = *reinterpret_cast<const float2 *>(sh.sums[w] + (f + 64) * 8 + 2 * t);
-                a.x += x.x, a.y += x.y, b.x += z.x, b.y += z.y;
-            }
-            if (whole) {
-                moe_finish<DOWN>(p, sh, tile, n * 8 + 2 * t, f, a, b);
-            } else {
-                __stcg(reinterpret_cast<float2 *>(mine + n * 1024 + f * 8 + 2 * t), a);
-                __stcg(reinterpret_cast<float2 *>(mine + n * 1024 + (f + 64) * 8 + 2 * t), b);
-            }
-            named_sync(1, kMoeWarps * 32);
-        }
-        if (!whole) {
-            const long long u0 = (long long)unit * l.steps;
+            for (int i = 0; i < G; ++i)
+                if (i < 8 * cols.groups) {
+                    __stcg(mine + i * 128, acc[0][i]);
+                    __stcg(mine + (kMoeGroup + i) * 128, acc[1][i]);
+                }
+            const long long u0 = (long long)g.unit * l.steps;
             const int first = l.holder(u0), last = l.holder(u0 + l.steps - 1);
             int *counter = p.counters + (DOWN ? gridDim.x : 0) + first;
             __threadfence();
-            named_sync(1, kMoeWarps * 32);
-            if (threadIdx.x == 0) sh.last = atomicAdd(counter, 1) == last - first;
-            named_sync(1, kMoeWarps * 32);
-            if (sh.last) {
-                __threadfence();
-                for (int n = 0; n < groups; ++n) {
-                    float2 a = make_float2(0, 0), b = make_float2(0, 0);
-                    for (int c = first; c <= last; ++c) {
-                        const float *from = p.parts + ((long long)c * 2 + (c == first)) * kMoeSums + n * 1024;
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(from + f * 8 + 2 * t));
-                        const float2 z = __ldcg(reinterpret_cast<const float2 *>(from + (f + 64) * 8 + 2 * t));
-                        a.x += x.x, a.y += x.y, b.x += z.x, b.y += z.y;
+            named_sync(1 + wg, 128);
+            if (f == 0) sh.last[wg] = atomicAdd(counter, 1) == last - first;
+            named_sync(1 + wg, 128);
+            if (!sh.last[wg]) continue;
+            __threadfence();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < G; ++i) acc[h][i] = 0.0f;
+            for (int c = first; c <= last; ++c) {
+                const float *part = p.parts + ((size_t)c * 2 + (c == first)) * kMoeSums + f;
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+                    if (j < cols.groups) {
+                        float v[16];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + (8 * j + i) * 128), v[8 + i] = __ldcg(part + (kMoeGroup + 8 * j + i) * 128);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) acc[0][8 * j + i] += v[i], acc[1][8 * j + i] += v[8 + i];
                     }
-                    moe_finish<DOWN>(p, sh, tile, n * 8 + 2 * t, f, a, b);
-                }
-                if (threadIdx.x == 0) *counter = 0;
             }
-            named_sync(1, kMoeWarps * 32);
+            if (f == 0) *counter = 0;
         }
-        s += k1 - k0;
+        if (DOWN) {
+#pragma unroll
+            for (int i = 0; i < G; ++i)
+                if (i < t.count) {
+                    float *to = p.out + (size_t)sh.list[t.start + i] * p.d + t.tile * 256 + f;
+                    if (t.tile * 256 + f < p.d) __stcg(to, acc[0][i]);
+                    if (t.tile * 256 + 128 + f < p.d) __stcg(to + 128, acc[1][i]);
+                }
+            continue;
+        }
+        // the intermediate, in pieces at the pair's place in the experts' order
+        constexpr int E = W8 ? 1 : 2;
+        const int feature = t.tile * 128 + f;
+        const size_t step = (size_t)p.n * p.k * p.ff * E;
+#pragma unroll
+        for (int i = 0; i < G; ++i)
+            if (i < 8 * cols.groups) {
+                acc[0][i] = acc[0][i] / (1.0f + expf(-acc[0][i])) * acc[1][i];
+                if (W8) {
+                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+                    if (lane == 0) sh.top[wg][warp & 3][i] = top;
+                }
+            }
+        if (W8) named_sync(1 + wg, 128);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+            int at = i < t.count ? t.start + i : -1;
+            if (by_token) {  // column i is token i's: its place, if it chose this expert
+                at = -1;
+                for (int q = 0; q < t.count; ++q)
+                    if (sh.list[t.start + q] / p.k == i) at = t.start + q;
+            }
+            if (at < 0) continue;
+            float up = 1.0f, back;
+            if (W8) {
+                moe_scale(max(max(sh.top[wg][0][i], sh.top[wg][1][i]), max(sh.top[wg][2][i], sh.top[wg][3][i])), up, back);
+                if (f == 0) p.hs[(size_t)at * ((p.ff + 127) / 128) + t.tile] = back;
+            }
+            if (feature < p.ff) moe_put<W8, PH>(p.hp + ((size_t)at * p.ff + feature) * E, step, acc[0][i], up);
+        }
+        if (W8) named_sync(1 + wg, 128);  // before sh.top is written again
     }
 }
 
@@ -632,16 +796,33 @@ template <bool W8, typename X>
 __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_constant__ MoeArgs p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    MoeShared &sh = *reinterpret_cast<MoeShared *>(smem_raw + (ring - smem_u32(smem_raw)) + kMoeStages * kMoeStageBytes);
+    unsigned char *ring_p = smem_raw + (ring - smem_u32(smem_raw));
+    MoeShared &sh = *reinterpret_cast<MoeShared *>(ring_p + kMoeRing);
     const int warp = threadIdx.x >> 5;
     constexpr bool XB = sizeof(X) == 2;
+    using C = MoeCfg<W8, XB>;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < kMoeStages; ++i) {
-            mbar_init(&sh.full[i], 1);
+        for (int i = 0; i < kMoeMaxStages; ++i) {
+            mbar_init(&sh.full[i], 2);
             mbar_init(&sh.empty[i], 1);
         }
+        for (int i = 0; i < kMoeSlots; ++i) {
+            mbar_init(&sh.s_full[i], 1);
+            mbar_init(&sh.s_empty[i], 4);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sh.t_full[0][i], 1);
+            mbar_init(&sh.t_full[1][i], 1);
+            mbar_init(&sh.t_empty[i], 4);
+        }
+        mbar_init(&sh.go, 1);
+        mbar_init(&sh.done, 1);
         sh.dead = 0;
         fence_mbarrier_init();
+    }
+    if (warp == 9) {
+        tmem_alloc(&sh.tmem, 512);
+        tmem_relinquish();
     }
     // logits: a warp takes an expert with one token, or with four where that still gives every warp some
     const int gw = blockIdx.x * (kMoeThreads / 32) + warp, gn = gridDim.x * (kMoeThreads / 32);
@@ -650,37 +831,77 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
     } else {
         for (int i = gw; i < (p.n + 3) / 4 * p.experts; i += gn) moe_logits<4>(p, i % p.experts, i / p.experts * 4);
     }
+    if (p.n <= kMoeByToken) {
+        moe_split_x<W8, C::kX>(p, nullptr, p.n);
+        moe_fence_copies();
+    }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = sh.tmem;
     if (threadIdx.x == 0) moe_meet(p.bars, &sh.dead, p.err);
     __syncthreads();
-    if (!sh.dead) {  // (the same for all: read between two barriers of the block)
-        moe_route(p, sh);
-        constexpr int step = W8 ? 128 : 64;
+    bool dead = sh.dead;  // (the same for all: between two barriers of the block)
+    __syncthreads();
+    if (!dead) {
+        moe_route<C::kGroup>(p, sh, reinterpret_cast<unsigned short *>(ring_p));
+        if (p.n > kMoeByToken) {
+            moe_split_x<W8, C::kX>(p, sh.list, p.n * p.k);
+            moe_fence_copies();
+            __syncthreads();
+            if (threadIdx.x == 0) moe_meet(p.bars + 1, &sh.dead, p.err);
+            __syncthreads();
+            dead = sh.dead;
+            __syncthreads();
+        }
+        // the choices lay in the ring: copies may overwrite them now
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        moe_fence_copies();
+        __syncthreads();
+    }
+    if (!dead) {
         const int jobs = sh.jobs[p.experts];
-        const MoeLine gu(jobs, (p.ff + 63) / 64, (p.d + step - 1) / step), dn(jobs, (p.d + 127) / 128, (p.ff + step - 1) / step);
-        long long fill = 0;
-        if (warp >= kMoeWarps) {
+        const MoeLine gu(jobs, (p.ff + 127) / 128, (p.d + C::kStep - 1) / C::kStep), dn(jobs, (p.d + 255) / 256, (p.ff + C::kStep - 1) / C::kStep);
+        if (warp >= 8) {
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMoeRegsOther));
-            if (threadIdx.x == kMoeWarps * 32) {
-                const uint64_t policy = policy_evict_first();
-                if (moe_fetch(p, sh, ring, gu, false, step, fill, policy)) moe_fetch(p, sh, ring, dn, true, step, fill, policy);
-                // the copies still under way land before the CTA ends
-                for (long long i = max(0ll, fill - kMoeStages); i < fill; ++i)
-                    mbar_wait(&sh.full[i % kMoeStages], (uint32_t)(i / kMoeStages) & 1, p.err);
+            MoeRing r;
+            if (warp == 8) {
+                moe_copies<C, false, C::kX>(p, sh, ring, gu, r);
+                moe_copies<C, true, C::kH>(p, sh, ring, dn, r);
+                // After a wait that gave up, copies may be under way that nobody waits for: they land within microseconds.
+                if (*(volatile int *)&sh.dead)
+                    for (const long long t0 = clock64(); clock64() - t0 < 20000000ll;) {}
+            } else if (warp == 9) {
+                int turn = 0;
+                moe_products<C, false, C::kX>(p, sh, ring, gu, r, tmem, turn);
+                moe_products<C, true, C::kH>(p, sh, ring, dn, r, tmem, turn);
+                const uint32_t one = stream_elect();
+                stream_commit(one, &sh.done);
+                mbar_wait(&sh.done, 0, p.err);
+            } else if (W8 && warp == 10) {
+                moe_scales<C::kGroup, false>(p, sh, gu, r);
+                moe_scales<C::kGroup, true>(p, sh, dn, r);
             }
         } else {
-            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoeRegsMain));
-            moe_phase<W8, false, X, W8 ? (XB ? 1 : 2) : (XB ? 1 : 3)>(p, sh, ring, gu, fill);
-            named_sync(1, kMoeWarps * 32);
-            if (threadIdx.x == 0) moe_meet(p.bars + 1, &sh.dead, p.err);
-            named_sync(1, kMoeWarps * 32);
-            moe_phase<W8, true, float, W8 ? 2 : (XB ? 2 : 3)>(p, sh, ring, dn, fill);
-            named_sync(1, kMoeWarps * 32);
-            if (threadIdx.x == 0) moe_meet(p.bars + 2, &sh.dead, p.err);
-            named_sync(1, kMoeWarps * 32);
+            asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoeRegsSum));
+            MoeRing r;
+            int turn = 0;
+            uint32_t seen = 0;  // phases of its buffers, a bit each
+            moe_sums<C, false, C::kX>(p, sh, gu, r, tmem, turn, seen);
+            moe_fence_copies();
+            named_sync(3, 256);
+            if (threadIdx.x == 0) {
+                moe_meet(p.bars + 2, &sh.dead, p.err);
+                moe_fence_copies();
+                mbar_arrive(&sh.go);
+            }
+            moe_sums<C, true, C::kH>(p, sh, dn, r, tmem, turn, seen);
+            named_sync(3, 256);
+            if (threadIdx.x == 0) moe_meet(p.bars + 3, &sh.dead, p.err);
+            named_sync(3, 256);
             // the weighted sum, four values a thread
             const int quads = p.d / 4;
-            for (long long i = (long long)blockIdx.x * kMoeWarps * 32 + threadIdx.x; i < (long long)p.n * quads; i += (long long)gridDim.x * kMoeWarps * 32) {
+            for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < (long long)p.n * quads; i += (long long)gridDim.x * 256) {
                 const int tok = (int)(i / quads), j = (int)(i - (long long)tok * quads) * 4;
                 const long long at = (long long)tok * p.d + j;
                 float4 v = make_float4(0, 0, 0, 0);
@@ -690,21 +911,23 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
                     const float4 o = __ldcg(reinterpret_cast<const float4 *>(p.out + pair * p.d + j));
                     v.x += w * o.x, v.y += w * o.y, v.z += w * o.z, v.w += w * o.w;
                 }
-                X *y = static_cast<X *>(p.y) + at;
                 const float o[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    const float r = p.residual ? load_as(p.residual, at + q, p.x_dtype) : 0.0f;
-                    store_as(y, q, p.x_dtype, r + o[q]);
+                    const float res = p.residual ? load_as(p.residual, at + q, p.x_dtype) : 0.0f;
+                    store_as(p.y, at + q, p.x_dtype, res + o[q]);
                 }
             }
         }
     }
+    tc_fence_before();
     __syncthreads();
+    tc_fence_after();
+    if (warp == 9) tmem_dealloc(tmem, 512);
     // the last CTA leaves the meeting counts as they were found
     if (threadIdx.x == 0) {
-        if (atomicAdd(p.bars + 3, 1) == (int)gridDim.x - 1) {
-            p.bars[0] = p.bars[1] = p.bars[2] = p.bars[3] = 0;
+        if (atomicAdd(p.bars + 4, 1) == (int)gridDim.x - 1) {
+            p.bars[0] = p.bars[1] = p.bars[2] = p.bars[3] = p.bars[4] = 0;
             __threadfence();
         }
     }
@@ -712,19 +935,27 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- host
 struct MoeSpace {
-    size_t bars, counters, logits, wts, h, parts, out, total;
+    size_t bars, counters, parts, logits, wts, out, xp, xs, hp, hs, total;
 };
 static MoeSpace moe_space(int64_t n, int64_t d, int64_t ff, int64_t experts, int64_t k) {
     MoeSpace s;
-    const size_t g = (size_t)sm_count(), pairs = (size_t)(n * k);
+    const size_t g = (size_t)sm_count(), pairs = (size_t)(n * k), rows = n <= kMoeByToken ? (size_t)n : pairs;
     size_t at = kWsHeader;
-    s.bars = at, at += 256;
-    s.counters = at, at += align_up(2 * g * 4, 256);
-    s.parts = at, at += g * 2 * kMoeSums * 4;
-    s.logits = at, at += align_up((size_t)(n * experts) * 8, 256);
-    s.wts = at, at += align_up(pairs * 4, 256);
-    s.h = at, at += align_up(pairs * ff * 4, 256);
-    s.out = at, at += align_up(pairs * d * 4, 256);
+    const auto take = [&](size_t bytes) {
+        const size_t was = at;
+        at += align_up(bytes, 256);
+        return was;
+    };
+    s.bars = take(256);
+    s.counters = take(2 * g * 4);
+    s.parts = take(g * 2 * kMoeSums * 4);
+    s.logits = take((size_t)(n * experts) * 8);
+    s.wts = take(pairs * 4);
+    s.out = take(pairs * d * 4);
+    s.xp = take(rows * d * 6);  // three pieces of two bytes or six of one
+    s.xs = take(rows * ((d + 127) / 128) * 4);
+    s.hp = take(pairs * ff * 6);
+    s.hs = take(pairs * ((ff + 127) / 128) * 4);
     s.total = at;
     return s;
 }
@@ -833,18 +1064,27 @@ extern "C" DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, in
     a.counters = reinterpret_cast<int *>(w + sp.counters);
     a.logits = reinterpret_cast<double *>(w + sp.logits);
     a.wts = reinterpret_cast<float *>(w + sp.wts);
-    a.h = reinterpret_cast<float *>(w + sp.h);
+    a.xp = reinterpret_cast<unsigned char *>(w + sp.xp);
+    a.hp = reinterpret_cast<unsigned char *>(w + sp.hp);
+    a.xs = reinterpret_cast<float *>(w + sp.xs);
+    a.hs = reinterpret_cast<float *>(w + sp.hs);
     a.parts = reinterpret_cast<float *>(w + sp.parts);
     a.out = reinterpret_cast<float *>(w + sp.out);
-    const int box = w8 ? 128 : 64;
+    const bool xb = x_dtype == DS_BF16;
+    const int box = w8 ? 128 : 64, px = w8 ? (xb ? MoeCfg<true, true>::kX : MoeCfg<true, false>::kX) : (xb ? MoeCfg<false, true>::kX : MoeCfg<false, false>::kX);
+    const int ph = w8 ? (xb ? MoeCfg<true, true>::kH : MoeCfg<true, false>::kH) : (xb ? MoeCfg<false, true>::kH : MoeCfg<false, false>::kH);
+    const long long pairs = n * top_k, xrows = n <= kMoeByToken ? n : pairs;
     const long long gdims[3] = {d, ff, 2LL * n_experts}, gst[2] = {d * ws, ff * d * ws};
     const long long ddims[3] = {ff, d, n_experts}, dst[2] = {ff * ws, ff * d * ws};
-    const int gbox[3] = {box, 64, 1}, dbox[3] = {box, 128, 1};
-    if (!encode_tiled_3d(&a.tgu, w_gate_up, w_dtype, gdims, gst, gbox, true) ||
-        !encode_tiled_3d(&a.td, w_down, w_dtype, ddims, dst, dbox, true))
+    const long long xdims[3] = {d, xrows, px}, xst[2] = {d * ws, xrows * d * ws};
+    const long long hdims[3] = {ff, pairs, ph}, hst[2] = {ff * ws, pairs * ff * ws};
+    const int wbox[3] = {box, 128, 1}, xbox[3] = {box, 8, px}, hbox[3] = {box, 8, ph};
+    if (!encode_tiled_3d(&a.tgu, w_gate_up, w_dtype, gdims, gst, wbox, true) ||
+        !encode_tiled_3d(&a.td, w_down, w_dtype, ddims, dst, wbox, true) ||
+        !encode_tiled_3d(&a.tx, a.xp, w_dtype, xdims, xst, xbox, true) ||
+        !encode_tiled_3d(&a.th, a.hp, w_dtype, hdims, hst, hbox, true))
         return DS_CUDA_ERROR;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const bool xb = x_dtype == DS_BF16;
     const cudaError_t e = w8 ? (xb ? moe_launch<true, __nv_bfloat16>(a, s) : moe_launch<true, float>(a, s))
                              : (xb ? moe_launch<false, __nv_bfloat16>(a, s) : moe_launch<false, float>(a, s));
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
