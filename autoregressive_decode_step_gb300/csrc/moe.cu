@@ -80,12 +80,13 @@ struct MoeArgs {
     int *ids;
     float *weights;
     int x_dtype, r_dtype;
-    int n, d, ff, experts, k, renormalize;
+    int n, d, ff, experts, k, renormalize, splits;
     // workspace
     int *err, *bars, *counters;  // counters [2][grid]: arrivals at the tile that a CTA's run ends in
-    double *logits;              // [n][experts]
+    float2 *logits;              // [splits][n][experts]: a sum and what its roundings lost
+    unsigned short *choices;     // [n k]
     float *wts;                  // [n k]
-    float *parts;                // [grid][2][2 x 32 x 128]
+    float *parts;                // [grid][4][2 x 32 x 128]: a run's first and last tile, whole tiles of either warpgroup
     float *out;                  // [n k][d]
     unsigned char *xp, *hp;      // pieces of x (by token, or by pair in the experts' order) and of the intermediate
     float *xs, *hs;              // e4m3: a scale for each 128 of their rows
@@ -99,20 +100,19 @@ struct MoeShared {
     uint32_t tmem;
     int dead, last[2];
     alignas(16) float scale[kMoeSlots][2][kMoeGroup];
-    unsigned top[2][4][kMoeGroup];
+    unsigned top[2][4][8];
     int offset[kMoeMaxExperts + 1], jobs[kMoeMaxExperts + 1];
     unsigned short job_expert[kMoeMaxJobs];
     unsigned short list[kMoeMaxPairs];  // pairs (token * k + slot) by expert
 };
 constexpr size_t kMoeSmem = 1024 + (size_t)kMoeRing + sizeof(MoeShared);
 static_assert(kMoeSmem <= 227 * 1024, "shared memory");
-static_assert(kMoeMaxPairs * 2 <= kMoeRing, "the choices lie in the ring until it is used");
 
 // ------------------------------------------------------------------ waits
 // One thread of every CTA: all of them have arrived, and what they wrote is seen.
 __device__ __forceinline__ void moe_meet(int *bar, volatile int *dead, int *err) {
     __threadfence();
-    atomicAdd(bar, 1);
+    asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(bar) : "memory");
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
         int v;
@@ -124,7 +124,15 @@ __device__ __forceinline__ void moe_meet(int *bar, volatile int *dead, int *err)
             break;
         }
     }
-    __threadfence();
+}
+
+// The same for all threads of the CTA; whether a wait gave up.
+__device__ __forceinline__ bool moe_meet_all(const MoeArgs &p, MoeShared &sh, int bar) {
+    if (threadIdx.x == 0) moe_meet(p.bars + bar, &sh.dead, p.err);
+    __syncthreads();
+    const bool dead = sh.dead;
+    __syncthreads();
+    return dead;
 }
 
 // ------------------------------------------------------------------ router
@@ -144,14 +152,37 @@ __device__ __forceinline__ void moe_dot2(float a, float b, float &s, float &c) {
     c = __fadd_rn(c, __fadd_rn(e, __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(p, z))));
     s = t;
 }
-// One expert's logits of T tokens by a warp.
+// (s, c) += (s2, c2).  The same whichever is added to which: a two-sum's results
+// do not depend on its operands' order.
+__device__ __forceinline__ void moe_add2(float &s, float &c, float s2, float c2) {
+    const float t = __fadd_rn(s, s2), z = __fsub_rn(t, s);
+    c = __fadd_rn(__fadd_rn(c, c2), __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(s2, z)));
+    s = t;
+}
+// How the logits are dealt out: T tokens with an expert and one of `splits` parts
+// of the sum (each a whole number of 256 values) make an item, a warp's work.
+struct MoeLogits {
+    int tokens, splits;
+};
+__host__ __device__ inline MoeLogits moe_logits_plan(long long n, long long d, long long experts, int warps) {
+    MoeLogits l;
+    l.tokens = n == 1 ? 1 : 4;
+    const long long items = (n + l.tokens - 1) / l.tokens * experts, whole = (d + 255) / 256;
+    long long s = 8LL * warps / items;  // several items a warp even out
+    s = s < 1 ? 1 : s > whole ? whole : s > 16 ? 16 : s;
+    const long long per = (whole + s - 1) / s;
+    l.splits = (int)((whole + per - 1) / per);
+    return l;
+}
+// Part s of the sum of one expert's logits of T tokens, by a warp.
 template <int T>
-__device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0) {
-    const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0, int split) {
+    const int lane = threadIdx.x & 31, per = ((p.d + 255) / 256 + p.splits - 1) / p.splits * 256;
+    const int end = min(p.d, (split + 1) * per);
     float s[T], c[T];
 #pragma unroll
     for (int i = 0; i < T; ++i) s[i] = c[i] = 0.0f;
-    for (int j = lane * 8; j < p.d; j += 256) {
+    for (int j = split * per + lane * 8; j < end; j += 256) {
         float r[8], x[T][8];
         moe_load8(p.router, (long long)e * p.d + j, p.r_dtype, r);
 #pragma unroll
@@ -162,12 +193,16 @@ __device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0) {
             for (int q = 0; q < 8; ++q) moe_dot2(x[i][q], r[q], s[i], c[i]);
     }
 #pragma unroll
-    for (int i = 0; i < T; ++i) {
-        // an infinite sum's lost part is NaN: the sum says it all
-        double v = fabsf(s[i]) < INFINITY ? (double)s[i] + (double)c[i] : (double)s[i];
+    for (int o = 16; o > 0; o >>= 1)  // (in two floats: doubles add at a sixty-fourth of the rate)
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-        if (lane == 0 && t0 + i < p.n) p.logits[(long long)(t0 + i) * p.experts + e] = v;
+        for (int i = 0; i < T; ++i)
+            moe_add2(s[i], c[i], __shfl_xor_sync(0xffffffffu, s[i], o), __shfl_xor_sync(0xffffffffu, c[i], o));
+    if (lane < T && t0 + lane < p.n) {
+        float sum = s[0], lost = c[0];
+#pragma unroll
+        for (int i = 1; i < T; ++i)
+            if (lane == i) sum = s[i], lost = c[i];
+        p.logits[((long long)split * p.n + t0 + lane) * p.experts + e] = make_float2(sum, lost);
     }
 }
 
@@ -178,54 +213,46 @@ __device__ __forceinline__ unsigned long long moe_key(double v) {
     const unsigned long long b = (unsigned long long)__double_as_longlong(v);
     return b >> 63 ? ~b : b | 1ull << 63;
 }
-// A token's k experts by a warp; PER: experts a lane holds.
-template <int PER>
-__device__ __forceinline__ void moe_choose(const MoeArgs &p, int t, unsigned short *chosen, bool tell) {
-    const int lane = threadIdx.x & 31;
-    unsigned long long key[PER];
-    double v[PER];
-#pragma unroll
-    for (int i = 0; i < PER; ++i) {
-        const int e = lane + 32 * i;
-        v[i] = e < p.experts ? __ldcg(p.logits + (long long)t * p.experts + e) : 0.0;
-        key[i] = e < p.experts ? moe_key(v[i]) : 0ull;
-    }
-    double top = 0.0;
-    float mine = 0.0f;  // lane i: the i-th choice's exponential
-    int mine_e = 0;
-    for (int c = 0; c < p.k; ++c) {
-        unsigned long long best = 0ull;
-        int at = 0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (key[i] > best) best = key[i], at = i;
-        const unsigned hi = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32));
-        const unsigned lo = __reduce_max_sync(0xffffffffu, (unsigned)(best >> 32) == hi ? (unsigned)best : 0u);
-        const bool is = (unsigned)(best >> 32) == hi && (unsigned)best == lo;
-        const int e = (int)__reduce_min_sync(0xffffffffu, is ? (unsigned)(lane + 32 * at) : 0xffffffffu);
-        double val = 0.0;
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i == e) {
-                key[i] = 0ull;
-                val = v[i];
-            }
-        val = __shfl_sync(0xffffffffu, val, e & 31);
-        if (c == 0) top = val;
-        if (lane == c) {
-            mine = expf((float)(val - top));
-            mine_e = e;
+__device__ __forceinline__ double moe_value(unsigned long long key) {
+    return __longlong_as_double((long long)(key >> 63 ? key & ~(1ull << 63) : ~key));
+}
+// The logits of tokens t0 ... t0 + n - 1, the parts of their sums added, as keys;
+// `id` of `step` threads.
+__device__ __forceinline__ void moe_keys(const MoeArgs &p, int t0, int n, unsigned long long *key, int id, int step) {
+    for (int i = id; i < n * p.experts; i += step) {
+        const float2 *from = p.logits + (long long)t0 * p.experts + i;
+        float sum = 0.0f, lost = 0.0f;
+#pragma unroll 8
+        for (int s = 0; s < p.splits; ++s) {
+            const float2 v = __ldcg(from + (long long)s * p.n * p.experts);
+            moe_add2(sum, lost, v.x, v.y);
         }
+        // an infinite sum's lost part is NaN: the sum says it all
+        key[i] = moe_key(fabsf(sum) < INFINITY ? (double)sum + (double)lost : (double)sum);
     }
-    if (lane < p.k) chosen[t * p.k + lane] = (unsigned short)mine_e;
-    if (!tell) return;
+}
+// The tokens' choices: an expert's place is the number of experts ahead of it, so
+// all are found at once.
+__device__ __forceinline__ void moe_choose(const MoeArgs &p, int n, const unsigned long long *key, unsigned short *chosen, int id, int step) {
+    for (int i = id; i < n * p.experts; i += step) {
+        const int t = i / p.experts, e = i - t * p.experts;
+        const unsigned long long *of = key + t * p.experts, mine = of[e];
+        int ahead = 0;
+#pragma unroll 4
+        for (int j = 0; j < p.experts; ++j) ahead += of[j] > mine || (of[j] == mine && j < e);
+        if (ahead < p.k) chosen[t * p.k + ahead] = (unsigned short)e;
+    }
+}
+// A token's weights, and what is told of its choices, by a warp.
+__device__ __forceinline__ void moe_weights(const MoeArgs &p, int t, const unsigned long long *key, const unsigned short *chosen) {
+    const int lane = threadIdx.x & 31, e = lane < p.k ? chosen[lane] : 0;
+    const double top = moe_value(key[chosen[0]]);
+    const float mine = lane < p.k ? expf((float)(moe_value(key[e]) - top)) : 0.0f;
     float sum = 0.0f;
     if (p.renormalize) {
         for (int c = 0; c < p.k; ++c) sum += __shfl_sync(0xffffffffu, mine, c);
     } else {
-#pragma unroll
-        for (int i = 0; i < PER; ++i)
-            if (lane + 32 * i < p.experts) sum += expf((float)(v[i] - top));
+        for (int i = lane; i < p.experts; i += 32) sum += expf((float)(moe_value(key[i]) - top));
         sum = warp_sum(sum);
     }
     if (lane < p.k) {
@@ -233,27 +260,45 @@ __device__ __forceinline__ void moe_choose(const MoeArgs &p, int t, unsigned sho
         const float w = mine / sum;
         p.wts[at] = w;
         if (p.weights) p.weights[at] = w;
-        if (p.ids) p.ids[at] = mine_e;
+        if (p.ids) p.ids[at] = e;
     }
 }
 
-// Every token's choices, and from them each expert's pairs in order and the
-// jobs (an expert with up to G of its pairs).  All threads.
+// From every token's choices each expert's pairs in order and the jobs (an
+// expert with up to G of its pairs).  A warp counts a stretch of the pairs;
+// lanes with the same expert find one another.  All threads.
+struct MoeRoute {
+    unsigned short chosen[kMoeMaxPairs], place[kMoeMaxPairs], count[kMoeThreads / 32][kMoeMaxExperts];
+    unsigned long long key[kMoeByToken][kMoeMaxExperts];  // logits
+};
+static_assert(sizeof(MoeRoute) <= kMoeRing, "the choices lie in the ring until it is used");
 template <int G>
-__device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh, unsigned short *chosen) {
+__device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh, MoeRoute &r) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.n * p.k;
-    for (int t = warp; t < p.n; t += kMoeThreads / 32) {
-        const bool tell = t % gridDim.x == blockIdx.x;
-        if (p.experts <= 64) moe_choose<2>(p, t, chosen, tell);
-        else if (p.experts <= 128) moe_choose<4>(p, t, chosen, tell);
-        else moe_choose<16>(p, t, chosen, tell);
+    const int per = (pairs + kMoeThreads - 1) / kMoeThreads * 32;  // pairs of a warp
+    for (int e = lane; e < p.experts; e += 32) r.count[warp][e] = 0;
+    __syncwarp();
+    for (int i = warp * per + lane; i - lane < min(pairs, (warp + 1) * per); i += 32) {
+        const unsigned e = i < pairs ? r.chosen[i] : 0xffffu;
+        const unsigned same = __match_any_sync(0xffffffffu, e), before = __popc(same & ((1u << lane) - 1));
+        const int base = i < pairs ? r.count[warp][e] : 0;
+        __syncwarp();
+        if (i < pairs) {
+            r.place[i] = (unsigned short)(base + before);
+            if (before == 0) r.count[warp][e] = (unsigned short)(base + __popc(same));
+        }
+        __syncwarp();
     }
-    for (int e = threadIdx.x; e <= p.experts; e += kMoeThreads) sh.offset[e] = 0;
+    if (threadIdx.x == 0) sh.offset[0] = sh.jobs[0] = 0;
     __syncthreads();
     for (int e = threadIdx.x; e < p.experts; e += kMoeThreads) {
-        int c = 0;
-        for (int i = 0; i < pairs; ++i) c += chosen[i] == e;
-        sh.offset[e + 1] = c;
+        int sum = 0;
+        for (int w = 0; w < kMoeThreads / 32; ++w) {
+            const int c = r.count[w][e];
+            r.count[w][e] = (unsigned short)sum;
+            sum += c;
+        }
+        sh.offset[e + 1] = sum;
     }
     __syncthreads();
     if (warp == 0) {  // running sums of the pairs and of the jobs
@@ -274,14 +319,11 @@ __device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh, unsig
             o += __shfl_sync(0xffffffffu, so, 31);
             j += __shfl_sync(0xffffffffu, sj, 31);
         }
-        if (lane == 0) sh.jobs[0] = 0;
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < p.experts; e += kMoeThreads) {
-        int at = sh.offset[e];
-        if (at == sh.offset[e + 1]) continue;
-        for (int i = 0; i < pairs; ++i)
-            if (chosen[i] == e) sh.list[at++] = (unsigned short)i;
+    for (int i = threadIdx.x; i < pairs; i += kMoeThreads) {
+        const int e = r.chosen[i];
+        sh.list[sh.offset[e] + r.count[i / per][e] + r.place[i]] = (unsigned short)i;
     }
     __syncthreads();
 }
@@ -712,83 +754,91 @@ __device__ __forceinline__ void moe_sums(const MoeArgs &p, MoeShared &sh, const 
             }
             r.buffer(C::kBufs);
         }
-        if (g.k0 != 0 || g.k1 != l.steps) {
-            // a cut tile: partial sums, added by whoever is last, in CTA order
-            float *mine = p.parts + ((size_t)blockIdx.x * 2 + (g.k0 == 0)) * kMoeSums + f;
+        // Sums go through memory, cut tile or not, so that what follows is one
+        // short loop over groups of eight tokens: a tile ends once or twice a
+        // phase and CTA, and code that runs once is paid for in fetches of it.
+        const bool whole = g.k0 == 0 && g.k1 == l.steps;
+        float *mine = p.parts + ((size_t)blockIdx.x * 4 + (whole ? 2 + wg : g.k0 == 0)) * kMoeSums + f;
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (i < 8 * cols.groups) {
+        for (int j = 0; j < NG; ++j)
+            if (j < cols.groups) {
+#pragma unroll
+                for (int i = 8 * j; i < 8 * j + 8; ++i) {
                     __stcg(mine + i * 128, acc[0][i]);
                     __stcg(mine + (kMoeGroup + i) * 128, acc[1][i]);
                 }
+            }
+        int first = blockIdx.x, last = blockIdx.x;
+        if (!whole) {  // a cut tile: whoever is last goes on
             const long long u0 = (long long)g.unit * l.steps;
-            const int first = l.holder(u0), last = l.holder(u0 + l.steps - 1);
+            first = l.holder(u0);
+            last = l.holder(u0 + l.steps - 1);
             int *counter = p.counters + (DOWN ? gridDim.x : 0) + first;
-            __threadfence();
             named_sync(1 + wg, 128);
-            if (f == 0) sh.last[wg] = atomicAdd(counter, 1) == last - first;
+            if (f == 0) {
+                __threadfence();  // for what the whole warpgroup wrote
+                const bool is = atomicAdd(counter, 1) == last - first;
+                if (is) {
+                    *counter = 0;
+                    __threadfence();
+                }
+                sh.last[wg] = is;
+            }
             named_sync(1 + wg, 128);
             if (!sh.last[wg]) continue;
-            __threadfence();
+        }
+        for (int j = 0; j < cols.groups; ++j) {
+            float a[8], b[8];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
+            for (int c = first; c <= last; ++c) {  // in CTA order
+                const float *part = p.parts + ((size_t)c * 4 + (whole ? 2 + wg : c == first)) * kMoeSums + j * 1024 + f;
+                float v[8], w[8];
 #pragma unroll
-                for (int i = 0; i < G; ++i) acc[h][i] = 0.0f;
-            for (int c = first; c <= last; ++c) {
-                const float *part = p.parts + ((size_t)c * 2 + (c == first)) * kMoeSums + f;
+                for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + i * 128), w[i] = __ldcg(part + (kMoeGroup + i) * 128);
 #pragma unroll
-                for (int j = 0; j < NG; ++j)
-                    if (j < cols.groups) {
-                        float v[16];
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + (8 * j + i) * 128), v[8 + i] = __ldcg(part + (kMoeGroup + 8 * j + i) * 128);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) acc[0][8 * j + i] += v[i], acc[1][8 * j + i] += v[8 + i];
-                    }
+                for (int i = 0; i < 8; ++i) a[i] += v[i], b[i] += w[i];
             }
-            if (f == 0) *counter = 0;
-        }
-        if (DOWN) {
+            if (DOWN) {
+                const int row = t.tile * 256 + f;
 #pragma unroll
-            for (int i = 0; i < G; ++i)
-                if (i < t.count) {
-                    float *to = p.out + (size_t)sh.list[t.start + i] * p.d + t.tile * 256 + f;
-                    if (t.tile * 256 + f < p.d) __stcg(to, acc[0][i]);
-                    if (t.tile * 256 + 128 + f < p.d) __stcg(to + 128, acc[1][i]);
-                }
-            continue;
-        }
-        // the intermediate, in pieces at the pair's place in the experts' order
-        constexpr int E = W8 ? 1 : 2;
-        const int feature = t.tile * 128 + f;
-        const size_t step = (size_t)p.n * p.k * p.ff * E;
+                for (int i = 0; i < 8; ++i)
+                    if (8 * j + i < t.count) {
+                        float *to = p.out + (size_t)sh.list[t.start + 8 * j + i] * p.d + row;
+                        if (row < p.d) __stcg(to, a[i]);
+                        if (row + 128 < p.d) __stcg(to + 128, b[i]);
+                    }
+                continue;
+            }
+            // the intermediate, in pieces at the pair's place in the experts' order
+            constexpr int E = W8 ? 1 : 2;
+            const int feature = t.tile * 128 + f;
+            const size_t step = (size_t)p.n * p.k * p.ff * E;
 #pragma unroll
-        for (int i = 0; i < G; ++i)
-            if (i < 8 * cols.groups) {
-                acc[0][i] = acc[0][i] / (1.0f + expf(-acc[0][i])) * acc[1][i];
-                if (W8) {
-                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(acc[0][i]) & 0x7fffffffu);
+            for (int i = 0; i < 8; ++i) a[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+            if (W8) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(a[i]) & 0x7fffffffu);
                     if (lane == 0) sh.top[wg][warp & 3][i] = top;
                 }
+                named_sync(1 + wg, 128);
             }
-        if (W8) named_sync(1 + wg, 128);
+            // by token: column c is token c's, and its place is looked for
+            for (int q = 0; q < (by_token ? t.count : min(8, t.count - 8 * j)); ++q) {
+                const int at = t.start + 8 * j + q, col = by_token ? sh.list[at] / p.k : q;
+                float h = a[0], up = 1.0f, back;
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            int at = i < t.count ? t.start + i : -1;
-            if (by_token) {  // column i is token i's: its place, if it chose this expert
-                at = -1;
-                for (int q = 0; q < t.count; ++q)
-                    if (sh.list[t.start + q] / p.k == i) at = t.start + q;
+                for (int i = 1; i < 8; ++i)
+                    if (i == col) h = a[i];
+                if (W8) {
+                    moe_scale(max(max(sh.top[wg][0][col], sh.top[wg][1][col]), max(sh.top[wg][2][col], sh.top[wg][3][col])), up, back);
+                    if (f == 0) p.hs[(size_t)at * ((p.ff + 127) / 128) + t.tile] = back;
+                }
+                if (feature < p.ff) moe_put<W8, PH>(p.hp + ((size_t)at * p.ff + feature) * E, step, h, up);
             }
-            if (at < 0) continue;
-            float up = 1.0f, back;
-            if (W8) {
-                moe_scale(max(max(sh.top[wg][0][i], sh.top[wg][1][i]), max(sh.top[wg][2][i], sh.top[wg][3][i])), up, back);
-                if (f == 0) p.hs[(size_t)at * ((p.ff + 127) / 128) + t.tile] = back;
-            }
-            if (feature < p.ff) moe_put<W8, PH>(p.hp + ((size_t)at * p.ff + feature) * E, step, acc[0][i], up);
+            if (W8) named_sync(1 + wg, 128);  // before sh.top is written again
         }
-        if (W8) named_sync(1 + wg, 128);  // before sh.top is written again
     }
 }
 
@@ -824,14 +874,15 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
         tmem_alloc(&sh.tmem, 512);
         tmem_relinquish();
     }
-    // logits: a warp takes an expert with one token, or with four where that still gives every warp some
+    const bool by_token = p.n <= kMoeByToken;
     const int gw = blockIdx.x * (kMoeThreads / 32) + warp, gn = gridDim.x * (kMoeThreads / 32);
-    if ((long long)p.n * p.experts <= 2 * gn) {
-        for (int i = gw; i < p.n * p.experts; i += gn) moe_logits<1>(p, i % p.experts, i / p.experts);
+    if (p.n == 1) {
+        for (int i = gw; i < p.experts * p.splits; i += gn) moe_logits<1>(p, i / p.splits, 0, i % p.splits);
     } else {
-        for (int i = gw; i < (p.n + 3) / 4 * p.experts; i += gn) moe_logits<4>(p, i % p.experts, i / p.experts * 4);
+        const int each = p.experts * p.splits;
+        for (int i = gw; i < (p.n + 3) / 4 * each; i += gn) moe_logits<4>(p, i % each / p.splits, i / each * 4, i % p.splits);
     }
-    if (p.n <= kMoeByToken) {
+    if (by_token) {
         moe_split_x<W8, C::kX>(p, nullptr, p.n);
         moe_fence_copies();
     }
@@ -839,20 +890,37 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
-    if (threadIdx.x == 0) moe_meet(p.bars, &sh.dead, p.err);
-    __syncthreads();
-    bool dead = sh.dead;  // (the same for all: between two barriers of the block)
-    __syncthreads();
+    MoeRoute &route = *reinterpret_cast<MoeRoute *>(ring_p);
+    bool dead = moe_meet_all(p, sh, 0);
     if (!dead) {
-        moe_route<C::kGroup>(p, sh, reinterpret_cast<unsigned short *>(ring_p));
-        if (p.n > kMoeByToken) {
+        if (by_token) {
+            moe_keys(p, 0, p.n, route.key[0], threadIdx.x, kMoeThreads);
+            __syncthreads();
+            moe_choose(p, p.n, route.key[0], route.chosen, threadIdx.x, kMoeThreads);
+            __syncthreads();
+            if (blockIdx.x == 0 && warp < p.n) moe_weights(p, warp, route.key[0] + warp * p.experts, route.chosen + warp * p.k);
+        } else {  // a token's by one CTA, for all
+            for (int t = blockIdx.x; t < p.n; t += gridDim.x) {
+                moe_keys(p, t, 1, route.key[0], threadIdx.x, kMoeThreads);
+                __syncthreads();
+                moe_choose(p, 1, route.key[0], route.chosen, threadIdx.x, kMoeThreads);
+                __syncthreads();
+                if (warp == 0) moe_weights(p, t, route.key[0], route.chosen);
+                if (threadIdx.x < p.k) p.choices[t * p.k + threadIdx.x] = route.chosen[threadIdx.x];
+                __syncthreads();
+            }
+            dead = moe_meet_all(p, sh, 1);
+            for (int i = threadIdx.x; i < p.n * p.k; i += kMoeThreads) route.chosen[i] = __ldcg(p.choices + i);
+        }
+        __syncthreads();
+    }
+    if (!dead) {
+        moe_route<C::kGroup>(p, sh, route);
+        if (!by_token) {
             moe_split_x<W8, C::kX>(p, sh.list, p.n * p.k);
             moe_fence_copies();
             __syncthreads();
-            if (threadIdx.x == 0) moe_meet(p.bars + 1, &sh.dead, p.err);
-            __syncthreads();
-            dead = sh.dead;
-            __syncthreads();
+            dead = moe_meet_all(p, sh, 2);
         }
         // the choices lay in the ring: copies may overwrite them now
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -891,13 +959,13 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
             moe_fence_copies();
             named_sync(3, 256);
             if (threadIdx.x == 0) {
-                moe_meet(p.bars + 2, &sh.dead, p.err);
+                moe_meet(p.bars + 3, &sh.dead, p.err);
                 moe_fence_copies();
                 mbar_arrive(&sh.go);
             }
             moe_sums<C, true, C::kH>(p, sh, dn, r, tmem, turn, seen);
             named_sync(3, 256);
-            if (threadIdx.x == 0) moe_meet(p.bars + 3, &sh.dead, p.err);
+            if (threadIdx.x == 0) moe_meet(p.bars + 4, &sh.dead, p.err);
             named_sync(3, 256);
             // the weighted sum, four values a thread
             const int quads = p.d / 4;
@@ -926,8 +994,8 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
     if (warp == 9) tmem_dealloc(tmem, 512);
     // the last CTA leaves the meeting counts as they were found
     if (threadIdx.x == 0) {
-        if (atomicAdd(p.bars + 4, 1) == (int)gridDim.x - 1) {
-            p.bars[0] = p.bars[1] = p.bars[2] = p.bars[3] = p.bars[4] = 0;
+        if (atomicAdd(p.bars + 5, 1) == (int)gridDim.x - 1) {
+            for (int i = 0; i < 6; ++i) p.bars[i] = 0;
             __threadfence();
         }
     }
@@ -935,7 +1003,8 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- host
 struct MoeSpace {
-    size_t bars, counters, parts, logits, wts, out, xp, xs, hp, hs, total;
+    size_t bars, counters, parts, logits, choices, wts, out, xp, xs, hp, hs, total;
+    int splits;
 };
 static MoeSpace moe_space(int64_t n, int64_t d, int64_t ff, int64_t experts, int64_t k) {
     MoeSpace s;
@@ -948,8 +1017,10 @@ static MoeSpace moe_space(int64_t n, int64_t d, int64_t ff, int64_t experts, int
     };
     s.bars = take(256);
     s.counters = take(2 * g * 4);
-    s.parts = take(g * 2 * kMoeSums * 4);
-    s.logits = take((size_t)(n * experts) * 8);
+    s.parts = take(g * 4 * kMoeSums * 4);
+    s.splits = moe_logits_plan(n, d, experts, sm_count() * (kMoeThreads / 32)).splits;
+    s.logits = take((size_t)(n * experts) * s.splits * 8);
+    s.choices = take(pairs * 2);
     s.wts = take(pairs * 4);
     s.out = take(pairs * d * 4);
     s.xp = take(rows * d * 6);  // three pieces of two bytes or six of one
@@ -1062,7 +1133,9 @@ extern "C" DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, in
     a.err = reinterpret_cast<int *>(w);
     a.bars = reinterpret_cast<int *>(w + sp.bars);
     a.counters = reinterpret_cast<int *>(w + sp.counters);
-    a.logits = reinterpret_cast<double *>(w + sp.logits);
+    a.logits = reinterpret_cast<float2 *>(w + sp.logits);
+    a.choices = reinterpret_cast<unsigned short *>(w + sp.choices);
+    a.splits = sp.splits;
     a.wts = reinterpret_cast<float *>(w + sp.wts);
     a.xp = reinterpret_cast<unsigned char *>(w + sp.xp);
     a.hp = reinterpret_cast<unsigned char *>(w + sp.hp);
