@@ -392,29 +392,33 @@ def ds_gqa_chunk_attn(q, n_rows, row_starts, seq_lens, n_seqs, k_cache, v_cache,
                                 _here(ws), nbytes(ws), stream_handle(stream)), "ds_gqa_chunk_attn")
 
 
-def _rows(t, shape, dtypes, name, dev, unit=1):
+def _rows(t, rows, cols, dtypes, name, dev, unit=1):
     """(address, elements, row stride) of a 2-D tensor of this shape and one of
     these types whose rows have no gaps; a lone row's stride is its width in
     whole units."""
-    if t.dtype not in dtypes or tuple(t.shape) != shape or (t.stride(1) != 1 and shape[1] > 1):
-        raise ValueError("%s: a tensor of shape %s with dense rows of %s is needed"
-                         % (name, shape, " or ".join(str(d) for d in dtypes)))
+    if t.dtype not in dtypes or t.shape != (rows, cols):
+        raise ValueError("%s: a tensor of shape %s of %s is needed"
+                         % (name, (rows, cols), " or ".join(str(d) for d in dtypes)))
+    stride, one = t.stride()
+    if one != 1 and cols > 1:
+        raise ValueError("%s: rows without gaps between elements are needed" % name)
     if t.get_device() != dev:
         raise _elsewhere(name)
-    stride = t.stride(0) if shape[0] > 1 else -(-shape[1] // unit) * unit
-    return t.data_ptr(), (shape[0] - 1) * stride + shape[1], stride
+    if rows == 1:
+        stride = -(-cols // unit) * unit
+    return t.data_ptr(), (rows - 1) * stride + cols, stride
 
 
 _E4M3, _FLOATS = (torch.float8_e4m3fn,), (torch.float32, torch.bfloat16)
 
 
 def _scales(t, shape, name, dev):
-    """Address and length of a contiguous fp32 tensor of block scales."""
-    if t.dtype != torch.float32 or tuple(t.shape) != shape or not t.is_contiguous():
+    """Address of a contiguous fp32 tensor of block scales."""
+    if t.dtype != torch.float32 or t.shape != shape or not t.is_contiguous():
         raise ValueError("%s: a contiguous fp32 tensor of shape %s is needed" % (name, shape))
     if t.get_device() != dev:
         raise _elsewhere(name)
-    return t.data_ptr(), t.numel()
+    return t.data_ptr()
 
 
 def ds_fp8_quantize(x, block_rows, q, scales, stream=None):
@@ -422,12 +426,13 @@ def ds_fp8_quantize(x, block_rows, q, scales, stream=None):
     (1: activations, 128: weights); the rows of x and q may be views of wider ones."""
     dev = torch._C._cuda_getDevice()
     rows, cols = x.shape
-    if block_rows not in (1, 128):
+    if block_rows != 1 and block_rows != 128:
         raise DecodeStepError(DS_BAD_ARGUMENT, "ds_fp8_quantize")
-    xp, xn, xs = _rows(x, (rows, cols), _FLOATS, "x", dev)
-    qp, qn, qs = _rows(q, (rows, cols), _E4M3, "q", dev)
-    sp, sn = _scales(scales, (-(-rows // block_rows), -(-cols // 128)), "scales", dev)
-    check(lib.ds_fp8_quantize(xp, xn, dtype_code(x), xs, rows, cols, block_rows, qp, qn, qs, sp, sn,
+    rb, kb = -(-rows // block_rows), -(-cols // 128)
+    xp, xn, xs = _rows(x, rows, cols, _FLOATS, "x", dev)
+    qp, qn, qs = _rows(q, rows, cols, _E4M3, "q", dev)
+    sp = _scales(scales, (rb, kb), "scales", dev)
+    check(lib.ds_fp8_quantize(xp, xn, dtype_code(x), xs, rows, cols, block_rows, qp, qn, qs, sp, rb * kb,
                               stream_handle(stream)), "ds_fp8_quantize")
 
 
@@ -439,13 +444,12 @@ def ds_gemm_fp8(W, w_scales, X, x_scales, Y, ws, stream=None):
     """Y [n][rows] = X [n][cols] W [rows][cols]^T of e4m3 codes and their block scales."""
     dev = ws.get_device()
     (rows, cols), n = W.shape, X.shape[0]
-    kb = -(-cols // 128)
-    wp, wn, wst = _rows(W, (rows, cols), _E4M3, "W", dev, 16)
-    xp, xn, xst = _rows(X, (n, cols), _E4M3, "X", dev, 16)
-    yp, yn, yst = _rows(Y, (n, rows), _FLOATS, "Y", dev)
-    wsp, wsn = _scales(w_scales, (-(-rows // 128), kb), "w_scales", dev)
-    xsp, xsn = _scales(x_scales, (n, kb), "x_scales", dev)
-    check(lib.ds_gemm_fp8(wp, wn, wst, wsp, wsn, xp, xn, xst, xsp, xsn, n, rows, cols, yp, yn, dtype_code(Y), yst,
+    rb, kb = -(-rows // 128), -(-cols // 128)
+    wp, wn, wst = _rows(W, rows, cols, _E4M3, "W", dev, 16)
+    xp, xn, xst = _rows(X, n, cols, _E4M3, "X", dev, 16)
+    yp, yn, yst = _rows(Y, n, rows, _FLOATS, "Y", dev)
+    check(lib.ds_gemm_fp8(wp, wn, wst, _scales(w_scales, (rb, kb), "w_scales", dev), rb * kb, xp, xn, xst,
+                          _scales(x_scales, (n, kb), "x_scales", dev), n * kb, n, rows, cols, yp, yn, dtype_code(Y), yst,
                           _here(ws), nbytes(ws), stream_handle(stream)), "ds_gemm_fp8")
 
 
@@ -461,22 +465,22 @@ def ds_moe_layer(x, w_router, top_k, renormalize, w_gate_up, gate_up_scales, w_d
     dev = ws.get_device()
     n, d = x.shape
     experts, _, ff, _ = w_gate_up.shape
-    if (tuple(w_router.shape) != (experts, d) or tuple(w_gate_up.shape) != (experts, 2, ff, d)
-            or tuple(w_down.shape) != (experts, d, ff) or tuple(y.shape) != (n, d) or y.dtype != x.dtype
-            or w_down.dtype != w_gate_up.dtype):
+    if (w_router.shape != (experts, d) or w_gate_up.shape != (experts, 2, ff, d) or w_down.shape != (experts, d, ff)
+            or y.shape != (n, d) or y.dtype != x.dtype or w_down.dtype != w_gate_up.dtype):
         raise ValueError("ds_moe_layer: shapes or types that do not go together")
-    if residual is not None and (tuple(residual.shape) != (n, d) or residual.dtype != x.dtype):
+    if residual is not None and (residual.shape != (n, d) or residual.dtype != x.dtype):
         raise ValueError("residual: x's shape and type are needed")
     e4m3 = w_gate_up.dtype == torch.float8_e4m3fn
     kb, fb = -(-d // 128), -(-ff // 128)
-    gs, gn = _scales(gate_up_scales, (experts, 2, fb, kb), "gate_up_scales", dev) if e4m3 else (None, 0)
-    dns, dn = _scales(down_scales, (experts, kb, fb), "down_scales", dev) if e4m3 else (None, 0)
+    gs = _scales(gate_up_scales, (experts, 2, fb, kb), "gate_up_scales", dev) if e4m3 else None
+    dns = _scales(down_scales, (experts, kb, fb), "down_scales", dev) if e4m3 else None
+    n_scales = experts * kb * fb if e4m3 else 0
     if expert_weights is not None and expert_weights.dtype != torch.float32:
         raise ValueError("expert_weights: an fp32 tensor is needed")
     check(lib.ds_moe_layer(_dense(x, 0, "x", dev), x.numel(), dtype_code(x), n, d, _dense(w_router, 0, "w_router", dev),
                            w_router.numel(), dtype_code(w_router), experts, top_k, 1 if renormalize else 0,
-                           _dense(w_gate_up, 0, "w_gate_up", dev), w_gate_up.numel(), gs, gn,
-                           _dense(w_down, 0, "w_down", dev), w_down.numel(), dns, dn, DS_E4M3 if e4m3 else dtype_code(w_gate_up), ff,
+                           _dense(w_gate_up, 0, "w_gate_up", dev), w_gate_up.numel(), gs, 2 * n_scales,
+                           _dense(w_down, 0, "w_down", dev), w_down.numel(), dns, n_scales, DS_E4M3 if e4m3 else dtype_code(w_gate_up), ff,
                            None if residual is None else _dense(residual, 0, "residual", dev), _dense(y, 0, "y", dev),
                            y.numel(), None if expert_ids is None else _i32(expert_ids, n * top_k, "expert_ids", dev),
                            None if expert_weights is None else _dense(expert_weights, n * top_k, "expert_weights", dev),

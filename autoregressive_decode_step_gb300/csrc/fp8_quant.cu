@@ -20,6 +20,7 @@ namespace ds {
 
 constexpr int kFqThreads = 256;
 constexpr int kFqGroups = kFqThreads / 16;  // rows of a block worked on at a time
+constexpr int kFqCtas = 4;                   // at a time on an SM
 constexpr float kFqTiny = 0x1p-96f;         // least maximum: 448 / top and the scale stay normal numbers
 
 struct FqArgs {
@@ -30,35 +31,59 @@ struct FqArgs {
     float *scales;
 };
 
-// Eight values from column c on, zeros behind the row's end; VEC: 16-byte loads.
+// Eight values as they are stored: 16 bytes of bf16, 32 of fp32.
+template <typename T>
+struct FqRaw;
+template <>
+struct FqRaw<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void set(int i, __nv_bfloat16 v) { reinterpret_cast<__nv_bfloat16 *>(&w)[i] = v; }
+    // the largest magnitude's bits: NaN above infinity above numbers
+    __device__ __forceinline__ unsigned top() const {
+        const unsigned m = __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu));
+        return max(m << 16, m & 0xffff0000u);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const { widen16(w, v); }
+};
+template <>
+struct FqRaw<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
+    __device__ __forceinline__ void set(int i, float v) { (i < 4 ? &a.x : &b.x)[i & 3] = v; }
+    __device__ __forceinline__ unsigned top() const {
+        float v[8];
+        get(v);
+        unsigned t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, __float_as_uint(v[i]) & 0x7fffffffu);
+        return t;
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+// From column c of a row on, zeros behind its end; VEC: 16 bytes at a time.
 template <typename T, bool VEC>
-__device__ __forceinline__ void fq_load(const T *row, int c, int cols, float (&v)[8]) {
+__device__ __forceinline__ void fq_load(FqRaw<T> &r, const T *row, int c, int cols) {
     if (VEC && c + 8 <= cols) {
-        if (sizeof(T) == 2) {
-            widen16(__ldg(reinterpret_cast<const uint4 *>(row + c)), v);
-        } else {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(row + c));
-            const float4 b = __ldg(reinterpret_cast<const float4 *>(row + c) + 1);
-            v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-        }
+        r.load(row + c);
         return;
     }
+    r.zero();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? to_f32(row[c + i]) : 0.0f;
+    for (int i = 0; i < 8; ++i)
+        if (c + i < cols) r.set(i, row[c + i]);
 }
 
-// The largest magnitude as the bits of a float: NaN above infinity above numbers.
-__device__ __forceinline__ unsigned fq_top(const float (&v)[8], unsigned top) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
-    return top;
-}
-
-// Scale and factor of a block; NaN for one that holds a NaN or an infinity.
-__device__ __forceinline__ void fq_scale(unsigned top, float &scale, float &factor) {
-    const float t = top < 0x7f800000u ? fmaxf(__uint_as_float(top), kFqTiny) : __int_as_float(0x7fffffff);
-    scale = __fdiv_rn(t, 448.0f);
-    factor = __fdiv_rn(448.0f, t);
+// A block's maximum from its bits; NaN for one that holds a NaN or an infinity.
+__device__ __forceinline__ float fq_top(unsigned top) {
+    return top < 0x7f800000u ? fmaxf(__uint_as_float(top), kFqTiny) : __int_as_float(0x7fffffff);
 }
 
 __device__ __forceinline__ unsigned fq_pair(float a, float b) {  // a in the low byte
@@ -67,8 +92,10 @@ __device__ __forceinline__ unsigned fq_pair(float a, float b) {  // a in the low
     return r;
 }
 
-template <bool VEC>
-__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const float (&v)[8], float factor) {
+template <typename T, bool VEC>
+__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const FqRaw<T> &r, float factor) {
+    float v[8];
+    r.get(v);
     const unsigned lo = fq_pair(v[0] * factor, v[1] * factor) | fq_pair(v[2] * factor, v[3] * factor) << 16;
     const unsigned hi = fq_pair(v[4] * factor, v[5] * factor) | fq_pair(v[6] * factor, v[7] * factor) << 16;
     if (VEC && c + 8 <= cols) {
@@ -80,34 +107,49 @@ __device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, co
         if (c + i < cols) row[c + i] = (unsigned char)((i < 4 ? lo : hi) >> (8 * (i & 3)));
 }
 
-// Blocks of 1 x 128: a group of sixteen threads takes block after block, the
-// next UNROLL of them requested together.
-template <typename T, bool VEC, int UNROLL>
-__global__ __launch_bounds__(kFqThreads) void fp8_rows_kernel(const FqArgs p) {
-    const int lane = threadIdx.x & 15;
+// Blocks of 1 x 128: a group of sixteen threads takes block after block, U of
+// them requested together.  Their 2 U quotients are formed side by side, one a
+// thread: an IEEE division costs as much as the rest of a block's eight values
+// (with one in every thread, and fewer CTAs at a time than the grid was made
+// for, 8,192 x 14,336 bf16 took 141 us).  DENSE: whole blocks, no gaps between
+// rows, so a block's place follows from its number.
+template <typename T, bool VEC, bool DENSE, int U>
+__global__ __launch_bounds__(kFqThreads, kFqCtas) void fp8_rows_kernel(const FqArgs p) {
+    const int lane = threadIdx.x & 15, half = threadIdx.x & 16;
     const long long n = (long long)p.rows * p.kb, step = (long long)gridDim.x * kFqGroups;
-    for (long long b0 = (long long)blockIdx.x * kFqGroups + (threadIdx.x >> 4); b0 - (threadIdx.x >> 4) < n; b0 += step * UNROLL) {
-        float v[UNROLL][8];
-        long long row[UNROLL];
-        int j[UNROLL];
+    for (long long b0 = (long long)blockIdx.x * kFqGroups + (threadIdx.x >> 4); b0 - (threadIdx.x >> 4) < n; b0 += step * U) {
+        FqRaw<T> v[U];
+        long long row[U];
+        int c[U];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
+        for (int u = 0; u < U; ++u) {
             const long long b = min(b0 + u * step, n - 1);
-            row[u] = n <= 0x7fffffffll ? (long long)((unsigned)b / (unsigned)p.kb) : b / p.kb;
-            j[u] = (int)(b - row[u] * p.kb);
-            fq_load<T, VEC>(static_cast<const T *>(p.x) + row[u] * p.ldx, j[u] * 128 + lane * 8, p.cols, v[u]);
+            if (DENSE) {
+                v[u].load(static_cast<const T *>(p.x) + b * 128 + lane * 8);
+            } else {
+                row[u] = n <= 0x7fffffffll ? (long long)((unsigned)b / (unsigned)p.kb) : b / p.kb;
+                c[u] = (int)(b - row[u] * p.kb) * 128 + lane * 8;
+                fq_load<T, VEC>(v[u], static_cast<const T *>(p.x) + row[u] * p.ldx, c[u], p.cols);
+            }
         }
+        float mine = 0.0f;  // lane: the maximum of block lane % U
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            unsigned top = fq_top(v[u], 0);
+        for (int u = 0; u < U; ++u) {
+            unsigned top = v[u].top();
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            float scale, factor;
-            fq_scale(top, scale, factor);
-            if (b0 + u * step < n) {
-                fq_store<VEC>(p.q + row[u] * p.ldq, j[u] * 128 + lane * 8, p.cols, v[u], factor);
-                if (lane == 0) p.scales[row[u] * p.kb + j[u]] = scale;
-            }
+            if (lane % U == u) mine = fq_top(top);
+        }
+        // lanes below U: 448 / top; the next U: top / 448
+        const bool is_scale = lane >= U;
+        const float quotient = __fdiv_rn(is_scale ? mine : 448.0f, is_scale ? 448.0f : mine);
+        if (is_scale && lane < 2 * U && b0 + (lane - U) * step < n) p.scales[b0 + (lane - U) * step] = quotient;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const float factor = __shfl_sync(0xffffffffu, quotient, half + u);
+            if (b0 + u * step >= n) continue;
+            if (DENSE) fq_store<T, true>(p.q + (b0 + u * step) * 128, lane * 8, 128, v[u], factor);
+            else fq_store<T, VEC>(p.q + row[u] * p.ldq, c[u], p.cols, v[u], factor);
         }
     }
 }
@@ -118,25 +160,24 @@ __global__ __launch_bounds__(kFqThreads) void fp8_blocks_kernel(const FqArgs p) 
     constexpr int kRows = 128 / kFqGroups;
     __shared__ unsigned tops[kFqThreads / 32];
     const int lane = threadIdx.x & 15, r0 = (int)(blockIdx.x / p.kb) * 128 + (threadIdx.x >> 4), c = (int)(blockIdx.x % p.kb) * 128 + lane * 8;
-    float v[kRows][8];
+    FqRaw<T> v[kRows];
     unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
         const int r = r0 + i * kFqGroups;
-        fq_load<T, VEC>(static_cast<const T *>(p.x) + (long long)min(r, p.rows - 1) * p.ldx, c, r < p.rows ? p.cols : 0, v[i]);
-        top = fq_top(v[i], top);
+        fq_load<T, VEC>(v[i], static_cast<const T *>(p.x) + (long long)min(r, p.rows - 1) * p.ldx, c, r < p.rows ? p.cols : 0);
+        top = max(top, v[i].top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kFqThreads / 32; ++i) top = max(top, tops[i]);
-    float scale, factor;
-    fq_scale(top, scale, factor);
+    const float t = fq_top(top), factor = __fdiv_rn(448.0f, t);
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        if (r0 + i * kFqGroups < p.rows) fq_store<VEC>(p.q + (long long)(r0 + i * kFqGroups) * p.ldq, c, p.cols, v[i], factor);
-    if (threadIdx.x == 0) p.scales[blockIdx.x] = scale;
+        if (r0 + i * kFqGroups < p.rows) fq_store<T, VEC>(p.q + (long long)(r0 + i * kFqGroups) * p.ldq, c, p.cols, v[i], factor);
+    if (threadIdx.x == 0) p.scales[blockIdx.x] = __fdiv_rn(t, 448.0f);
 }
 
 template <typename T, bool VEC>
@@ -145,12 +186,15 @@ static cudaError_t fq_launch(const FqArgs &a, int block_rows, cudaStream_t s) {
         const long long grid = (long long)((a.rows + 127) / 128) * a.kb;
         return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqThreads), 0, s, false, a);
     }
-    const long long groups = ((long long)a.rows * a.kb + kFqGroups - 1) / kFqGroups;
-    constexpr int kUnroll = sizeof(T) == 2 ? 4 : 2;
-    const long long most = 8LL * sm_count();
-    if (groups <= most) return launch_ex(fp8_rows_kernel<T, VEC, 1>, dim3((unsigned)groups), dim3(kFqThreads), 0, s, false, a);
-    return launch_ex(fp8_rows_kernel<T, VEC, kUnroll>, dim3((unsigned)std::min(most, (groups + kUnroll - 1) / kUnroll)),
-                     dim3(kFqThreads), 0, s, false, a);
+    const long long groups = ((long long)a.rows * a.kb + kFqGroups - 1) / kFqGroups, most = (long long)kFqCtas * sm_count();
+    const bool dense = VEC && a.cols % 128 == 0 && a.ldx == a.cols && a.ldq == a.cols;
+    constexpr int U = sizeof(T) == 2 ? 4 : 2;
+    const unsigned grid = (unsigned)std::min(most, groups <= most ? groups : (groups + U - 1) / U);
+    const dim3 g(grid), b(kFqThreads);
+    // few blocks: one a group; many: U, on a full card
+    if (groups <= most)
+        return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, 1>, g, b, 0, s, false, a) : launch_ex(fp8_rows_kernel<T, VEC, false, 1>, g, b, 0, s, false, a);
+    return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, U>, g, b, 0, s, false, a) : launch_ex(fp8_rows_kernel<T, VEC, false, U>, g, b, 0, s, false, a);
 }
 
 }  // namespace ds
