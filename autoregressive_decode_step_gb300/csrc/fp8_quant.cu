@@ -26,7 +26,7 @@ constexpr float kFqTiny = 0x1p-96f;         // least maximum: 448 / top and the 
 struct FqArgs {
     const void *x;
     long long ldx, ldq;
-    int rows, cols, kb;
+    int rows, cols, kb, q8;  // q8: rows of q start on 8 bytes
     unsigned char *q;
     float *scales;
 };
@@ -92,19 +92,31 @@ __device__ __forceinline__ unsigned fq_pair(float a, float b) {  // a in the low
     return r;
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const FqRaw<T> &r, float factor) {
+// Codes from column c of a row on: eight bytes a thread, or where rows do not
+// start on 8 bytes sixteen neighbouring bytes of the sixteen threads at a time.
+template <typename T>
+__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const FqRaw<T> &r, float factor, bool q8) {
     float v[8];
     r.get(v);
     const unsigned lo = fq_pair(v[0] * factor, v[1] * factor) | fq_pair(v[2] * factor, v[3] * factor) << 16;
     const unsigned hi = fq_pair(v[4] * factor, v[5] * factor) | fq_pair(v[6] * factor, v[7] * factor) << 16;
-    if (VEC && c + 8 <= cols) {
+    if (q8 && c + 8 <= cols) {
         *reinterpret_cast<uint2 *>(row + c) = make_uint2(lo, hi);
         return;
     }
+    if (q8) {  // a row's end
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        if (c + i < cols) row[c + i] = (unsigned char)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        for (int i = 0; i < 8; ++i)
+            if (c + i < cols) row[c + i] = (unsigned char)((i < 4 ? lo : hi) >> (8 * (i & 3)));
+        return;
+    }
+    const int lane = threadIdx.x & 15, half = threadIdx.x & 16, c0 = c - lane * 8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int from = half + (lane >> 3) + 2 * i;
+        const unsigned a = __shfl_sync(0xffffu << half, lo, from), b = __shfl_sync(0xffffu << half, hi, from);
+        if (c0 + 16 * i + lane < cols) row[c0 + 16 * i + lane] = (unsigned char)((lane & 4 ? b : a) >> (8 * (lane & 3)));
+    }
 }
 
 // Blocks of 1 x 128: a group of sixteen threads takes block after block, U of
@@ -148,8 +160,8 @@ __global__ __launch_bounds__(kFqThreads, kFqCtas) void fp8_rows_kernel(const FqA
         for (int u = 0; u < U; ++u) {
             const float factor = __shfl_sync(0xffffffffu, quotient, half + u);
             if (b0 + u * step >= n) continue;
-            if (DENSE) fq_store<T, true>(p.q + (b0 + u * step) * 128, lane * 8, 128, v[u], factor);
-            else fq_store<T, VEC>(p.q + row[u] * p.ldq, c[u], p.cols, v[u], factor);
+            if (DENSE) fq_store<T>(p.q + (b0 + u * step) * 128, lane * 8, 128, v[u], factor, true);
+            else fq_store<T>(p.q + row[u] * p.ldq, c[u], p.cols, v[u], factor, p.q8);
         }
     }
 }
@@ -176,7 +188,7 @@ __global__ __launch_bounds__(kFqThreads) void fp8_blocks_kernel(const FqArgs p) 
     const float t = fq_top(top), factor = __fdiv_rn(448.0f, t);
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-        if (r0 + i * kFqGroups < p.rows) fq_store<T, VEC>(p.q + (long long)(r0 + i * kFqGroups) * p.ldq, c, p.cols, v[i], factor);
+        if (r0 + i * kFqGroups < p.rows) fq_store<T>(p.q + (long long)(r0 + i * kFqGroups) * p.ldq, c, p.cols, v[i], factor, p.q8);
     if (threadIdx.x == 0) p.scales[blockIdx.x] = __fdiv_rn(t, 448.0f);
 }
 
@@ -187,7 +199,7 @@ static cudaError_t fq_launch(const FqArgs &a, int block_rows, cudaStream_t s) {
         return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqThreads), 0, s, false, a);
     }
     const long long groups = ((long long)a.rows * a.kb + kFqGroups - 1) / kFqGroups, most = (long long)kFqCtas * sm_count();
-    const bool dense = VEC && a.cols % 128 == 0 && a.ldx == a.cols && a.ldq == a.cols;
+    const bool dense = VEC && a.q8 && a.cols % 128 == 0 && a.ldx == a.cols && a.ldq == a.cols;
     constexpr int U = sizeof(T) == 2 ? 4 : 2;
     const unsigned grid = (unsigned)std::min(most, groups <= most ? groups : (groups + U - 1) / U);
     const dim3 g(grid), b(kFqThreads);
@@ -232,7 +244,8 @@ extern "C" DS_API int ds_fp8_quantize(const void *x, int64_t x_len, int x_dtype,
     a.kb = (int)kb;
     a.q = static_cast<unsigned char *>(q);
     a.scales = scales;
-    const bool vec = (uintptr_t)x % 16 == 0 && (rows == 1 || x_stride * es % 16 == 0) && (uintptr_t)q % 8 == 0 && (rows == 1 || q_stride % 8 == 0);
+    const bool vec = (uintptr_t)x % 16 == 0 && (rows == 1 || x_stride * es % 16 == 0);
+    a.q8 = (uintptr_t)q % 8 == 0 && (rows == 1 || q_stride % 8 == 0);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = x_dtype == DS_BF16 ? (vec ? fq_launch<__nv_bfloat16, true>(a, block_rows, s) : fq_launch<__nv_bfloat16, false>(a, block_rows, s))
                                              : (vec ? fq_launch<float, true>(a, block_rows, s) : fq_launch<float, false>(a, block_rows, s));

@@ -244,12 +244,18 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
             if (sg.split < 0 || NB > kF8Inline) continue;
             int first, last;
             f8_contributors(p, gridDim.x, sg.split, first, last);
-            __threadfence();
             named_sync(1, 256);
-            if (threadIdx.x == 0) sh.last = atomicAdd(p.counters + sg.split, 1) == last - first;
+            if (threadIdx.x == 0) {
+                __threadfence();  // for what both warpgroups wrote
+                const bool is = atomicAdd(p.counters + sg.split, 1) == last - first;
+                if (is) {
+                    p.counters[sg.split] = 0;
+                    __threadfence();
+                }
+                sh.last = is;
+            }
             named_sync(1, 256);
             if (sh.last) {
-                __threadfence();
                 constexpr int HB = NB / 2;
                 float sum[HB];
 #pragma unroll
@@ -262,7 +268,6 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                 }
 #pragma unroll
                 for (int i = 0; i < HB; ++i) f8_store(p, wg * HB + i, feature, sum[i]);
-                if (threadIdx.x == 0) p.counters[sg.split] = 0;
             }
             named_sync(1, 256);  // before sh.last is written again
         }
@@ -273,26 +278,17 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
     if (warp == 9) tmem_dealloc(tmem, C::kTmem);
 }
 
-// Adds a split tile's partials, 16 of its rows a block; thread r is feature r.
+// Adds a split tile's partials, 8 of its rows a block; thread r is feature r.
+constexpr int kF8JoinCols = 8;
 __global__ __launch_bounds__(kF8M) void fp8_join_kernel(const __grid_constant__ F8Args p, int grid) {
-    constexpr int C = 16;
+    constexpr int C = kF8JoinCols;
     grid_dependency_wait();
     const int chunks = p.bn / C, split = blockIdx.x / chunks, c0 = (int)(blockIdx.x % chunks) * C;
     int first, last;
     f8_contributors(p, grid, split, first, last);
     if (first == last || c0 >= p.n) return;  // one CTA had all of it
     float acc[C];
-#pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.0f;
-#pragma unroll 2
-    for (int c = first; c <= last; ++c) {
-        const float *from = p.partials + (((size_t)c + split) * p.bn + c0) * kF8M + threadIdx.x;
-        float v[C];
-#pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = __ldcg(from + i * kF8M);
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] += v[i];
-    }
+    f8_join<C, kF8M>(p.partials + (((size_t)first + split) * p.bn + c0) * kF8M + threadIdx.x, (size_t)p.bn * kF8M, last - first + 1, acc);
     const int tile = p.rounds * grid + split;
 #pragma unroll
     for (int i = 0; i < C; ++i) f8_store(p, c0 + i, tile * kF8M + threadIdx.x, acc[i]);
@@ -346,7 +342,7 @@ static cudaError_t f8_launch(const F8Args &a, const F8Plan &t, cudaStream_t s) {
     }
     e = launch_ex(fp8_gemm_kernel<NB>, dim3(t.grid), dim3(kF8Threads), F8Cfg<NB>::kSmem, s, false, a);
     if (e != cudaSuccess || NB <= kF8Inline || t.split == 0) return e;
-    return launch_ex(fp8_join_kernel, dim3(t.split * (NB / 16)), dim3(kF8M), 0, s, true, a, t.grid);
+    return launch_ex(fp8_join_kernel, dim3(t.split * (NB / kF8JoinCols)), dim3(kF8M), 0, s, true, a, t.grid);
 }
 
 }  // namespace ds

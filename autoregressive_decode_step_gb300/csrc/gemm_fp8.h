@@ -21,8 +21,10 @@ struct F8Args {
     int *err;
 };
 
-// The split tiles' w steps are cut into runs, one a CTA (a pair), a step at least.
-__host__ __device__ inline int f8_runs(long long w, int grid) { return w < 1 ? 1 : w < grid ? (int)w : grid; }
+// The split tiles' w steps are cut into runs, one a CTA (a pair), of four steps
+// at least: of fewer, joining what they leave takes longer than they do (333
+// rows by 1,000 x 1,416 in runs of one or two: 21 us).
+__host__ __device__ inline int f8_runs(long long w, int grid) { return w < 8 ? 1 : w / 4 < grid ? (int)(w / 4) : grid; }
 // The first and last run that hold steps of a split tile.
 __device__ __forceinline__ void f8_contributors(const F8Args &p, int grid, int split, int &first, int &last) {
     const long long w = (long long)p.split * p.kb, t = (long long)split * p.kb;
@@ -63,6 +65,26 @@ struct F8Walk {
         return true;
     }
 };
+
+// Adds `parts` partial sums of C columns, COLS floats apart, in order; several
+// partials' loads under way at a time.
+template <int C, int COLS>
+__device__ __forceinline__ void f8_join(const float *from, size_t part, int parts, float (&acc)[C]) {
+    constexpr int AT = 32 / C;
+#pragma unroll
+    for (int i = 0; i < C; ++i) acc[i] = 0.0f;
+    for (int c = 0; c < parts; c += AT) {
+        float v[AT][C];
+#pragma unroll
+        for (int a = 0; a < AT; ++a)
+#pragma unroll
+            for (int i = 0; i < C; ++i) v[a][i] = __ldcg(from + (size_t)min(c + a, parts - 1) * part + i * COLS);
+#pragma unroll
+        for (int a = 0; a < AT; ++a)
+#pragma unroll
+            for (int i = 0; i < C; ++i) acc[i] += c + a < parts ? v[a][i] : 0.0f;
+    }
+}
 
 constexpr int kF8WideRows = 256, kF8WideFeatures = 256;  // a pair's tile
 // More rows of X than this run on pairs of SMs.

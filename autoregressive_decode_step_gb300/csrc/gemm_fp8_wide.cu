@@ -112,37 +112,6 @@ __device__ __forceinline__ void fw_tile(const F8Args &p, int tile, int &rt, int 
     rt = g * kFwGroup + (tile - g * per) % nn;
 }
 
-// N neighbouring outputs of a row.
-template <int N>
-__device__ __forceinline__ void fw_store(const F8Args &p, int row, int f0, const float *v) {
-    if (row >= p.n || f0 >= p.rows) return;
-    const long long at = row * p.ldy + f0;
-    const int es = p.y_dtype == DS_BF16 ? 2 : 4;
-    char *to = static_cast<char *>(p.y) + at * es;
-    if (f0 + N <= p.rows && ((uintptr_t)to & 31) == 0) {
-        uint32_t w[8];
-        if (p.y_dtype == DS_BF16) {
-#pragma unroll
-            for (int i = 0; i < N; i += 16) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = stream_bf16x2(v[i + 2 * j], v[i + 2 * j + 1]);
-                stream_store32(to + i * 2, w);
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < N; i += 8) {
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[i + j]);
-                stream_store32(to + i * 4, w);
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (f0 + i < p.rows) store_as(p.y, at + i, p.y_dtype, v[i]);
-}
-
 // A warp's 32 rows (lane r row row0 + r) by 64 outputs, through shared memory:
 // four lanes store 64 neighbouring bytes of a row, where a thread's own row at
 // a time took a quarter of the kernel (a line a lane).
@@ -376,11 +345,12 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
     if (warp == 19) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
-// Adds a split tile's partials, 16 columns of one SM's rows a block; thread r is row r.
+// Adds a split tile's partials, 8 columns of one SM's rows a block; thread r is row r.
+constexpr int kFwJoinCols = 8;
 __global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constant__ F8Args p, int pairs) {
-    constexpr int C = 16;
+    constexpr int C = kFwJoinCols, kChunks = kF8WideFeatures / C;
     grid_dependency_wait();
-    const int chunk = blockIdx.x % (kF8WideFeatures / C), rank = blockIdx.x / (kF8WideFeatures / C) % 2, split = blockIdx.x / (2 * kF8WideFeatures / C);
+    const int chunk = blockIdx.x % kChunks, rank = blockIdx.x / kChunks % 2, split = blockIdx.x / (2 * kChunks);
     int first, last, rt, ft;
     f8_contributors(p, pairs, split, first, last);
     if (first == last) return;  // one pair had all of it
@@ -388,18 +358,22 @@ __global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constan
     const int row = rt * kF8WideRows + rank * 128 + threadIdx.x, f0 = ft * kF8WideFeatures + chunk * C;
     if (row - (int)threadIdx.x >= p.n || f0 >= p.rows) return;
     float acc[C];
+    f8_join<C, 128>(p.partials + (((size_t)first + split) * 2 + rank) * kFwPart + (size_t)chunk * C * 128 + threadIdx.x, 2 * (size_t)kFwPart,
+                    last - first + 1, acc);
+    if (row >= p.n) return;
+    char *to = static_cast<char *>(p.y) + (row * p.ldy + f0) * (p.y_dtype == DS_BF16 ? 2 : 4);
+    if (f0 + C <= p.rows && ((uintptr_t)to & 31) == 0 && p.y_dtype == DS_F32) {
+        uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < C; ++i) acc[i] = 0.0f;
-#pragma unroll 2
-    for (int c = first; c <= last; ++c) {
-        const float *from = p.partials + (((size_t)c + split) * 2 + rank) * kFwPart + (size_t)chunk * C * 128 + threadIdx.x;
-        float v[C];
+        for (int i = 0; i < C; ++i) w[i] = __float_as_uint(acc[i]);
+        stream_store32(to, w);
+    } else if (f0 + C <= p.rows && ((uintptr_t)to & 15) == 0 && p.y_dtype == DS_BF16) {
+        *reinterpret_cast<uint4 *>(to) = make_uint4(stream_bf16x2(acc[0], acc[1]), stream_bf16x2(acc[2], acc[3]), stream_bf16x2(acc[4], acc[5]), stream_bf16x2(acc[6], acc[7]));
+    } else {
 #pragma unroll
-        for (int i = 0; i < C; ++i) v[i] = __ldcg(from + i * 128);
-#pragma unroll
-        for (int i = 0; i < C; ++i) acc[i] += v[i];
+        for (int i = 0; i < C; ++i)
+            if (f0 + i < p.rows) store_as(p.y, row * p.ldy + f0 + i, p.y_dtype, acc[i]);
     }
-    fw_store<C>(p, row, f0, acc);
 }
 
 // ---------------------------------------------------------------- host
@@ -420,7 +394,7 @@ cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream) {
     const int pairs = f8_wide_pairs();
     e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, false, a);
     if (e != cudaSuccess || a.split == 0) return e;
-    return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / 16)), dim3(128), 0, stream, true, a, pairs);
+    return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / kFwJoinCols)), dim3(128), 0, stream, true, a, pairs);
 }
 
 }  // namespace ds
