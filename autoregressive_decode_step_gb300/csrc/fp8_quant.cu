@@ -127,6 +127,8 @@ __device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, co
 // rows, so a block's place follows from its number.
 template <typename T, bool VEC, bool DENSE, int U>
 __global__ __launch_bounds__(kFqThreads, kFqCtas) void fp8_rows_kernel(const FqArgs p) {
+    allow_dependent_launch();
+    grid_dependency_wait();
     const int lane = threadIdx.x & 15, half = threadIdx.x & 16;
     const long long n = (long long)p.rows * p.kb, step = (long long)gridDim.x * kFqGroups;
     for (long long b0 = (long long)blockIdx.x * kFqGroups + (threadIdx.x >> 4); b0 - (threadIdx.x >> 4) < n; b0 += step * U) {
@@ -171,6 +173,8 @@ template <typename T, bool VEC>
 __global__ __launch_bounds__(kFqThreads) void fp8_blocks_kernel(const FqArgs p) {
     constexpr int kRows = 128 / kFqGroups;
     __shared__ unsigned tops[kFqThreads / 32];
+    allow_dependent_launch();
+    grid_dependency_wait();
     const int lane = threadIdx.x & 15, r0 = (int)(blockIdx.x / p.kb) * 128 + (threadIdx.x >> 4), c = (int)(blockIdx.x % p.kb) * 128 + lane * 8;
     FqRaw<T> v[kRows];
     unsigned top = 0;
@@ -196,7 +200,7 @@ template <typename T, bool VEC>
 static cudaError_t fq_launch(const FqArgs &a, int block_rows, cudaStream_t s) {
     if (block_rows == 128) {
         const long long grid = (long long)((a.rows + 127) / 128) * a.kb;
-        return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqThreads), 0, s, false, a);
+        return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqThreads), 0, s, true, a);
     }
     const long long groups = ((long long)a.rows * a.kb + kFqGroups - 1) / kFqGroups, most = (long long)kFqCtas * sm_count();
     const bool dense = VEC && a.q8 && a.cols % 128 == 0 && a.ldx == a.cols && a.ldq == a.cols;
@@ -205,8 +209,8 @@ static cudaError_t fq_launch(const FqArgs &a, int block_rows, cudaStream_t s) {
     const dim3 g(grid), b(kFqThreads);
     // few blocks: one a group; many: U, on a full card
     if (groups <= most)
-        return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, 1>, g, b, 0, s, false, a) : launch_ex(fp8_rows_kernel<T, VEC, false, 1>, g, b, 0, s, false, a);
-    return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, U>, g, b, 0, s, false, a) : launch_ex(fp8_rows_kernel<T, VEC, false, U>, g, b, 0, s, false, a);
+        return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, 1>, g, b, 0, s, true, a) : launch_ex(fp8_rows_kernel<T, VEC, false, 1>, g, b, 0, s, true, a);
+    return dense ? launch_ex(fp8_rows_kernel<T, VEC, VEC, U>, g, b, 0, s, true, a) : launch_ex(fp8_rows_kernel<T, VEC, false, U>, g, b, 0, s, true, a);
 }
 
 }  // namespace ds

@@ -10,9 +10,10 @@
 // TMEM is feature r) by all the rows of X, rounded up to 16, 32, 64 or 128 (its
 // N): one token costs an MMA of 16 columns.  All tiles' steps are one line, cut
 // into equal runs, one a CTA, so that every SM streams the same bytes; a cut
-// tile's partial sums meet in the workspace and are added in CTA order: by
-// whichever CTA arrives last for up to 32 rows (16 KB a partial), by a second
-// launch for more.  No CTA waits for another.
+// tile's partial sums meet in the workspace and are added in CTA order by
+// whichever CTA arrives last (256 KB of them at most: a second launch for the
+// wider ones took 12 us of 35 with 64 rows by 28,672 x 4,096).  No CTA waits for
+// another.  A launch may begin while the one in front ends.
 //
 // Two warpgroups take turns at batches of steps, up to 128 columns of TMEM each
 // and four in flight, so that a batch's waits and TMEM's latency (some 700
@@ -35,7 +36,6 @@ constexpr int kF8RegsSum = 216, kF8RegsOther = 72;
 constexpr int kF8MaxStages = 10;
 constexpr int kF8Slots = 8;   // batches' scales ahead
 constexpr int kF8Bufs = 4;    // batches in TMEM
-constexpr int kF8Inline = 32; // widest tile whose partials the last CTA adds
 constexpr size_t kF8SmemLimit = 227 * 1024;
 
 struct F8Shared {
@@ -77,6 +77,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
     volatile int *dead = &sh.dead;
 
     if (threadIdx.x == 0) {
+        stream_prefetch_map(&p.tw);
+        stream_prefetch_map(&p.tx);
         for (int i = 0; i < C::kStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
@@ -102,6 +104,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     allow_dependent_launch();
+    grid_dependency_wait();
 
     F8Walk walk(p, blockIdx.x, gridDim.x);
     F8Seg sg;
@@ -110,16 +113,17 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
         if (warp == 8) {
             // copies
             const uint32_t one = stream_elect();
+            const uint64_t policy = policy_evict_first();  // weights are read once
             int s = 0;
             uint32_t ph = 1;
             long long issued = 0;
             while (walk.next(p, sg)) {
                 for (int k = sg.k0; k < sg.k1; ++k) {
-                    stream_wait(&sh.empty[s], ph, dead, p.err);
+                    if (issued >= C::kStages) stream_wait(&sh.empty[s], ph, dead, p.err);
                     if (*dead) break;
                     if (one) mbar_arrive_expect_tx(&sh.full[s], C::kStageBytes);
                     const uint32_t dst = base + s * C::kStageBytes, bar = smem_u32(&sh.full[s]);
-                    stream_box2(one, dst, &p.tw, k * kF8K, sg.tile * kF8M, bar);
+                    stream_box2(one, dst, &p.tw, k * kF8K, sg.tile * kF8M, bar, policy);
                     stream_box2(one, dst + kF8M * kF8K, &p.tx, k * kF8K, 0, bar);
                     ++issued;
                     if (++s == C::kStages) s = 0, ph ^= 1;
@@ -241,9 +245,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                 }
                 named_sync(1, 256);
             }
-            if (sg.split < 0 || NB > kF8Inline) continue;
+            if (sg.split < 0) continue;
             int first, last;
-            f8_contributors(p, gridDim.x, sg.split, first, last);
+            f8_contributors(p, sg.split, first, last);
             named_sync(1, 256);
             if (threadIdx.x == 0) {
                 __threadfence();  // for what both warpgroups wrote
@@ -256,18 +260,13 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
             }
             named_sync(1, 256);
             if (sh.last) {
-                constexpr int HB = NB / 2;
-                float sum[HB];
+                constexpr int HB = NB / 2, AT = HB < 32 ? HB : 32;  // columns at a time
+                for (int c = wg * HB; c < wg * HB + HB; c += AT) {
+                    float sum[AT];
+                    f8_join<AT, kF8M>(p.partials + (((size_t)first + sg.split) * NB + c) * kF8M + r, (size_t)NB * kF8M, last - first + 1, sum);
 #pragma unroll
-                for (int i = 0; i < HB; ++i) sum[i] = 0.0f;
-#pragma unroll 4
-                for (int c = first; c <= last; ++c) {
-                    const float *part = p.partials + (((size_t)c + sg.split) * NB + wg * HB) * kF8M + r;
-#pragma unroll
-                    for (int i = 0; i < HB; ++i) sum[i] += __ldcg(part + i * kF8M);
+                    for (int i = 0; i < AT; ++i) f8_store(p, c + i, feature, sum[i]);
                 }
-#pragma unroll
-                for (int i = 0; i < HB; ++i) f8_store(p, wg * HB + i, feature, sum[i]);
             }
             named_sync(1, 256);  // before sh.last is written again
         }
@@ -278,26 +277,11 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
     if (warp == 9) tmem_dealloc(tmem, C::kTmem);
 }
 
-// Adds a split tile's partials, 8 of its rows a block; thread r is feature r.
-constexpr int kF8JoinCols = 8;
-__global__ __launch_bounds__(kF8M) void fp8_join_kernel(const __grid_constant__ F8Args p, int grid) {
-    constexpr int C = kF8JoinCols;
-    grid_dependency_wait();
-    const int chunks = p.bn / C, split = blockIdx.x / chunks, c0 = (int)(blockIdx.x % chunks) * C;
-    int first, last;
-    f8_contributors(p, grid, split, first, last);
-    if (first == last || c0 >= p.n) return;  // one CTA had all of it
-    float acc[C];
-    f8_join<C, kF8M>(p.partials + (((size_t)first + split) * p.bn + c0) * kF8M + threadIdx.x, (size_t)p.bn * kF8M, last - first + 1, acc);
-    const int tile = p.rounds * grid + split;
-#pragma unroll
-    for (int i = 0; i < C; ++i) f8_store(p, c0 + i, tile * kF8M + threadIdx.x, acc[i]);
-}
-
 // ---------------------------------------------------------------- host
 struct F8Plan {
     bool wide;
     int bn, m_tiles, n_tiles, grid, rounds, split;
+    unsigned runs;
 };
 
 static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
@@ -317,10 +301,11 @@ static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
         while (t.bn < n) t.bn *= 2;
         tiles = t.m_tiles = (int)((rows + kF8M - 1) / kF8M);
         t.n_tiles = 1;
-        t.grid = (int)std::min<int64_t>(sm_count(), tiles * kb);
+        t.grid = (int)std::min<int64_t>(sm_count(), std::max(tiles, tiles * kb / 4));
         t.rounds = (int)(tiles / t.grid);
     }
     t.split = (int)(tiles - (int64_t)t.rounds * t.grid);
+    t.runs = f8_runs(t.split, (int)kb, t.grid, t.wide ? 0 : 512 / t.bn);
     return t;
 }
 static size_t f8_ws_bytes(const F8Plan &t) {
@@ -340,9 +325,7 @@ static cudaError_t f8_launch(const F8Args &a, const F8Plan &t, cudaStream_t s) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    e = launch_ex(fp8_gemm_kernel<NB>, dim3(t.grid), dim3(kF8Threads), F8Cfg<NB>::kSmem, s, false, a);
-    if (e != cudaSuccess || NB <= kF8Inline || t.split == 0) return e;
-    return launch_ex(fp8_join_kernel, dim3(t.split * (NB / kF8JoinCols)), dim3(kF8M), 0, s, true, a, t.grid);
+    return launch_ex(fp8_gemm_kernel<NB>, dim3(t.grid), dim3(kF8Threads), F8Cfg<NB>::kSmem, s, true, a);
 }
 
 }  // namespace ds
@@ -395,6 +378,7 @@ extern "C" DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride
     a.n_tiles = t.n_tiles;
     a.rounds = t.rounds;
     a.split = t.split;
+    a.runs = t.runs;
     a.y = Y;
     a.y_dtype = y_dtype;
     a.ldy = y_stride;

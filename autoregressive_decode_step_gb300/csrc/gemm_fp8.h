@@ -13,6 +13,7 @@ struct F8Args {
     int bn;              // columns of an MMA: rows of X, or features (wide)
     int m_tiles, n_tiles;
     int rounds, split;   // whole tiles a CTA (a pair) takes; tiles behind them that are cut
+    unsigned runs;       // into so many runs
     void *y;
     int y_dtype;
     long long ldy;
@@ -21,16 +22,22 @@ struct F8Args {
     int *err;
 };
 
-// The split tiles' w steps are cut into runs, one a CTA (a pair), of four steps
-// at least: of fewer, joining what they leave takes longer than they do (333
-// rows by 1,000 x 1,416 in runs of one or two: 21 us).
-__host__ __device__ inline int f8_runs(long long w, int grid) { return w < 8 ? 1 : w / 4 < grid ? (int)(w / 4) : grid; }
+// The split tiles' steps are cut into runs, one a CTA (a pair), of four steps at
+// least: of fewer, joining what they leave takes longer than they do (333 rows
+// by 1,000 x 1,416 in runs of one or two: 21 us, of four 13).  `most`: runs that
+// meet in a tile at most, where one CTA adds them up.  Steps times runs stay
+// below 2^32: fewer split tiles than CTAs, 2^17 steps a tile.
+__host__ __device__ inline unsigned f8_runs(int split, int kb, int grid, int most) {
+    const long long w = (long long)split * kb;
+    long long r = w / 4 < grid ? w / 4 : grid;
+    if (most && r > (long long)split * (most - 1)) r = (long long)split * (most - 1);
+    return r < 1 ? 1u : (unsigned)r;
+}
 // The first and last run that hold steps of a split tile.
-__device__ __forceinline__ void f8_contributors(const F8Args &p, int grid, int split, int &first, int &last) {
-    const long long w = (long long)p.split * p.kb, t = (long long)split * p.kb;
-    const int runs = f8_runs(w, grid);
-    first = (int)(((t + 1) * runs - 1) / w);
-    last = (int)(((t + p.kb) * runs - 1) / w);
+__device__ __forceinline__ void f8_contributors(const F8Args &p, int split, int &first, int &last) {
+    const unsigned w = (unsigned)p.split * p.kb, t = (unsigned)split * p.kb;
+    first = (int)(((t + 1) * p.runs - 1) / w);
+    last = (int)(((t + p.kb) * p.runs - 1) / w);
 }
 
 // A run's segments: whole tiles in rounds, then its steps of the split tiles.
@@ -40,12 +47,11 @@ struct F8Seg {
 };
 struct F8Walk {
     int id, grid, round = 0;
-    long long u, u1;
+    unsigned u, u1;
     __device__ F8Walk(const F8Args &p, int id_, int grid_) : id(id_), grid(grid_) {
-        const long long w = (long long)p.split * p.kb;
-        const int runs = f8_runs(w, grid);
-        u = w * min(id, runs) / runs;
-        u1 = w * min(id + 1, runs) / runs;
+        const unsigned w = (unsigned)p.split * p.kb;
+        u = w * min((unsigned)id, p.runs) / p.runs;
+        u1 = w * min((unsigned)id + 1, p.runs) / p.runs;
     }
     __device__ bool next(const F8Args &p, F8Seg &s) {
         if (round < p.rounds) {
@@ -56,10 +62,10 @@ struct F8Walk {
             return true;
         }
         if (u >= u1) return false;
-        s.split = (int)(u / p.kb);
+        s.split = (int)(u / (unsigned)p.kb);
         s.tile = p.rounds * grid + s.split;
-        s.k0 = (int)(u - (long long)s.split * p.kb);
-        s.k1 = (int)min((long long)p.kb, s.k0 + u1 - u);
+        s.k0 = (int)(u - (unsigned)s.split * p.kb);
+        s.k1 = min(p.kb, s.k0 + (int)(u1 - u));
         u += s.k1 - s.k0;
         if (s.k0 == 0 && s.k1 == p.kb) s.split = -1;
         return true;
@@ -70,7 +76,7 @@ struct F8Walk {
 // partials' loads under way at a time.
 template <int C, int COLS>
 __device__ __forceinline__ void f8_join(const float *from, size_t part, int parts, float (&acc)[C]) {
-    constexpr int AT = 32 / C;
+    constexpr int AT = C >= 32 ? 3 : C >= 16 ? 4 : 32 / C;
 #pragma unroll
     for (int i = 0; i < C; ++i) acc[i] = 0.0f;
     for (int c = 0; c < parts; c += AT) {

@@ -172,6 +172,8 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
     volatile int *dead = &sh.dead;
 
     if (threadIdx.x == 0) {
+        stream_prefetch_map(&p.tw);
+        stream_prefetch_map(&p.tx);
         for (int i = 0; i < kFwStages; ++i) {
             mbar_init(&sh.full[i], 1);
             mbar_init(&sh.empty[i], 1);
@@ -198,6 +200,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
     tc_fence_after();
     const uint32_t tmem = sh.tmem;
     allow_dependent_launch();
+    grid_dependency_wait();
 
     F8Walk walk(p, blockIdx.x >> 1, gridDim.x >> 1);
     F8Seg sg;
@@ -213,7 +216,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             while (walk.next(p, sg)) {
                 fw_tile(p, sg.tile, rt, ft);
                 for (int k = sg.k0; k < sg.k1; ++k) {
-                    stream_wait(&sh.empty[s], ph, dead, p.err);
+                    if (issued >= kFwStages) stream_wait(&sh.empty[s], ph, dead, p.err);
                     if (*dead) break;
                     if (one && rank == 0) mbar_arrive_expect_tx(&sh.full[s], 2 * kFwStageBytes);
                     const uint32_t dst = base + s * kFwStageBytes, bar = fw_lead(&sh.full[s]);
@@ -349,10 +352,11 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
 constexpr int kFwJoinCols = 8;
 __global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constant__ F8Args p, int pairs) {
     constexpr int C = kFwJoinCols, kChunks = kF8WideFeatures / C;
+    allow_dependent_launch();
     grid_dependency_wait();
     const int chunk = blockIdx.x % kChunks, rank = blockIdx.x / kChunks % 2, split = blockIdx.x / (2 * kChunks);
     int first, last, rt, ft;
-    f8_contributors(p, pairs, split, first, last);
+    f8_contributors(p, split, first, last);
     if (first == last) return;  // one pair had all of it
     fw_tile(p, p.rounds * pairs + split, rt, ft);
     const int row = rt * kF8WideRows + rank * 128 + threadIdx.x, f0 = ft * kF8WideFeatures + chunk * C;
@@ -392,7 +396,7 @@ cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream) {
         ready.fetch_or(bit, std::memory_order_release);
     }
     const int pairs = f8_wide_pairs();
-    e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, false, a);
+    e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, true, a);
     if (e != cudaSuccess || a.split == 0) return e;
     return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / kFwJoinCols)), dim3(128), 0, stream, true, a, pairs);
 }

@@ -65,6 +65,9 @@ __device__ __forceinline__ uint32_t stream_elect() {
         : "=r"(one));
     return one;
 }
+__device__ __forceinline__ void stream_prefetch_map(const CUtensorMap *map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void stream_box2(uint32_t one, uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
@@ -72,6 +75,16 @@ __device__ __forceinline__ void stream_box2(uint32_t one, uint32_t dst, const CU
         "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(
             dst),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one)
+        : "memory");
+}
+// The same with an L2 policy.
+__device__ __forceinline__ void stream_box2(uint32_t one, uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.u32 q, %5, 0;\n\t"
+        "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3}], "
+        "[%4], %6;\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(one), "l"(policy)
         : "memory");
 }
 // D[tmem] (+)= A[smem] x B[smem] of 8-bit floats.
