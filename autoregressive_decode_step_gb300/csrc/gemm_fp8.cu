@@ -6,19 +6,20 @@
 // so scales need not be powers of two, and every sum in it is short.
 //
 // This file: up to 128 rows of X, where the weights' bytes are the bound
-// (gemm_fp8_wide.cu: more).  A tile is 128 features (the MMA's M: lane r of
-// TMEM is feature r) by all the rows of X, rounded up to 16, 32, 64 or 128 (its
-// N): one token costs an MMA of 16 columns.  All tiles' steps are one line, cut
-// into equal runs, one a CTA, so that every SM streams the same bytes; a cut
-// tile's partial sums meet in the workspace and are added in CTA order by
-// whichever CTA arrives last (256 KB of them at most: a second launch for the
-// wider ones took 12 us of 35 with 64 rows by 28,672 x 4,096).  No CTA waits for
-// another.  A launch may begin while the one in front ends.
+// (gemm_fp8_wide.cu: more).  A tile is 128 features (an MMA's M: lane r of TMEM
+// is feature r), for more than 32 rows 256 in two halves, by all the rows of X,
+// rounded up to 16, 32, 64 or 128 (the MMA's N): one token costs 16 columns.  All tiles' steps
+// are one line, cut into equal runs, one a CTA, so that every SM streams the same
+// bytes; a cut tile's partial sums meet in the workspace and are added in CTA
+// order by whichever CTA arrives last (a second launch for the wider ones took
+// 12 us of 35 with 64 rows by 28,672 x 4,096).  No CTA waits for another.  A
+// launch may begin while the one in front ends.
 //
-// Two warpgroups take turns at batches of steps, up to 128 columns of TMEM each
-// and four in flight, so that a batch's waits and TMEM's latency (some 700
-// cycles, two steps' worth of weights) lie beside the next batch's products;
-// at a segment's end they exchange halves of their sums and finish one each.
+// A step brings its weights in one copy (16 KB for few rows, where the runs are
+// short and even ones count: one token 9.9 us against 11.2; else 32 KB: 64 rows by
+// 28,672 x 4,096 29 us against 33), and up to four steps' columns are a batch:
+// barriers and the latency of TMEM are paid once a batch.  A warpgroup for each
+// half of the features adds it up.
 #include <algorithm>
 #include <atomic>
 
@@ -28,48 +29,62 @@
 
 namespace ds {
 
-constexpr int kF8M = 128, kF8K = 128;
+constexpr int kF8K = 128;
 constexpr int kF8Threads = 384;  // two warpgroups that add up; copies, products, scales, one idle
 // Registers a thread: 168 at launch (384 x 168), moved to the warps that add
 // up: 2 x 216 + 72 = 3 x 168.
 constexpr int kF8RegsSum = 216, kF8RegsOther = 72;
 constexpr int kF8MaxStages = 10;
 constexpr int kF8Slots = 8;   // batches' scales ahead
-constexpr int kF8Bufs = 4;    // batches in TMEM
+constexpr int kF8MaxBufs = 4; // batches in TMEM
 constexpr size_t kF8SmemLimit = 227 * 1024;
 
 struct F8Shared {
     uint64_t full[kF8MaxStages], empty[kF8MaxStages];
     uint64_t s_full[kF8Slots], s_empty[kF8Slots];
-    uint64_t t_full[kF8Bufs], t_empty[kF8Bufs];
+    uint64_t t_full[kF8MaxBufs], t_empty[kF8MaxBufs];
     uint64_t done;
     uint32_t tmem;
     int dead, last;
-    alignas(16) float scale[kF8Slots][128];
-    float swap[2][32][128];  // sums on their way to the other warpgroup
+    alignas(16) float scale[kF8Slots][2][128];
 };
 
 template <int NB>
 struct F8Cfg {
-    static constexpr int kBatch = NB >= 128 ? 1 : NB >= 64 ? 2 : 4;  // steps of a batch
-    static constexpr int kCols = kBatch * NB;                        // TMEM columns of a batch
-    static constexpr int kTmem = kF8Bufs * kCols;
-    static constexpr int kStageBytes = (kF8M + NB) * kF8K;
+    static constexpr int kHalves = NB <= 32 ? 1 : 2, kM = 128 * kHalves;
+    static constexpr int kBatch = NB >= 64 ? 1 : NB >= 32 ? 2 : 4;  // steps of a batch
+    static constexpr int kCols = kBatch * NB;                       // TMEM columns of a batch and half
+    static constexpr int kBufs = NB >= 128 ? 2 : 4, kTmem = kBufs * kHalves * kCols;
+    static constexpr int kStageBytes = (kM + NB) * kF8K;
     static constexpr int kFit = (int)((kF8SmemLimit - 1024 - sizeof(F8Shared)) / kStageBytes);
     static constexpr int kStages = kFit < kF8MaxStages ? kFit : kF8MaxStages;
     static constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(F8Shared);
-    static constexpr int kHalf = NB / 2 < 32 ? NB / 2 : 32;  // columns exchanged at a time
 };
 
-__device__ __forceinline__ void f8_store(const F8Args &p, int row, int feature, float v) {
-    if (row < p.n && feature < p.rows) store_as(p.y, row * p.ldy + feature, p.y_dtype, v);
+// A feature's outputs of rows row0 ... row0 + N - 1.
+template <int N>
+__device__ __forceinline__ void f8_store(const F8Args &p, int row0, int feature, const float (&v)[N]) {
+    if (feature >= p.rows) return;
+    const int n = p.n - row0;
+    const long long at = row0 * p.ldy + feature;
+    if (p.y_dtype == DS_BF16) {
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < N; ++i, y += p.ldy)
+            if (i < n) *y = __float2bfloat16_rn(v[i]);
+    } else {
+        float *y = static_cast<float *>(p.y) + at;
+#pragma unroll
+        for (int i = 0; i < N; ++i, y += p.ldy)
+            if (i < n) *y = v[i];
+    }
 }
 
 // NB: columns of an MMA, rows of X rounded up.
 template <int NB>
 __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_constant__ F8Args p) {
     using C = F8Cfg<NB>;
-    constexpr int BS = C::kBatch, CH = NB < 32 ? NB : 32, H = C::kHalf;
+    constexpr int BS = C::kBatch, CH = NB < 32 ? NB : 32, kBufs = C::kBufs, HV = C::kHalves, kM = C::kM;
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     F8Shared &sh = *reinterpret_cast<F8Shared *>(smem_raw + (base - smem_u32(smem_raw)) + C::kStages * C::kStageBytes);
@@ -85,11 +100,11 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
         }
         for (int i = 0; i < kF8Slots; ++i) {
             mbar_init(&sh.s_full[i], 1);
-            mbar_init(&sh.s_empty[i], 4);
+            mbar_init(&sh.s_empty[i], 4 * HV);
         }
-        for (int i = 0; i < kF8Bufs; ++i) {
+        for (int i = 0; i < kBufs; ++i) {
             mbar_init(&sh.t_full[i], 1);
-            mbar_init(&sh.t_empty[i], 4);
+            mbar_init(&sh.t_empty[i], 4 * HV);
         }
         mbar_init(&sh.done, 1);
         sh.dead = 0;
@@ -123,8 +138,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                     if (*dead) break;
                     if (one) mbar_arrive_expect_tx(&sh.full[s], C::kStageBytes);
                     const uint32_t dst = base + s * C::kStageBytes, bar = smem_u32(&sh.full[s]);
-                    stream_box2(one, dst, &p.tw, k * kF8K, sg.tile * kF8M, bar, policy);
-                    stream_box2(one, dst + kF8M * kF8K, &p.tx, k * kF8K, 0, bar);
+                    stream_box2(one, dst, &p.tw, k * kF8K, sg.tile * kM, bar, policy);
+                    stream_box2(one, dst + kM * kF8K, &p.tx, k * kF8K, 0, bar);
                     ++issued;
                     if (++s == C::kStages) s = 0, ph ^= 1;
                 }
@@ -136,7 +151,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
         } else if (warp == 9) {
             // products
             const uint32_t one = stream_elect();
-            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NB >> 3) << 17) | ((uint32_t)(kF8M >> 4) << 24);
+            constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(NB >> 3) << 17) | (8u << 24);
             int s = 0, b = 0;
             uint32_t ph = 0, bph = 1;
             while (walk.next(p, sg)) {
@@ -147,15 +162,17 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                         stream_wait(&sh.full[s], ph, dead, p.err);
                         tc_fence_after();
                         const uint64_t ad = smem_desc(base + s * C::kStageBytes, 16, 1024);
-                        const uint64_t bd = smem_desc(base + s * C::kStageBytes + kF8M * kF8K, 16, 1024);
+                        const uint64_t bd = smem_desc(base + s * C::kStageBytes + kM * kF8K, 16, 1024);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
-                            stream_mma_f8(one, tmem + b * C::kCols + j * NB, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+                        for (int h = 0; h < HV; ++h)
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
+                                stream_mma_f8(one, tmem + (HV * b + h) * C::kCols + j * NB, ad + h * (128 * 128 / 16) + 2 * i, bd + 2 * i, idesc, i > 0);
                         stream_commit(one, &sh.empty[s]);
                         if (++s == C::kStages) s = 0, ph ^= 1;
                     }
                     stream_commit(one, &sh.t_full[b]);
-                    if (++b == kF8Bufs) b = 0, bph ^= 1;
+                    if (++b == kBufs) b = 0, bph ^= 1;
                 }
             }
             stream_commit(one, &sh.done);
@@ -166,20 +183,26 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
             int slot = 0;
             uint32_t ph = 1;
             while (walk.next(p, sg)) {
-                const float *ws = p.ws + (long long)sg.tile * p.kb;
+                const float *w0 = p.ws + (long long)(HV * sg.tile) * p.kb, *w1 = HV > 1 && 2 * sg.tile + 1 < (p.rows + 127) / 128 ? w0 + p.kb : w0;
                 for (int k = sg.k0; k < sg.k1; k += 4) {
-                    float v[kVals];
+                    float v[kVals], a[kVals], b[kVals];
 #pragma unroll
                     for (int i = 0; i < kVals; ++i) {
                         const int at = i * 32 + lane, j = k + at / NB, c = at % NB;
-                        v[i] = j < sg.k1 && c < p.n ? __ldg(p.xs + (long long)c * p.kb + j) * __ldg(ws + j) : 0.0f;
+                        v[i] = j < sg.k1 && c < p.n ? __ldg(p.xs + (long long)c * p.kb + j) : 0.0f;
+                        a[i] = j < sg.k1 ? __ldg(w0 + j) : 0.0f;
+                        b[i] = HV > 1 && j < sg.k1 ? __ldg(w1 + j) : 0.0f;
                     }
 #pragma unroll
                     for (int j = 0; j < 4; j += BS) {
                         if (k + j >= sg.k1) break;
                         stream_wait(&sh.s_empty[slot], ph, dead, p.err);
 #pragma unroll
-                        for (int i = 0; i < kPer; ++i) sh.scale[slot][i * 32 + lane] = v[j / BS * kPer + i];
+                        for (int i = 0; i < kPer; ++i) {
+                            const int q = j / BS * kPer + i;
+                            sh.scale[slot][0][i * 32 + lane] = v[q] * a[q];
+                            if (HV > 1) sh.scale[slot][1][i * 32 + lane] = v[q] * b[q];
+                        }
                         __syncwarp();
                         if (lane == 0) mbar_arrive(&sh.s_full[slot]);
                         if (++slot == kF8Slots) slot = 0, ph ^= 1;
@@ -189,28 +212,28 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kF8RegsSum));
-        // sums: thread r of a warpgroup is feature r; the warpgroups take turns at batches
-        const int wg = warp >> 2, r = threadIdx.x & 127;
-        const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21);
+        // sums: thread r of warpgroup h is feature r of half h
+        const int half = warp >> 2, r = threadIdx.x & 127;
+        const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * C::kCols, one = lane == 0;
+        const uint32_t s_full0 = smem_u32(&sh.s_full[0]), s_empty0 = smem_u32(&sh.s_empty[0]), t_full0 = smem_u32(&sh.t_full[0]), t_empty0 = smem_u32(&sh.t_empty[0]);
         unsigned batch = 0;
-        while (walk.next(p, sg)) {
+        while (half < HV && walk.next(p, sg)) {
             float acc[NB];
 #pragma unroll
             for (int i = 0; i < NB; ++i) acc[i] = 0.0f;
             for (int k = sg.k0; k < sg.k1; k += BS, ++batch) {
-                if ((batch & 1) != (unsigned)wg) continue;
-                const int b = batch % kF8Bufs, slot = batch % kF8Slots;
-                stream_wait(&sh.s_full[slot], (batch / kF8Slots) & 1, dead, p.err);
-                stream_wait(&sh.t_full[b], (batch / kF8Bufs) & 1, dead, p.err);
+                const unsigned b = batch % kBufs, slot = batch % kF8Slots;
+                stream_wait(s_full0 + slot * 8, (batch / kF8Slots) & 1, dead, p.err);
+                stream_wait(t_full0 + b * 8, (batch / kBufs) & 1, dead, p.err);
                 tc_fence_after();
 #pragma unroll
                 for (int j = 0; j < BS; ++j) {
                     if (k + j < sg.k1) {
-                        const float *scale = sh.scale[slot] + j * NB;
+                        const float *scale = sh.scale[slot][half] + j * NB;
 #pragma unroll
                         for (int c = 0; c < NB; c += CH) {
                             float v[CH];
-                            stream_ld<CH>(from + b * C::kCols + j * NB + c, v);
+                            stream_ld<CH>(from + b * HV * C::kCols + j * NB + c, v);
 #pragma unroll
                             for (int i = 0; i < CH; i += 4) {
                                 const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(scale + c + i);
@@ -222,33 +245,21 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&sh.t_empty[b]);
-                    mbar_arrive(&sh.s_empty[slot]);
-                }
+                stream_arrive(one, t_empty0 + b * 8);
+                stream_arrive(one, s_empty0 + slot * 8);
             }
-            // Warpgroup w finishes columns [2 H i + w H, + H) of every 2 H.
-            const int feature = sg.tile * kF8M + r;
-            float *mine = p.partials + ((size_t)blockIdx.x + max(sg.split, 0)) * NB * kF8M + r;
-#pragma unroll
-            for (int c = 0; c < NB; c += 2 * H) {
-#pragma unroll
-                for (int i = 0; i < H; ++i) sh.swap[wg][i][r] = wg ? acc[c + i] : acc[c + H + i];
-                named_sync(1, 256);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    const int col = c + wg * H + i;
-                    // the first warpgroup's sum first, so that the order does not depend on who adds
-                    const float a = wg ? acc[c + H + i] : acc[c + i], o = sh.swap[wg ^ 1][i][r], sum = wg ? o + a : a + o;
-                    if (sg.split < 0) f8_store(p, col, feature, sum);
-                    else __stcg(mine + col * kF8M, sum);
-                }
-                named_sync(1, 256);
+            const int feature = sg.tile * kM + half * 128 + r;
+            if (sg.split < 0) {
+                f8_store<NB>(p, 0, feature, acc);
+                continue;
             }
-            if (sg.split < 0) continue;
+            constexpr size_t part = HV * NB * 128;  // floats of a partial sum, a half after the other
+            float *mine = p.partials + ((size_t)blockIdx.x + sg.split) * part + half * NB * 128 + r;
+#pragma unroll
+            for (int i = 0; i < NB; ++i) __stcg(mine + i * 128, acc[i]);
             int first, last;
             f8_contributors(p, sg.split, first, last);
-            named_sync(1, 256);
+            named_sync(1, 128 * HV);
             if (threadIdx.x == 0) {
                 __threadfence();  // for what both warpgroups wrote
                 const bool is = atomicAdd(p.counters + sg.split, 1) == last - first;
@@ -258,17 +269,17 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
                 }
                 sh.last = is;
             }
-            named_sync(1, 256);
+            named_sync(1, 128 * HV);
             if (sh.last) {
-                constexpr int HB = NB / 2, AT = HB < 32 ? HB : 32;  // columns at a time
-                for (int c = wg * HB; c < wg * HB + HB; c += AT) {
+                constexpr int AT = NB < 32 ? NB : 32;  // columns at a time
+#pragma unroll 1
+                for (int c = 0; c < min(NB, p.n); c += AT) {
                     float sum[AT];
-                    f8_join<AT, kF8M>(p.partials + (((size_t)first + sg.split) * NB + c) * kF8M + r, (size_t)NB * kF8M, last - first + 1, sum);
-#pragma unroll
-                    for (int i = 0; i < AT; ++i) f8_store(p, c + i, feature, sum[i]);
+                    f8_join<AT, 128>(p.partials + ((size_t)first + sg.split) * part + (half * NB + c) * 128 + r, part, last - first + 1, sum);
+                    f8_store<AT>(p, c, feature, sum);
                 }
             }
-            named_sync(1, 256);  // before sh.last is written again
+            named_sync(1, 128 * HV);  // before sh.last is written again
         }
     }
     tc_fence_before();
@@ -299,7 +310,8 @@ static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
     } else {
         t.bn = 16;
         while (t.bn < n) t.bn *= 2;
-        tiles = t.m_tiles = (int)((rows + kF8M - 1) / kF8M);
+        const int m = t.bn <= 32 ? F8Cfg<32>::kM : F8Cfg<64>::kM;
+        tiles = t.m_tiles = (int)((rows + m - 1) / m);
         t.n_tiles = 1;
         t.grid = (int)std::min<int64_t>(sm_count(), std::max(tiles, tiles * kb / 4));
         t.rounds = (int)(tiles / t.grid);
@@ -309,7 +321,7 @@ static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
     return t;
 }
 static size_t f8_ws_bytes(const F8Plan &t) {
-    const size_t floats = t.wide ? f8_wide_partial_floats(t.split) : t.split ? ((size_t)t.grid + t.split) * t.bn * kF8M : 0;
+    const size_t floats = t.wide ? f8_wide_partial_floats(t.split) : t.split ? ((size_t)t.grid + t.split) * t.bn * F8Cfg<64>::kM : 0;
     return kWsHeader + align_up((size_t)sm_count() * 4, 256) + floats * 4;
 }
 
@@ -386,7 +398,7 @@ extern "C" DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride
     a.err = reinterpret_cast<int *>(w);
     a.counters = reinterpret_cast<int *>(w + kWsHeader);
     a.partials = reinterpret_cast<float *>(w + kWsHeader + align_up((size_t)sm_count() * 4, 256));
-    if (!encode_tiled_2d(&a.tw, W, DS_E4M3, cols, rows, w_stride, kF8K, 128, true) ||
+    if (!encode_tiled_2d(&a.tw, W, DS_E4M3, cols, rows, w_stride, kF8K, t.wide || t.bn <= 32 ? 128 : 256, true) ||
         !encode_tiled_2d(&a.tx, X, DS_E4M3, cols, n, x_stride, kF8K, t.wide ? 128 : t.bn, true))
         return DS_CUDA_ERROR;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

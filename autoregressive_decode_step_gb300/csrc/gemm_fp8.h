@@ -7,7 +7,7 @@
 namespace ds {
 
 struct F8Args {
-    CUtensorMap tw, tx;  // bytes, boxes {128, 128} and {128, bn} (wide: {128, 128}), 128-byte swizzle
+    CUtensorMap tw, tx;  // bytes, boxes {128, a tile's features} and {128, bn} (wide: {128, 128} both), 128-byte swizzle
     const float *ws, *xs;
     int rows, n, kb;
     int bn;              // columns of an MMA: rows of X, or features (wide)
