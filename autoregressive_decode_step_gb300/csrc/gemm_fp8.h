@@ -76,7 +76,7 @@ struct F8Walk {
 // partials' loads under way at a time.
 template <int C, int COLS>
 __device__ __forceinline__ void f8_join(const float *from, size_t part, int parts, float (&acc)[C]) {
-    constexpr int AT = C >= 32 ? 3 : C >= 16 ? 4 : 32 / C;
+    constexpr int AT = C >= 32 ? 3 : C >= 16 ? 4 : 6;
 #pragma unroll
     for (int i = 0; i < C; ++i) acc[i] = 0.0f;
     for (int c = 0; c < parts; c += AT) {

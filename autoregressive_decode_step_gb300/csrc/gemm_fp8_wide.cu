@@ -24,12 +24,12 @@
 
 namespace ds {
 
-constexpr int kFwThreads = 640;  // sixteen warps that add up; copies, products, scales, one idle
+constexpr int kFwThreads = 640;  // sixteen warps that add up; copies, products of one half, scales, products of the other
 // Registers a thread: 96 at launch (640 x 96), moved to the warps that add up:
 // 4 x 104 + 64 = 5 x 96.
 constexpr int kFwRegsSum = 104, kFwRegsOther = 64;
 constexpr int kFwStages = 5, kFwHalf = 128 * 128, kFwStageBytes = 2 * kFwHalf;
-constexpr int kFwSlots = 8;   // steps' factors ahead
+constexpr int kFwSlots = 8;   // steps' factors; see where they are written
 constexpr int kFwBufs = 4;    // TMEM buffers of 128 columns, two a step
 constexpr int kFwGroup = 8;   // row tiles that follow one another before the next features
 constexpr int kFwOutRow = 80;  // 64 bytes of a row and 16 that keep rows apart on the banks
@@ -37,7 +37,6 @@ constexpr int kFwPart = 128 * kF8WideFeatures;  // floats of one SM's share of a
 
 struct FwShared {
     uint64_t full[kFwStages], empty[kFwStages];
-    uint64_t s_full[kFwSlots], s_empty[kFwSlots];
     uint64_t t_full[kFwBufs], t_empty[kFwBufs];
     uint64_t done;
     uint32_t tmem;
@@ -175,18 +174,14 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
         stream_prefetch_map(&p.tw);
         stream_prefetch_map(&p.tx);
         for (int i = 0; i < kFwStages; ++i) {
-            mbar_init(&sh.full[i], 1);
-            mbar_init(&sh.empty[i], 1);
-        }
-        for (int i = 0; i < kFwSlots; ++i) {
-            mbar_init(&sh.s_full[i], 2);  // both CTAs' factors, on the first one's barrier
-            mbar_init(&sh.s_empty[i], 16);
+            mbar_init(&sh.full[i], 3);  // the copies of both CTAs and, on the first one's barrier, both CTAs' factors
+            mbar_init(&sh.empty[i], 2);  // a commit of either half's products
         }
         for (int i = 0; i < kFwBufs; ++i) {
             mbar_init(&sh.t_full[i], 1);
             mbar_init(&sh.t_empty[i], 16);
         }
-        mbar_init(&sh.done, 1);
+        mbar_init(&sh.done, 2);
         sh.dead = 0;
         fence_mbarrier_init();
     }
@@ -231,30 +226,29 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             if (rank == 0)
                 for (long long i = max(0ll, issued - kFwStages); i < issued; ++i)
                     mbar_wait(&sh.full[i % kFwStages], (uint32_t)(i / kFwStages) & 1, p.err);
-        } else if (warp == 17) {
-            // products, from the first CTA
+        } else if (warp != 18) {
+            // Products, from the first CTA: a warp for each half, 64 of either
+            // CTA's 128 features.  (From one warp its four waits a step, some 100
+            // cycles each however long done, took longer than the products.)
             const uint32_t one = stream_elect();
+            const int h = warp == 17 ? 0 : 1;
             if (rank == 0) {
                 constexpr uint32_t idesc = (1u << 4) | ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(kF8WideRows >> 4) << 24);
                 int s = 0;
                 uint32_t ph = 0, n = 0;  // n: steps so far
                 while (walk.next(p, sg)) {
                     for (int k = sg.k1 - sg.k0; k > 0; --k, ++n) {
-                        // a step's factors are there before its products start, so whoever sees these needs no other wait
-                        stream_wait(&sh.s_full[n % kFwSlots], n / kFwSlots & 1, dead, p.err);
-                        stream_wait(&sh.full[s], ph, dead, p.err);
-                        const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
-                        const uint64_t bd = smem_desc(base + s * kFwStageBytes + kFwHalf, 16, 1024);
                         const uint32_t b = n & 1;
+                        stream_wait(&sh.t_empty[2 * b + h], (n >> 1 & 1) ^ 1, dead, p.err);
+                        // a step's factors are there before its products start, so whoever sees these needs no other wait
+                        stream_wait(&sh.full[s], ph, dead, p.err);
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
+                        const uint64_t bd = smem_desc(base + s * kFwStageBytes + kFwHalf + h * 64 * 128, 16, 1024);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {  // 64 of either CTA's 128 features
-                            stream_wait(&sh.t_empty[2 * b + h], (n >> 1 & 1) ^ 1, dead, p.err);
-                            tc_fence_after();
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
-                                fw_mma(one, tmem + b * 256 + h * 128, ad + 2 * i, bd + h * (64 * 128 / 16) + 2 * i, idesc, i > 0);
-                            fw_commit(one, &sh.t_full[2 * b + h]);
-                        }
+                        for (int i = 0; i < 4; ++i)  // 32 bytes of every row a product
+                            fw_mma(one, tmem + b * 256 + h * 128, ad + 2 * i, bd + 2 * i, idesc, i > 0);
+                        fw_commit(one, &sh.t_full[2 * b + h]);
                         fw_commit(one, &sh.empty[s]);
                         if (++s == kFwStages) s = 0, ph ^= 1;
                     }
@@ -262,9 +256,13 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
                 fw_commit(one, &sh.done);
             }
             mbar_wait(&sh.done, 0, p.err);
-        } else if (warp == 18) {
-            // factors: four steps' scales requested together, so that a step's come before its product is done
-            int slot = 0;
+        } else {
+            // Factors: four steps' scales requested together, so that a step's come
+            // before its products start.  Once the products of the stage's last
+            // step, n - 5, are done, those of n - 7 and before have been taken out
+            // (a buffer waits for that), so slot n - 8 may be written over.
+            static_assert(kFwSlots > kFwStages + 2, "slots");
+            int slot = 0, s = 0;
             uint32_t ph = 1;
             while (walk.next(p, sg)) {
                 fw_tile(p, sg.tile, rt, ft);
@@ -284,15 +282,16 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (k + j >= sg.k1) break;
-                        stream_wait(&sh.s_empty[slot], ph, dead, p.err);
+                        stream_wait(&sh.empty[s], ph, dead, p.err);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             sh.factor[slot][0][32 * i + lane] = v[j][i] * a[j];
                             sh.factor[slot][1][32 * i + lane] = v[j][i] * b[j];
                         }
                         __syncwarp();
-                        fw_arrive(lane == 0, fw_lead(&sh.s_full[slot]));
-                        if (++slot == kFwSlots) slot = 0, ph ^= 1;
+                        fw_arrive(lane == 0, fw_lead(&sh.full[s]));
+                        if (++slot == kFwSlots) slot = 0;
+                        if (++s == kFwStages) s = 0, ph ^= 1;
                     }
                 }
             }
@@ -304,7 +303,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
         const int wg = warp >> 2, half = wg >> 1, sub = wg & 1, r = threadIdx.x & 127, f0 = sub * 128 + half * 64;
         const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * 128 + sub * 64;
         const uint32_t full0 = smem_u32(&sh.t_full[half]), freed0 = fw_lead(&sh.t_empty[half]);
-        const uint32_t factor0 = smem_u32(&sh.factor[0][sub][r]), s_empty0 = smem_u32(&sh.s_empty[0]), one = stream_elect();
+        const uint32_t factor0 = smem_u32(&sh.factor[0][sub][r]), one = stream_elect();
         uint32_t n = 0;  // steps so far
         while (walk.next(p, sg)) {
             float acc[64];
@@ -321,11 +320,10 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
                 for (int c = 0; c < 64; c += 32) {
                     float v[32];
                     stream_ld<32>(from + b * 256 + c, v);
-                    if (c == 32) {  // the buffer and the factors are read out
+                    if (c == 32) {  // the buffer is read out
                         tc_fence_before();
                         __syncwarp();
                         fw_arrive(one, freed0 + b * 16);
-                        stream_arrive(one, s_empty0 + slot * 8);
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
