@@ -261,12 +261,8 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
             f8_contributors(p, sg.split, first, last);
             named_sync(1, 128 * HV);
             if (threadIdx.x == 0) {
-                __threadfence();  // for what both warpgroups wrote
-                const bool is = atomicAdd(p.counters + sg.split, 1) == last - first;
-                if (is) {
-                    p.counters[sg.split] = 0;
-                    __threadfence();
-                }
+                const bool is = stream_count(p.counters + sg.split) == last - first;
+                if (is) p.counters[sg.split] = 0;
                 sh.last = is;
             }
             named_sync(1, 128 * HV);

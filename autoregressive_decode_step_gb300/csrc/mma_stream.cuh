@@ -54,6 +54,14 @@ __device__ __forceinline__ void stream_arrive(uint32_t one, uint32_t bar) {
         : "memory");
 }
 
+// Count an arrival: what this thread's block wrote before (behind a barrier of
+// the block) is seen by whoever sees the count, and the other way round.
+__device__ __forceinline__ int stream_count(int *counter) {
+    int was;
+    asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(was) : "l"(counter) : "memory");
+    return was;
+}
+
 // One lane of the warp: the others run the same code with 0, so that addresses
 // and descriptors stay in uniform registers.
 __device__ __forceinline__ uint32_t stream_elect() {

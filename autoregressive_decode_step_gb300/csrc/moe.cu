@@ -111,8 +111,7 @@ static_assert(kMoeSmem <= 227 * 1024, "shared memory");
 // ------------------------------------------------------------------ waits
 // One thread of every CTA: all of them have arrived, and what they wrote is seen.
 __device__ __forceinline__ void moe_meet(int *bar, volatile int *dead, int *err) {
-    __threadfence();
-    asm volatile("red.relaxed.gpu.global.add.s32 [%0], 1;" ::"l"(bar) : "memory");
+    asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(bar) : "memory");
     const long long t0 = clock64();
     for (uint32_t it = 1;; ++it) {
         int v;
@@ -159,25 +158,22 @@ __device__ __forceinline__ void moe_add2(float &s, float &c, float s2, float c2)
     c = __fadd_rn(__fadd_rn(c, c2), __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(s2, z)));
     s = t;
 }
-// How the logits are dealt out: T tokens with an expert and one of `splits` parts
-// of the sum (each a whole number of 256 values) make an item, a warp's work.
-struct MoeLogits {
-    int tokens, splits;
-};
-__host__ __device__ inline MoeLogits moe_logits_plan(long long n, long long d, long long experts, int warps) {
-    MoeLogits l;
-    l.tokens = n == 1 ? 1 : 4;
-    const long long items = (n + l.tokens - 1) / l.tokens * experts, whole = (d + 255) / 256;
-    long long s = 8LL * warps / items;  // several items a warp even out
+// How many parts the logits' sums are cut into (each a whole number of 256
+// values): a part with an expert and four tokens is a warp's work, and several
+// of them a warp even out.  Few tokens: one part, a CTA's work.
+__host__ __device__ inline int moe_splits(long long n, long long d, long long experts, int warps) {
+    if (n <= kMoeByToken) return 1;
+    const long long items = (n + 3) / 4 * experts, whole = (d + 255) / 256;
+    long long s = 8LL * warps / items;
     s = s < 1 ? 1 : s > whole ? whole : s > 16 ? 16 : s;
     const long long per = (whole + s - 1) / s;
-    l.splits = (int)((whole + per - 1) / per);
-    return l;
+    return (int)((whole + per - 1) / per);
 }
-// Part s of the sum of one expert's logits of T tokens, by a warp.
+// Part `split` of the sum of one expert's logits of tokens t0 ... t0 + T - 1, by a
+// warp, a token's `stride` behind the one before's.
 template <int T>
-__device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0, int split) {
-    const int lane = threadIdx.x & 31, per = ((p.d + 255) / 256 + p.splits - 1) / p.splits * 256;
+__device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0, int split, int splits, float2 *to, int stride) {
+    const int lane = threadIdx.x & 31, per = ((p.d + 255) / 256 + splits - 1) / splits * 256;
     const int end = min(p.d, (split + 1) * per);
     float s[T], c[T];
 #pragma unroll
@@ -202,7 +198,7 @@ __device__ __forceinline__ void moe_logits(const MoeArgs &p, int e, int t0, int 
 #pragma unroll
         for (int i = 1; i < T; ++i)
             if (lane == i) sum = s[i], lost = c[i];
-        p.logits[((long long)split * p.n + t0 + lane) * p.experts + e] = make_float2(sum, lost);
+        to[(long long)lane * stride] = make_float2(sum, lost);
     }
 }
 
@@ -231,17 +227,24 @@ __device__ __forceinline__ void moe_keys(const MoeArgs &p, int t0, int n, unsign
         key[i] = moe_key(fabsf(sum) < INFINITY ? (double)sum + (double)lost : (double)sum);
     }
 }
-// The tokens' choices: an expert's place is the number of experts ahead of it, so
-// all are found at once.
-__device__ __forceinline__ void moe_choose(const MoeArgs &p, int n, const unsigned long long *key, unsigned short *chosen, int id, int step) {
-    for (int i = id; i < n * p.experts; i += step) {
-        const int t = i / p.experts, e = i - t * p.experts;
+// n tokens' choices: an expert's place is the number of experts ahead of it, so
+// all are found at once.  All threads, several an expert where there are few.
+__device__ __forceinline__ void moe_choose(const MoeArgs &p, int n, const unsigned long long *key, int *ahead, unsigned short *chosen) {
+    const int m = n * p.experts, parts = max(1, min(4, kMoeThreads / m)), per = (p.experts + parts - 1) / parts;
+    for (int i = threadIdx.x; i < m; i += kMoeThreads) ahead[i] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < m * parts; i += kMoeThreads) {
+        const int part = i / m, at = i - part * m, t = at / p.experts, e = at - t * p.experts;
         const unsigned long long *of = key + t * p.experts, mine = of[e];
-        int ahead = 0;
+        int count = 0;
 #pragma unroll 4
-        for (int j = 0; j < p.experts; ++j) ahead += of[j] > mine || (of[j] == mine && j < e);
-        if (ahead < p.k) chosen[t * p.k + ahead] = (unsigned short)e;
+        for (int j = part * per; j < min(p.experts, (part + 1) * per); ++j) count += of[j] > mine || (of[j] == mine && j < e);
+        atomicAdd(ahead + at, count);
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += kMoeThreads)
+        if (ahead[i] < p.k) chosen[i / p.experts * p.k + ahead[i]] = (unsigned short)(i % p.experts);
+    __syncthreads();
 }
 // A token's weights, and what is told of its choices, by a warp.
 __device__ __forceinline__ void moe_weights(const MoeArgs &p, int t, const unsigned long long *key, const unsigned short *chosen) {
@@ -270,11 +273,46 @@ __device__ __forceinline__ void moe_weights(const MoeArgs &p, int t, const unsig
 struct MoeRoute {
     unsigned short chosen[kMoeMaxPairs], place[kMoeMaxPairs], count[kMoeThreads / 32][kMoeMaxExperts];
     unsigned long long key[kMoeByToken][kMoeMaxExperts];  // logits
+    int ahead[kMoeByToken * kMoeMaxExperts];
 };
 static_assert(sizeof(MoeRoute) <= kMoeRing, "the choices lie in the ring until it is used");
 template <int G>
 __device__ __forceinline__ void moe_route(const MoeArgs &p, MoeShared &sh, MoeRoute &r) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = p.n * p.k;
+    if (pairs <= 32) {  // a lane a pair; only the entries of chosen experts are written, and read
+        if (warp == 0) {
+            const int e = lane < pairs ? r.chosen[lane] : 0x7fffffff;
+            int at = 0, behind = 0;
+            bool head = true;
+            for (int j = 0; j < pairs; ++j) {
+                const int o = __shfl_sync(0xffffffffu, e, j);
+                at += o < e || (o == e && j < lane);
+                behind += o == e;
+                head &= o != e || j >= lane;
+            }
+            // heads in the order of their places: jobs (a pair's expert has one: at most 32 tokens, G at a time)
+            int job = 0;
+            for (int j = 0; j < pairs; ++j) {
+                const int o = __shfl_sync(0xffffffffu, e, j), n = __shfl_sync(0xffffffffu, behind, j);
+                const bool h = __shfl_sync(0xffffffffu, (int)head, j);
+                if (h && o < e) job += (n + G - 1) / G;
+            }
+            if (lane < pairs) sh.list[at] = (unsigned short)lane;
+            const int jobs = (behind + G - 1) / G;
+            __syncwarp();
+            if (lane < pairs && head) {
+                sh.offset[e] = at;
+                sh.offset[e + 1] = at + behind;
+                sh.jobs[e] = job;
+                sh.jobs[e + 1] = job + jobs;
+                for (int i = 0; i < jobs; ++i) sh.job_expert[job + i] = (unsigned short)e;
+            }
+            const int total = __reduce_max_sync(0xffffffffu, lane < pairs ? job + jobs : 0);
+            if (lane == 0) sh.jobs[p.experts] = total;
+        }
+        __syncthreads();
+        return;
+    }
     const int per = (pairs + kMoeThreads - 1) / kMoeThreads * 32;  // pairs of a warp
     for (int e = lane; e < p.experts; e += 32) r.count[warp][e] = 0;
     __syncwarp();
@@ -776,12 +814,8 @@ __device__ __forceinline__ void moe_sums(const MoeArgs &p, MoeShared &sh, const 
             int *counter = p.counters + (DOWN ? gridDim.x : 0) + first;
             named_sync(1 + wg, 128);
             if (f == 0) {
-                __threadfence();  // for what the whole warpgroup wrote
-                const bool is = atomicAdd(counter, 1) == last - first;
-                if (is) {
-                    *counter = 0;
-                    __threadfence();
-                }
+                const bool is = stream_count(counter) == last - first;
+                if (is) *counter = 0;
                 sh.last[wg] = is;
             }
             named_sync(1 + wg, 128);
@@ -876,11 +910,26 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
     }
     const bool by_token = p.n <= kMoeByToken;
     const int gw = blockIdx.x * (kMoeThreads / 32) + warp, gn = gridDim.x * (kMoeThreads / 32);
-    if (p.n == 1) {
-        for (int i = gw; i < p.experts * p.splits; i += gn) moe_logits<1>(p, i / p.splits, 0, i % p.splits);
+    if (by_token) {  // a CTA an expert and up to four tokens, its warps' parts added here
+        const int parts = kMoeThreads / 32;
+        float2(&part)[2][kMoeThreads / 32][4] = *reinterpret_cast<float2(*)[2][kMoeThreads / 32][4]>(ring_p);
+        for (int i = blockIdx.x, odd = 0; i < (p.n + 3) / 4 * p.experts; i += gridDim.x, odd ^= 1) {
+            const int e = i % p.experts, t0 = i / p.experts * 4;
+            if (p.n == 1) moe_logits<1>(p, e, t0, warp, parts, part[odd][warp], 1);
+            else moe_logits<4>(p, e, t0, warp, parts, part[odd][warp], 1);
+            __syncthreads();
+            if (threadIdx.x < min(4, p.n - t0)) {
+                float2 v = part[odd][0][threadIdx.x];
+                for (int w = 1; w < parts; ++w) moe_add2(v.x, v.y, part[odd][w][threadIdx.x].x, part[odd][w][threadIdx.x].y);
+                p.logits[(long long)(t0 + threadIdx.x) * p.experts + e] = v;
+            }
+        }
     } else {
         const int each = p.experts * p.splits;
-        for (int i = gw; i < (p.n + 3) / 4 * each; i += gn) moe_logits<4>(p, i % each / p.splits, i / each * 4, i % p.splits);
+        for (int i = gw; i < (p.n + 3) / 4 * each; i += gn) {
+            const int e = i % each / p.splits, t0 = i / each * 4, split = i % p.splits;
+            moe_logits<4>(p, e, t0, split, p.splits, p.logits + ((long long)split * p.n + t0) * p.experts + e, p.experts);
+        }
     }
     if (by_token) {
         moe_split_x<W8, C::kX>(p, nullptr, p.n);
@@ -896,15 +945,13 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
         if (by_token) {
             moe_keys(p, 0, p.n, route.key[0], threadIdx.x, kMoeThreads);
             __syncthreads();
-            moe_choose(p, p.n, route.key[0], route.chosen, threadIdx.x, kMoeThreads);
-            __syncthreads();
+            moe_choose(p, p.n, route.key[0], route.ahead, route.chosen);
             if (blockIdx.x == 0 && warp < p.n) moe_weights(p, warp, route.key[0] + warp * p.experts, route.chosen + warp * p.k);
         } else {  // a token's by one CTA, for all
             for (int t = blockIdx.x; t < p.n; t += gridDim.x) {
                 moe_keys(p, t, 1, route.key[0], threadIdx.x, kMoeThreads);
                 __syncthreads();
-                moe_choose(p, 1, route.key[0], route.chosen, threadIdx.x, kMoeThreads);
-                __syncthreads();
+                moe_choose(p, 1, route.key[0], route.ahead, route.chosen);
                 if (warp == 0) moe_weights(p, t, route.key[0], route.chosen);
                 if (threadIdx.x < p.k) p.choices[t * p.k + threadIdx.x] = route.chosen[threadIdx.x];
                 __syncthreads();
@@ -1018,7 +1065,7 @@ static MoeSpace moe_space(int64_t n, int64_t d, int64_t ff, int64_t experts, int
     s.bars = take(256);
     s.counters = take(2 * g * 4);
     s.parts = take(g * 4 * kMoeSums * 4);
-    s.splits = moe_logits_plan(n, d, experts, sm_count() * (kMoeThreads / 32)).splits;
+    s.splits = moe_splits(n, d, experts, sm_count() * (kMoeThreads / 32));
     s.logits = take((size_t)(n * experts) * s.splits * 8);
     s.choices = take(pairs * 2);
     s.wts = take(pairs * 4);
@@ -1063,7 +1110,7 @@ using namespace ds;
 static int moe_sizes(int64_t n, int64_t d, int64_t ff, int n_experts, int top_k) {
     if (n < 1 || d < 1 || ff < 1 || n_experts < 1 || top_k < 1) return DS_EMPTY_DIMENSION;
     if (n > kMoeMaxTokens || n_experts > kMoeMaxExperts || top_k > kMoeMaxK || d > DS_MAX_DIM || ff > DS_MAX_DIM) return DS_DIMENSION_TOO_LARGE;
-    if (d * ff * 2 * n_experts > (int64_t)1 << 42) return DS_DIMENSION_TOO_LARGE;
+    if (d * ff > ((int64_t)1 << 38) / n_experts) return DS_DIMENSION_TOO_LARGE;  // past any memory, and a copy's strides
     return DS_OK;
 }
 

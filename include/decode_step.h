@@ -253,8 +253,8 @@ DS_API size_t ds_gemm_fp8_workspace_bytes(int64_t n, int64_t rows, int64_t cols)
  *   dimension or stride.  A NaN code or scale reaches the outputs whose sums
  *   it is part of and no other.
  *   workspace: ds_gemm_fp8_workspace_bytes(n, rows, cols) bytes, 256-byte
- *   aligned, zeroed before first use; calls whose GPU work may overlap need
- *   one each. */
+ *   aligned, zeroed before first use (and again after a DS_ERR_WAIT_TIMEOUT);
+ *   calls whose GPU work may overlap need one each. */
 DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride, const float *w_scales,
                        int64_t w_scales_len, const void *X, int64_t x_len, int64_t x_stride,
                        const float *x_scales, int64_t x_scales_len, int64_t n, int64_t rows, int64_t cols,
@@ -288,8 +288,8 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   128)] (NULL and 0 with bf16).  569 for a weight's or scale's length.
  *   expert_ids, expert_weights: e_i and p_i [n][top_k], either may be NULL.
  * Logits are exact to some 45 bits, the choice of experts that of 64-bit
- * arithmetic; everything else is fp32, rounded once.  A bf16 y sees an
- * intermediate of 16 bits at least.  Weights are finite; a value of x that is
+ * arithmetic; products, sums and the intermediate are fp32's (24 bits of every
+ * factor), y is rounded once.  A bf16 y sees an intermediate of 16 bits.  Weights are finite; a value of x that is
  * not, or a product that overflows fp32, makes outputs of its own token (and
  * of no other) NaN or infinite.
  *   n <= 256, n_experts <= 512, top_k <= 16 (564), top_k <= n_experts (577);
@@ -297,8 +297,9 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   router and the experts' matrices 16-byte aligned (577).  y may be x or
  *   residual itself; otherwise no output overlaps an input or another output
  *   (577).  workspace: ds_moe_layer_workspace_bytes(...) bytes, 256-byte
- *   aligned, zeroed before first use; calls whose GPU work may overlap need
- *   one each.  A cooperative launch: it starts when the whole GPU is free. */
+ *   aligned, zeroed before first use (and again after a DS_ERR_WAIT_TIMEOUT);
+ *   calls whose GPU work may overlap need one each.  A cooperative launch: its
+ *   blocks wait for one another, so it runs when every SM has room for one. */
 DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, int64_t n, int64_t d,
                         const void *w_router, int64_t router_len, int router_dtype, int n_experts,
                         int top_k, int renormalize, const void *w_gate_up, int64_t gate_up_len,
