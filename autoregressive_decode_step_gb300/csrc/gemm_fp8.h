@@ -23,13 +23,15 @@ struct F8Args {
 };
 
 // The split tiles' steps are cut into runs, one a CTA (a pair), of four steps at
-// least: of fewer, joining what they leave takes longer than they do (333 rows
-// by 1,000 x 1,416 in runs of one or two: 21 us, of four 13).  `most`: runs that
-// meet in a tile at most, where one CTA adds them up.  Steps times runs stay
-// below 2^32: fewer split tiles than CTAs, 2^17 steps a tile.
+// least, or a tile's if it has fewer: joining what shorter ones leave takes
+// longer than they do (333 rows by 1,000 x 1,416 in runs of one or two: 21 us,
+// of four 11).  `most`: runs that meet in a tile at most, where one CTA adds them
+// up.  Steps times runs stay below 2^32: fewer split tiles than CTAs, 2^17 steps
+// a tile.
 __host__ __device__ inline unsigned f8_runs(int split, int kb, int grid, int most) {
     const long long w = (long long)split * kb;
-    long long r = w / 4 < grid ? w / 4 : grid;
+    long long r = w / 4 < split ? split : w / 4;
+    if (r > grid) r = grid;
     if (most && r > (long long)split * (most - 1)) r = (long long)split * (most - 1);
     return r < 1 ? 1u : (unsigned)r;
 }
