@@ -9,8 +9,7 @@
 // Sixteen threads hold a block's row, eight values each: one 16-byte load of
 // bf16 (two of fp32), a maximum over four shuffles, one 8-byte store.  The
 // values stay in registers between the maximum and the rounding, so each is
-// read once.  A 128 x 128 block is one CTA of sixteen such groups, eight rows
-// each.
+// read once.
 #include "common.cuh"
 #include "internal.h"
 
@@ -20,6 +19,7 @@ namespace ds {
 
 constexpr int kFqThreads = 256;
 constexpr int kFqGroups = kFqThreads / 16;  // rows of a block worked on at a time
+constexpr int kFqBlockThreads = 1024;         // of a 128 x 128 block
 constexpr int kFqCtas = 4;                   // at a time on an SM
 constexpr float kFqTiny = 0x1p-96f;         // least maximum: 448 / top and the scale stay normal numbers
 
@@ -68,17 +68,22 @@ struct FqRaw<float> {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
 };
-// From column c of a row on, zeros behind its end; VEC: 16 bytes at a time.
-template <typename T, bool VEC>
-__device__ __forceinline__ void fq_load(FqRaw<T> &r, const T *row, int c, int cols) {
-    if (VEC && c + 8 <= cols) {
-        r.load(row + c);
-        return;
-    }
+// From column c of a row on, zeros behind its end, value by value.  (Functions of
+// their own where a path is rare or long: its code is then fetched once, and a
+// small call's time is fetching code.)
+template <typename T>
+__device__ __noinline__ FqRaw<T> fq_load_slow(const T *row, int c, int cols) {
+    FqRaw<T> r;
     r.zero();
 #pragma unroll
     for (int i = 0; i < 8; ++i)
         if (c + i < cols) r.set(i, row[c + i]);
+    return r;
+}
+template <typename T, bool VEC>
+__device__ __forceinline__ void fq_load(FqRaw<T> &r, const T *row, int c, int cols) {
+    if (VEC && c + 8 <= cols) r.load(row + c);
+    else r = fq_load_slow<T>(row, c, cols);
 }
 
 // A block's maximum from its bits; NaN for one that holds a NaN or an infinity.
@@ -92,19 +97,11 @@ __device__ __forceinline__ unsigned fq_pair(float a, float b) {  // a in the low
     return r;
 }
 
-// Codes from column c of a row on: eight bytes a thread, or where rows do not
-// start on 8 bytes sixteen neighbouring bytes of the sixteen threads at a time.
-template <typename T>
-__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const FqRaw<T> &r, float factor, bool q8) {
-    float v[8];
-    r.get(v);
-    const unsigned lo = fq_pair(v[0] * factor, v[1] * factor) | fq_pair(v[2] * factor, v[3] * factor) << 16;
-    const unsigned hi = fq_pair(v[4] * factor, v[5] * factor) | fq_pair(v[6] * factor, v[7] * factor) << 16;
-    if (q8 && c + 8 <= cols) {
-        *reinterpret_cast<uint2 *>(row + c) = make_uint2(lo, hi);
-        return;
-    }
-    if (q8) {  // a row's end
+// Eight codes from column c of a row on that are not eight bytes at once: a row's
+// end, or (q8 false) rows that do not start on 8 bytes, where the sixteen threads
+// store sixteen neighbouring bytes at a time.
+__device__ __noinline__ void fq_store_slow(unsigned char *row, int c, int cols, unsigned lo, unsigned hi, bool q8) {
+    if (q8) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
             if (c + i < cols) row[c + i] = (unsigned char)((i < 4 ? lo : hi) >> (8 * (i & 3)));
@@ -117,6 +114,15 @@ __device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, co
         const unsigned a = __shfl_sync(0xffffu << half, lo, from), b = __shfl_sync(0xffffu << half, hi, from);
         if (c0 + 16 * i + lane < cols) row[c0 + 16 * i + lane] = (unsigned char)((lane & 4 ? b : a) >> (8 * (lane & 3)));
     }
+}
+template <typename T>
+__device__ __forceinline__ void fq_store(unsigned char *row, int c, int cols, const FqRaw<T> &r, float factor, bool q8) {
+    float v[8];
+    r.get(v);
+    const unsigned lo = fq_pair(v[0] * factor, v[1] * factor) | fq_pair(v[2] * factor, v[3] * factor) << 16;
+    const unsigned hi = fq_pair(v[4] * factor, v[5] * factor) | fq_pair(v[6] * factor, v[7] * factor) << 16;
+    if (q8 && c + 8 <= cols) *reinterpret_cast<uint2 *>(row + c) = make_uint2(lo, hi);
+    else fq_store_slow(row, c, cols, lo, hi, q8);
 }
 
 // Blocks of 1 x 128: a group of sixteen threads takes block after block, U of
@@ -168,11 +174,13 @@ __global__ __launch_bounds__(kFqThreads, kFqCtas) void fp8_rows_kernel(const FqA
     }
 }
 
-// Blocks of 128 x 128, a CTA each.
+// Blocks of 128 x 128, a CTA of 64 groups each, two rows a group (of sixteen
+// groups, eight rows each: 4,099 x 1,001 bf16 8.4 us, the loads' latency one row
+// after another).
 template <typename T, bool VEC>
-__global__ __launch_bounds__(kFqThreads) void fp8_blocks_kernel(const FqArgs p) {
-    constexpr int kRows = 128 / kFqGroups;
-    __shared__ unsigned tops[kFqThreads / 32];
+__global__ __launch_bounds__(kFqBlockThreads) void fp8_blocks_kernel(const FqArgs p) {
+    constexpr int kGroups = kFqBlockThreads / 16, kRows = 128 / kGroups;
+    __shared__ unsigned tops[kFqBlockThreads / 32];
     allow_dependent_launch();
     grid_dependency_wait();
     const int lane = threadIdx.x & 15, r0 = (int)(blockIdx.x / p.kb) * 128 + (threadIdx.x >> 4), c = (int)(blockIdx.x % p.kb) * 128 + lane * 8;
@@ -180,19 +188,20 @@ __global__ __launch_bounds__(kFqThreads) void fp8_blocks_kernel(const FqArgs p) 
     unsigned top = 0;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const int r = r0 + i * kFqGroups;
+        const int r = r0 + i * kGroups;
         fq_load<T, VEC>(v[i], static_cast<const T *>(p.x) + (long long)min(r, p.rows - 1) * p.ldx, c, r < p.rows ? p.cols : 0);
         top = max(top, v[i].top());
     }
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kFqThreads / 32; ++i) top = max(top, tops[i]);
+    top = __reduce_max_sync(0xffffffffu, tops[threadIdx.x & 31]);
     const float t = fq_top(top), factor = __fdiv_rn(448.0f, t);
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-        if (r0 + i * kFqGroups < p.rows) fq_store<T>(p.q + (long long)(r0 + i * kFqGroups) * p.ldq, c, p.cols, v[i], factor, p.q8);
+    for (int i = 0; i < kRows; ++i) {
+        const int r = r0 + i * kGroups;
+        if (r < p.rows) fq_store<T>(p.q + (long long)r * p.ldq, c, p.cols, v[i], factor, p.q8);
+    }
     if (threadIdx.x == 0) p.scales[blockIdx.x] = __fdiv_rn(t, 448.0f);
 }
 
@@ -200,7 +209,7 @@ template <typename T, bool VEC>
 static cudaError_t fq_launch(const FqArgs &a, int block_rows, cudaStream_t s) {
     if (block_rows == 128) {
         const long long grid = (long long)((a.rows + 127) / 128) * a.kb;
-        return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqThreads), 0, s, true, a);
+        return launch_ex(fp8_blocks_kernel<T, VEC>, dim3((unsigned)grid), dim3(kFqBlockThreads), 0, s, true, a);
     }
     const long long groups = ((long long)a.rows * a.kb + kFqGroups - 1) / kFqGroups, most = (long long)kFqCtas * sm_count();
     const bool dense = VEC && a.q8 && a.cols % 128 == 0 && a.ldx == a.cols && a.ldq == a.cols;

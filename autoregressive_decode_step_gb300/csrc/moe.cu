@@ -52,6 +52,7 @@ constexpr int kMoeWeightBytes = 2 * 128 * 128;  // of a step
 constexpr int kMoeRing = 200 * 1024;  // four stages with 128 columns, five with 64 or 32
 constexpr int kMoeSlots = 8;  // steps' scales ahead
 constexpr int kMoeBatch = 16; // steps between two sums of bf16 products
+constexpr int kMoeAtOnce = 2; // partial sums of a cut tile under way at a time
 constexpr int kMoeSums = 2 * kMoeGroup * 128;  // floats of a tile
 
 // How many pieces an activation and the intermediate are cut into, and how many
@@ -480,10 +481,12 @@ struct MoeLine {
     __device__ MoeLine(int jobs, int tiles_, int steps_) : tiles(tiles_), steps(steps_) {
         total = (long long)jobs * tiles * steps;
         runs = (int)min((long long)gridDim.x, total);
-        s0 = total * min((int)blockIdx.x, runs) / runs;
-        s1 = total * min((int)blockIdx.x + 1, runs) / runs;
+        s0 = quotient(total * min((int)blockIdx.x, runs), runs);
+        s1 = quotient(total * min((int)blockIdx.x + 1, runs), runs);
     }
-    __device__ int holder(long long s) const { return (int)(((s + 1) * runs - 1) / total); }
+    __device__ int holder(long long s) const { return (int)quotient((s + 1) * runs - 1, total); }
+    // (64-bit divisions take some 500 cycles each)
+    __device__ static long long quotient(long long a, long long b) { return a >> 32 ? a / b : (long long)((unsigned)a / (unsigned)b); }
 };
 struct MoeTile {
     int expert, tile, start, count;  // its pairs: list[start ...]
@@ -723,6 +726,9 @@ __device__ __forceinline__ void moe_scales(const MoeArgs &p, MoeShared &sh, cons
     }
 }
 
+// silu(gate) * up; a function of its own, so that its code is fetched once.
+__device__ __noinline__ float moe_act(float gate, float up) { return gate / (1.0f + expf(-gate)) * up; }
+
 template <int N>
 __device__ __forceinline__ void moe_ld(uint32_t t, float *v) {
     if constexpr (N == 24) {
@@ -825,13 +831,21 @@ __device__ __forceinline__ void moe_sums(const MoeArgs &p, MoeShared &sh, const 
             float a[8], b[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) a[i] = b[i] = 0.0f;
-            for (int c = first; c <= last; ++c) {  // in CTA order
-                const float *part = p.parts + ((size_t)c * 4 + (whole ? 2 + wg : c == first)) * kMoeSums + j * 1024 + f;
-                float v[8], w[8];
+            const float *parts = p.parts + (size_t)first * 4 * kMoeSums + j * 1024 + f;
+            for (int c = 0; c <= last - first; c += kMoeAtOnce) {  // in CTA order, several requested together
+                float v[kMoeAtOnce][16];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) v[i] = __ldcg(part + i * 128), w[i] = __ldcg(part + (kMoeGroup + i) * 128);
+                for (int q = 0; q < kMoeAtOnce; ++q) {
+                    const int k = min(c + q, last - first);
+                    const float *part = parts + (size_t)(4 * k + (whole ? 2 + wg : k == 0)) * kMoeSums;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) a[i] += v[i], b[i] += w[i];
+                    for (int i = 0; i < 8; ++i) v[q][i] = __ldcg(part + i * 128), v[q][8 + i] = __ldcg(part + (kMoeGroup + i) * 128);
+                }
+#pragma unroll
+                for (int q = 0; q < kMoeAtOnce; ++q)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (c + q <= last - first) a[i] += v[q][i], b[i] += v[q][8 + i];
             }
             if (DOWN) {
                 const int row = t.tile * 256 + f;
@@ -848,8 +862,7 @@ __device__ __forceinline__ void moe_sums(const MoeArgs &p, MoeShared &sh, const 
             constexpr int E = W8 ? 1 : 2;
             const int feature = t.tile * 128 + f;
             const size_t step = (size_t)p.n * p.k * p.ff * E;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) a[i] = a[i] / (1.0f + expf(-a[i])) * b[i];
+            for (int i = 0; i < 8; ++i) a[i] = moe_act(a[i], b[i]);
             if (W8) {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
@@ -1020,6 +1033,7 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
                 const int tok = (int)(i / quads), j = (int)(i - (long long)tok * quads) * 4;
                 const long long at = (long long)tok * p.d + j;
                 float4 v = make_float4(0, 0, 0, 0);
+#pragma unroll 2
                 for (int c = 0; c < p.k; ++c) {
                     const long long pair = (long long)tok * p.k + c;
                     const float w = __ldcg(p.wts + pair);
