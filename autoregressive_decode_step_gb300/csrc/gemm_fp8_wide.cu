@@ -8,14 +8,18 @@
 // against 64 bytes a cycle from L2; alone it would fetch 48 KB.
 //
 // A row's scale and its block of 128 features' make one factor a thread and
-// step, so the sums cost one packed multiply-add per two columns: four
-// warpgroups take 64 columns each out of TMEM, add them to registers and free
-// the buffer before they do, so that two buffers keep the tensor cores busy.
-// Rows are lanes, so a thread's outputs are 64 neighbours of one row, stored 32
-// bytes at a time.
+// step, so the sums cost one packed multiply-add per two columns.  Two warps issue
+// the products of half a step each (64 of either SM's features: 128 columns of
+// TMEM, four buffers); four warpgroups take 64 columns each out of TMEM, add
+// them to registers and free the buffer before they do.
 //
 // Tiles are dealt out whole, one a pair and round; what is left over is cut into
 // equal runs of steps whose partial sums a second launch adds in order.
+//
+// Measured in a graph: 8,192 rows by 28,672 x 4,096 690 us (2.79 PFLOP/s, 1.46 of
+// the measured bf16 rate; on values of a wide spread 790 us at the power limit),
+// the tensor pipe active 61 % of the cycles (the issue slots 54 %: half of it the
+// sums); 256 by 4,096 x 14,336 27 us, 8 of them joining six partial sums a tile.
 #include <algorithm>
 #include <atomic>
 

@@ -59,21 +59,28 @@ class Layer:
         gu, dn = self.widened()
         y = torch.zeros_like(x) if self.residual is None else self.residual.double()
         far = 2.0 ** -24 * y.abs()
-        # a 22-bit piece pair of fp32 values before e4m3 weights, 16 bits of an intermediate before a bf16 output
-        piece = 2.0 ** -22 if self.gs is not None else 0.0
-        mid = 2.0 ** -16 if self.x.dtype == BF16 and self.gs is None else piece
+        # pieces: 24 bits of fp32 values, 16 of an intermediate before a bf16 output; before e4m3 weights no more than
+        # a share of the largest of 128 (six pieces of a sixteenth each from 2^-10 on, beside 2^7: 2^-37, and so on)
+        half = self.x.dtype == BF16
+        piece, mid = 2.0 ** -24, 2.0 ** -16 if half else 2.0 ** -24
+        tiny, tiny_mid = (0.0, 0.0) if self.gs is None else (2.0 ** -25, 2.0 ** -29) if half else (2.0 ** -37, 2.0 ** -37)
+
+        def largest(v):
+            b = torch.nn.functional.pad(v.abs(), (0, -v.shape[1] % 128)).view(len(v), -1, 128).amax(2)
+            return b.repeat_interleave(128, 1)[:, :v.shape[1]]
         for s in range(self.k):
             for e in ids[:, s].unique():
                 at = (ids[:, s] == e).nonzero()[:, 0]
                 a, g, u, w = x[at], gu[e, 0], gu[e, 1], dn[e]
                 gate, up = a @ g.t(), a @ u.t()
-                dg = ((self.d + 16) * U + piece) * (a.abs() @ g.abs().t())
-                du = ((self.d + 16) * U + piece) * (a.abs() @ u.abs().t())
+                off = ((self.d + 16) * U + piece) * a.abs() + tiny * largest(a)
+                dg, du = off @ g.abs().t(), off @ u.abs().t()
                 act = gate * torch.sigmoid(gate)
                 h = act * up
                 # silu's slope is at most 1.1; exp, division and products round six times.  A product below
                 # 2^-126 (a token of 1e-30 has gate and up of some 1e-26 each, so 1e-52) may become 0 in fp32.
                 dh = 1.1 * dg * (up.abs() + du) + act.abs() * du + (6 * U + mid) * h.abs() + 2.0 ** -126
+                dh = dh + tiny_mid * largest(h.abs() + dh)
                 o = h @ w.t()
                 do = dh @ w.abs().t() + (self.ff + 16) * U * ((h.abs() + dh) @ w.abs().t())
                 q = p[at, s][:, None]
@@ -135,10 +142,11 @@ def test_layer_digits(abi, w):
         Layer(40, 16, 16, 4, 2, w=w, seed=seed).check(abi)
 
 
-def test_layer_sizes_within_a_block(abi):
+@pytest.mark.parametrize("x", [F32, BF16])
+def test_layer_sizes_within_a_block(abi, x):
     """e4m3 experts, activations of very different sizes within 128 values, a zero token, a large one."""
-    a = Layer(6, 256, 128, 4, 2, w=E4M3, seed=9)
-    a.x *= torch.exp(4 * torch.randn(256, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda"))
+    a = Layer(6, 256, 128, 4, 2, x=x, w=E4M3, seed=9)
+    a.x *= torch.exp(4 * torch.randn(256, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda")).to(x)
     a.x[2] = 0
     a.x[3] *= 1e-30
     a.x[4] *= 1e4
