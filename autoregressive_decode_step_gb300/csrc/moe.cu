@@ -26,13 +26,13 @@
 // three for bf16 (two hold its 8 bits; the third those of values below 2^-14 of
 // the largest, to 2^-26 of it).  The intermediate is fp32 and goes in three bf16
 // or six e4m3 pieces, before bf16 outputs in two or four (16 bits).  Sums leave
-// the tensor core every 1,024 products (e4m3: every block of 128, for its scale)
-// and are fp32.  The logits are sums of exact products with their rounding errors
+// the tensor core every 128 products (e4m3: a block, for its scale; bf16: see
+// kMoeBatch) and are fp32.  The logits are sums of exact products with their rounding errors
 // carried along (two floats, added up in 64 bits): the choice of experts is that
 // of 64 bits.
 //
 // Measured in a graph: 64 tokens through 2 of 8 experts of 4,096 x 14,336 (fp32,
-// bf16 weights) 476 us, 5.9 TB/s of 6.8; 64 through 8 of 128 of 2,048 x 768 (bf16,
+// bf16 weights) 477 us, 5.9 TB/s of 6.8; 64 through 8 of 128 of 2,048 x 768 (bf16,
 // e4m3) 137 us, 4.4 TB/s; one token through those in bf16 37 us, 2.1 TB/s: some 20
 // us are the phases' latencies (a layer of no size takes 21), 6 of them the ends of
 // the two products (partial sums out, counted, read, and code that runs once: some
@@ -60,7 +60,11 @@ constexpr int kMoeMaxStages = 5;
 constexpr int kMoeWeightBytes = 2 * 128 * 128;  // of a step
 constexpr int kMoeRing = 200 * 1024;  // four stages with 128 columns, five with 64 or 32
 constexpr int kMoeSlots = 8;  // steps' scales ahead
-constexpr int kMoeBatch = 16; // steps between two sums of bf16 products
+// Steps between two sums of bf16 products in registers.  The tensor cores cut an
+// fp32 sum's low bits off at every addition, always towards zero, so a long run of
+// them drifts: 64 fp32 tokens, 8 experts of 14336, are 3.2e-6 off the exact result
+// with 16 steps, 8e-7 with 4 and 5e-7 with 2, at 475, 477 and 477 us.
+constexpr int kMoeBatch = 2;
 constexpr int kMoeAtOnce = 2; // partial sums of a cut tile under way at a time
 constexpr int kMoeSums = 2 * kMoeGroup * 128;  // floats of a tile
 
