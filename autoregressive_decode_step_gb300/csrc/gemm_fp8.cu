@@ -9,20 +9,21 @@
 // (gemm_fp8_wide.cu: more).  A tile is 128 features (an MMA's M: lane r of TMEM
 // is feature r), for more than 32 rows 256 in two halves, by all the rows of X,
 // rounded up to 16, 32, 64 or 128 (the MMA's N): one token costs 16 columns.
-// All tiles' steps are one line, cut into equal runs, one a CTA, so that every SM
-// streams the same bytes; a cut tile's partial sums meet in the workspace and are
-// added in CTA order by whichever CTA arrives last (a second launch for the wider
-// ones took 12 us of 35 with 64 rows by 28,672 x 4,096).  No CTA waits for
+// Tiles, or equal runs of their steps (f8_runs), go one to a CTA; a cut tile's
+// partial sums meet in the workspace and are added in CTA order by whichever CTA
+// arrives last (a second launch for the wider ones took 12 us of 35 with 64 rows
+// by 28,672 x 4,096).  No CTA waits for
 // another.  A launch may begin while the one in front ends.
 //
 // A step brings its weights in one copy (16 KB for few rows, where the runs are
 // short and even ones count: one token 9.9 us against 11.2; else 32 KB: 64 rows by
-// 28,672 x 4,096 29 us against 33), and up to four steps' columns are a batch:
+// 28,672 x 4,096 29 us against 33, in equal runs), and up to four steps' columns are a batch:
 // barriers and the latency of TMEM are paid once a batch.  A warpgroup for each
 // half of the features adds it up.
 //
-// Measured in a graph: one token through 6,144 x 4,096 8.8 us (2.9 TB/s: ten steps,
-// the rest start and end), 64 through 28,672 x 4,096 29.7 us (4.1 TB/s), 128 35 us.
+// Measured in a graph: one token through 6,144 x 4,096 7.7 us (3.3 TB/s: eleven
+// steps, the rest start and end), 64 through 28,672 x 4,096 22.6 us (5.4 TB/s), 128
+// 27 us.
 #include <algorithm>
 #include <atomic>
 
@@ -305,22 +306,22 @@ static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
         t.n_tiles = (int)((n + kF8WideRows - 1) / kF8WideRows);
         tiles = (int64_t)t.m_tiles * t.n_tiles;
         t.grid = f8_wide_pairs();
-        t.rounds = (int)(tiles / t.grid);
     } else {
         t.bn = 16;
         while (t.bn < n) t.bn *= 2;
         const int m = t.bn <= 32 ? F8Cfg<32>::kM : F8Cfg<64>::kM;
         tiles = t.m_tiles = (int)((rows + m - 1) / m);
         t.n_tiles = 1;
-        t.grid = (int)std::min<int64_t>(sm_count(), std::max(tiles, tiles * kb / 4));
-        t.rounds = (int)(tiles / t.grid);
+        t.grid = sm_count();
     }
+    t.rounds = (int)(tiles / t.grid);
     t.split = (int)(tiles - (int64_t)t.rounds * t.grid);
-    t.runs = f8_runs(t.split, (int)kb, t.grid, t.wide ? 0 : 512 / t.bn);
+    t.runs = f8_runs(t.split, (int)kb, t.grid, t.bn);
+    if (t.rounds == 0) t.grid = (int)t.runs;
     return t;
 }
 static size_t f8_ws_bytes(const F8Plan &t) {
-    const size_t floats = t.wide ? f8_wide_partial_floats(t.split) : t.split ? ((size_t)t.grid + t.split) * t.bn * F8Cfg<64>::kM : 0;
+    const size_t floats = t.wide ? f8_wide_partial_floats(t.split, t.runs) : f8_cut(t.split, t.runs) ? ((size_t)t.runs + t.split) * t.bn * F8Cfg<64>::kM : 0;
     return kWsHeader + align_up((size_t)sm_count() * 4, 256) + floats * 4;
 }
 
@@ -401,7 +402,7 @@ extern "C" DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride
         !encode_tiled_2d(&a.tx, X, DS_E4M3, cols, n, x_stride, kF8K, t.wide ? 128 : t.bn, true))
         return DS_CUDA_ERROR;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = t.wide ? f8_wide_launch(a, s) : t.bn == 16 ? f8_launch<16>(a, t, s) : t.bn == 32 ? f8_launch<32>(a, t, s)
+    const cudaError_t e = t.wide ? f8_wide_launch(a, t.grid, s) : t.bn == 16 ? f8_launch<16>(a, t, s) : t.bn == 32 ? f8_launch<32>(a, t, s)
                         : t.bn == 64 ? f8_launch<64>(a, t, s) : f8_launch<128>(a, t, s);
     return e == cudaSuccess ? DS_OK : DS_CUDA_ERROR;
 }

@@ -6,6 +6,8 @@
 
 namespace ds {
 
+constexpr int kF8WideRows = 256, kF8WideFeatures = 256;  // a pair's tile
+
 struct F8Args {
     CUtensorMap tw, tx;  // bytes, boxes {128, a tile's features} and {128, bn} (wide: {128, 128} both), 128-byte swizzle
     const float *ws, *xs;
@@ -22,19 +24,34 @@ struct F8Args {
     int *err;
 };
 
-// The split tiles' steps are cut into runs, one a CTA (a pair), of four steps at
-// least, or a tile's if it has fewer: joining what shorter ones leave takes
-// longer than they do (333 rows by 1,000 x 1,416 in runs of one or two: 21 us,
-// of four 11).  `most`: runs that meet in a tile at most, where one CTA adds them
-// up.  Steps times runs stay below 2^32: fewer split tiles than CTAs, 2^17 steps
-// a tile.
-__host__ __device__ inline unsigned f8_runs(int split, int kb, int grid, int most) {
-    const long long w = (long long)split * kb;
-    long long r = w / 4 < split ? split : w / 4;
-    if (r > grid) r = grid;
-    if (most && r > (long long)split * (most - 1)) r = (long long)split * (most - 1);
-    return r < 1 ? 1u : (unsigned)r;
+// The split tiles' steps are cut into runs, one a CTA (a pair): as many a tile as
+// cost least, counted in steps.  A tile in one run costs its steps; cut, the
+// partial sums' way out, their counting and their joining take as long as some
+// twelve steps (with the pairs' second launch 18, and a sixth for each run), and
+// more for every few that are joined: 64 rows by 4,096 x 4,096 take 15.6 us with
+// one run a tile, 12.0 with three, 15.2 with seven.  Runs of equal length without
+// regard to the tiles leave most CTAs the parts of two, with an end and a partial
+// sum each: 64 rows by 28,672 x 4,096 take 29.9 us like that, with 112 CTAs of 152
+// and a tile each 22.5; 28,672 x 1,024 15.7 and 8.1.  They pay where whole tiles
+// would leave many SMs idle for long.  Steps times runs stay below 2^32: fewer
+// split tiles than CTAs, 2^17 steps a tile.
+inline unsigned f8_runs(int split, int kb, int ctas, int bn) {
+    if (split == 0) return 1;
+    const auto join = [&](int m) {  // of m partial sums a tile
+        return bn == kF8WideFeatures ? 18 + split * m / 6 + 9 * ((m - 1) / 6) : bn >= 64 ? 12 + 7 * ((m - 1) / 3) : 12 + 3 * ((m - 1) / 4);
+    };
+    unsigned best = (unsigned)split;
+    int least = kb;
+    for (int m = 2; m <= kb && m * split <= ctas; ++m) {
+        const int cost = (kb + m - 1) / m + join(m);
+        if (cost < least) least = cost, best = (unsigned)(m * split);
+    }
+    const long long steps = (long long)split * kb;
+    if (steps >= ctas && steps / ctas + 24 + join(ctas / split + 1) < least) best = (unsigned)ctas;
+    return best;
 }
+// Whether there are partial sums.
+inline bool f8_cut(int split, unsigned runs) { return split > 0 && runs != (unsigned)split; }
 // The first and last run that hold steps of a split tile.
 __device__ __forceinline__ void f8_contributors(const F8Args &p, int split, int &first, int &last) {
     const unsigned w = (unsigned)p.split * p.kb, t = (unsigned)split * p.kb;
@@ -94,11 +111,10 @@ __device__ __forceinline__ void f8_join(const float *from, size_t part, int part
     }
 }
 
-constexpr int kF8WideRows = 256, kF8WideFeatures = 256;  // a pair's tile
 // More rows of X than this run on pairs of SMs.
 constexpr int kF8Narrow = 128;
-size_t f8_wide_partial_floats(int split);
+size_t f8_wide_partial_floats(int split, unsigned runs);
 int f8_wide_pairs();
-cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream);
+cudaError_t f8_wide_launch(const F8Args &a, int pairs, cudaStream_t stream);
 
 }  // namespace ds

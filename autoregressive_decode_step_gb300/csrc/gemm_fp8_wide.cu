@@ -13,13 +13,14 @@
 // TMEM, four buffers); four warpgroups take 64 columns each out of TMEM, add
 // them to registers and free the buffer before they do.
 //
-// Tiles are dealt out whole, one a pair and round; what is left over is cut into
-// equal runs of steps whose partial sums a second launch adds in order.
+// Tiles are dealt out whole, one a pair and round; what is left over goes
+// one to a pair or is cut into runs of steps (f8_runs) whose partial sums a second
+// launch adds in order.
 //
-// Measured in a graph: 8,192 rows by 28,672 x 4,096 690 us (2.79 PFLOP/s, 1.46 of
+// Measured in a graph: 8,192 rows by 28,672 x 4,096 664 us (2.90 PFLOP/s, 1.51 of
 // the measured bf16 rate; on values of a wide spread 790 us at the power limit),
 // the tensor pipe active 61 % of the cycles (the issue slots 54 %: half of it the
-// sums); 256 by 4,096 x 14,336 27 us, 8 of them joining six partial sums a tile.
+// sums); 256 by 4,096 x 14,336 25 us, 7 of them joining four partial sums a tile.
 #include <algorithm>
 #include <atomic>
 
@@ -384,9 +385,9 @@ __global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constan
 
 // ---------------------------------------------------------------- host
 int f8_wide_pairs() { return std::max(1, sm_count() / 2); }
-size_t f8_wide_partial_floats(int split) { return split ? ((size_t)f8_wide_pairs() + split) * 2 * kFwPart : 0; }
+size_t f8_wide_partial_floats(int split, unsigned runs) { return f8_cut(split, runs) ? ((size_t)runs + split) * 2 * kFwPart : 0; }
 
-cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream) {
+cudaError_t f8_wide_launch(const F8Args &a, int pairs, cudaStream_t stream) {
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised, a bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -397,9 +398,8 @@ cudaError_t f8_wide_launch(F8Args &a, cudaStream_t stream) {
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    const int pairs = f8_wide_pairs();
     e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, true, a);
-    if (e != cudaSuccess || a.split == 0) return e;
+    if (e != cudaSuccess || !f8_cut(a.split, a.runs)) return e;
     return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / kFwJoinCols)), dim3(128), 0, stream, true, a, pairs);
 }
 
