@@ -5,8 +5,8 @@
 // times the block's scale, to fp32 registers.  No scale enters the tensor core,
 // so scales need not be powers of two, and every sum in it is short.
 //
-// This file: up to 128 rows of X, where the weights' bytes are the bound
-// (gemm_fp8_wide.cu: more).  A tile is 128 features (an MMA's M: lane r of TMEM
+// This file: up to 64 rows of X, and up to 128 by very many features, where the
+// weights' bytes are the bound (gemm_fp8_wide.cu: the others).  A tile is 128 features (an MMA's M: lane r of TMEM
 // is feature r), for more than 32 rows 256 in two halves, by all the rows of X,
 // rounded up to 16, 32, 64 or 128 (the MMA's N): one token costs 16 columns.
 // Tiles, or equal runs of their steps (f8_runs), go one to a CTA; a cut tile's
@@ -298,7 +298,7 @@ struct F8Plan {
 static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
     F8Plan t;
     const int64_t kb = (cols + kF8K - 1) / kF8K;
-    t.wide = n > kF8Narrow;
+    t.wide = n > kF8NarrowMost || (n > kF8Narrow && (rows + kF8WideFeatures - 1) / kF8WideFeatures <= f8_wide_pairs());
     int64_t tiles;
     if (t.wide) {  // m_tiles: features, n_tiles: rows of X
         t.bn = kF8WideFeatures;

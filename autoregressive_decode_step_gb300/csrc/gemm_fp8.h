@@ -1,5 +1,5 @@
-// What ds_gemm_fp8's two kernels share: gemm_fp8.cu (up to 128 rows of X) and
-// gemm_fp8_wide.cu (more).
+// What ds_gemm_fp8's two kernels share: gemm_fp8.cu (few rows of X) and
+// gemm_fp8_wide.cu (many).
 #pragma once
 
 #include "internal.h"
@@ -111,8 +111,11 @@ __device__ __forceinline__ void f8_join(const float *from, size_t part, int part
     }
 }
 
-// More rows of X than this run on pairs of SMs.
-constexpr int kF8Narrow = 128;
+// Pairs of SMs take more than 128 rows of X, and more than 64 unless the features
+// are more tiles than pairs (the other kernel's tiles have as many features and
+// twice as many CTAs): 128 rows by 4,096 x 4,096 take 15.9 us against 19.8, 65 by
+// 14,336 x 4,096 17.4 against 22.3, 128 by 28,672 x 4,096 33.7 against 27.0.
+constexpr int kF8Narrow = 64, kF8NarrowMost = 128;
 size_t f8_wide_partial_floats(int split, unsigned runs);
 int f8_wide_pairs();
 cudaError_t f8_wide_launch(const F8Args &a, int pairs, cudaStream_t stream);

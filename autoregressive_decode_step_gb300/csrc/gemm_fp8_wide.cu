@@ -1,4 +1,4 @@
-// ds_gemm_fp8 for more than 128 rows of X: pairs of SMs on tiles of 256 rows by
+// ds_gemm_fp8 for many rows of X (kF8Narrow): pairs of SMs on tiles of 256 rows by
 // 256 features.
 //
 // One tcgen05.mma of cta_group::2 spans both SMs of a pair: each holds 128 rows

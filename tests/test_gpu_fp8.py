@@ -277,3 +277,20 @@ def test_product_offsets_past_32_bits(abi):
     abi.ds_gemm_fp8(w, ws, x, xs, y, abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols)))
     for s in (slice(0, 64), slice(n - 64, n)):
         close(y[s], *product(w, ws, x[s], xs[s]), cols)
+
+
+# Few tiles with long sums (cut in pieces in line with the tiles), many with very long ones (equal runs that pass from
+# tile to tile), whole tiles in rounds before cut ones; features that are more tiles than pairs of SMs.
+@pytest.mark.parametrize("n,rows,cols", [
+    (1, 64, 4096), (16, 160 * 128, 4096), (1, 100 * 128, 15360), (64, 1000, 14336), (64, 80 * 256, 15360), (65, 300, 4096),
+    (96, 19456, 300), (100, 19457, 300), (128, 80 * 256, 15360), (128, 40000, 1000), (300, 39 * 256, 4096),
+    (256, 40 * 256, 15360), (1500, 1000, 4096)])
+def test_product_divisions(abi, n, rows, cols):
+    w, ws, x, xs = operands(n, rows, cols, n + rows + cols)
+    space = abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols))
+    want = product(w, ws, x, xs)
+    for _ in range(2):  # the second finds what the first left in the workspace
+        y = torch.full((n, rows), math.nan, dtype=torch.float32, device="cuda")
+        abi.ds_gemm_fp8(w, ws, x, xs, y, space)
+        assert abi.ds_workspace_error(space) == 0
+        close(y, *want, cols)
