@@ -116,13 +116,18 @@ __device__ __forceinline__ void fw_tile(const F8Args &p, int tile, int &rt, int 
     rt = g * kFwGroup + (tile - g * per) % nn;
 }
 
-// A warp's 32 rows (lane r row row0 + r) by 64 outputs, through shared memory:
-// four lanes store 64 neighbouring bytes of a row, where a thread's own row at
-// a time took a quarter of the kernel (a line a lane).
+// A warp's 32 rows (lane r row row0 + r) by 64 outputs, through shared memory.
+// Rows that start on 16 bytes (Dense): four lanes store 64 neighbouring bytes of a
+// row, where a thread's own row at a time took a quarter of the kernel (a line a
+// lane).  Others: a value a lane, side by side (128 rows by 300 x 128: 8 us, where 16
+// bytes of a row a lane took 19).  Kernels of their own: one with both had registers
+// spilled, and 8,192 rows by 28,672 x 4,096 took 686 us against 677.
+template <bool Dense>
 __device__ __forceinline__ void fw_store_tile(const F8Args &p, unsigned char *out, int row0, int f0, const float (&acc)[64]) {
     const int lane = threadIdx.x & 31, es = p.y_dtype == DS_BF16 ? 2 : 4, per = 64 / es;
     char *y = static_cast<char *>(p.y);
-    const bool dense = (((uintptr_t)y | (uintptr_t)(p.ldy * es)) & 15) == 0;
+    // (what Dense says; with the test at run time too nothing is spilled, without it 68 bytes)
+    const bool aligned = (((uintptr_t)y | (uintptr_t)(p.ldy * es)) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < 64; i += 16) {  // 16 values: 64 bytes of fp32, half of that of bf16
         uint4 *to = reinterpret_cast<uint4 *>(out + lane * kFwOutRow);
@@ -142,31 +147,36 @@ __device__ __forceinline__ void fw_store_tile(const F8Args &p, unsigned char *ou
         }
         __syncwarp();
         const int c0 = f0 + i / per * per;  // first column of these 64 bytes
+        if (Dense) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int at = j * 32 + lane, row = row0 + (at >> 2), col = c0 + (at & 3) * (16 / es);
-            if (row >= p.n || col >= p.rows) continue;
-            const uint4 v = *reinterpret_cast<const uint4 *>(out + (at >> 2) * kFwOutRow + (at & 3) * 16);
-            char *q = y + (row * p.ldy + col) * es;
-            if (dense && col + 16 / es <= p.rows) {
-                *reinterpret_cast<uint4 *>(q) = v;
-            } else {
-                const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                if (es == 4) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        if (col + k < p.rows) reinterpret_cast<uint32_t *>(q)[k] = w[k];
+            for (int j = 0; j < 4; ++j) {
+                const int at = j * 32 + lane, row = row0 + (at >> 2), col = c0 + (at & 3) * (16 / es);
+                if (row >= p.n || col >= p.rows) continue;
+                const unsigned char *v = out + (at >> 2) * kFwOutRow + (at & 3) * 16;
+                char *q = y + (row * p.ldy + col) * es;
+                if (aligned && col + 16 / es <= p.rows) {
+                    *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(v);
                 } else {
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        if (col + k < p.rows) reinterpret_cast<unsigned short *>(q)[k] = (unsigned short)(w[k >> 1] >> (16 * (k & 1)));
+#pragma unroll 1
+                    for (int k = 0; k < (p.rows - col) * es; k += 2) *reinterpret_cast<unsigned short *>(q + k) = *reinterpret_cast<const unsigned short *>(v + k);
                 }
+            }
+        } else {
+            const int col = lane & (per - 1);
+#pragma unroll 4
+            for (int r = lane / per; r < 32; r += 32 / per) {
+                if (row0 + r >= p.n || c0 + col >= p.rows) continue;
+                const unsigned char *v = out + r * kFwOutRow + col * es;
+                char *q = y + ((row0 + r) * p.ldy + c0 + col) * es;
+                if (es == 4) *reinterpret_cast<uint32_t *>(q) = *reinterpret_cast<const uint32_t *>(v);
+                else *reinterpret_cast<unsigned short *>(q) = *reinterpret_cast<const unsigned short *>(v);
             }
         }
         __syncwarp();
     }
 }
 
+template <bool Dense>
 __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_gemm_wide_kernel(const __grid_constant__ F8Args p) {
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -336,7 +346,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             }
             fw_tile(p, sg.tile, rt, ft);
             if (sg.split < 0) {
-                fw_store_tile(p, sh.out[warp], rt * kF8WideRows + rank * 128 + (warp & 3) * 32, ft * kF8WideFeatures + f0, acc);
+                fw_store_tile<Dense>(p, sh.out[warp], rt * kF8WideRows + rank * 128 + (warp & 3) * 32, ft * kF8WideFeatures + f0, acc);
             } else {
                 float *mine = p.partials + (((size_t)walk.id + sg.split) * 2 + rank) * kFwPart + (size_t)f0 * 128 + r;
 #pragma unroll
@@ -387,18 +397,23 @@ __global__ __launch_bounds__(128) void fp8_join_wide_kernel(const __grid_constan
 int f8_wide_pairs() { return std::max(1, sm_count() / 2); }
 size_t f8_wide_partial_floats(int split, unsigned runs) { return f8_cut(split, runs) ? ((size_t)runs + split) * 2 * kFwPart : 0; }
 
-cudaError_t f8_wide_launch(const F8Args &a, int pairs, cudaStream_t stream) {
+template <bool Dense>
+static cudaError_t f8_wide_kernel(const F8Args &a, int pairs, cudaStream_t stream) {
     static std::atomic<unsigned long long> ready{0};  // devices whose limit is raised, a bit each
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const unsigned long long bit = 1ull << (dev & 63);
     if (!(ready.load(std::memory_order_acquire) & bit)) {
-        e = cudaFuncSetAttribute(fp8_gemm_wide_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwSmem);
+        e = cudaFuncSetAttribute(fp8_gemm_wide_kernel<Dense>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFwSmem);
         if (e != cudaSuccess) return e;
         ready.fetch_or(bit, std::memory_order_release);
     }
-    e = launch_ex(fp8_gemm_wide_kernel, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, true, a);
+    return launch_ex(fp8_gemm_wide_kernel<Dense>, dim3(2 * pairs), dim3(kFwThreads), kFwSmem, stream, true, a);
+}
+cudaError_t f8_wide_launch(const F8Args &a, int pairs, cudaStream_t stream) {
+    const bool dense = (((uintptr_t)a.y | (uintptr_t)(a.ldy * (a.y_dtype == DS_BF16 ? 2 : 4))) & 15) == 0;
+    const cudaError_t e = dense ? f8_wide_kernel<true>(a, pairs, stream) : f8_wide_kernel<false>(a, pairs, stream);
     if (e != cudaSuccess || !f8_cut(a.split, a.runs)) return e;
     return launch_ex(fp8_join_wide_kernel, dim3(a.split * 2 * (kF8WideFeatures / kFwJoinCols)), dim3(128), 0, stream, true, a, pairs);
 }
