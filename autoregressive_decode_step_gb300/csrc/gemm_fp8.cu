@@ -6,20 +6,20 @@
 // so scales need not be powers of two, and every sum in it is short.
 //
 // This file: up to 64 rows of X, and up to 128 by very many features, where the
-// weights' bytes are the bound (gemm_fp8_wide.cu: the others).  A tile is 128 features (an MMA's M: lane r of TMEM
-// is feature r), for more than 32 rows 256 in two halves, by all the rows of X,
-// rounded up to 16, 32, 64 or 128 (the MMA's N): one token costs 16 columns.
-// Tiles, or equal runs of their steps (f8_runs), go one to a CTA; a cut tile's
-// partial sums meet in the workspace and are added in CTA order by whichever CTA
-// arrives last (a second launch for the wider ones took 12 us of 35 with 64 rows
-// by 28,672 x 4,096).  No CTA waits for
-// another.  A launch may begin while the one in front ends.
+// weights' bytes are the bound (gemm_fp8_wide.cu: the others).  A tile is 128
+// features (an MMA's M: lane r of TMEM is feature r), for more than 32 rows 256 in
+// two halves, by all the rows of X, rounded up to 16, 32, 64 or 128 (the MMA's N):
+// one token costs 16 columns.  Tiles, or equal runs of their steps (f8_runs), go
+// one to a CTA; a cut tile's partial sums meet in the workspace and are added in
+// CTA order by whichever CTA arrives last (a second launch for the wider ones took
+// 12 us of 35 with 64 rows by 28,672 x 4,096).  No CTA waits for another.  A launch
+// may begin while the one in front ends.
 //
 // A step brings its weights in one copy (16 KB for few rows, where the runs are
 // short and even ones count: one token 9.9 us against 11.2; else 32 KB: 64 rows by
-// 28,672 x 4,096 29 us against 33, in equal runs), and up to four steps' columns are a batch:
-// barriers and the latency of TMEM are paid once a batch.  A warpgroup for each
-// half of the features adds it up.
+// 28,672 x 4,096 29 us against 33; both in equal runs), and up to four steps'
+// columns are a batch: barriers and the latency of TMEM are paid once a batch.  A
+// warpgroup for each half of the features adds it up.
 //
 // Measured in a graph: one token through 6,144 x 4,096 7.7 us (3.3 TB/s: eleven
 // steps, the rest start and end), 64 through 28,672 x 4,096 22.6 us (5.4 TB/s), 128
