@@ -25,8 +25,8 @@
 // brings the largest below 2^8: six for fp32 (24 bits, to 2^-38 of the largest),
 // three for bf16 (two hold its 8 bits; the third those of values below 2^-14 of
 // the largest, to 2^-26 of it).  The intermediate is fp32 and goes in three bf16
-// or six e4m3 pieces, before bf16 outputs in two or four (16 bits).  Sums leave
-// the tensor core every 128 products (e4m3: a block, for its scale; bf16: see
+// pieces (24 bits) or six e4m3 ones, before bf16 outputs in four of e4m3 (16 bits
+// and more: see MoeCfg).  Sums leave the tensor core every 128 products (e4m3: a block, for its scale; bf16: see
 // kMoeBatch) and are fp32.  The logits are sums of exact products with their rounding errors
 // carried along (two floats, added up in 64 bits): the choice of experts is that
 // of 64 bits.
@@ -69,11 +69,16 @@ constexpr int kMoeAtOnce = 2; // partial sums of a cut tile under way at a time
 constexpr int kMoeSums = 2 * kMoeGroup * 128;  // floats of a tile
 
 // How many pieces an activation and the intermediate are cut into, and how many
-// tokens fit beside one another in 128 columns.
+// tokens fit beside one another in 128 columns.  e4m3 before bf16 outputs: four
+// pieces, so that 32 tokens fit.  Six, and 16 tokens, read an expert's weights twice
+// as often: 64 tokens through 2 of 8 experts of 4,096 x 14,336 337 us against 260,
+// 256 of them 1,080 against 642; of 131,072 outputs 31 against 50 were not the exact
+// result rounded (plain fp32: 184).  (Of bf16 two in the place of three gained
+// nothing: 463 us against 462, one token 35.1 against 34.5.)
 template <bool W8, bool XB>
 struct MoeCfg {
     static constexpr int kX = W8 ? (XB ? 3 : 6) : (XB ? 1 : 3);
-    static constexpr int kH = W8 ? (XB ? 4 : 6) : (XB ? 2 : 3);
+    static constexpr int kH = W8 ? (XB ? 4 : 6) : 3;
     static constexpr int kGroup = W8 && !XB ? 16 : 32;
     static constexpr int kElem = W8 ? 1 : 2, kStep = 128 / kElem;  // values of a step
     // Both phases share the ring and TMEM: columns of a half of the sums, buffers

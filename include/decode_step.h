@@ -288,8 +288,8 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   128)] (NULL and 0 with bf16).  569 for a weight's or scale's length.
  *   expert_ids, expert_weights: e_i and p_i [n][top_k], either may be NULL.
  * Logits are exact to some 45 bits, the choice of experts that of 64-bit
- * arithmetic; sums are fp32, of factors of 24 bits (before a bf16 y the
- * intermediate has 16); y is rounded once.  Before e4m3 weights a value of x or
+ * arithmetic; sums are fp32, of factors of 24 bits (with e4m3 experts before a
+ * bf16 y the intermediate has 16); y is rounded once.  Before e4m3 weights a value of x or
  * of the intermediate is held to 2^-38 (bf16 x: 2^-26, intermediate 2^-30) of the
  * largest of its 128, whatever its own size.  Weights are finite; a value of x that is
  * not, or a product that overflows fp32, makes outputs of its own token (and
