@@ -322,7 +322,7 @@ static F8Plan f8_plan(int64_t n, int64_t rows, int64_t cols) {
 }
 static size_t f8_ws_bytes(const F8Plan &t) {
     const size_t floats = t.wide ? f8_wide_partial_floats(t.split, t.runs) : f8_cut(t.split, t.runs) ? ((size_t)t.runs + t.split) * t.bn * F8Cfg<64>::kM : 0;
-    return kWsHeader + align_up((size_t)sm_count() * 4, 256) + floats * 4;
+    return stream_ws_data() + floats * 4;
 }
 
 template <int NB>
@@ -396,8 +396,8 @@ extern "C" DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride
     a.ldy = y_stride;
     char *w = static_cast<char *>(workspace);
     a.err = reinterpret_cast<int *>(w);
-    a.counters = reinterpret_cast<int *>(w + kWsHeader);
-    a.partials = reinterpret_cast<float *>(w + kWsHeader + align_up((size_t)sm_count() * 4, 256));
+    a.counters = reinterpret_cast<int *>(w + stream_ws_counters());
+    a.partials = reinterpret_cast<float *>(w + stream_ws_data());
     if (!encode_tiled_2d(&a.tw, W, DS_E4M3, cols, rows, w_stride, kF8K, t.wide || t.bn <= 32 ? 128 : 256, true) ||
         !encode_tiled_2d(&a.tx, X, DS_E4M3, cols, n, x_stride, kF8K, t.wide ? 128 : t.bn, true))
         return DS_CUDA_ERROR;

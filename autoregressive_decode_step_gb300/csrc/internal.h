@@ -20,6 +20,14 @@ inline size_t align_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 // SM count of the current device (cached per device).
 int sm_count();
 
+// ds_gemm_fp8's and ds_moe_layer's workspaces share their first bytes, so that one
+// may serve both: behind the header the counts of the grid's meetings, then counters
+// of arrivals, two a CTA.  Everything there is zero between calls; what either keeps
+// behind it is written before it is read.
+constexpr size_t kStreamMeetings = 256;
+inline size_t stream_ws_counters() { return kWsHeader + kStreamMeetings; }
+inline size_t stream_ws_data() { return stream_ws_counters() + align_up(2 * (size_t)sm_count() * 4, 256); }
+
 // Launch `kernel` with cudaLaunchKernelEx; `pdl` adds the programmatic
 // stream-serialisation attribute so the kernel may begin while its
 // predecessor on the stream finishes.

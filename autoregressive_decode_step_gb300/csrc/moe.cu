@@ -1082,20 +1082,18 @@ __global__ __launch_bounds__(kMoeThreads, 1) void moe_kernel(const __grid_consta
 
 // ---------------------------------------------------------------- host
 struct MoeSpace {
-    size_t bars, counters, parts, logits, choices, wts, out, xp, xs, hp, hs, total;
+    size_t parts, logits, choices, wts, out, xp, xs, hp, hs, total;
     int splits;
 };
 static MoeSpace moe_space(int64_t n, int64_t d, int64_t ff, int64_t experts, int64_t k) {
     MoeSpace s;
     const size_t g = (size_t)sm_count(), pairs = (size_t)(n * k), rows = n <= kMoeByToken ? (size_t)n : pairs;
-    size_t at = kWsHeader;
+    size_t at = stream_ws_data();
     const auto take = [&](size_t bytes) {
         const size_t was = at;
         at += align_up(bytes, 256);
         return was;
     };
-    s.bars = take(256);
-    s.counters = take(2 * g * 4);
     s.parts = take(g * 4 * kMoeSums * 4);
     s.splits = moe_splits(n, d, experts, sm_count() * (kMoeThreads / 32));
     s.logits = take((size_t)(n * experts) * s.splits * 8);
@@ -1210,8 +1208,8 @@ extern "C" DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, in
     a.renormalize = renormalize != 0;
     char *w = static_cast<char *>(workspace);
     a.err = reinterpret_cast<int *>(w);
-    a.bars = reinterpret_cast<int *>(w + sp.bars);
-    a.counters = reinterpret_cast<int *>(w + sp.counters);
+    a.bars = reinterpret_cast<int *>(w + kWsHeader);
+    a.counters = reinterpret_cast<int *>(w + stream_ws_counters());
     a.logits = reinterpret_cast<float2 *>(w + sp.logits);
     a.choices = reinterpret_cast<unsigned short *>(w + sp.choices);
     a.splits = sp.splits;

@@ -7,7 +7,9 @@
  *    allocations", "Inside the engine", section 1, "CausalLM: the forward
  *    path").  Scratch space is a caller-supplied workspace whose size a
  *    *_workspace_bytes call reports; a workspace must be zero-filled before
- *    its first use and is left ready for the next call by every call.
+ *    its first use and is left ready for the next call of the same operation
+ *    and sizes by every call.  For another operation, or other sizes, it has to
+ *    be zeroed again unless the calls say that they may share it.
  *  - Calls are asynchronous on `stream` (a cudaStream_t; NULL is the legacy
  *    default stream) and return before the GPU work finishes.
  *  - Every length argument is an element count.  Each buffer's real length
@@ -233,9 +235,8 @@ DS_API int ds_fp8_quantize(const void *x, int64_t x_len, int x_dtype, int64_t x_
                            int64_t cols, int block_rows, void *q, int64_t q_len, int64_t q_stride,
                            float *scales, int64_t scales_len, ds_stream_t stream);
 
-/* Workspace bytes ds_gemm_fp8 needs for these sizes (a workspace that several
- * sizes share is as large as the largest of their answers; a larger n may need
- * less); 0 for a dimension < 1 or past DS_MAX_DIM. */
+/* Workspace bytes ds_gemm_fp8 needs for these sizes; 0 for a dimension
+ * < 1 or past DS_MAX_DIM. */
 DS_API size_t ds_gemm_fp8_workspace_bytes(int64_t n, int64_t rows, int64_t cols);
 
 /* Y[s][r] = sum_b x_scales[s][b] * w_scales[r / 128][b]
@@ -254,7 +255,9 @@ DS_API size_t ds_gemm_fp8_workspace_bytes(int64_t n, int64_t rows, int64_t cols)
  *   it is part of and no other.
  *   workspace: ds_gemm_fp8_workspace_bytes(n, rows, cols) bytes, 256-byte
  *   aligned, zeroed before first use (and again after a DS_ERR_WAIT_TIMEOUT);
- *   calls whose GPU work may overlap need one each. */
+ *   calls whose GPU work may overlap need one each.  Calls of several sizes, of
+ *   this operation and of ds_moe_layer, may share one that is as large as the
+ *   largest of their answers (a larger n may need less). */
 DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride, const float *w_scales,
                        int64_t w_scales_len, const void *X, int64_t x_len, int64_t x_stride,
                        const float *x_scales, int64_t x_scales_len, int64_t n, int64_t rows, int64_t cols,
@@ -300,7 +303,8 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   residual itself; otherwise no output overlaps an input or another output
  *   (577).  workspace: ds_moe_layer_workspace_bytes(...) bytes, 256-byte
  *   aligned, zeroed before first use (and again after a DS_ERR_WAIT_TIMEOUT);
- *   calls whose GPU work may overlap need one each.  A cooperative launch: its
+ *   calls whose GPU work may overlap need one each, others may share one, with
+ *   ds_gemm_fp8 as well (see there).  A cooperative launch: its
  *   blocks wait for one another, so it runs when every SM has room for one. */
 DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, int64_t n, int64_t d,
                         const void *w_router, int64_t router_len, int router_dtype, int n_experts,

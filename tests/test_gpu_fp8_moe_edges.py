@@ -1,7 +1,10 @@
 """Edges of the 8-bit projections and the experts."""
+import math
+
 import pytest
 import torch
 
+from tests.test_gpu_fp8 import operands
 from tests.test_gpu_moe import Layer
 
 pytestmark = pytest.mark.gpu
@@ -40,3 +43,30 @@ def test_intermediate_digits_before_bf16(abi, n, w, off):
     a.x = a.x.to(BF16)
     y, _, _ = a.run(abi)
     assert (y == 64 * 2.0 ** -off).all()
+
+
+# ---------------------------------------------------------------- workspaces
+def test_product_and_experts_on_one_workspace(abi):
+    """One workspace, as large as the largest answer, for both operators in turn: whole and cut tiles, pairs of SMs and
+    not, few and many tokens.  The outputs are those of a workspace each."""
+    products = [(1, 6144, 4096), (30, 1000, 4096), (256, 1024, 4096), (300, 500, 640), (64, 2048, 8192)]
+    shapes = [(1, 2048, 768, 128, 8), (64, 512, 256, 8, 2), (7, 1000, 344, 60, 4), (33, 128, 640, 3, 3)]
+    space = abi.workspace(max([abi.ds_gemm_fp8_workspace_bytes(*s) for s in products] +
+                              [abi.ds_moe_layer_workspace_bytes(*s) for s in shapes]))
+    layers = [Layer(*s, seed=i) for i, s in enumerate(shapes)]
+    ops = [operands(*s, seed=i) for i, s in enumerate(products)]
+
+    def multiply(i, ws):
+        n, rows, _ = products[i]
+        y = torch.full((n, rows), math.nan, device="cuda")
+        w, wsc, x, xsc = ops[i]
+        abi.ds_gemm_fp8(w, wsc, x, xsc, y, ws)
+        return y
+
+    alone = [multiply(i, abi.workspace(abi.ds_gemm_fp8_workspace_bytes(*s))) for i, s in enumerate(products)]
+    layer_alone = [a.run(abi)[0] for a in layers]
+    for i in range(len(products)):
+        for j in range(len(shapes)):
+            assert torch.equal(multiply(i, space), alone[i])
+            assert torch.equal(layers[j].run(abi, ws=space)[0], layer_alone[j])
+    assert abi.ds_workspace_error(space) == 0
