@@ -74,6 +74,9 @@ __device__ __forceinline__ void widen16(const uint4 &w, float (&f)[4]) {
 // stream-serialisation attribute may start while its predecessor runs; it
 // must execute grid_dependency_wait() before touching anything the
 // predecessor writes.  Weights never change, so they may be fetched earlier.
+// What any launch in front may write is read with plain or L2 loads behind the
+// wait: __ldg() promises that nothing writes it while the kernel runs, and a
+// kernel runs from before its predecessors have ended.
 __device__ __forceinline__ void grid_dependency_wait() {
     asm volatile("griddepcontrol.wait;" ::: "memory");
 }

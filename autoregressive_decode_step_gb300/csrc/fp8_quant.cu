@@ -35,13 +35,14 @@ struct FqArgs {
     float *scales;
 };
 
-// Eight values as they are stored: 16 bytes of bf16, 32 of fp32.
+// Eight values as they are stored: 16 bytes of bf16, 32 of fp32.  (Plain loads: the
+// launch in front may have written them.)
 template <typename T>
 struct FqRaw;
 template <>
 struct FqRaw<__nv_bfloat16> {
     uint4 w;
-    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { w = *reinterpret_cast<const uint4 *>(p); }
     __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void set(int i, __nv_bfloat16 v) { reinterpret_cast<__nv_bfloat16 *>(&w)[i] = v; }
     // the largest magnitude's bits: NaN above infinity above numbers
@@ -55,8 +56,8 @@ template <>
 struct FqRaw<float> {
     float4 a, b;
     __device__ __forceinline__ void load(const float *p) {
-        a = __ldg(reinterpret_cast<const float4 *>(p));
-        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+        a = reinterpret_cast<const float4 *>(p)[0];
+        b = reinterpret_cast<const float4 *>(p)[1];
     }
     __device__ __forceinline__ void zero() { a = b = make_float4(0, 0, 0, 0); }
     __device__ __forceinline__ void set(int i, float v) { (i < 4 ? &a.x : &b.x)[i & 3] = v; }

@@ -183,6 +183,7 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
             mbar_wait(&sh.done, 0, p.err);
         } else if (warp == 10) {
             // scales: four steps' requested together, so that a batch's come before its products are done
+            // (plain loads: the launch in front may have written them, weights' as well)
             constexpr int kVals = 4 * NB / 32, kPer = BS * NB / 32;  // values a lane holds, and of a batch
             int slot = 0;
             uint32_t ph = 1;
@@ -193,9 +194,9 @@ __global__ __launch_bounds__(kF8Threads, 1) void fp8_gemm_kernel(const __grid_co
 #pragma unroll
                     for (int i = 0; i < kVals; ++i) {
                         const int at = i * 32 + lane, j = k + at / NB, c = at % NB;
-                        v[i] = j < sg.k1 && c < p.n ? __ldg(p.xs + (long long)c * p.kb + j) : 0.0f;
-                        a[i] = j < sg.k1 ? __ldg(w0 + j) : 0.0f;
-                        b[i] = HV > 1 && j < sg.k1 ? __ldg(w1 + j) : 0.0f;
+                        v[i] = j < sg.k1 && c < p.n ? p.xs[(long long)c * p.kb + j] : 0.0f;
+                        a[i] = j < sg.k1 ? w0[j] : 0.0f;
+                        b[i] = HV > 1 && j < sg.k1 ? w1[j] : 0.0f;
                     }
 #pragma unroll
                     for (int j = 0; j < 4; j += BS) {

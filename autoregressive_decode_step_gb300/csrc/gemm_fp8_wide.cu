@@ -276,6 +276,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             // before its products start.  Once the products of the stage's last
             // step, n - 5, are done, those of n - 7 and before have been taken out
             // (a buffer waits for that), so slot n - 8 may be written over.
+            // (Plain loads: the launch in front may have written any of the scales.)
             static_assert(kFwSlots > kFwStages + 2, "slots");
             int slot = 0, s = 0;
             uint32_t ph = 1;
@@ -289,10 +290,10 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const bool in = k + j < sg.k1;
-                        a[j] = in ? __ldg(w0 + k + j) : 0.0f;
-                        b[j] = in ? __ldg(w1 + k + j) : 0.0f;
+                        a[j] = in ? w0[k + j] : 0.0f;
+                        b[j] = in ? w1[k + j] : 0.0f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[j][i] = in && row + 32 * i < p.n ? __ldg(xs + (long long)(32 * i) * p.kb + k + j) : 0.0f;
+                        for (int i = 0; i < 4; ++i) v[j][i] = in && row + 32 * i < p.n ? xs[(long long)(32 * i) * p.kb + k + j] : 0.0f;
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {

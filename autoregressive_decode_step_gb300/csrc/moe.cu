@@ -154,12 +154,13 @@ __device__ __forceinline__ bool moe_meet_all(const MoeArgs &p, MoeShared &sh, in
 }
 
 // ------------------------------------------------------------------ router
+// (Plain loads: x may be y, which the kernel writes in the end.)
 __device__ __forceinline__ void moe_load8(const void *base, long long i, int dtype, float (&v)[8]) {
     if (dtype == DS_BF16) {
-        widen16(__ldg(reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + i)), v);
+        widen16(*reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(base) + i), v);
     } else {
         const float4 *p = reinterpret_cast<const float4 *>(static_cast<const float *>(base) + i);
-        const float4 a = __ldg(p), b = __ldg(p + 1);
+        const float4 a = p[0], b = p[1];
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
 }
@@ -463,11 +464,11 @@ __device__ __forceinline__ void moe_split_x(const MoeArgs &p, const unsigned sho
         float v[4] = {0, 0, 0, 0};
         if (j < p.d) {  // (d is a multiple of 8)
             if (p.x_dtype == DS_BF16) {
-                const uint2 w = __ldg(reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (size_t)tok * p.d + j));
+                const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const __nv_bfloat16 *>(p.x) + (size_t)tok * p.d + j);
                 v[0] = __uint_as_float(w.x << 16), v[1] = __uint_as_float(w.x & 0xffff0000u);
                 v[2] = __uint_as_float(w.y << 16), v[3] = __uint_as_float(w.y & 0xffff0000u);
             } else {
-                const float4 w = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + (size_t)tok * p.d + j));
+                const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(p.x) + (size_t)tok * p.d + j);
                 v[0] = w.x, v[1] = w.y, v[2] = w.z, v[3] = w.w;
             }
         }

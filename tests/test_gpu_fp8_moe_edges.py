@@ -70,3 +70,34 @@ def test_product_and_experts_on_one_workspace(abi):
             assert torch.equal(multiply(i, space), alone[i])
             assert torch.equal(layers[j].run(abi, ws=space)[0], layer_alone[j])
     assert abi.ds_workspace_error(space) == 0
+
+
+# ---------------------------------------------------------------- launches that overlap
+@pytest.mark.parametrize("n,rows,cols", [(1, 6144, 4096), (8, 512, 4096), (64, 28672, 1024), (128, 512, 2048),
+                                         (256, 1024, 4096), (700, 300, 1000)])
+def test_quantise_and_multiply_back_to_back(abi, n, rows, cols):
+    """Step after step into the same codes and scales, other inputs each, nothing waited for in between: every step's
+    product is that of its own inputs."""
+    steps, kb = 40, -(-cols // 128)
+    weights, w_scales, _, _ = operands(n, rows, cols, 2)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    size = torch.exp(torch.randn(steps, n, 1, generator=g, device="cuda"))
+    x = torch.randn(steps, n, cols, generator=g, device="cuda") * size
+    ld = -(-cols // 16) * 16
+    q = torch.zeros(n, ld, dtype=torch.uint8, device="cuda").view(E4M3)[:, :cols]
+    xs = torch.zeros(n, kb, device="cuda")
+    y = torch.empty(steps, n, rows, device="cuda")
+    space = abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols))
+    torch.cuda.synchronize()
+    for i in range(steps):
+        abi.ds_fp8_quantize(x[i], 1, q, xs)
+        abi.ds_gemm_fp8(weights, w_scales, q, xs, y[i], space)
+    torch.cuda.synchronize()
+    for i in range(steps):
+        abi.ds_fp8_quantize(x[i], 1, q, xs)
+        torch.cuda.synchronize()
+        alone = torch.empty(n, rows, device="cuda")
+        abi.ds_gemm_fp8(weights, w_scales, q, xs, alone, space)
+        torch.cuda.synchronize()
+        assert torch.equal(alone, y[i])
+    assert abi.ds_workspace_error(space) == 0
