@@ -1,10 +1,11 @@
 """Edges of the 8-bit projections and the experts."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_fp8 import operands
+from tests.test_gpu_fp8 import operands, quantized, run_quantize, same_codes
 from tests.test_gpu_moe import Layer
 
 pytestmark = pytest.mark.gpu
@@ -101,3 +102,23 @@ def test_quantise_and_multiply_back_to_back(abi, n, rows, cols):
         torch.cuda.synchronize()
         assert torch.equal(alone, y[i])
     assert abi.ds_workspace_error(space) == 0
+
+
+# ---------------------------------------------------------------- quantisation of many blocks
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,pad,q_pad", [
+    (3001, 1001, 0, 0), (3001, 1001, 23, 1), (2999, 1024, 0, 0), (2999, 1024, 8, 8), (2999, 1024, 23, 7), (9729, 1000, 8, 0),
+    (1500, 1001, 7, 23), (1250, 1024, 0, 0), (20000, 130, 0, 6)])
+def test_quantize_many_blocks(abi, rows, cols, pad, q_pad, dtype):
+    """More blocks than the grid has groups, so that each takes several at a time: ends that do not fill them, rows of
+    sizes of their own, whole blocks and ragged ones, rows that start on 16 bytes and that do not.  Every code and scale."""
+    g = torch.Generator(device="cuda").manual_seed(rows + cols + pad)
+    x = torch.randn(rows, cols + pad, generator=g, device="cuda")
+    x *= torch.exp(4 * torch.randn(rows, 1, generator=g, device="cuda"))
+    x = (x * torch.exp(torch.randn(cols + pad, generator=g, device="cuda"))).to(dtype)[:, :cols]
+    buf = torch.full((rows, cols + q_pad), 0x55, dtype=torch.uint8, device="cuda")
+    q, scales = run_quantize(abi, x, 1, buf.view(E4M3)[:, :cols])
+    want, scale = quantized(x, 1)
+    assert np.array_equal(scales.cpu().numpy(), scale)
+    same_codes(q, want)
+    assert (buf[:, cols:] == 0x55).all()
