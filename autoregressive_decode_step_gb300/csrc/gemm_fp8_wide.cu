@@ -34,7 +34,7 @@ constexpr int kFwThreads = 640;  // sixteen warps that add up; copies, products 
 // 4 x 104 + 64 = 5 x 96.
 constexpr int kFwRegsSum = 104, kFwRegsOther = 64;
 constexpr int kFwStages = 5, kFwHalf = 128 * 128, kFwStageBytes = 2 * kFwHalf;
-constexpr int kFwSlots = 8;   // steps' factors; see where they are written
+constexpr int kFwFactors = 4;  // slots of factors, four steps each
 constexpr int kFwBufs = 4;    // TMEM buffers of 128 columns, two a step
 constexpr int kFwGroup = 8;   // row tiles that follow one another before the next features
 constexpr int kFwOutRow = 80;  // 64 bytes of a row and 16 that keep rows apart on the banks
@@ -43,10 +43,11 @@ constexpr int kFwPart = 128 * kF8WideFeatures;  // floats of one SM's share of a
 struct FwShared {
     uint64_t full[kFwStages], empty[kFwStages];
     uint64_t t_full[kFwBufs], t_empty[kFwBufs];
+    uint64_t f_full[kFwFactors], f_empty[kFwFactors];
     uint64_t done;
     uint32_t tmem;
     int dead;
-    alignas(16) float factor[kFwSlots][2][128];
+    alignas(16) float factor[kFwFactors][4][2][128];
     alignas(16) unsigned char out[16][32 * kFwOutRow];  // a warp's outputs on their way
 };
 constexpr size_t kFwSmem = 1024 + (size_t)kFwStages * kFwStageBytes + sizeof(FwShared);
@@ -95,10 +96,10 @@ __device__ __forceinline__ void fw_commit(uint32_t one, uint64_t *bar) {
         "h"((unsigned short)3), "r"(one)
         : "memory");
 }
-// Arrive on a barrier of either CTA.  (Release at CTA scope: what it orders are
-// TMEM loads, complete and fenced by tcgen05.fence, and a CTA's own reads and
-// writes.  At cluster scope each arrival cost a memory barrier: 1.62 ms for
-// 8,192 rows by 28,672 x 4,096.)
+// Arrive on a barrier of either CTA: a TMEM buffer is read out.  (Release at CTA
+// scope: what it orders are TMEM loads alone, complete and fenced by tcgen05.fence.
+// At cluster scope each arrival cost a memory barrier: 1.62 ms for 8,192 rows by
+// 28,672 x 4,096.)
 __device__ __forceinline__ void fw_arrive(uint32_t one, uint32_t bar) {
     asm volatile(
         "{\n\t.reg .pred q;\n\t"
@@ -126,8 +127,6 @@ template <bool Dense>
 __device__ __forceinline__ void fw_store_tile(const F8Args &p, unsigned char *out, int row0, int f0, const float (&acc)[64]) {
     const int lane = threadIdx.x & 31, es = p.y_dtype == DS_BF16 ? 2 : 4, per = 64 / es;
     char *y = static_cast<char *>(p.y);
-    // (what Dense says; with the test at run time too nothing is spilled, without it 68 bytes)
-    const bool aligned = (((uintptr_t)y | (uintptr_t)(p.ldy * es)) & 15) == 0;
 #pragma unroll
     for (int i = 0; i < 64; i += 16) {  // 16 values: 64 bytes of fp32, half of that of bf16
         uint4 *to = reinterpret_cast<uint4 *>(out + lane * kFwOutRow);
@@ -154,7 +153,7 @@ __device__ __forceinline__ void fw_store_tile(const F8Args &p, unsigned char *ou
                 if (row >= p.n || col >= p.rows) continue;
                 const unsigned char *v = out + (at >> 2) * kFwOutRow + (at & 3) * 16;
                 char *q = y + (row * p.ldy + col) * es;
-                if (aligned && col + 16 / es <= p.rows) {
+                if (col + 16 / es <= p.rows) {
                     *reinterpret_cast<uint4 *>(q) = *reinterpret_cast<const uint4 *>(v);
                 } else {
 #pragma unroll 1
@@ -181,7 +180,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
     extern __shared__ unsigned char smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     FwShared &sh = *reinterpret_cast<FwShared *>(smem_raw + (base - smem_u32(smem_raw)) + kFwStages * kFwStageBytes);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (uniform, so that addresses of barriers are)
     const int rank = (int)fw_rank();
     volatile int *dead = &sh.dead;
 
@@ -189,12 +188,16 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
         stream_prefetch_map(&p.tw);
         stream_prefetch_map(&p.tx);
         for (int i = 0; i < kFwStages; ++i) {
-            mbar_init(&sh.full[i], 3);  // the copies of both CTAs and, on the first one's barrier, both CTAs' factors
+            mbar_init(&sh.full[i], 1);  // the first one's: the copies of both CTAs
             mbar_init(&sh.empty[i], 2);  // a commit of either half's products
         }
         for (int i = 0; i < kFwBufs; ++i) {
             mbar_init(&sh.t_full[i], 1);
             mbar_init(&sh.t_empty[i], 16);
+        }
+        for (int i = 0; i < kFwFactors; ++i) {
+            mbar_init(&sh.f_full[i], 1);
+            mbar_init(&sh.f_empty[i], 16);
         }
         mbar_init(&sh.done, 2);
         sh.dead = 0;
@@ -255,7 +258,6 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
                     for (int k = sg.k1 - sg.k0; k > 0; --k, ++n) {
                         const uint32_t b = n & 1;
                         stream_wait(&sh.t_empty[2 * b + h], (n >> 1 & 1) ^ 1, dead, p.err);
-                        // a step's factors are there before its products start, so whoever sees these needs no other wait
                         stream_wait(&sh.full[s], ph, dead, p.err);
                         tc_fence_after();
                         const uint64_t ad = smem_desc(base + s * kFwStageBytes, 16, 1024);
@@ -272,14 +274,12 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
             }
             mbar_wait(&sh.done, 0, p.err);
         } else {
-            // Factors: four steps' scales requested together, so that a step's come
-            // before its products start.  Once the products of the stage's last
-            // step, n - 5, are done, those of n - 7 and before have been taken out
-            // (a buffer waits for that), so slot n - 8 may be written over.
-            // (Plain loads: the launch in front may have written any of the scales.)
-            static_assert(kFwSlots > kFwStages + 2, "slots");
-            int slot = 0, s = 0;
-            uint32_t ph = 1;
+            // Factors: four steps' scales requested together, and four steps' factors
+            // handed over together (a segment's last with the next one's first), by
+            // barriers of this CTA alone: memory that one CTA writes and reads is
+            // ordered within it.  (Plain loads: the launch in front may have written
+            // any of the scales.)
+            uint32_t n = 0;  // steps so far
             while (walk.next(p, sg)) {
                 fw_tile(p, sg.tile, rt, ft);
                 const int row = rt * kF8WideRows + rank * 128 + lane, blocks = (p.rows + 127) / 128;
@@ -298,19 +298,20 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (k + j >= sg.k1) break;
-                        stream_wait(&sh.empty[s], ph, dead, p.err);
+                        const uint32_t at = (n >> 2) % kFwFactors;
+                        if ((n & 3) == 0) stream_wait(&sh.f_empty[at], (n / (4 * kFwFactors) & 1) ^ 1, dead, p.err);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            sh.factor[slot][0][32 * i + lane] = v[j][i] * a[j];
-                            sh.factor[slot][1][32 * i + lane] = v[j][i] * b[j];
+                            sh.factor[at][n & 3][0][32 * i + lane] = v[j][i] * a[j];
+                            sh.factor[at][n & 3][1][32 * i + lane] = v[j][i] * b[j];
                         }
                         __syncwarp();
-                        fw_arrive(lane == 0, fw_lead(&sh.full[s]));
-                        if (++slot == kFwSlots) slot = 0;
-                        if (++s == kFwStages) s = 0, ph ^= 1;
+                        stream_arrive(lane == 0 && (n & 3) == 3, smem_u32(&sh.f_full[at]));
+                        ++n;
                     }
                 }
             }
+            stream_arrive(lane == 0 && (n & 3) != 0, smem_u32(&sh.f_full[(n >> 2) % kFwFactors]));
         }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kFwRegsSum));
@@ -319,18 +320,19 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
         const int wg = warp >> 2, half = wg >> 1, sub = wg & 1, r = threadIdx.x & 127, f0 = sub * 128 + half * 64;
         const uint32_t from = tmem + ((uint32_t)(warp & 3) << 21) + half * 128 + sub * 64;
         const uint32_t full0 = smem_u32(&sh.t_full[half]), freed0 = fw_lead(&sh.t_empty[half]);
-        const uint32_t factor0 = smem_u32(&sh.factor[0][sub][r]), one = stream_elect();
+        const uint32_t factor0 = smem_u32(&sh.factor[0][0][sub][r]), f_full0 = smem_u32(&sh.f_full[0]), one = stream_elect();
         uint32_t n = 0;  // steps so far
         while (walk.next(p, sg)) {
             float acc[64];
 #pragma unroll
             for (int i = 0; i < 64; ++i) acc[i] = 0.0f;
             for (int k = sg.k1 - sg.k0; k > 0; --k, ++n) {
-                const uint32_t slot = n % kFwSlots, b = n & 1;
+                const uint32_t b = n & 1;
+                if ((n & 3) == 0) stream_wait(f_full0 + (n >> 2) % kFwFactors * 8, n / (4 * kFwFactors) & 1, dead, p.err);
+                float factor;
+                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(factor) : "r"(factor0 + n % (4 * kFwFactors) * 1024));
                 stream_wait(full0 + b * 16, n >> 1 & 1, dead, p.err);
                 tc_fence_after();
-                float factor;
-                asm volatile("ld.shared.f32 %0, [%1];" : "=f"(factor) : "r"(factor0 + slot * 1024));
                 const uint64_t f = stream_pair(factor, factor);
 #pragma unroll
                 for (int c = 0; c < 64; c += 32) {
@@ -340,6 +342,7 @@ __global__ __cluster_dims__(2, 1, 1) __launch_bounds__(kFwThreads, 1) void fp8_g
                         tc_fence_before();
                         __syncwarp();
                         fw_arrive(one, freed0 + b * 16);
+                        stream_arrive(one && (n & 3) == 3, f_full0 + ((n >> 2) % kFwFactors + kFwFactors) * 8);  // f_empty
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) stream_fma2(acc[c + i], acc[c + i + 1], v[i], v[i + 1], f);
