@@ -472,6 +472,9 @@ def ds_moe_layer(x, w_router, top_k, renormalize, w_gate_up, gate_up_scales, w_d
         raise ValueError("residual: x's shape and type are needed")
     e4m3 = w_gate_up.dtype == torch.float8_e4m3fn
     kb, fb = -(-d // 128), -(-ff // 128)
+    for name, t in (("gate_up_scales", gate_up_scales), ("down_scales", down_scales)):
+        if (t is not None) != e4m3:
+            raise ValueError("%s: e4m3 experts have scales, others have none" % name)
     gs = _scales(gate_up_scales, (experts, 2, fb, kb), "gate_up_scales", dev) if e4m3 else None
     dns = _scales(down_scales, (experts, kb, fb), "down_scales", dev) if e4m3 else None
     n_scales = experts * kb * fb if e4m3 else 0

@@ -1166,14 +1166,14 @@ extern "C" DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, in
     const int64_t db = (d + 127) / 128, fb = (ff + 127) / 128, unit = w8 ? 16 : 8;
     if (x_len != n * d) return DS_GEMV_X_LENGTH_MISMATCH;
     if (router_len != n_experts * d || gate_up_len != n_experts * 2 * ff * d || down_len != n_experts * d * ff) return DS_GEMV_A_LENGTH_MISMATCH;
-    if (w8 && (gate_up_scales_len != n_experts * 2 * fb * db || down_scales_len != n_experts * db * fb)) return DS_GEMV_A_LENGTH_MISMATCH;
+    if (gate_up_scales_len != (w8 ? n_experts * 2 * fb * db : 0) || down_scales_len != (w8 ? n_experts * db * fb : 0)) return DS_GEMV_A_LENGTH_MISMATCH;
     if (y_len != n * d) return DS_A_LENGTH_MISMATCH;
     if (top_k > n_experts || d % unit || ff % unit) return DS_BAD_ARGUMENT;
-    if (!x || !w_router || !w_gate_up || !w_down || !y || (w8 && (!gate_up_scales || !down_scales))) return DS_BAD_ARGUMENT;
+    if (!x || !w_router || !w_gate_up || !w_down || !y || w8 != (gate_up_scales != nullptr) || w8 != (down_scales != nullptr)) return DS_BAD_ARGUMENT;
     if (((uintptr_t)x | (uintptr_t)w_router | (uintptr_t)w_gate_up | (uintptr_t)w_down) & 15) return DS_BAD_ARGUMENT;
     const int es = x_dtype == DS_BF16 ? 2 : 4;
     if (((uintptr_t)y | (uintptr_t)residual) % es || ((uintptr_t)expert_ids | (uintptr_t)expert_weights) & 3) return DS_BAD_ARGUMENT;
-    if (w8 && (((uintptr_t)gate_up_scales | (uintptr_t)down_scales) & 3)) return DS_BAD_ARGUMENT;
+    if (((uintptr_t)gate_up_scales | (uintptr_t)down_scales) & 3) return DS_BAD_ARGUMENT;
     const MoeSpace sp = moe_space(n, d, ff, n_experts, top_k);
     if (!workspace || workspace_bytes < sp.total) return DS_WORKSPACE_TOO_SMALL;
     if ((uintptr_t)workspace & 255) return DS_BAD_ARGUMENT;
@@ -1184,7 +1184,7 @@ extern "C" DS_API int ds_moe_layer(const void *x, int64_t x_len, int x_dtype, in
         int64_t n;
     } span[] = {{y, yb}, {expert_ids, n * top_k * 4}, {expert_weights, n * top_k * 4}, {x, yb}, {residual, yb},
                 {w_router, router_len * rs}, {w_gate_up, gate_up_len * ws}, {w_down, down_len * ws},
-                {w8 ? gate_up_scales : nullptr, gate_up_scales_len * 4}, {w8 ? down_scales : nullptr, down_scales_len * 4}};
+                {gate_up_scales, gate_up_scales_len * 4}, {down_scales, down_scales_len * 4}};
     for (int i = 0; i < 3; ++i)
         for (int j = i + 1; j < 10; ++j) {
             if (!span[i].p || !span[j].p || (i == 0 && (j == 3 || j == 4) && span[j].p == y)) continue;

@@ -288,7 +288,7 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   [n_experts][d][ff]; both bf16, or e4m3 with a scale for each 128 x 128
  *   block of every matrix (w_dtype): gate_up_scales [n_experts][2][ceil(ff /
  *   128)][ceil(d / 128)], down_scales [n_experts][ceil(d / 128)][ceil(ff /
- *   128)] (NULL and 0 with bf16).  569 for a weight's or scale's length.
+ *   128)] (with bf16 NULL, else 577, and 0).  569 for a weight's or scale's length.
  *   expert_ids, expert_weights: e_i and p_i [n][top_k], either may be NULL.
  * Logits are exact to some 45 bits, the choice of experts that of 64-bit
  * arithmetic; sums are fp32, of factors of 24 bits (with e4m3 experts before a
