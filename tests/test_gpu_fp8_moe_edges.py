@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_fp8 import operands, quantized, run_quantize, same_codes
+from tests.test_gpu_fp8 import close, operands, product, quantized, run_quantize, same_codes
 from tests.test_gpu_moe import Layer
 
 pytestmark = pytest.mark.gpu
@@ -122,3 +122,103 @@ def test_quantize_many_blocks(abi, rows, cols, pad, q_pad, dtype):
     assert np.array_equal(scales.cpu().numpy(), scale)
     same_codes(q, want)
     assert (buf[:, cols:] == 0x55).all()
+
+
+# ---------------------------------------------------------------- the product, few rows and many
+@pytest.mark.parametrize("n,rows,cols", [
+    (1, 300, 700), (12, 300, 700), (30, 5000, 2100), (50, 300, 700), (64, 2048, 4096),  # few rows
+    (128, 77 * 256, 300),                                                               # up to 128 by very many features
+    (200, 300, 700), (300, 1000, 4096), (130, 301, 300)])                               # pairs of SMs, whole tiles and cut ones
+def test_product_not_a_number_in_each_kernel(abi, n, rows, cols):
+    """A NaN code, a NaN scale or an infinite one reaches the outputs it is part of and no other."""
+    w, ws, x, xs = operands(n, rows, cols, 5)
+    kb = -(-cols // 128)
+    bad_x, bad_w, bad_xs = n // 2, rows - 10, n - 1
+    off = torch.zeros(n, rows, dtype=torch.bool, device="cuda")
+    if n > 4:  # (a single row has nothing that stays)
+        x.view(torch.uint8)[bad_x, 3] = 0x7f
+        xs[bad_xs, kb - 1] = math.nan
+        off[bad_x], off[bad_xs] = True, True
+    w.view(torch.uint8)[bad_w, cols - 1] = 0xff
+    ws[1, 2] = math.inf
+    off[:, bad_w], off[:, 128:256] = True, True
+    y = torch.zeros(n, rows, device="cuda")
+    space = abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols))
+    abi.ds_gemm_fp8(w, ws, x, xs, y, space)
+    assert (~torch.isfinite(y) == off).all()
+    if n > 4:
+        x.view(torch.uint8)[bad_x, 3] = 0
+        xs[bad_xs, kb - 1] = 1
+    w.view(torch.uint8)[bad_w, cols - 1] = 0
+    ws[1, 2] = 1
+    want, size = product(w, ws, x, xs)
+    close(y[~off], want[~off], size[~off], cols)
+    abi.ds_gemm_fp8(w, ws, x, xs, y, space)  # and nothing of it is left
+    close(y, want, size, cols)
+
+
+@pytest.mark.parametrize("n,rows,cols,pad,dtype", [
+    (256, 1024, 4096, 0, torch.float32), (256, 1024, 4096, 0, BF16), (300, 1001, 2048, 2, torch.float32),
+    (200, 1001, 4096, 2, BF16), (2600, 2048, 1024, 0, BF16)])
+def test_pairs_captured_and_on_two_streams(abi, n, rows, cols, pad, dtype):
+    """Quantisation, the pairs' product and the launch that joins cut tiles in a graph, replayed on other inputs without a
+    wait in between; two streams with a workspace each.  Rows of y that start on 16 bytes and that do not."""
+    w, ws, _, _ = operands(n, rows, cols, 2)
+    x = torch.randn(n, cols, device="cuda")
+    q, xs = torch.empty(n, cols, dtype=torch.uint8, device="cuda").view(E4M3), torch.empty(n, cols // 128, device="cuda")
+    spaces = [abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols)) for _ in range(2)]
+
+    def output():
+        return torch.zeros(n, rows + pad, dtype=dtype, device="cuda")[:, :rows]
+
+    y = output()
+
+    def step():
+        abi.ds_fp8_quantize(x, 1, q, xs)
+        abi.ds_gemm_fp8(w, ws, q, xs, y, spaces[0])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+    torch.cuda.synchronize()
+    inputs = [torch.randn(n, cols, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda") for i in range(4)]
+    outs = [output() for _ in inputs]
+    for v, o in zip(inputs, outs):
+        x.copy_(v)
+        graph.replay()
+        o.copy_(y)
+    torch.cuda.synchronize()
+    for v, o in zip(inputs, outs):
+        abi.ds_fp8_quantize(v, 1, q, xs)
+        close(o, *product(w, ws, q, xs), cols)
+    last = outs[-1]  # of the codes and scales that lie there now
+    streams, outs = [torch.cuda.Stream(), torch.cuda.Stream()], [[output() for _ in range(12)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(12):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                abi.ds_gemm_fp8(w, ws, q, xs, outs[i][k], spaces[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, last) for out in outs for o in out)
+    assert all(abi.ds_workspace_error(s) == 0 for s in spaces)
+
+
+@pytest.mark.parametrize("n,rows,cols", [
+    (1, 64, 4096), (16, 160 * 128, 4096), (1, 100 * 128, 15360), (64, 1000, 14336), (64, 80 * 256, 15360), (65, 300, 4096),
+    (96, 19456, 300), (100, 19457, 300), (128, 80 * 256, 15360), (128, 40000, 1000), (300, 39 * 256, 4096),
+    (256, 40 * 256, 15360), (1500, 1000, 4096), (700, 1003, 8192)])
+def test_product_divisions_in_bf16(abi, n, rows, cols):
+    """Every division of the tiles with bf16 outputs, rows apart and not; the gaps stay as they were."""
+    w, ws, x, xs = operands(n, rows, cols, n + rows + cols)
+    space = abi.workspace(abi.ds_gemm_fp8_workspace_bytes(n, rows, cols))
+    want = product(w, ws, x, xs)
+    for pad in (0, 3, 8):
+        buf = torch.full((n, rows + pad), 7.0, dtype=BF16, device="cuda")
+        abi.ds_gemm_fp8(w, ws, x, xs, buf[:, :rows], space)
+        assert abi.ds_workspace_error(space) == 0
+        close(buf[:, :rows], *want, cols)
+        assert (buf[:, rows:] == 7).all()
