@@ -33,8 +33,10 @@ struct F8Args {
 // regard to the tiles leave most CTAs the parts of two, with an end and a partial
 // sum each: 64 rows by 28,672 x 4,096 take 29.9 us like that, with 112 CTAs of 152
 // and a tile each 22.5; 28,672 x 1,024 15.7 and 8.1.  They pay where whole tiles
-// would leave many SMs idle for long.  Steps times runs stay below 2^32: fewer
-// split tiles than CTAs, 2^17 steps a tile.
+// would leave many SMs idle for long.  (Measured on three matrices in turn, which
+// fit L2 together but for those of 28,672 x 4,096: of the smaller ones' steps from
+// HBM a join may cost fewer.)  Steps times runs stay below 2^32: fewer split tiles
+// than CTAs, 2^17 steps a tile.
 inline unsigned f8_runs(int split, int kb, int ctas, int bn) {
     if (split == 0) return 1;
     const auto join = [&](int m) {  // of m partial sums a tile

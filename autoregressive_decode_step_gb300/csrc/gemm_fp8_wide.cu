@@ -17,10 +17,11 @@
 // one to a pair or is cut into runs of steps (f8_runs) whose partial sums a second
 // launch adds in order.
 //
-// Measured in a graph: 8,192 rows by 28,672 x 4,096 664 us (2.90 PFLOP/s, 1.51 of
-// the measured bf16 rate; on values of a wide spread 790 us at the power limit),
-// the tensor pipe active 61 % of the cycles (the issue slots 54 %: half of it the
-// sums); 256 by 4,096 x 14,336 25 us, 7 of them joining four partial sums a tile.
+// Measured in a graph: 8,192 rows by 28,672 x 4,096 661 us (2.91 PFLOP/s, 1.52 of
+// the measured bf16 rate) until the card is at its power limit, where an SM runs at
+// 1.58 GHz, 750 us then; the tensor pipe active 63 % of the cycles (the issue slots
+// 54 %: half of it the sums); 256 by 4,096 x 14,336 25 us, some 8 of them joining
+// four partial sums a tile.
 #include <algorithm>
 #include <atomic>
 

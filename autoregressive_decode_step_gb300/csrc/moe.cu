@@ -22,18 +22,21 @@
 // type, side by side as further columns, that add up to it: one bf16 piece for
 // bf16 activations, three (24 bits, exact) for fp32; e4m3 pieces of four bits
 // each, a sixteenth apart, behind a power of two per token and 128 values that
-// brings the largest below 2^8: six for fp32 (24 bits, to 2^-38 of the largest),
-// three for bf16 (two hold its 8 bits; the third those of values below 2^-14 of
-// the largest, to 2^-26 of it).  The intermediate is fp32 and goes in three bf16
+// brings the largest to [2^7, 2^8): six for fp32 (24 bits, to 2^-37 of the largest:
+// the last piece is off by half of e4m3's least step, 2^-10, and counts 2^-20), three
+// for bf16 (two hold its 8 bits; the third those of values below 2^-14 of the
+// largest, to 2^-25 of it).  The intermediate is fp32 and goes in three bf16
 // pieces (24 bits) or six e4m3 ones, before bf16 outputs in four of e4m3 (16 bits
-// and more: see MoeCfg).  Sums leave the tensor core every 128 products (e4m3: a block, for its scale; bf16: see
-// kMoeBatch) and are fp32.  The logits are sums of exact products with their rounding errors
-// carried along (two floats, added up in 64 bits): the choice of experts is that
-// of 64 bits.
+// and more: see MoeCfg).  Sums leave the tensor core every 128 products (e4m3: a
+// block, for its scale; bf16: see kMoeBatch) and are fp32.  The logits are sums of
+// products with the rounding errors of both carried along (two floats, some 45 bits
+// of the products' magnitudes, fewer of products below 2^-102, whose errors leave
+// fp32's range; compared in 64 bits): the choice of experts is that of 64 bits
+// unless two are as close as that.
 //
 // Measured in a graph: 64 tokens through 2 of 8 experts of 4,096 x 14,336 (fp32,
-// bf16 weights) 477 us, 5.9 TB/s of 6.8; 64 through 8 of 128 of 2,048 x 768 (bf16,
-// e4m3) 137 us, 4.4 TB/s; one token through those in bf16 37 us, 2.1 TB/s: some 20
+// bf16 weights) 476 us, 5.9 TB/s of 6.8; 64 through 8 of 128 of 2,048 x 768 (bf16,
+// e4m3) 138 us, 4.3 TB/s; one token through those in bf16 37 us, 2.1 TB/s: some 20
 // us are the phases' latencies (a layer of no size takes 21), 6 of them the ends of
 // the two products (partial sums out, counted, read, and code that runs once: some
 // 25 cycles an instruction until it is fetched).

@@ -24,8 +24,8 @@
  *    the workspace's error word (see ds_workspace_error).
  *  - Identical inputs give bit-identical outputs run to run: no reduction
  *    depends on the order in which thread blocks finish.
- *  - fp32 activations; weights fp32 or bf16; KV cache fp32 or bf16; fp32
- *    accumulation.
+ *  - fp32 activations and fp32 or bf16 weights, unless a call names others;
+ *    KV cache fp32 or bf16; fp32 accumulation.
  */
 #ifndef DECODE_STEP_H
 #define DECODE_STEP_H
@@ -242,7 +242,8 @@ DS_API size_t ds_gemm_fp8_workspace_bytes(int64_t n, int64_t rows, int64_t cols)
 /* Y[s][r] = sum_b x_scales[s][b] * w_scales[r / 128][b]
  *           * sum_{c in [128 b, 128 b + 128), c < cols} X[s][c] * W[r][c]
  * for s < n, r < rows: ds_gemm's untransposed product of e4m3 operands, the
- * products of a block summed by the tensor cores in fp32, the blocks in fp32.
+ * products of a block summed by the tensor cores in fp32, the blocks in fp32,
+ * the two scales multiplied first, in fp32 (past its range infinite or zero).
  * n is any count from a single token to a whole prompt.
  *   W: e4m3, rows w_stride bytes apart; w_scales: fp32 [ceil(rows / 128)]
  *   [ceil(cols / 128)] (569).  X: e4m3 [n], rows x_stride bytes apart;
@@ -269,7 +270,8 @@ DS_API int ds_gemm_fp8(const void *W, int64_t w_len, int64_t w_stride, const flo
  *
  * The feed-forward of a decoder whose tokens each go through a few of many
  * experts, for a decode step's tokens: of the weights only the chosen
- * experts' are read, each once.
+ * experts' are read, once for each 32 tokens of an expert (16 with fp32 x and
+ * e4m3 weights), one after the other.
  * ------------------------------------------------------------------- */
 
 /* Workspace bytes ds_moe_layer needs; 0 for sizes that it refuses. */
@@ -290,13 +292,15 @@ DS_API size_t ds_moe_layer_workspace_bytes(int64_t n, int64_t d, int64_t ff, int
  *   128)][ceil(d / 128)], down_scales [n_experts][ceil(d / 128)][ceil(ff /
  *   128)] (with bf16 NULL, else 577, and 0).  569 for a weight's or scale's length.
  *   expert_ids, expert_weights: e_i and p_i [n][top_k], either may be NULL.
- * Logits are exact to some 45 bits, the choice of experts that of 64-bit
- * arithmetic; sums are fp32, of factors of 24 bits (with e4m3 experts before a
- * bf16 y the intermediate has 16); y is rounded once.  Before e4m3 weights a value of x or
- * of the intermediate is held to 2^-38 (bf16 x: 2^-26, intermediate 2^-30) of the
- * largest of its 128, whatever its own size.  Weights are finite; a value of x that is
- * not, or a product that overflows fp32, makes outputs of its own token (and
- * of no other) NaN or infinite.
+ * Logits are held to some 2^-45 of the sum of their products' magnitudes
+ * (products above 2^-102; of smaller ones fewer bits are left), and the choice of
+ * experts is that of 64-bit arithmetic where logits are farther apart than that.
+ * Sums are fp32, of factors of 24 bits (with e4m3 experts before a bf16 y the
+ * intermediate has 16); y is rounded once.  Before e4m3 weights a value of x or
+ * of the intermediate is held to 2^-37 (bf16 x: 2^-25, intermediate 2^-29) of
+ * the largest of its 128, whatever its own size: a smaller one may be lost.
+ * Weights are finite; a value of x that is not, or a product that overflows
+ * fp32, makes outputs of its own token (and of no other) NaN or infinite.
  *   n <= 256, n_experts <= 512, top_k <= 16 (564), top_k <= n_experts (577);
  *   d and ff multiples of 8 with bf16 weights, of 16 with e4m3 (577); x, the
  *   router and the experts' matrices 16-byte aligned (577).  y may be x or
