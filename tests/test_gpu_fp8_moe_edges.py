@@ -73,6 +73,57 @@ def test_product_and_experts_on_one_workspace(abi):
     assert abi.ds_workspace_error(space) == 0
 
 
+def test_two_graphs_share_a_workspace(abi):
+    """A graph of products and the experts and one of the experts and a product, on one workspace, replayed in turn
+    without a wait in between."""
+    products = [(30, 1000, 4096), (256, 1024, 4096), (1, 6144, 4096)]
+    layers = [Layer(7, 1000, 344, 60, 4, x=BF16, seed=1), Layer(33, 128, 640, 3, 3, w=E4M3, seed=2)]
+    space = abi.workspace(max([abi.ds_gemm_fp8_workspace_bytes(*s) for s in products] +
+                              [abi.ds_moe_layer_workspace_bytes(a.n, a.d, a.ff, a.e, a.k) for a in layers]))
+    ops = [operands(*s, seed=i) for i, s in enumerate(products)]
+    ys = [torch.zeros(n, rows, device="cuda") for n, rows, _ in products]
+    zs = [torch.zeros_like(a.x) for a in layers]
+
+    def multiply(i):
+        w, wsc, x, xsc = ops[i]
+        abi.ds_gemm_fp8(w, wsc, x, xsc, ys[i], space)
+
+    def layer(i):
+        a = layers[i]
+        abi.ds_moe_layer(a.x, a.router, a.k, a.norm, a.gu, a.gs, a.dn, a.ds, a.residual, zs[i], None, None, space)
+
+    def first():
+        multiply(0)
+        layer(0)
+        multiply(1)
+
+    def second():
+        layer(1)
+        multiply(2)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    with torch.cuda.stream(side):
+        for f in (first, second):
+            f()
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=side):
+                f()
+    torch.cuda.synchronize()
+    eager = [t.clone() for t in ys + zs]
+    for t in ys + zs:
+        t.zero_()
+    for _ in range(10):
+        for g in graphs:
+            g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(t, e) for t, e in zip(ys + zs, eager))
+    for i, (n, rows, cols) in enumerate(products):
+        close(ys[i], *product(*ops[i]), cols)
+    assert abi.ds_workspace_error(space) == 0
+
+
 # ---------------------------------------------------------------- launches that overlap
 @pytest.mark.parametrize("n,rows,cols", [(1, 6144, 4096), (8, 512, 4096), (64, 28672, 1024), (128, 512, 2048),
                                          (256, 1024, 4096), (700, 300, 1000)])
